@@ -17,6 +17,8 @@ import torch
 
 from . import _abi
 from ._abi import BdrError, BDR_BF16, BDR_BF16_PACKED, BDR_F32  # noqa: F401
+from .training import (dspark_ce_backward, dspark_ce_loss, dspark_distill_backward,
+                       dspark_distill_loss, dspark_norm, dspark_norm_backward)
 
 __all__ = [
     "dflash_fuse_fc", "dspark_lm_head", "dspark_markov_argmax", "dspark_draft_block",
@@ -24,6 +26,8 @@ __all__ = [
     "spec_verify_greedy", "dspark_gumbel_noise", "dspark_markov_sample", "spec_verify_sample",
     "spec_commit", "dflash_fuse_fc_rows", "dflash_fuse_fc_fp8", "dspark_lm_head_fp8",
     "dflash_hc_average", "dflash_fuse_fc_rows_fp8", "PackedWeight", "pack_weight",
+    "dspark_norm", "dspark_norm_backward", "dspark_ce_loss", "dspark_ce_backward",
+    "dspark_distill_loss", "dspark_distill_backward",
     "workspace_bytes", "lib", "BdrError", "set_markov_poll_timeout_us",
     "set_markov_forced_time_out", "MARKOV_TIMED_OUT",
 ]

@@ -20,6 +20,8 @@ BDR_EHIP = -4
 MAX_TAPS = 8
 MAX_K = 16
 MAX_RANK = 128
+MAX_TEACHER = 256
+MAX_NORM_HIDDEN = 16384
 
 _vp = C.c_void_p
 _i64 = C.c_int64
@@ -72,6 +74,21 @@ SIGNATURES = {
     "dflash_fuse_fc_rows_workspace_bytes": (_sz, [_i64, _i64, _int, _int]),
     "dflash_fuse_fc_rows": (_int, [C.POINTER(_vp), _int, _i64, _i64, _int, _vp, _vp, _i64, _vp,
                                    _vp, _vp, _sz, _vp]),
+    "dspark_norm": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _vp, C.c_float, _vp, _vp, _vp, _vp]),
+    "dspark_norm_backward_workspace_bytes": (_sz, [_i64, _i64]),
+    "dspark_norm_backward": (_int, [_vp, _i64, _vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _vp,
+                                    _vp, _vp, _vp, _sz, _vp]),
+    "dspark_ce_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int, _int]),
+    "dspark_ce_loss": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp, _vp, _vp,
+                              _vp, _sz, _vp]),
+    "dspark_ce_backward": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp, _vp,
+                                  _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dspark_distill_workspace_bytes": (_sz, [_i64, _i64, _i64, _int, _int, _int, _int]),
+    "dspark_distill_loss": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp, _vp,
+                                   _int, _int, C.c_float, _vp, _vp, _vp, _vp, _sz, _vp]),
+    "dspark_distill_backward": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp,
+                                       _vp, _int, _int, C.c_float, _vp, _vp, _vp, _vp, _vp, _vp,
+                                       _vp, _vp, _sz, _vp]),
 }
 
 _lib = None

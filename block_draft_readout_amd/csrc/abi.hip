@@ -784,4 +784,315 @@ int dflash_fuse_fc_rows_fp8(const void* const* taps, int n_taps, int64_t rows, i
   return BDR_OK;
 }
 
+// ---------------------------------------------------------------------------- training: row norm
+namespace {
+
+int norm_shape(int64_t rows, int64_t hidden, int dt) {
+  if (!valid_dtype(dt)) return fail(BDR_EINVAL, "unknown dtype %d", dt);
+  if (rows < 0) return fail(BDR_EINVAL, "rows must be >= 0");
+  if (hidden <= 0) return fail(BDR_EINVAL, "hidden must be > 0");
+  if (hidden > BDR_MAX_NORM_HIDDEN)
+    return fail(BDR_EUNSUPPORTED, "hidden %lld > %d", static_cast<long long>(hidden),
+                BDR_MAX_NORM_HIDDEN);
+  const int e = dt == BDR_BF16 ? 8 : 4;
+  if (hidden % e)
+    return fail(BDR_EUNSUPPORTED, "hidden %lld must be a multiple of %d for this dtype",
+                static_cast<long long>(hidden), e);
+  if (rows > kMaxVocab) return fail(BDR_EUNSUPPORTED, "rows must be < 2^31 - 1");
+  return BDR_OK;
+}
+
+int norm_stride(int64_t rows, int64_t hidden, int64_t stride, int dt, const char* name) {
+  const int e = dt == BDR_BF16 ? 8 : 4;
+  if (stride < hidden || stride % e)
+    return fail(BDR_EINVAL, "%s must be a multiple of %d and at least hidden", name, e);
+  if (rows > 0 && stride > kMaxElems / rows) return fail(BDR_EUNSUPPORTED, "%s too large", name);
+  return BDR_OK;
+}
+
+// [p, p + bytes) and [q, q + qbytes) share an address
+bool overlap(const void* p, int64_t bytes, const void* q, int64_t qbytes) {
+  const uintptr_t a = reinterpret_cast<uintptr_t>(p), b = reinterpret_cast<uintptr_t>(q);
+  return a < b + static_cast<uintptr_t>(qbytes) && b < a + static_cast<uintptr_t>(bytes);
+}
+
+}  // namespace
+
+int dspark_norm(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, bdr_dtype dt,
+                const void* weight, const void* bias, float eps, void* y, float* mean,
+                float* rstd, void* stream) {
+  BDR_TRY(norm_shape(rows, hidden, dt));
+  BDR_TRY(norm_stride(rows, hidden, x_stride, dt, "x_stride"));
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(BDR_EINVAL, "eps must be finite and >= 0");
+  if (rows == 0) return BDR_OK;
+  BDR_TRY(need_ptr(x, "x"));
+  BDR_TRY(need_ptr(weight, "weight"));
+  if (bias) BDR_TRY(need_ptr(bias, "bias"));
+  BDR_TRY(need_ptr(y, "y"));
+  if (mean) BDR_TRY(need_ptr(mean, "mean", 4));
+  BDR_TRY(need_ptr(rstd, "rstd", 4));
+  const int64_t es = dt == BDR_BF16 ? 2 : 4;
+  if (!(x == y && x_stride == hidden) &&
+      overlap(x, ((rows - 1) * x_stride + hidden) * es, y, rows * hidden * es))
+    return fail(BDR_EINVAL, "y overlaps x (only y == x with x_stride == hidden may)");
+  BDR_TRY(check_device());
+  const hipError_t e = launch_norm(x, rows, hidden, x_stride, dt, weight, bias, eps, y, mean, rstd,
+                                   as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "dspark_norm launch");
+  return BDR_OK;
+}
+
+size_t dspark_norm_backward_workspace_bytes(int64_t rows, int64_t hidden) {
+  if (norm_shape(rows, hidden, BDR_F32) != BDR_OK || rows == 0) return 0;
+  return norm_workspace(rows, hidden);
+}
+
+int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                         int64_t rows, int64_t hidden, bdr_dtype dt, const void* weight,
+                         const float* mean, const float* rstd, void* dx, void* dweight,
+                         void* dbias, void* workspace, size_t workspace_bytes, void* stream) {
+  BDR_TRY(norm_shape(rows, hidden, dt));
+  BDR_TRY(norm_stride(rows, hidden, x_stride, dt, "x_stride"));
+  BDR_TRY(norm_stride(rows, hidden, dy_stride, dt, "dy_stride"));
+  if (dweight) BDR_TRY(need_ptr(dweight, "dweight"));
+  if (dbias) BDR_TRY(need_ptr(dbias, "dbias"));
+  const int64_t es = dt == BDR_BF16 ? 2 : 4;
+  if (rows == 0) {
+    if (!dweight && !dbias) return BDR_OK;
+    BDR_TRY(check_device());
+    for (void* p : {dweight, dbias})
+      if (p) {
+        const hipError_t e = launch_clear(p, hidden * es, as_stream(stream));
+        if (e != hipSuccess) return hip_fail(e, "dspark_norm_backward clear");
+      }
+    return BDR_OK;
+  }
+  if (!dx && !dweight && !dbias) return fail(BDR_EINVAL, "no gradient is wanted");
+  BDR_TRY(need_ptr(dy, "dy"));
+  BDR_TRY(need_ptr(x, "x"));
+  BDR_TRY(need_ptr(weight, "weight"));
+  if (mean) BDR_TRY(need_ptr(mean, "mean", 4));
+  BDR_TRY(need_ptr(rstd, "rstd", 4));
+  if (dx) {
+    BDR_TRY(need_ptr(dx, "dx"));
+    const int64_t out = rows * hidden * es;
+    if ((!(dx == dy && dy_stride == hidden) &&
+         overlap(dy, ((rows - 1) * dy_stride + hidden) * es, dx, out)) ||
+        overlap(x, ((rows - 1) * x_stride + hidden) * es, dx, out))
+      return fail(BDR_EINVAL, "dx overlaps dy or x (only dx == dy with dy_stride == hidden may)");
+  }
+  if (dweight || dbias) BDR_TRY(need_ws(workspace, workspace_bytes, norm_workspace(rows, hidden)));
+  BDR_TRY(check_device());
+  const hipError_t e = launch_norm_backward(dy, dy_stride, x, x_stride, rows, hidden, dt, weight,
+                                            mean, rstd, dx, dweight, dbias, workspace,
+                                            as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "dspark_norm_backward launch");
+  return BDR_OK;
+}
+
+// ---------------------------------------------------------------------------- training: losses
+namespace {
+
+constexpr int64_t kMaxLossRows = int64_t(1) << 20;
+constexpr int64_t kMaxLossHidden = int64_t(1) << 20;
+
+// the sizes of a loss call (top == 0: cross entropy)
+int loss_shape(int64_t rows, int64_t hidden, int64_t vocab, int rank, int dt, int top, bool distill) {
+  if (!valid_dtype(dt)) return fail(BDR_EINVAL, "unknown dtype %d", dt);
+  if (rows < 0) return fail(BDR_EINVAL, "rows must be >= 0");
+  if (hidden <= 0) return fail(BDR_EINVAL, "hidden must be > 0");
+  if (vocab <= 0) return fail(BDR_EINVAL, "vocab must be > 0");
+  if (rank < 0) return fail(BDR_EINVAL, "rank must be >= 0");
+  if (rows > kMaxLossRows || hidden > kMaxLossHidden || vocab > kMaxMarkovVocab)
+    return fail(BDR_EUNSUPPORTED, "rows and hidden must be <= 2^20 and vocab <= 2^21 here");
+  if (rank > BDR_MAX_RANK) return fail(BDR_EUNSUPPORTED, "rank %d > %d", rank, BDR_MAX_RANK);
+  const int e = dt == BDR_BF16 ? 8 : 4;
+  if (hidden % e || rank % e)
+    return fail(BDR_EUNSUPPORTED, "hidden %lld and rank %d must be multiples of %d for this dtype",
+                static_cast<long long>(hidden), rank, e);
+  if (distill && top < 1) return fail(BDR_EINVAL, "top must be >= 1, got %d", top);
+  if (distill && top > BDR_MAX_TEACHER)
+    return fail(BDR_EUNSUPPORTED, "top %d > %d", top, BDR_MAX_TEACHER);
+  return BDR_OK;
+}
+
+LossProblem loss_sizes(int64_t rows, int64_t hidden, int64_t vocab, int rank, bdr_dtype dt, int top) {
+  LossProblem p{};
+  p.rows = rows;
+  p.hidden = hidden;
+  p.vocab = vocab;
+  p.rank = rank;
+  p.dt = dt;
+  p.top = top;
+  p.temperature = 1.0f;
+  return p;
+}
+
+// the tensors every loss call reads
+int loss_inputs(const LossProblem& p) {
+  BDR_TRY(need_ptr(p.x, "hidden"));
+  BDR_TRY(need_ptr(p.w, "lm_head_w"));
+  if (p.rank) {
+    BDR_TRY(need_ptr(p.w1, "markov_w1"));
+    BDR_TRY(need_ptr(p.w2, "markov_w2"));
+    BDR_TRY(need_ptr(p.prev, "prev_token", 4));
+  }
+  if (p.top) {
+    BDR_TRY(need_ptr(p.ids, "teacher_ids", 4));
+    BDR_TRY(need_ptr(p.u, "teacher_logits", p.u_dt == BDR_BF16 ? 2 : 4));
+  } else {
+    BDR_TRY(need_ptr(p.labels, "labels", 4));
+  }
+  return BDR_OK;
+}
+
+int loss_run_forward(const LossProblem& p, float* loss, float* lse, float* picked, void* workspace,
+                     size_t workspace_bytes, void* stream, const char* name) {
+  if (p.rows == 0) return BDR_OK;
+  BDR_TRY(loss_inputs(p));
+  BDR_TRY(need_ptr(loss, "loss", 4));
+  BDR_TRY(need_ptr(lse, "lse", 4));
+  if (p.top) BDR_TRY(need_ptr(picked, "picked", 4));
+  BDR_TRY(need_ws(workspace, workspace_bytes, loss_workspace(p, false)));
+  BDR_TRY(check_device());
+  const hipError_t e = launch_loss_forward(p, workspace, loss, lse, picked, as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, name);
+  return BDR_OK;
+}
+
+int loss_run_backward(const LossProblem& p, const LossGrads& o, const float* lse,
+                      const float* picked, const float* loss_grad, void* workspace,
+                      size_t workspace_bytes, void* stream, const char* name) {
+  if (!p.rank && (o.w1 || o.w2))
+    return fail(BDR_EINVAL, "Markov gradients are wanted without a Markov head");
+  if (o.hidden && p.rows) BDR_TRY(need_ptr(o.hidden, "d_hidden"));
+  if (o.w) BDR_TRY(need_ptr(o.w, "d_lm_head_w"));
+  if (o.w1) BDR_TRY(need_ptr(o.w1, "d_markov_w1"));
+  if (o.w2) BDR_TRY(need_ptr(o.w2, "d_markov_w2"));
+  if (p.rows == 0) {
+    if (!o.w && !o.w1 && !o.w2) return BDR_OK;
+    BDR_TRY(check_device());
+    const hipError_t e = launch_loss_clear(p, o, as_stream(stream));
+    if (e != hipSuccess) return hip_fail(e, name);
+    return BDR_OK;
+  }
+  if (!o.hidden && !o.w && !o.w1 && !o.w2) return fail(BDR_EINVAL, "no gradient is wanted");
+  BDR_TRY(loss_inputs(p));
+  BDR_TRY(need_ptr(lse, "lse", 4));
+  if (p.top) BDR_TRY(need_ptr(picked, "picked", 4));
+  BDR_TRY(need_ptr(loss_grad, "loss_grad", 4));
+  BDR_TRY(need_ws(workspace, workspace_bytes, loss_workspace(p, true)));
+  BDR_TRY(check_device());
+  const hipError_t e = launch_loss_backward(p, o, workspace, lse, picked, loss_grad,
+                                            as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, name);
+  return BDR_OK;
+}
+
+// the Markov head of a loss call: both matrices or neither, neither meaning rank 0
+int loss_markov(LossProblem& p, const void* w1, const void* w2, const int32_t* prev) {
+  if ((w1 == nullptr) != (w2 == nullptr) && p.rank && p.rows)
+    return fail(BDR_EINVAL, "markov_w1 and markov_w2 must both be given or both be NULL");
+  if (!w1 && !w2 && p.rows) p.rank = 0;
+  p.w1 = w1;
+  p.w2 = w2;
+  p.prev = prev;
+  return BDR_OK;
+}
+
+}  // namespace
+
+size_t dspark_ce_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab, int rank,
+                                 bdr_dtype dt, int backward) {
+  if (loss_shape(rows, hidden, vocab, rank, dt, 0, false) != BDR_OK || rows == 0) return 0;
+  return loss_workspace(loss_sizes(rows, hidden, vocab, rank, dt, 0), backward != 0);
+}
+
+int dspark_ce_loss(const void* hidden, int64_t rows, int64_t hidden_size, int64_t vocab,
+                   bdr_dtype dt, const void* lm_head_w, const void* markov_w1,
+                   const void* markov_w2, int rank, const int32_t* prev_token,
+                   const int32_t* labels, float* loss, float* lse, void* workspace,
+                   size_t workspace_bytes, void* stream) {
+  BDR_TRY(loss_shape(rows, hidden_size, vocab, rank, dt, 0, false));
+  LossProblem p = loss_sizes(rows, hidden_size, vocab, rank, dt, 0);
+  BDR_TRY(loss_markov(p, markov_w1, markov_w2, prev_token));
+  p.x = hidden;
+  p.w = lm_head_w;
+  p.labels = labels;
+  return loss_run_forward(p, loss, lse, nullptr, workspace, workspace_bytes, stream,
+                          "dspark_ce_loss launch");
+}
+
+int dspark_ce_backward(const void* hidden, int64_t rows, int64_t hidden_size, int64_t vocab,
+                       bdr_dtype dt, const void* lm_head_w, const void* markov_w1,
+                       const void* markov_w2, int rank, const int32_t* prev_token,
+                       const int32_t* labels, const float* lse, const float* loss_grad,
+                       void* d_hidden, void* d_lm_head_w, void* d_markov_w1, void* d_markov_w2,
+                       void* workspace, size_t workspace_bytes, void* stream) {
+  BDR_TRY(loss_shape(rows, hidden_size, vocab, rank, dt, 0, false));
+  LossProblem p = loss_sizes(rows, hidden_size, vocab, rank, dt, 0);
+  BDR_TRY(loss_markov(p, markov_w1, markov_w2, prev_token));
+  p.x = hidden;
+  p.w = lm_head_w;
+  p.labels = labels;
+  return loss_run_backward(p, LossGrads{d_hidden, d_lm_head_w, d_markov_w1, d_markov_w2}, lse,
+                           nullptr, loss_grad, workspace, workspace_bytes, stream,
+                           "dspark_ce_backward launch");
+}
+
+size_t dspark_distill_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab, int rank,
+                                      int top, bdr_dtype dt, int backward) {
+  if (loss_shape(rows, hidden, vocab, rank, dt, top, true) != BDR_OK || rows == 0) return 0;
+  return loss_workspace(loss_sizes(rows, hidden, vocab, rank, dt, top), backward != 0);
+}
+
+namespace {
+
+int distill_problem(LossProblem& p, const void* hidden, const void* lm_head_w,
+                    const int32_t* ids, const void* logits, int teacher_dt, float temperature) {
+  if (!valid_dtype(teacher_dt)) return fail(BDR_EINVAL, "unknown teacher dtype %d", teacher_dt);
+  if (!(temperature > 0.f) || !std::isfinite(temperature))
+    return fail(BDR_EINVAL, "temperature must be finite and > 0");
+  p.x = hidden;
+  p.w = lm_head_w;
+  p.ids = ids;
+  p.u = logits;
+  p.u_dt = static_cast<bdr_dtype>(teacher_dt);
+  p.temperature = temperature;
+  return BDR_OK;
+}
+
+}  // namespace
+
+int dspark_distill_loss(const void* hidden, int64_t rows, int64_t hidden_size, int64_t vocab,
+                        bdr_dtype dt, const void* lm_head_w, const void* markov_w1,
+                        const void* markov_w2, int rank, const int32_t* prev_token,
+                        const int32_t* teacher_ids, const void* teacher_logits, int top,
+                        bdr_dtype teacher_dt, float temperature, float* loss, float* lse,
+                        float* picked, void* workspace, size_t workspace_bytes, void* stream) {
+  BDR_TRY(loss_shape(rows, hidden_size, vocab, rank, dt, top, true));
+  LossProblem p = loss_sizes(rows, hidden_size, vocab, rank, dt, top);
+  BDR_TRY(loss_markov(p, markov_w1, markov_w2, prev_token));
+  BDR_TRY(distill_problem(p, hidden, lm_head_w, teacher_ids, teacher_logits, teacher_dt, temperature));
+  return loss_run_forward(p, loss, lse, picked, workspace, workspace_bytes, stream,
+                          "dspark_distill_loss launch");
+}
+
+int dspark_distill_backward(const void* hidden, int64_t rows, int64_t hidden_size, int64_t vocab,
+                            bdr_dtype dt, const void* lm_head_w, const void* markov_w1,
+                            const void* markov_w2, int rank, const int32_t* prev_token,
+                            const int32_t* teacher_ids, const void* teacher_logits, int top,
+                            bdr_dtype teacher_dt, float temperature, const float* lse,
+                            const float* picked, const float* loss_grad, void* d_hidden,
+                            void* d_lm_head_w, void* d_markov_w1, void* d_markov_w2,
+                            void* workspace, size_t workspace_bytes, void* stream) {
+  BDR_TRY(loss_shape(rows, hidden_size, vocab, rank, dt, top, true));
+  LossProblem p = loss_sizes(rows, hidden_size, vocab, rank, dt, top);
+  BDR_TRY(loss_markov(p, markov_w1, markov_w2, prev_token));
+  BDR_TRY(distill_problem(p, hidden, lm_head_w, teacher_ids, teacher_logits, teacher_dt, temperature));
+  return loss_run_backward(p, LossGrads{d_hidden, d_lm_head_w, d_markov_w1, d_markov_w2}, lse,
+                           picked, loss_grad, workspace, workspace_bytes, stream,
+                           "dspark_distill_backward launch");
+}
+
 }  // extern "C"

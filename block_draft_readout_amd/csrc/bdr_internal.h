@@ -70,6 +70,54 @@ hipError_t launch_fc_rows_fp8(const void* const* taps, int n_taps, int64_t rows,
                               int64_t max_rows, const uint8_t* fc_q, const float* fc_scale,
                               void* out, void* workspace, hipStream_t stream);
 
+// ----------------------------------------------------------------------------
+// Row normalisation, forward and backward.
+// ----------------------------------------------------------------------------
+size_t norm_workspace(int64_t rows, int64_t hidden);
+hipError_t launch_norm(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, bdr_dtype dt,
+                       const void* w, const void* b, float eps, void* y, float* mean, float* rstd,
+                       hipStream_t stream);
+hipError_t launch_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                                int64_t rows, int64_t hidden, bdr_dtype dt, const void* w,
+                                const float* mean, const float* rstd, void* dx, void* dw, void* db,
+                                void* workspace, hipStream_t stream);
+
+// ----------------------------------------------------------------------------
+// Vocabulary losses: cross entropy (top == 0) and distillation.
+// ----------------------------------------------------------------------------
+struct LossProblem {
+  const void* x;           // [rows, hidden]
+  int64_t rows, hidden, vocab;
+  bdr_dtype dt;
+  const void* w;           // [vocab, hidden]
+  const void* w1;          // [vocab, rank]
+  const void* w2;
+  int rank;
+  const int32_t* prev;     // [rows]
+  const int32_t* labels;   // cross entropy [rows]
+  int top;                 // distillation: teacher entries per row
+  const int32_t* ids;      // [rows, top]
+  const void* u;           // [rows, top]
+  bdr_dtype u_dt;
+  float temperature;       // 1 for cross entropy
+};
+struct LossGrads {         // each may be NULL
+  void* hidden;
+  void* w;
+  void* w1;
+  void* w2;
+};
+size_t loss_workspace(const LossProblem& p, bool backward);
+hipError_t launch_loss_forward(const LossProblem& p, void* workspace, float* loss, float* lse,
+                               float* picked, hipStream_t stream);
+hipError_t launch_loss_backward(const LossProblem& p, const LossGrads& out, void* workspace,
+                                const float* lse, const float* picked, const float* loss_grad,
+                                hipStream_t stream);
+// zero fill of bytes % 16 == 0 with vector stores
+hipError_t launch_clear(void* p, int64_t bytes, hipStream_t stream);
+// the gradients of a call without rows: zeros
+hipError_t launch_loss_clear(const LossProblem& p, const LossGrads& out, hipStream_t stream);
+
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace bdr

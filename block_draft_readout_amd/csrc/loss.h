@@ -1,0 +1,22 @@
+// Host-side description of one vocabulary-loss call (cross entropy or
+// distillation), shared by the loss translation units.
+#pragma once
+
+#include "loss_gemm.h"
+
+namespace bdr {
+
+// Kinds of matrix products, each with its own translation unit:
+// the logits' statistics and d logits (reduction fast on both sides), d hidden
+// (d logits fast, weights slow) and d weight (both slow).
+hipError_t launch_loss_stats(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
+hipError_t launch_loss_dlogits(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
+hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
+hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
+
+// vocabulary columns of one statistics tile
+int loss_stats_cols(bdr_dtype dt, int64_t rows);
+// reduction splits of a d hidden product over `width` vocabulary entries
+int loss_dfeat_splits(bdr_dtype dt, int64_t rows, int64_t cols, int64_t width);
+
+}  // namespace bdr

@@ -1,0 +1,653 @@
+// The vocabulary losses that train a drafter (gfx950): softmax cross entropy
+// and distillation from a teacher's top logits, over the logits the drafter
+// drafts with (LM head plus Markov bias), forward and backward, without the
+// logits ever being stored.
+//
+//   z[n, v] = sum_h hidden[n, h] W[v, h] + sum_j w1[prev[n], j] w2[v, j]
+//   lse[n]  = log sum_v exp(z[n, v] / T)
+//   cross entropy (T = 1): loss = lse - z[label],    d z = g (softmax(z) - onehot)
+//   distillation: t = softmax_j(u_j / T) over the row's valid entries,
+//     loss = T^2 sum_j t_j (log t_j - z[id_j] / T + lse),
+//     d z  = g T (softmax(z / T) - sum_j t_j onehot(id_j))
+//
+// The Markov embedding of the previous token is a second stretch of the
+// reduction, so the logits are one product of [hidden | w1[prev]] with
+// [W | w2], and the gradients are the two products of d z with these.
+//
+// Rows without a target take no part: a first pass compacts the others
+// (hidden, embedding and per-row values) into the workspace, and every product
+// runs on the compacted rows, whose count stays on the device.
+//
+// The forward pass keeps a maximum and a sum per row and vocabulary tile; the
+// backward pass walks the vocabulary in pieces and recomputes a piece's logits
+// straight into d z (the only logits-sized buffer, one piece wide).  Per-row
+// values, softmax sums and d hidden across pieces are fp32; d z is rounded to
+// the storage type, as an operand of matrix products has to be.
+//
+// Every sum has a fixed order: the same inputs give the same bits.
+
+#include <algorithm>
+
+#include "loss.h"
+
+namespace bdr {
+
+namespace {
+
+constexpr int64_t kPieceBytes = int64_t(256) << 20;   // d logits of one piece
+constexpr int64_t kPieceCols = 2560;                  // pieces are multiples of this
+
+// What the row kernels read and write, besides the products.
+struct LossRows {
+  const void* hidden;
+  const void* w1;
+  const void* w2;
+  const void* w;
+  const int32_t* prev;
+  const int32_t* label;    // cross entropy: labels; distillation: 0 or -1 per row
+  const int32_t* ids;      // distillation [rows, top]
+  const void* u;
+  int u_bf16;
+  int64_t rows;
+  int hidden_size, vocab, rank, top;
+  float inv_t, temperature;
+  const float* lse;        // backward inputs
+  const float* loss_grad;
+  // workspace
+  int32_t* live;           // [1]
+  int32_t* pos;            // [rows] compacted row or -1
+  int32_t* row_of;         // [live] original row
+  int32_t* label_c;        // [live]
+  int32_t* prev_c;         // [live] previous token or -1
+  void* x;                 // [live, H]
+  void* e;                 // [live, r]
+  float* lse2;             // [live]
+  float* coef;             // [live]
+  float* t;                // [rows, top]
+  float2* stat;            // [live, tiles]
+  int tiles;
+  float* z_label;          // [live]
+};
+
+// ---------------------------------------------------------------- targets of the distillation
+// t = softmax of a row's valid teacher logits over T, and whether it has any
+// mass; one wave per row.
+__global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, int32_t* has) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (n >= g.rows) return;
+  const int32_t* ids = g.ids + n * g.top;
+  float v[BDR_MAX_TEACHER / 64];
+  float mx = -INFINITY;
+  bool any = false;
+#pragma unroll
+  for (int c = 0; c < BDR_MAX_TEACHER / 64; ++c) {
+    const int j = c * 64 + lane;
+    v[c] = -INFINITY;
+    if (j < g.top && static_cast<uint32_t>(ids[j]) < static_cast<uint32_t>(g.vocab)) {
+      const float u = g.u_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(g.u)[n * g.top + j])
+                               : static_cast<const float*>(g.u)[n * g.top + j];
+      v[c] = u / g.temperature;
+    }
+    mx = fmaxf(mx, v[c]);
+    any |= !(v[c] == -INFINITY);
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) mx = fmaxf(mx, __shfl_xor(mx, m));
+  const bool row_any = __ballot(any) != 0ull;
+  float sum = 0.f;
+#pragma unroll
+  for (int c = 0; c < BDR_MAX_TEACHER / 64; ++c) {
+    v[c] = v[c] == -INFINITY ? 0.f : expf(v[c] - mx);
+    sum += v[c];
+  }
+  sum = wave_sum(sum);
+#pragma unroll
+  for (int c = 0; c < BDR_MAX_TEACHER / 64; ++c) {
+    const int j = c * 64 + lane;
+    if (j < g.top) g.t[n * g.top + j] = row_any ? v[c] / sum : 0.f;
+  }
+  if (lane == 0) has[n] = row_any ? 0 : -1;
+}
+
+// ---------------------------------------------------------------- compaction
+// One workgroup per row: counts the rows with a target before it (its place),
+// copies its hidden state and its Markov embedding there.  Reading the labels
+// before the row again in every workgroup is cheaper than a scan in a launch of
+// its own: 4 bytes a row from L2 against 2 H bytes copied.
+template <typename S, bool BACKWARD>
+__global__ __launch_bounds__(256) void loss_gather_kernel(const LossRows g) {
+  __shared__ int counts[4];
+  const int64_t n = blockIdx.x;
+  const uint32_t V = static_cast<uint32_t>(g.vocab);
+  int c = 0;
+  for (int64_t i = threadIdx.x; i < n; i += 256) c += static_cast<uint32_t>(g.label[i]) < V;
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) c += __shfl_xor(c, m);
+  if ((threadIdx.x & 63) == 0) counts[threadIdx.x >> 6] = c;
+  __syncthreads();
+  const int at = counts[0] + counts[1] + counts[2] + counts[3];
+  const int32_t label = g.label[n];
+  const bool in = static_cast<uint32_t>(label) < V;
+  const int32_t p = g.rank ? g.prev[n] : -1;
+  const bool has_prev = static_cast<uint32_t>(p) < V;
+  if (threadIdx.x == 0) {
+    g.pos[n] = in ? at : -1;
+    if (n == g.rows - 1) *g.live = at + (in ? 1 : 0);
+    if (in) {
+      g.label_c[at] = label;
+      g.row_of[at] = static_cast<int32_t>(n);
+      if (g.rank) g.prev_c[at] = has_prev ? p : -1;
+      if (BACKWARD) {
+        g.lse2[at] = g.lse[n] * kLog2e;
+        g.coef[at] = g.loss_grad[n] * g.temperature;
+      }
+    }
+  }
+  if (!in) return;
+  const int chunks = g.hidden_size / Elem<S>::PER16;
+  const u32x4_t* src = reinterpret_cast<const u32x4_t*>(static_cast<const S*>(g.hidden) +
+                                                        n * g.hidden_size);
+  u32x4_t* dst = reinterpret_cast<u32x4_t*>(static_cast<S*>(g.x) +
+                                            static_cast<int64_t>(at) * g.hidden_size);
+  for (int i = static_cast<int>(threadIdx.x); i < chunks; i += 256) dst[i] = src[i];
+  const int rchunks = g.rank / Elem<S>::PER16;
+  if (static_cast<int>(threadIdx.x) < rchunks) {
+    u32x4_t v{0, 0, 0, 0};
+    if (has_prev)
+      v = reinterpret_cast<const u32x4_t*>(static_cast<const S*>(g.w1) +
+                                           static_cast<int64_t>(p) * g.rank)[threadIdx.x];
+    reinterpret_cast<u32x4_t*>(static_cast<S*>(g.e) + static_cast<int64_t>(at) * g.rank)[threadIdx.x] = v;
+  }
+}
+
+// ---------------------------------------------------------------- loss values
+// log2 of the softmax denominator of one compacted row, in every lane of a wave
+__device__ __forceinline__ float row_lse2(const float2* stat, int tiles, int lane) {
+  float2 v{-INFINITY, 0.f};
+  for (int i = lane; i < tiles; i += 64) v = merge_stat(v, stat[i]);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1)
+    v = merge_stat(v, float2{__shfl_xor(v.x, m), __shfl_xor(v.y, m)});
+  return v.x + __builtin_amdgcn_logf(v.y);
+}
+
+// one wave per original row
+__global__ __launch_bounds__(256) void ce_loss_kernel(const LossRows g, float* loss, float* lse) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (n >= g.rows) return;
+  const int p = g.pos[n];
+  float l = 0.f, out = 0.f;
+  if (p >= 0) {
+    l = row_lse2(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane) * kLn2;
+    out = l - g.z_label[p];
+  }
+  if (lane == 0) {
+    loss[n] = out;
+    lse[n] = l;
+  }
+}
+
+// logits at the teacher's entries: picked[n, j] = z[n, id_j].  Grid (rows,
+// ceil(top / 16)); each wave takes four entries, so a hidden chunk serves four
+// weight rows.
+template <typename S>
+__global__ __launch_bounds__(256) void distill_pick_kernel(const LossRows g, float* picked) {
+  constexpr int PER = Elem<S>::PER16;
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t n = blockIdx.x;
+  const int p = g.pos[n];
+  const int j0 = static_cast<int>(blockIdx.y) * 16 + static_cast<int>(threadIdx.x >> 6) * 4;
+  if (j0 >= g.top) return;
+  int id[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    id[q] = p >= 0 && j0 + q < g.top ? g.ids[n * g.top + j0 + q] : -1;
+    if (static_cast<uint32_t>(id[q]) >= static_cast<uint32_t>(g.vocab)) id[q] = -1;
+  }
+  float s[4] = {0.f, 0.f, 0.f, 0.f};
+  auto dots = [&](const void* xv, const void* wv, int len) {
+    const S* x = static_cast<const S*>(xv) + static_cast<int64_t>(p) * len;
+    for (int c = lane * PER; c < len; c += 64 * PER) {
+      const u32x4_t xr = load16(x + c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        if (id[q] < 0) continue;   // uniform over the wave
+        const u32x4_t wr = load16(static_cast<const S*>(wv) + static_cast<int64_t>(id[q]) * len + c);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          if constexpr (sizeof(S) == 2) {
+            s[q] += __uint_as_float(xr[k] << 16) * __uint_as_float(wr[k] << 16);
+            s[q] += __uint_as_float(xr[k] & 0xFFFF0000u) * __uint_as_float(wr[k] & 0xFFFF0000u);
+          } else {
+            s[q] += __uint_as_float(xr[k]) * __uint_as_float(wr[k]);
+          }
+        }
+      }
+    }
+  };
+  if (p >= 0) {
+    dots(g.x, g.w, g.hidden_size);
+    if (g.rank) dots(g.e, g.w2, g.rank);
+  }
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const float v = wave_sum(s[q]);
+    if (lane == 0 && j0 + q < g.top) picked[n * g.top + j0 + q] = v;
+  }
+}
+
+// one wave per original row; entries without mass add nothing
+__global__ __launch_bounds__(256) void distill_loss_kernel(const LossRows g, const float* picked,
+                                                           float* loss, float* lse) {
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
+  if (n >= g.rows) return;
+  const int p = g.pos[n];
+  float l = 0.f, out = 0.f;
+  if (p >= 0) {
+    l = row_lse2(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane) * kLn2;
+    for (int j = lane; j < g.top; j += 64) {
+      const float t = g.t[n * g.top + j];
+      if (t != 0.f) out += t * (logf(t) - (picked[n * g.top + j] * g.inv_t - l));
+    }
+    out = wave_sum(out) * (g.temperature * g.temperature);
+  }
+  if (lane == 0) {
+    loss[n] = out;
+    lse[n] = l;
+  }
+}
+
+// ---------------------------------------------------------------- d logits at the teacher's entries
+// The product wrote coef * softmax everywhere; the entries with teacher mass
+// are written again from the stored logit, coef (softmax - sum of the row's t
+// at this id).  An id listed twice is written twice with the same value.
+template <typename S>
+__global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, const float* picked,
+                                                          S* dz, int64_t ld, int v0, int width,
+                                                          float scale2) {
+  const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
+  const int p = static_cast<int>(i / g.top);
+  if (p >= *g.live) return;
+  const int j = static_cast<int>(i - static_cast<int64_t>(p) * g.top);
+  const int64_t n = g.row_of[p];
+  const int32_t* ids = g.ids + n * g.top;
+  const int id = ids[j];
+  if (id < v0 || id >= v0 + width) return;
+  float t = 0.f;
+  for (int q = 0; q < g.top; ++q)
+    if (ids[q] == id) t += g.t[n * g.top + q];
+  const float pr = __builtin_amdgcn_exp2f(picked[n * g.top + j] * scale2 - g.lse2[p]);
+  const float v = g.coef[p] * (pr - t);
+  dz[p * ld + (id - v0)] = rounded<S>(v);
+}
+
+// ---------------------------------------------------------------- gradients out
+// d hidden: the reduction splits added in order, rounded, back at the original
+// rows (zeros for rows without a target).  One workgroup per row.
+template <typename S>
+__global__ __launch_bounds__(256) void loss_dhidden_kernel(const int32_t* pos, const float* part,
+                                                           int splits, int64_t slab, int hidden,
+                                                           S* out) {
+  const int64_t n = blockIdx.x;
+  const int p = pos[n];
+  for (int c = static_cast<int>(threadIdx.x) * 4; c < hidden; c += 1024) {
+    f32x4_t v{0.f, 0.f, 0.f, 0.f};
+    if (p >= 0)
+      for (int s = 0; s < splits; ++s)
+        v += *reinterpret_cast<const f32x4_t*>(part + s * slab + static_cast<int64_t>(p) * hidden + c);
+    store4(out + n * hidden + c, v);
+  }
+}
+
+// d w1[prev] = sum of the embedding gradients of the rows with that previous
+// token, in row order.  One workgroup per compacted row; the first row with a
+// token does the sum for it (d w1 was cleared before).
+template <typename S>
+__global__ __launch_bounds__(256) void loss_dw1_kernel(const LossRows g, const float* part,
+                                                       int splits, int64_t slab, S* out) {
+  __shared__ int first;
+  __shared__ int list[256];
+  __shared__ int wave_n[4];
+  __shared__ float sums[256];
+  const int live = *g.live;
+  const int p = static_cast<int>(blockIdx.x);
+  if (p >= live) return;
+  const int tok = g.prev_c[p];
+  if (tok < 0) return;
+  const int tid = static_cast<int>(threadIdx.x);
+  if (tid == 0) first = 1;
+  __syncthreads();
+  for (int i = tid; i < p; i += 256)
+    if (g.prev_c[i] == tok) first = 0;
+  __syncthreads();
+  if (!first) return;
+  // column r of group gr of the workgroup: rows of the list strided by groups
+  const int r = g.rank;
+  const int groups = 256 / r;
+  const int col = tid % r, gr = tid / r;
+  const int lane = tid & 63, wave = tid >> 6;
+  float acc = 0.f;
+  for (int base = p; base < live; base += 256) {
+    const int i = base + tid;
+    const bool hit = i < live && g.prev_c[i] == tok;
+    const unsigned long long b = __ballot(hit);
+    if (lane == 0) wave_n[wave] = __popcll(b);
+    __syncthreads();
+    int before = 0, total = 0;
+    for (int w = 0; w < 4; ++w) {
+      if (w < wave) before += wave_n[w];
+      total += wave_n[w];
+    }
+    if (hit) list[before + __popcll(b & ((1ull << lane) - 1ull))] = i;
+    __syncthreads();
+    if (gr < groups)
+      for (int q = gr; q < total; q += groups) {
+        const float* src = part + static_cast<int64_t>(list[q]) * r + col;
+        float v = 0.f;
+        for (int s = 0; s < splits; ++s) v += src[s * slab];
+        acc += v;
+      }
+    __syncthreads();   // the list is rewritten
+  }
+  sums[tid] = acc;
+  __syncthreads();
+  if (gr == 0) {
+    float v = 0.f;
+    for (int q = 0; q < groups; ++q) v += sums[q * r + col];
+    out[static_cast<int64_t>(tok) * r + col] = rounded<S>(v);
+  }
+}
+
+__global__ __launch_bounds__(256) void clear_kernel(u32x4_t* p, int64_t n16) {
+  for (int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; i < n16;
+       i += static_cast<int64_t>(gridDim.x) * 256)
+    p[i] = u32x4_t{0, 0, 0, 0};
+}
+
+// ---------------------------------------------------------------- plan and workspace
+struct LossPlan {
+  int64_t piece;       // vocabulary entries per piece (backward)
+  int64_t ld;          // row length of the piece's d logits buffer
+  int splits_x, splits_e;
+  int stat_tiles;
+};
+
+LossPlan plan_loss(const LossProblem& p) {
+  LossPlan q{};
+  const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
+  const int cols = loss_stats_cols(p.dt, p.rows);
+  q.stat_tiles = static_cast<int>((p.vocab + cols - 1) / cols);
+  // whole vocabulary where its d logits fit, else equal pieces
+  int64_t most = kPieceBytes / (p.rows * es) / kPieceCols * kPieceCols;
+  most = std::max<int64_t>(most, kPieceCols);
+  const int64_t pieces = (p.vocab + most - 1) / most;
+  q.piece = ((p.vocab + pieces - 1) / pieces + kPieceCols - 1) / kPieceCols * kPieceCols;
+  q.piece = std::min(q.piece, p.vocab);
+  q.ld = (q.piece + 63) / 64 * 64;
+  q.splits_x = loss_dfeat_splits(p.dt, p.rows, p.hidden, q.piece);
+  q.splits_e = p.rank ? loss_dfeat_splits(p.dt, p.rows, p.rank, q.piece) : 0;
+  return q;
+}
+
+// Workspace layout; with base NULL only the size counts.
+struct LossSpace {
+  char* base;
+  size_t used = 0;
+  template <typename U> U* take(int64_t count) {
+    U* p = reinterpret_cast<U*>(base + used);
+    used += align256(static_cast<size_t>(count) * sizeof(U));
+    return p;
+  }
+};
+
+struct LossBuffers {
+  LossRows r;
+  int32_t* has;
+  char* dz;
+  float* part_x;
+  float* part_e;
+};
+
+size_t lay_out(const LossProblem& p, const LossPlan& q, bool backward, char* base, LossBuffers& b) {
+  LossSpace s{base};
+  const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
+  LossRows& r = b.r;
+  r.live = s.take<int32_t>(1);
+  r.pos = s.take<int32_t>(p.rows);
+  r.row_of = s.take<int32_t>(p.rows);
+  r.label_c = s.take<int32_t>(p.rows);
+  r.prev_c = s.take<int32_t>(p.rows);
+  r.x = s.take<char>(p.rows * p.hidden * es);
+  r.e = s.take<char>(p.rows * p.rank * es);
+  if (p.top) {
+    r.t = s.take<float>(p.rows * p.top);
+    b.has = s.take<int32_t>(p.rows);
+  }
+  if (!backward) {
+    r.z_label = s.take<float>(p.rows);
+    r.stat = s.take<float2>(p.rows * q.stat_tiles);
+  } else {
+    r.lse2 = s.take<float>(p.rows);
+    r.coef = s.take<float>(p.rows);
+    b.dz = s.take<char>(p.rows * q.ld * es);
+    b.part_x = s.take<float>(q.splits_x * p.rows * p.hidden);
+    b.part_e = s.take<float>(q.splits_e * p.rows * p.rank);
+  }
+  return s.used;
+}
+
+void fill_rows(const LossProblem& p, const LossPlan& q, LossBuffers& b) {
+  LossRows& r = b.r;
+  r.hidden = p.x;
+  r.w = p.w;
+  r.w1 = p.w1;
+  r.w2 = p.w2;
+  r.prev = p.prev;
+  r.label = p.top ? b.has : p.labels;
+  r.ids = p.ids;
+  r.u = p.u;
+  r.u_bf16 = p.u_dt == BDR_BF16;
+  r.rows = p.rows;
+  r.hidden_size = static_cast<int>(p.hidden);
+  r.vocab = static_cast<int>(p.vocab);
+  r.rank = p.rank;
+  r.top = p.top;
+  r.temperature = p.temperature;
+  r.inv_t = 1.0f / p.temperature;
+  r.tiles = q.stat_tiles;
+}
+
+#define BDR_LAUNCH(x)                 \
+  do {                                \
+    const hipError_t e_ = (x);        \
+    if (e_ != hipSuccess) return e_;  \
+  } while (0)
+
+unsigned waves4(int64_t rows) { return static_cast<unsigned>((rows + 3) / 4); }
+
+template <typename S>
+hipError_t gather(const LossProblem& p, const LossBuffers& b, bool backward, hipStream_t st) {
+  if (p.top) {
+    hipLaunchKernelGGL(distill_target_kernel, dim3(waves4(p.rows)), dim3(256), 0, st, b.r, b.has);
+    BDR_LAUNCH(hipGetLastError());
+  }
+  if (backward)
+    hipLaunchKernelGGL((loss_gather_kernel<S, true>), dim3(static_cast<unsigned>(p.rows)), dim3(256),
+                       0, st, b.r);
+  else
+    hipLaunchKernelGGL((loss_gather_kernel<S, false>), dim3(static_cast<unsigned>(p.rows)),
+                       dim3(256), 0, st, b.r);
+  return hipGetLastError();
+}
+
+// the logits product over vocabulary entries [v0, v0 + width)
+LossGemm logits_gemm(const LossProblem& p, const LossRows& r, int64_t v0, int64_t width) {
+  const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
+  LossGemm g{};
+  g.seg[0] = LossSeg{r.x, static_cast<const char*>(p.w) + v0 * p.hidden * es, p.hidden, p.hidden,
+                     p.hidden};
+  if (p.rank)
+    g.seg[1] = LossSeg{r.e, static_cast<const char*>(p.w2) + v0 * p.rank * es, p.rank, p.rank,
+                       p.rank};
+  else
+    g.seg[1] = LossSeg{g.seg[0].a, g.seg[0].b, p.hidden, p.hidden, 0};
+  g.live = r.live;
+  g.M = p.rows;
+  g.N = width;
+  g.live_m = 1;
+  g.band = 4;
+  g.splits = 1;
+  g.scale2 = kLog2e / p.temperature;
+  return g;
+}
+
+template <typename S>
+hipError_t forward(const LossProblem& p, void* workspace, float* loss, float* lse, float* picked,
+                   hipStream_t st) {
+  const LossPlan q = plan_loss(p);
+  LossBuffers b{};
+  lay_out(p, q, false, static_cast<char*>(workspace), b);
+  fill_rows(p, q, b);
+  BDR_LAUNCH(gather<S>(p, b, false, st));
+  LossGemm g = logits_gemm(p, b.r, 0, p.vocab);
+  g.label = p.top ? nullptr : b.r.label_c;
+  g.picked = b.r.z_label;
+  g.stat = b.r.stat;
+  BDR_LAUNCH(launch_loss_stats(p.dt, p.rows, g, st));
+  if (p.top) {
+    hipLaunchKernelGGL(distill_pick_kernel<S>,
+                       dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.top + 15) / 16)),
+                       dim3(256), 0, st, b.r, picked);
+    BDR_LAUNCH(hipGetLastError());
+    hipLaunchKernelGGL(distill_loss_kernel, dim3(waves4(p.rows)), dim3(256), 0, st, b.r, picked,
+                       loss, lse);
+  } else {
+    hipLaunchKernelGGL(ce_loss_kernel, dim3(waves4(p.rows)), dim3(256), 0, st, b.r, loss, lse);
+  }
+  return hipGetLastError();
+}
+
+template <typename S>
+hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, const float* lse,
+                    const float* picked, const float* loss_grad, hipStream_t st) {
+  const LossPlan q = plan_loss(p);
+  const int64_t es = sizeof(S);
+  LossBuffers b{};
+  lay_out(p, q, true, static_cast<char*>(workspace), b);
+  fill_rows(p, q, b);
+  b.r.lse = lse;
+  b.r.loss_grad = loss_grad;
+  BDR_LAUNCH(gather<S>(p, b, true, st));
+  for (int64_t v0 = 0; v0 < p.vocab; v0 += q.piece) {
+    const int64_t width = std::min(q.piece, p.vocab - v0);
+    const int64_t ld = (width + 63) / 64 * 64;
+    LossGemm g = logits_gemm(p, b.r, v0, width);
+    if (!p.top) {
+      g.label = b.r.label_c;
+      g.label0 = static_cast<int>(v0);
+    }
+    g.lse2 = b.r.lse2;
+    g.coef = b.r.coef;
+    g.out = b.dz;
+    g.ldo = ld;
+    BDR_LAUNCH(launch_loss_dlogits(p.dt, p.rows, g, st));
+    if (p.top) {
+      hipLaunchKernelGGL(distill_fix_kernel<S>,
+                         dim3(static_cast<unsigned>((p.rows * p.top + 255) / 256)), dim3(256), 0, st,
+                         b.r, picked, reinterpret_cast<S*>(b.dz), ld, static_cast<int>(v0),
+                         static_cast<int>(width), g.scale2);
+      BDR_LAUNCH(hipGetLastError());
+    }
+    // d hidden and d embedding: reduction over this piece's entries
+    auto dfeat = [&](const void* w, int64_t cols, float* part, int splits) {
+      LossGemm d{};
+      d.seg[0] = LossSeg{b.dz, static_cast<const char*>(w) + v0 * cols * es, ld, cols, width};
+      d.seg[1] = LossSeg{d.seg[0].a, d.seg[0].b, ld, cols, 0};
+      d.live = b.r.live;
+      d.M = p.rows;
+      d.N = cols;
+      d.live_m = 1;
+      d.band = 4;
+      d.splits = splits;
+      d.out = part;
+      d.ldo = cols;
+      d.slab = p.rows * cols;
+      d.accumulate = v0 > 0;
+      return launch_loss_dfeat(p.dt, p.rows, d, st);
+    };
+    // d weight and d w2: reduction over the rows
+    auto dweight = [&](const void* feat, int64_t cols, void* out) {
+      LossGemm d{};
+      d.seg[0] = LossSeg{b.dz, feat, ld, cols, p.rows};
+      d.seg[1] = LossSeg{d.seg[0].a, d.seg[0].b, ld, cols, 0};
+      d.live = b.r.live;
+      d.M = width;
+      d.N = cols;
+      d.live_k = 1;
+      d.band = 4;
+      d.splits = 1;
+      d.out = static_cast<char*>(out) + v0 * cols * es;
+      d.ldo = cols;
+      return launch_loss_dweight(p.dt, p.rows, d, st);
+    };
+    if (o.hidden) BDR_LAUNCH(dfeat(p.w, p.hidden, b.part_x, q.splits_x));
+    if (o.w1) BDR_LAUNCH(dfeat(p.w2, p.rank, b.part_e, q.splits_e));
+    if (o.w) BDR_LAUNCH(dweight(b.r.x, p.hidden, o.w));
+    if (o.w2) BDR_LAUNCH(dweight(b.r.e, p.rank, o.w2));
+  }
+  if (o.hidden) {
+    hipLaunchKernelGGL(loss_dhidden_kernel<S>, dim3(static_cast<unsigned>(p.rows)), dim3(256), 0, st,
+                       b.r.pos, b.part_x, q.splits_x, p.rows * p.hidden, static_cast<int>(p.hidden),
+                       static_cast<S*>(o.hidden));
+    BDR_LAUNCH(hipGetLastError());
+  }
+  if (o.w1) {
+    BDR_LAUNCH(launch_clear(o.w1, p.vocab * p.rank * es, st));
+    hipLaunchKernelGGL(loss_dw1_kernel<S>, dim3(static_cast<unsigned>(p.rows)), dim3(256), 0, st,
+                       b.r, b.part_e, q.splits_e, p.rows * p.rank, static_cast<S*>(o.w1));
+    BDR_LAUNCH(hipGetLastError());
+  }
+  return hipSuccess;
+}
+
+}  // namespace
+
+hipError_t launch_clear(void* p, int64_t bytes, hipStream_t stream) {
+  const int64_t n16 = bytes / 16;
+  const int64_t blocks = std::max<int64_t>(1, std::min<int64_t>((n16 + 255) / 256, 8192));
+  hipLaunchKernelGGL(clear_kernel, dim3(static_cast<unsigned>(blocks)), dim3(256), 0, stream,
+                     static_cast<u32x4_t*>(p), n16);
+  return hipGetLastError();
+}
+
+size_t loss_workspace(const LossProblem& p, bool backward) {
+  LossBuffers b{};
+  return lay_out(p, plan_loss(p), backward, nullptr, b);
+}
+
+hipError_t launch_loss_forward(const LossProblem& p, void* workspace, float* loss, float* lse,
+                               float* picked, hipStream_t stream) {
+  return p.dt == BDR_BF16 ? forward<uint16_t>(p, workspace, loss, lse, picked, stream)
+                          : forward<float>(p, workspace, loss, lse, picked, stream);
+}
+
+hipError_t launch_loss_backward(const LossProblem& p, const LossGrads& out, void* workspace,
+                                const float* lse, const float* picked, const float* loss_grad,
+                                hipStream_t stream) {
+  return p.dt == BDR_BF16
+             ? backward<uint16_t>(p, out, workspace, lse, picked, loss_grad, stream)
+             : backward<float>(p, out, workspace, lse, picked, loss_grad, stream);
+}
+
+hipError_t launch_loss_clear(const LossProblem& p, const LossGrads& o, hipStream_t stream) {
+  const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
+  if (o.w) BDR_LAUNCH(launch_clear(o.w, p.vocab * p.hidden * es, stream));
+  if (o.w1) BDR_LAUNCH(launch_clear(o.w1, p.vocab * p.rank * es, stream));
+  if (o.w2) BDR_LAUNCH(launch_clear(o.w2, p.vocab * p.rank * es, stream));
+  return hipSuccess;
+}
+
+}  // namespace bdr

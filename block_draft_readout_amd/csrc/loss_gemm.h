@@ -1,0 +1,440 @@
+// The matrix products of the vocabulary losses (gfx950): logits, and the
+// gradients that come back through them.
+//
+//   C[m, n] = sum_k A(m, k) B(n, k), fp32 accumulation, with either operand
+//   stored with the reduction index fast (rows of k: hidden states, weights as
+//   the logits read them) or slow (columns of k: weights as d hidden reads
+//   them, d logits and hidden states as d weight reads them).  Both directions
+//   read the tensors as they lie in memory; nothing is transposed in HBM.
+//
+// A workgroup of WM x WN waves owns a tile of C, a wave WTM x WTN MFMA tiles of
+// 16 x 16.  The reduction advances 128 bytes per operand row and step (64 bf16
+// or 32 fp32 elements); a step's slices are copied global -> LDS by
+// buffer-to-LDS loads into a ring of STAGES stages, one workgroup barrier per
+// step.
+//  * reduction fast: an LDS row is one operand row's 128 bytes, its eight
+//    16-byte chunks XOR-permuted by the row; an MFMA operand is one 16-byte read.
+//  * reduction slow: an LDS row is one k with the tile's columns side by side;
+//    an MFMA operand of bf16 is two transposing reads (ds_read_b64_tr_b16: 16
+//    lanes read 4 k x 16 columns, lane i receives column i's four values), of
+//    fp32 four 4-byte reads.  The 32-byte units of a bf16 LDS row are
+//    XOR-permuted by k so the 16 pieces of one read fall on distinct banks.
+// Loads place the permuted data by choosing which bytes each lane fetches.
+//
+// Everything past a tensor's edge reads as zero: rows and slow-k slices end
+// with the buffer descriptor, a fast-k tail is cut per lane.  The number of
+// rows that take part is a device value (rows without a target are compacted
+// away before the products run), so grids are sized for all rows and
+// workgroups past the last live tile leave at once.
+#pragma once
+
+#include "train_device.h"
+
+namespace bdr {
+
+enum LossEpilogue {
+  LE_STATS,     // per row and tile: running maximum and sum of exp of the scaled logits
+  LE_DLOGITS,   // coef (softmax - onehot), rounded to the storage type
+  LE_PARTIAL,   // fp32, one slab per reduction split, stored or added to
+  LE_OUT        // rounded to the storage type
+};
+
+// One stretch of the reduction: operand bases, row strides (elements) and extent.
+struct LossSeg {
+  const void* a;
+  const void* b;
+  int64_t lda, ldb;
+  int64_t k;
+};
+
+struct LossGemm {
+  LossSeg seg[2];          // the second one with the reduction fast on both sides only
+  const int32_t* live;     // device: rows that take part
+  int64_t M, N;            // extents of C (M: an upper bound where live_m)
+  int live_m, live_k;      // the row count is *live / the first segment's extent is *live
+  int tiles_n;
+  int tiles;               // grid tiles (all rows)
+  int band;                // tile rows per band of the tile order
+  int splits;              // reduction splits (LE_PARTIAL)
+  // logits epilogues
+  float scale2;            // log2(e) / temperature
+  const int32_t* label;    // [M] target entry or NULL
+  int label0;              // vocabulary entry of column 0
+  float2* stat;            // [M, tiles_n] (maximum, sum) in units of log2
+  float* picked;           // [M] logit of the label
+  const float* lse2;       // [M] log2 of the softmax denominator
+  const float* coef;       // [M] gradient factor
+  void* out;               // LE_DLOGITS [M, ldo], LE_PARTIAL [splits, slab], LE_OUT [M, ldo]
+  int64_t ldo, slab;
+  int accumulate;          // LE_PARTIAL: add to what is there
+};
+
+template <typename S_, bool AKS_, bool BKS_, int WM_, int WN_, int WTM_, int WTN_, int STAGES_>
+struct LossTile {
+  using S = S_;
+  static constexpr bool AKS = AKS_, BKS = BKS_;   // reduction slow
+  static constexpr int WM = WM_, WN = WN_, WTM = WTM_, WTN = WTN_, STAGES = STAGES_;
+  static constexpr int WAVES = WM * WN;
+  static constexpr int BM = 16 * WM * WTM, BN = 16 * WN * WTN;
+  static constexpr int KB = 128 / static_cast<int>(sizeof(S));
+  static constexpr int A_BYTES = BM * 128, STAGE_BYTES = (BM + BN) * 128;
+  static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int LOADS_A = BM / 8 / WAVES, LOADS_B = BN / 8 / WAVES;
+  static constexpr int LOADS = LOADS_A + LOADS_B;
+  static constexpr int SLOW_READS = sizeof(S) == 2 ? 2 : 4;
+  static constexpr int READS = WTM * (AKS ? SLOW_READS : 1) + WTN * (BKS ? SLOW_READS : 1);
+  static constexpr int MFMAS = WTM * WTN * Elem<S>::MFMA_PER16;   // per half step
+  static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "loads split evenly over the waves");
+  static_assert((!AKS || BM % 64 == 0) && (!BKS || BN % 64 == 0), "slow rows are multiples of 128 bytes");
+  static_assert(LDS_BYTES <= 160 * 1024, "tile fits");
+};
+
+// XOR of the 32-byte unit index in a reduction-slow bf16 LDS row of ROWB bytes:
+// one transposing read takes the rows {8 g + j : g, j < 4} (or those plus 4), and
+// (row * ROWB + unit * 32) mod 512 has to differ between all 16 of them.
+template <int ROWB>
+__device__ __forceinline__ uint32_t slow_swizzle(uint32_t kr) {
+  const uint32_t g = (kr >> 3) & 3u, j = kr & 3u;
+  if constexpr (ROWB % 512 == 0) return g | (j << 2);
+  if constexpr (ROWB % 512 == 256) return g | ((j >> 1) << 2);
+  return g;
+}
+
+// 16 bytes per lane, global -> LDS: lane l's land at dst + 16 l (dst uniform)
+__device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t off, char* dst) {
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, off,
+                                           0, 0, 0);
+}
+
+// four 16-bit values of column lane % 16, from the 4 rows x 16 columns whose
+// 8-byte pieces the 16 lanes of a group name
+__device__ __forceinline__ uint2 lds_read_tr4(const char* p) {
+  typedef short s16x4_t __attribute__((ext_vector_type(4)));
+  return __builtin_bit_cast(
+      uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p));
+}
+
+// Joins two running (maximum, sum of 2^(x - maximum)) pairs.
+__device__ __forceinline__ float2 merge_stat(float2 a, float2 b) {
+  const float m = fmaxf(a.x, b.x);
+  const float ref = m == -INFINITY ? 0.f : m;
+  return float2{m, a.y * __builtin_amdgcn_exp2f(a.x - ref) + b.y * __builtin_amdgcn_exp2f(b.x - ref)};
+}
+
+__device__ __forceinline__ void store4(uint16_t* p, f32x4_t v) {
+  *reinterpret_cast<uint2*>(p) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
+}
+__device__ __forceinline__ void store4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
+
+template <typename T, int EPI>
+__global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm g) {
+  using S = typename T::S;
+  constexpr int ES = static_cast<int>(sizeof(S));
+  __shared__ __attribute__((aligned(16))) char lds[T::LDS_BYTES];
+  const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+  const int lane = static_cast<int>(threadIdx.x) & 63;
+  const int r16 = lane & 15;
+  const int grp = lane >> 4;
+  const int wm = wave % T::WM;
+  const int wn = wave / T::WM;
+
+  // tile of this workgroup: each XCD (workgroup b runs on XCD b % 8) takes a
+  // contiguous run of the band-ordered tiles, so its workgroups share operand
+  // slices in that XCD's L2
+  const int live = *g.live;
+  const int64_t M = g.live_m ? live : g.M;
+  const int tiles_m = static_cast<int>((M + T::BM - 1) / T::BM);
+  const int tiles = tiles_m * g.tiles_n;
+  const int per_xcd = (tiles + 7) / 8;
+  const int bi = static_cast<int>(blockIdx.x / 8);
+  const int t = static_cast<int>(blockIdx.x % 8) * per_xcd + bi;
+  if (bi >= per_xcd || t >= tiles) return;   // whole workgroup
+  const int band = t / (g.band * g.tiles_n);
+  const int bh = min(g.band, tiles_m - g.band * band);
+  const int bidx = t - g.band * g.tiles_n * band;
+  const int tm = g.band * band + bidx % bh;
+  const int tn = bidx / bh;
+  const int64_t m0 = static_cast<int64_t>(tm) * T::BM;
+  const int64_t n0 = static_cast<int64_t>(tn) * T::BN;
+
+  // reduction steps of this workgroup: the first segment's, then the second's
+  const int64_t k0 = g.live_k ? live : g.seg[0].k;
+  const int steps0 = static_cast<int>((k0 + T::KB - 1) / T::KB);
+  const int total = steps0 + static_cast<int>((g.seg[1].k + T::KB - 1) / T::KB);
+  int s_lo = 0, s_hi = total;
+  if constexpr (EPI == LE_PARTIAL) {
+    s_lo = static_cast<int>(static_cast<int64_t>(total) * blockIdx.y / g.splits);
+    s_hi = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.y + 1) / g.splits);
+  }
+
+  // per-lane offsets of this wave's loads
+  const uint32_t lrow = static_cast<uint32_t>(lane >> 3);
+  const uint32_t lchunk = (static_cast<uint32_t>(lane) & 7u) ^ lrow;
+  const int64_t rows_a = min<int64_t>(T::BM, M - m0);
+  const int64_t rows_b = min<int64_t>(T::BN, g.N - n0);
+  // byte offset of load q's chunk of this lane inside the step's slice of an
+  // operand with row stride ld
+  auto lane_off = [&](auto slow, auto rowbytes, int q, uint32_t ld) -> uint32_t {
+    const uint32_t i = static_cast<uint32_t>(wave + T::WAVES * q);
+    if constexpr (!decltype(slow)::value) {
+      return (8u * i + lrow) * ld * ES + lchunk * 16u;
+    } else {
+      constexpr uint32_t ROWB = decltype(rowbytes)::value;
+      const uint32_t o = i * 1024u + static_cast<uint32_t>(lane) * 16u;
+      const uint32_t kr = o / ROWB;
+      uint32_t p = o % ROWB;
+      if constexpr (ES == 2) p = (((p >> 5) ^ slow_swizzle<ROWB>(kr)) << 5) | (p & 16u);
+      return kr * ld * ES + p;
+    }
+  };
+  typedef std::integral_constant<bool, T::AKS> ASlow;
+  typedef std::integral_constant<bool, T::BKS> BSlow;
+  typedef std::integral_constant<uint32_t, T::BM * ES> ARow;
+  typedef std::integral_constant<uint32_t, T::BN * ES> BRow;
+
+  // One step's loads: descriptors prepared once, load q issued by dma_one.  A
+  // step past the end reads zeros (empty descriptors), so that every step
+  // issues the same loads and the waits count alike.
+  rsrc_t ra, rb;
+  uint32_t ld_a = 0, ld_b = 0, cut = 0;   // cut: kOOB in the lanes past a fast-k tail
+  char* ld_dst = lds;
+  auto dma_prep = [&](int step, int buf) {
+    const bool in = step < s_hi;
+    const bool second = step >= steps0;
+    const LossSeg& sg = second ? g.seg[1] : g.seg[0];
+    const int64_t kk = static_cast<int64_t>(second ? step - steps0 : step) * T::KB;
+    const int64_t krem = (second ? sg.k : k0) - kk;
+    ld_a = static_cast<uint32_t>(sg.lda);
+    ld_b = static_cast<uint32_t>(sg.ldb);
+    cut = static_cast<int64_t>(lchunk) * Elem<S>::PER16 < krem ? 0u : kOOB;
+    const int64_t krows = min<int64_t>(T::KB, krem);
+    const char* pa = static_cast<const char*>(sg.a);
+    const char* pb = static_cast<const char*>(sg.b);
+    uint32_t na, nb;
+    if constexpr (T::AKS) {
+      pa += (kk * sg.lda + m0) * ES;
+      na = static_cast<uint32_t>((krows * sg.lda - m0) * ES);
+    } else {
+      pa += (m0 * sg.lda + kk) * ES;
+      na = static_cast<uint32_t>((rows_a * sg.lda - kk) * ES);
+    }
+    if constexpr (T::BKS) {
+      pb += (kk * sg.ldb + n0) * ES;
+      nb = static_cast<uint32_t>((krows * sg.ldb - n0) * ES);
+    } else {
+      pb += (n0 * sg.ldb + kk) * ES;
+      nb = static_cast<uint32_t>((rows_b * sg.ldb - kk) * ES);
+    }
+    ra = make_rsrc(pa, in ? na : 0u);
+    rb = make_rsrc(pb, in ? nb : 0u);
+    ld_dst = lds + buf * T::STAGE_BYTES;
+  };
+  auto dma_one = [&](auto qc) {
+    constexpr int q = decltype(qc)::value;
+    if constexpr (q < T::LOADS_A) {
+      const uint32_t off = lane_off(ASlow{}, ARow{}, q, ld_a);
+      load_lds16(ra, T::AKS ? off : off | cut, ld_dst + (wave + T::WAVES * q) * 1024);
+    } else {
+      constexpr int p = q - T::LOADS_A;
+      const uint32_t off = lane_off(BSlow{}, BRow{}, p, ld_b);
+      load_lds16(rb, T::BKS ? off : off | cut, ld_dst + T::A_BYTES + (wave + T::WAVES * p) * 1024);
+    }
+  };
+
+  f32x4_t acc[T::WTM][T::WTN];
+  static_for<T::WTM>([&](auto i) {
+    static_for<T::WTN>([&](auto j) { acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
+  });
+  typedef u32x4_t FragA[T::WTM];
+  typedef u32x4_t FragB[T::WTN];
+  // operand of MFMA tile `tile` (16 rows of the operand) in half `half` of a step
+  auto read_op = [&](auto slow, auto rowbytes, const char* base, int tile, int half) -> u32x4_t {
+    if constexpr (!decltype(slow)::value) {
+      const uint32_t c = (static_cast<uint32_t>(4 * half + grp) ^ static_cast<uint32_t>(lane & 7)) * 16u;
+      return *reinterpret_cast<const u32x4_t*>(base + static_cast<uint32_t>(tile * 16 + r16) * 128u + c);
+    } else if constexpr (ES == 2) {
+      constexpr uint32_t ROWB = decltype(rowbytes)::value;
+      const uint32_t kr = static_cast<uint32_t>(8 * grp + (r16 >> 2));
+      const uint32_t off = kr * ROWB + ((static_cast<uint32_t>(tile) ^ slow_swizzle<ROWB>(kr)) << 5) +
+                           static_cast<uint32_t>(lane & 3) * 8u + static_cast<uint32_t>(half) * 32u * ROWB;
+      const uint2 lo = lds_read_tr4(base + off);
+      const uint2 hi = lds_read_tr4(base + off + 4 * ROWB);
+      return u32x4_t{lo.x, lo.y, hi.x, hi.y};
+    } else {
+      constexpr uint32_t ROWB = decltype(rowbytes)::value;
+      const char* p = base + static_cast<uint32_t>(16 * half + 4 * grp) * ROWB +
+                      static_cast<uint32_t>(tile * 16 + r16) * 4u;
+      u32x4_t v;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const uint32_t*>(p + e * ROWB);
+      return v;
+    }
+  };
+  auto read_frags = [&](int buf, int half, FragA& a, FragB& b) {
+    const char* base = lds + buf * T::STAGE_BYTES;
+    static_for<T::WTM>([&](auto i) {
+      a[i] = read_op(ASlow{}, ARow{}, base, wm * T::WTM + decltype(i)::value, half);
+    });
+    static_for<T::WTN>([&](auto j) {
+      b[j] = read_op(BSlow{}, BRow{}, base + T::A_BYTES, wn * T::WTN + decltype(j)::value, half);
+    });
+  };
+
+  // Per step: wait for its loads, one barrier, then per half the operand reads
+  // and the MFMAs; the loads of step s + STAGES - 1 are spread over the first
+  // half's MFMAs (all before them where there are fewer MFMAs than loads).
+  static_for<T::STAGES - 1>([&](auto c) {
+    dma_prep(s_lo + decltype(c)::value, decltype(c)::value);
+    static_for<T::LOADS>([&](auto q) { dma_one(q); });
+  });
+  dma_prep(s_lo + T::STAGES - 1, T::STAGES - 1);
+  constexpr int NT = T::WTM * T::WTN;
+  constexpr bool kSpread = NT >= T::LOADS;
+  FragA a;
+  FragB b;
+  int buf = 0;
+  for (int s = s_lo; s < s_hi; ++s) {
+    // this wave's loads of step s have landed when at most those of the
+    // STAGES - 2 steps after it remain; after the barrier every wave's have,
+    // and every wave is done with the stage the next loads overwrite
+    BDR_WAIT_VM_LGKM((T::STAGES - 2) * T::LOADS, 0);
+    BDR_WG_BARRIER();
+    if constexpr (!kSpread) static_for<T::LOADS>([&](auto q) { dma_one(q); });
+    read_frags(buf, 0, a, b);
+    static_for<NT>([&](auto ec) {
+      constexpr int e = decltype(ec)::value;
+      constexpr int every = kSpread ? NT / T::LOADS : NT;
+      acc[e / T::WTN][e % T::WTN] =
+          mma16(b[e % T::WTN], a[e / T::WTN], acc[e / T::WTN][e % T::WTN], S());
+      if constexpr (kSpread && e % every == every - 1 && e / every < T::LOADS)
+        dma_one(std::integral_constant<int, e / every>{});
+    });
+    read_frags(buf, 1, a, b);
+    static_for<NT>([&](auto ec) {
+      constexpr int e = decltype(ec)::value;
+      acc[e / T::WTN][e % T::WTN] =
+          mma16(b[e % T::WTN], a[e / T::WTN], acc[e / T::WTN][e % T::WTN], S());
+    });
+    if constexpr (kSpread) {   // keep that order through scheduling
+      constexpr int every = NT / T::LOADS * Elem<S>::MFMA_PER16;
+      __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
+      static_for<T::LOADS>([&](auto) {
+        __builtin_amdgcn_sched_group_barrier(0x008, every, 0);
+        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+      });
+      if constexpr (T::MFMAS - every * T::LOADS > 0)
+        __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS - every * T::LOADS, 0);
+      __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS, 0);
+    }
+    buf = buf + 1 == T::STAGES ? 0 : buf + 1;
+    // where step s + STAGES goes (the stage of step s)
+    dma_prep(s + T::STAGES, buf == 0 ? T::STAGES - 1 : buf - 1);
+  }
+  BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads
+
+  // Lane holds C[m][n .. n + 3] of each of its tiles: rows r16, columns 4 grp ..
+  const int64_t mw = m0 + wm * 16 * T::WTM + r16;
+  const int64_t nw = n0 + wn * 16 * T::WTN + 4 * grp;
+  if constexpr (EPI == LE_STATS) {
+    // maximum and sum of 2^(x scale2 - maximum) over the tile's columns: lanes,
+    // then the four lane groups, then the waves side by side through LDS
+    BDR_WG_BARRIER();   // every wave is done with the stages
+    float2* part = reinterpret_cast<float2*>(lds);   // [WN][BM]
+    static_for<T::WTM>([&](auto i) {
+      const int64_t m = mw + decltype(i)::value * 16;
+      const bool row_in = m < M;
+      const int64_t lab = g.label && row_in ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
+      float mx = -INFINITY;
+      static_for<T::WTN>([&](auto j) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          const int64_t n = nw + decltype(j)::value * 16 + c;
+          const float z = acc[i][j][c];
+          if (n == lab) g.picked[m] = z;
+          const float x = n < g.N ? z * g.scale2 : -INFINITY;
+          acc[i][j][c] = x;
+          mx = fmaxf(mx, x);
+        }
+      });
+      mx = fmaxf(mx, __shfl_xor(mx, 16));
+      mx = fmaxf(mx, __shfl_xor(mx, 32));
+      const float ref = mx == -INFINITY ? 0.f : mx;
+      float sum = 0.f;
+      static_for<T::WTN>([&](auto j) {
+#pragma unroll
+        for (int c = 0; c < 4; ++c) sum += __builtin_amdgcn_exp2f(acc[i][j][c] - ref);
+      });
+      sum += __shfl_xor(sum, 16);
+      sum += __shfl_xor(sum, 32);
+      if (grp == 0)
+        part[wn * T::BM + wm * 16 * T::WTM + decltype(i)::value * 16 + r16] = float2{mx, sum};
+    });
+    BDR_WAIT_VM_LGKM(0, 0);
+    BDR_WG_BARRIER();
+    for (int r = static_cast<int>(threadIdx.x); r < T::BM; r += 64 * T::WAVES) {
+      if (m0 + r >= M) continue;
+      float2 v = part[r];
+#pragma unroll
+      for (int w = 1; w < T::WN; ++w) v = merge_stat(v, part[w * T::BM + r]);
+      g.stat[(m0 + r) * g.tiles_n + tn] = v;
+    }
+  } else if constexpr (EPI == LE_DLOGITS) {
+    // rounded to the storage type: the operand of two more matrix products,
+    // with as much relative error as their rounded results carry anyway
+    static_for<T::WTM>([&](auto i) {
+      const int64_t m = mw + decltype(i)::value * 16;
+      if (m < M) {
+        const int64_t lab = g.label ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
+        const float l2 = g.lse2[m], cf = g.coef[m];
+        S* row = static_cast<S*>(g.out) + m * g.ldo;
+        static_for<T::WTN>([&](auto j) {
+          const int64_t n = nw + decltype(j)::value * 16;
+          if (n < g.ldo) {   // columns from N to the padded width hold zeros
+            f32x4_t v;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const float p = __builtin_amdgcn_exp2f(acc[i][j][c] * g.scale2 - l2);
+              v[c] = n + c < g.N ? cf * (n + c == lab ? p - 1.f : p) : 0.f;
+            }
+            store4(row + n, v);
+          }
+        });
+      }
+    });
+  } else if constexpr (EPI == LE_PARTIAL) {
+    float* out = static_cast<float*>(g.out) + static_cast<int64_t>(blockIdx.y) * g.slab;
+    static_for<T::WTM>([&](auto i) {
+      const int64_t m = mw + decltype(i)::value * 16;
+      static_for<T::WTN>([&](auto j) {
+        const int64_t n = nw + decltype(j)::value * 16;
+        if (m < M && n < g.N) {
+          f32x4_t* p = reinterpret_cast<f32x4_t*>(out + m * g.ldo + n);
+          *p = g.accumulate ? *p + acc[i][j] : acc[i][j];
+        }
+      });
+    });
+  } else {
+    static_for<T::WTM>([&](auto i) {
+      const int64_t m = mw + decltype(i)::value * 16;
+      static_for<T::WTN>([&](auto j) {
+        const int64_t n = nw + decltype(j)::value * 16;
+        if (m < M && n < g.N) store4(static_cast<S*>(g.out) + m * g.ldo + n, acc[i][j]);
+      });
+    });
+  }
+}
+
+template <typename T, int EPI>
+static hipError_t launch_loss_gemm(LossGemm g, hipStream_t stream) {
+  const int64_t tiles_m = (g.M + T::BM - 1) / T::BM;
+  g.tiles_n = static_cast<int>((g.N + T::BN - 1) / T::BN);
+  const int64_t tiles = tiles_m * g.tiles_n;
+  g.tiles = static_cast<int>(tiles);
+  const dim3 grid(static_cast<unsigned>((tiles + 7) / 8 * 8),
+                  static_cast<unsigned>(EPI == LE_PARTIAL ? g.splits : 1));
+  hipLaunchKernelGGL((loss_gemm_kernel<T, EPI>), grid, dim3(64 * T::WAVES), 0, stream, g);
+  return hipGetLastError();
+}
+
+}  // namespace bdr

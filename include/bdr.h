@@ -14,7 +14,8 @@
  *   - Tensor arguments are DEVICE pointers to row-major, contiguous memory owned
  *     by the caller, 16-byte aligned; workspaces are 256-byte aligned.  The
  *     library never allocates or frees device memory and never synchronises.
- *   - Workspaces hold cross-workgroup counters and argmax keys: a workspace
+ *   - Workspaces hold cross-workgroup counters and argmax keys (those of the
+ *     training calls at the end hold none): a workspace
  *     must be zero-filled once before its first use, and every call that
  *     completes leaves its counters and hand-off slots zero-filled again (the
  *     Markov error word too when the call is given a status word), so it can
@@ -66,6 +67,8 @@ typedef enum bdr_dtype { BDR_F32 = 0, BDR_BF16 = 1, BDR_BF16_PACKED = 2 } bdr_dt
 #define BDR_MAX_K      16
 #define BDR_MAX_RANK   128
 #define BDR_MAX_HC     16
+#define BDR_MAX_TEACHER 256       /* teacher entries per row */
+#define BDR_MAX_NORM_HIDDEN 16384 /* features of a normalised row */
 
 /* Version of this interface (incremented on any signature change or change
  * of a documented data layout). */
@@ -578,6 +581,152 @@ int dflash_fuse_fc_rows_fp8(const void* const* taps, int n_taps, int64_t rows,
                             int64_t hidden, const int32_t* row_index,
                             const int32_t* row_count, int64_t max_rows,
                             const uint8_t* fc_q, const float* fc_scale, void* out,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Training the drafter's readout: the row normalisation in front of the LM
+ * head and two losses over the logits the drafter drafts with (LM head plus
+ * Markov bias), each forward and backward.
+ *
+ * The published drafters are trained with SpecForge ([recipe] summary).  The
+ * pages give no training arithmetic; the textbook definitions below are used.
+ *
+ * Rows are drafted positions (any number of sequences).  A gradient argument
+ * that is NULL is not computed; gradients overwrite their output.  Every sum
+ * has a fixed order, so the same inputs give the same bits.  The workspaces of
+ * these calls hold no state: any contents will do, nothing needs clearing.
+ * ------------------------------------------------------------------------- */
+
+/* dspark_norm -- normalise each row (layer norm, or root-mean-square norm).
+ *
+ *   mean = sum_h x[m, h] / H            (0 when mean is NULL: root mean square)
+ *   rstd = (sum_h (x[m, h] - mean)^2 / H + eps)^-1/2
+ *   y[m, h] = (x[m, h] - mean) * rstd * weight[h] + bias[h]
+ *
+ * Statistics and products are fp32, y is rounded once.
+ *
+ *   x        [rows, H] dtype, row m at x + m * x_stride elements (x_stride >= H,
+ *            rows 16-byte aligned: a multiple of 8 (bf16) or 4 (f32))
+ *   rows     >= 0; 0 < H <= BDR_MAX_NORM_HIDDEN, H % 8 == 0 (bf16) or H % 4 == 0
+ *   weight   [H] dtype; bias [H] dtype or NULL
+ *   eps      finite, >= 0
+ *   y        [rows, H] dtype, contiguous; may be x itself where x_stride == H
+ *   mean     [rows] fp32 out, or NULL for the root-mean-square form
+ *   rstd     [rows] fp32 out
+ *
+ * dspark_norm_backward -- its gradients, from the saved statistics:
+ *   xh = (x - mean) rstd,  gy = dy * weight
+ *   dx = rstd (gy - sum_h gy / H - xh sum_h(gy xh) / H)   (no sum_h gy term
+ *                                                          where mean is NULL)
+ *   dweight[h] = sum_m dy[m, h] xh[m, h],  dbias[h] = sum_m dy[m, h]
+ *   dy       [rows, H] dtype at row stride dy_stride (as x)
+ *   dx       [rows, H] dtype, contiguous, or NULL; may be dy itself where
+ *            dy_stride == H
+ *   dweight, dbias [H] dtype or NULL (zeros where rows == 0)
+ *   workspace >= dspark_norm_backward_workspace_bytes(rows, H); may be NULL
+ *            when neither dweight nor dbias is wanted
+ */
+int dspark_norm(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, bdr_dtype dt,
+                const void* weight, const void* bias, float eps, void* y, float* mean,
+                float* rstd, void* stream);
+size_t dspark_norm_backward_workspace_bytes(int64_t rows, int64_t hidden);
+int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64_t x_stride,
+                         int64_t rows, int64_t hidden, bdr_dtype dt, const void* weight,
+                         const float* mean, const float* rstd, void* dx, void* dweight,
+                         void* dbias, void* workspace, size_t workspace_bytes, void* stream);
+
+/* dspark_ce_loss -- softmax cross entropy over the full vocabulary, without
+ * storing the logits.
+ *
+ *   z[m, v] = sum_h hidden[m, h] lm_head_w[v, h]
+ *           + sum_j markov_w1[prev_token[m], j] markov_w2[v, j]
+ *   lse[m]  = log sum_v exp(z[m, v]),  loss[m] = lse[m] - z[m, labels[m]]
+ *
+ * z is what dspark_lm_head and the Markov head give with the previous tokens
+ * known (teacher forcing).  A previous token outside [0, V) adds no bias.  A
+ * label outside [0, V) leaves its row out: loss and lse are 0, every gradient
+ * of the row is 0, and its hidden state, previous token and loss_grad are not
+ * used (they may hold anything, NaN too).  The product takes the dtype's
+ * operands and sums in fp32; lse and loss are fp32.
+ *
+ *   hidden     [rows, H] dtype; 0 <= rows <= 2^20; 0 < H <= 2^20, H % 8 == 0
+ *              (bf16) or H % 4 == 0 (f32)
+ *   lm_head_w  [V, H] dtype; 0 < V <= 2^21
+ *   markov_w1, markov_w2 [V, r] dtype, prev_token [rows] int32; both matrices
+ *              NULL or rank == 0: no bias; rank as in dspark_markov_argmax
+ *   labels     [rows] int32
+ *   loss, lse  [rows] fp32 out
+ *   workspace  >= dspark_ce_workspace_bytes(rows, H, V, rank, dt, 0)
+ *
+ * dspark_ce_backward -- the gradients of sum_m loss_grad[m] loss[m].
+ *   dz[m, v] = loss_grad[m] (exp(z[m, v] - lse[m]) - [v == labels[m]])
+ *   d_hidden = dz lm_head_w,            d_lm_head_w = dz^T hidden
+ *   d_markov_w2 = dz^T markov_w1[prev], d_markov_w1[p] = sum_{m: prev[m] = p} dz[m] markov_w2
+ * dz is recomputed a piece of the vocabulary at a time and rounded to the dtype
+ * as an operand of these products, which sum in fp32; each gradient is rounded
+ * once more, on output.  Rows of the weight gradients that no row reaches are 0.
+ *   lse        [rows] as written by dspark_ce_loss for the same inputs
+ *   loss_grad  [rows] fp32
+ *   d_hidden [rows, H], d_lm_head_w [V, H], d_markov_w1, d_markov_w2 [V, r]:
+ *              dtype, each may be NULL (a frozen head costs nothing)
+ *   workspace  >= dspark_ce_workspace_bytes(rows, H, V, rank, dt, 1)
+ * rows == 0 clears the weight gradients that are given.
+ */
+size_t dspark_ce_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab, int rank,
+                                 bdr_dtype dt, int backward);
+int dspark_ce_loss(const void* hidden, int64_t rows, int64_t hidden_size, int64_t vocab,
+                   bdr_dtype dt, const void* lm_head_w, const void* markov_w1,
+                   const void* markov_w2, int rank, const int32_t* prev_token,
+                   const int32_t* labels, float* loss, float* lse, void* workspace,
+                   size_t workspace_bytes, void* stream);
+int dspark_ce_backward(const void* hidden, int64_t rows, int64_t hidden_size, int64_t vocab,
+                       bdr_dtype dt, const void* lm_head_w, const void* markov_w1,
+                       const void* markov_w2, int rank, const int32_t* prev_token,
+                       const int32_t* labels, const float* lse, const float* loss_grad,
+                       void* d_hidden, void* d_lm_head_w, void* d_markov_w1, void* d_markov_w2,
+                       void* workspace, size_t workspace_bytes, void* stream);
+
+/* dspark_distill_loss -- distillation from the target's top logits: the
+ * divergence of the drafter's softmax over the full vocabulary from the
+ * target's softmax over its `top` listed entries, both at temperature T.
+ *
+ *   t[m, .]  = softmax over the listed entries j of teacher_logits[m, j] / T
+ *   lse[m]   = log sum_v exp(z[m, v] / T)          (z as in dspark_ce_loss)
+ *   picked[m, j] = z[m, teacher_ids[m, j]]
+ *   loss[m]  = T^2 sum_j t[m, j] (log t[m, j] - picked[m, j] / T + lse[m])
+ *
+ * An entry whose id is outside [0, V) is not listed (its teacher logit may
+ * hold anything); an entry with teacher logit -inf has no mass.  A row without
+ * mass is left out as a row of dspark_ce_loss without a label is.  An id listed
+ * twice counts as two entries.
+ *
+ *   teacher_ids    [rows, top] int32; 1 <= top <= BDR_MAX_TEACHER
+ *   teacher_logits [rows, top] teacher_dt (BDR_F32 or BDR_BF16)
+ *   temperature    finite, > 0
+ *   loss, lse      [rows] fp32 out; picked [rows, top] fp32 out (0 for entries
+ *                  that are not listed and rows that are left out)
+ *   workspace      >= dspark_distill_workspace_bytes(rows, H, V, rank, top, dt, 0)
+ *
+ * dspark_distill_backward -- the gradients of sum_m loss_grad[m] loss[m]:
+ *   dz[m, v] = loss_grad[m] T (exp(z[m, v] / T - lse[m]) - sum_{j: id_j = v} t[m, j])
+ * and from it as in dspark_ce_backward; lse and picked as dspark_distill_loss
+ * wrote them.  No gradient reaches the teacher's logits.
+ */
+size_t dspark_distill_workspace_bytes(int64_t rows, int64_t hidden, int64_t vocab, int rank,
+                                      int top, bdr_dtype dt, int backward);
+int dspark_distill_loss(const void* hidden, int64_t rows, int64_t hidden_size, int64_t vocab,
+                        bdr_dtype dt, const void* lm_head_w, const void* markov_w1,
+                        const void* markov_w2, int rank, const int32_t* prev_token,
+                        const int32_t* teacher_ids, const void* teacher_logits, int top,
+                        bdr_dtype teacher_dt, float temperature, float* loss, float* lse,
+                        float* picked, void* workspace, size_t workspace_bytes, void* stream);
+int dspark_distill_backward(const void* hidden, int64_t rows, int64_t hidden_size, int64_t vocab,
+                            bdr_dtype dt, const void* lm_head_w, const void* markov_w1,
+                            const void* markov_w2, int rank, const int32_t* prev_token,
+                            const int32_t* teacher_ids, const void* teacher_logits, int top,
+                            bdr_dtype teacher_dt, float temperature, const float* lse,
+                            const float* picked, const float* loss_grad, void* d_hidden,
+                            void* d_lm_head_w, void* d_markov_w1, void* d_markov_w2,
                             void* workspace, size_t workspace_bytes, void* stream);
 
 #ifdef __cplusplus

@@ -1,0 +1,473 @@
+"""GPU parity of the vocabulary losses (dspark_ce_*, dspark_distill_*) against
+oracle.training.
+
+Exact cases.  With hidden = 0 (or every weight 0) the logits are 0, the softmax is 1 / V
+for every entry, and d logits are two known numbers per row; against small whole numbers
+every product is a multiple of one power of two, so where the sum of magnitudes is below
+2^24 of it the fp32 partial sums are exact and d hidden (or a weight gradient) is one
+rounding of a number the test computes; a longer sum is off by its fp32 additions, (K / 4 +
+40) u times the sum of magnitudes, before that rounding.  These pin the tiles, operand
+layouts, edges and pieces.
+
+Tolerances elsewhere.  u = 2^-24.  A logit is off by at most zerr = (K / 4 + 40) u zabs (an
+MFMA adds to its accumulator at least four products of fp32, thirty-two of bf16, at a
+time; zabs is the sum of the products' magnitudes) and the loss by 2 zerr T plus 64 u
+(1 + |lse| + ...) of the exponentials, logarithms and row sums.  A softmax entry has
+then relative error ep = 2 zerr / T + 64 u (1 + |lse| + max |z| / T).  d logits are off by
+gp ep + rnd |dz|, rnd being the storage rounding (bf16 2^-8, fp32 u), which the product
+carries to sum |.| |operand|; its own sums add (K / 4 + 40) u times the sum of magnitudes
+and the output one more rounding.  Below the normal range, where an exponential or a
+product of fp32 or bf16 may come out as 0, each number is off by at most TINY = 2^-126: d logits
+by that, and a product of K of them by TINY (K + sum |operand|) at most.
+"""
+import numpy as np
+import pytest
+
+import oracle
+from oracle import training as T
+from workloads import synth
+from gpu_util import dev, host_bits, log
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+U = 2.0 ** -24
+TINY = 2.0 ** -126
+RND = {"bf16": 2.0 ** -8, "f32": U}
+ALL = ("hidden", "lm_head_w", "markov_w1", "markov_w2")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    import block_draft_readout_amd as bdr
+    bdr.lib()
+
+
+def bdr():
+    import block_draft_readout_amd as m
+    return m
+
+
+def _st(a, dtype):
+    return synth.store(np.ascontiguousarray(a, dtype=np.float32), dtype)
+
+
+def _opt(a):
+    return None if a is None else dev(a)
+
+
+def _case(seed, N, H, V, r, dtype, top=0, empty=0.2):
+    g = np.random.default_rng(seed)
+    c = dict(dtype=dtype, N=N, V=V, hidden=_st(g.standard_normal((N, H)), dtype),
+             w=_st(g.standard_normal((V, H)) * 2 / np.sqrt(H), dtype), w1=None, w2=None, prev=None,
+             g=(g.random(N) + 0.2).astype(np.float32))
+    if r:
+        c["w1"] = _st(g.standard_normal((V, r)), dtype)
+        c["w2"] = _st(g.standard_normal((V, r)) * 0.3, dtype)
+        c["prev"] = np.where(g.random(N) < 0.4, g.integers(0, max(1, V // 50), N),
+                             g.integers(-1, V + 1, N)).astype(np.int32)
+    out = g.random(N) < empty
+    if top:
+        ids = g.integers(0, V, (N, top))
+        if top > 1:
+            ids[:, 1] = np.where(g.random(N) < 0.3, ids[:, 0], ids[:, 1])   # an id twice
+        bad = (g.random((N, top)) < 0.2) | out[:, None]
+        c["ids"] = np.where(bad, g.choice([-1, V, -(2 ** 31), 2 ** 31 - 1], (N, top)), ids).astype(np.int32)
+        u = g.standard_normal((N, top)) * 2
+        u = np.where(g.random((N, top)) < 0.05, -np.inf, u)
+        c["u"] = np.where(bad, np.nan, u).astype(np.float32)
+    else:
+        c["labels"] = np.where(out, g.choice([-100, -1, V, 2 ** 31 - 1], N), g.integers(0, V, N)).astype(np.int32)
+        if N > 1:
+            c["labels"][1] = V - 1
+    return c
+
+
+def _markov(c):
+    return dict(markov_w1=_opt(c["w1"]), markov_w2=_opt(c["w2"]), prev_token=_opt(c["prev"]))
+
+
+def _run(c, temp=1.0, grads=None, udt=torch.float32):
+    """(loss, lse, picked or None, gradients) of the library's calls."""
+    m = bdr()
+    x, w, g, mk = dev(c["hidden"]), dev(c["w"]), dev(c["g"]), _markov(c)
+    if "labels" in c:
+        lab = dev(c["labels"])
+        loss, lse = m.dspark_ce_loss(x, w, lab, **mk)
+        return loss, lse, None, m.dspark_ce_backward(x, w, lab, lse, g, grads=grads, **mk)
+    ids, u = dev(c["ids"]), dev(c["u"]).to(udt)
+    loss, lse, picked = m.dspark_distill_loss(x, w, ids, u, temperature=temp, **mk)
+    return loss, lse, picked, m.dspark_distill_backward(x, w, ids, u, lse, picked, g,
+                                                        temperature=temp, grads=grads, **mk)
+
+
+def _oracle(c, temp=1.0, **kw):
+    t = dict(labels=c["labels"]) if "labels" in c else dict(ids=c["ids"], u=c["u"], T=temp)
+    return T.loss(c["hidden"], c["w"], c["dtype"], w1=c["w1"], w2=c["w2"], prev=c["prev"],
+                  loss_grad=c["g"], **t, **kw)
+
+
+def _np(t, dtype=None):
+    return oracle.widen(host_bits(t), dtype) if dtype else t.cpu().numpy().astype(np.float64)
+
+
+def _within(name, got, ref, tol):
+    err = np.abs(got - ref)
+    ok = err <= tol
+    assert ok.all(), (name, np.argwhere(~ok)[:3].tolist(), float(np.nanmax(err / np.maximum(tol, 1e-300))))
+    return float((err / np.maximum(tol, 1e-300)).max()) if err.size else 0.0
+
+
+def _check(c, temp=1.0, udt=torch.float32):
+    dtype, rnd = c["dtype"], RND[c["dtype"]]
+    loss, lse, picked, grads = _run(c, temp, udt=udt)
+    o = _oracle(c, temp)
+    live = o["live"]
+    H = c["hidden"].shape[1] + (c["w1"].shape[1] if c["w1"] is not None else 0)
+    zerr = (H / 4 + 40) * U * o["zabs"]
+    mag = 1 + np.abs(o["lse"]) + o["zabs"] / temp
+    ep = 2 * zerr / temp + 64 * U * mag
+    got = _np(loss)
+    assert not got[~live].any() and not _np(lse)[~live].any()
+    logt = 0.0
+    if picked is not None:
+        t = T.teacher_targets(c["ids"], c["u"], c["V"], temp)
+        logt = np.abs(np.log(np.where(t > 0, t, 1.0))).max(axis=1)
+        pk = _np(picked)
+        assert not pk[o["picked"] == 0].any()
+        _within("picked", pk, o["picked"], zerr[:, None] + U)
+    worst = [_within("lse", _np(lse), o["lse"], (zerr / temp + 64 * U * mag) * live),
+             _within("loss", got, o["loss"], temp * temp * (ep + 64 * U * (mag + logt)) * live)]
+    E = o["gp"] * ep[:, None] + (rnd + 4 * U) * np.abs(o["dz"]) + TINY * live[:, None]
+    W = np.abs(oracle.widen(c["w"], dtype))
+    X = np.where(live[:, None], np.abs(oracle.widen(c["hidden"], dtype)), 0.0)
+    N, V = c["N"], c["V"]
+    moved = dict(hidden=E @ W, lm_head_w=E.T @ X)
+    if c["w1"] is not None:
+        W2 = np.abs(oracle.widen(c["w2"], dtype))
+        has = (c["prev"] >= 0) & (c["prev"] < V) & live
+        e = np.zeros((N, W2.shape[1]))
+        e[has] = np.abs(oracle.widen(c["w1"], dtype))[c["prev"][has]]
+        d1 = np.zeros_like(W2)
+        np.add.at(d1, c["prev"][has], (E @ W2)[has])
+        moved.update(markov_w1=d1, markov_w2=E.T @ e)
+    chain = dict(hidden=V, lm_head_w=N, markov_w1=V + 4 * N, markov_w2=N)
+    assert set(grads) == set(moved)
+    for k, v in grads.items():
+        tol = moved[k] + (chain[k] / 4 + 40) * U * o["abs_" + k] + rnd * np.abs(o[k])
+        tol = tol + TINY * chain[k]
+        worst.append(_within(k, _np(v, dtype), o[k], tol))
+        if k == "hidden":
+            assert not _np(v, dtype)[~live].any()
+    return max(worst)
+
+
+CE = [("f32", 1, 4, 1, 0), ("f32", 5, 64, 1000, 8), ("f32", 60, 64, 1000, 0), ("f32", 33, 132, 257, 128),
+      ("f32", 200, 36, 2600, 4), ("f32", 130, 260, 129, 12),
+      ("bf16", 1, 8, 2, 0), ("bf16", 1, 72, 1000, 8), ("bf16", 7, 320, 4001, 32), ("bf16", 64, 64, 127, 64),
+      ("bf16", 129, 136, 2561, 24), ("bf16", 300, 520, 1031, 128), ("bf16", 513, 200, 517, 0),
+      ("bf16", 31, 1000, 5003, 40)]
+
+
+@pytest.mark.parametrize("dtype,N,H,V,r", CE)
+def test_cross_entropy(dtype, N, H, V, r):
+    w = _check(_case(N * 31 + V, N, H, V, r, dtype, empty=0.0 if N == 1 else 0.2))
+    log(f"ce {dtype} {N}x{H} V={V} r={r}: worst error / tolerance {w:.3f}")
+
+
+DISTILL = [("f32", 5, 64, 1000, 8, 4, 1.0), ("f32", 70, 36, 300, 0, 256, 2.0), ("f32", 40, 68, 65, 4, 65, 0.5),
+           ("bf16", 1, 72, 1000, 8, 1, 1.0), ("bf16", 19, 320, 4001, 32, 20, 2.0),
+           ("bf16", 140, 136, 2561, 24, 64, 1.0), ("bf16", 300, 264, 1031, 128, 7, 3.5),
+           ("bf16", 65, 64, 2, 0, 3, 1.0)]
+
+
+@pytest.mark.parametrize("dtype,N,H,V,r,top,temp", DISTILL)
+def test_distillation(dtype, N, H, V, r, top, temp):
+    w = _check(_case(N * 17 + V, N, H, V, r, dtype, top=top, empty=0.0 if N == 1 else 0.2), temp)
+    log(f"distill {dtype} {N}x{H} V={V} r={r} top={top} T={temp}: worst error / tolerance {w:.3f}")
+
+
+def test_distillation_with_bf16_teacher_logits():
+    c = _case(5, 33, 64, 500, 8, "bf16", top=9)
+    keep = np.isfinite(c["u"])
+    c["u"][keep] = oracle.widen(synth.to_bf16_bits(c["u"][keep]), "bf16")
+    _check(c, 1.5, udt=torch.bfloat16)
+
+
+FLAT = [(1, 64, 256, 8), (3, 200, 1000, 0), (130, 328, 2560, 64), (257, 72, 130, 16), (40, 2568, 5000, 128),
+        (700, 136, 3001, 8), (16, 640, 20011, 32)]
+
+
+@pytest.mark.parametrize("N,H,V,r", FLAT)
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_flat_softmax_is_exact(N, H, V, r, dtype):
+    """hidden = 0: d hidden = (mean of W - W[label]) g; then W = 0: d W from whole hidden."""
+    g = np.random.default_rng(N + V)
+    small = lambda *s: _st(g.integers(-3, 4, s), dtype)
+    prev = g.integers(0, min(V, 5), N).astype(np.int32)
+    labels = np.where(g.random(N) < 0.2, -1, g.integers(0, V, N)).astype(np.int32)
+    gr = 2.0 ** g.integers(-2, 3, N).astype(np.float32)
+    live = labels >= 0
+    p = 1.0 / V
+    rd = T.round_bf16 if dtype == "bf16" else lambda a: np.asarray(a, np.float32).astype(np.float64)
+    # the two values of d logits / g, which powers of two scale exactly.  (p - 1 in fp32 depends on
+    # the last bit of p; only bf16's values are pinned exactly, far from a rounding border.)
+    lo, hi = float(rd(p)), float(rd(p - 1.0))
+    for v in (p, p - 1.0):
+        if dtype == "bf16":
+            assert rd(v * (1 + 1e-5)) == rd(v * (1 - 1e-5))
+    base = dict(dtype=dtype, N=N, V=V, prev=prev if r else None, labels=labels, g=gr)
+    zero = lambda *s: _st(np.zeros(s), dtype)
+    one = np.zeros((N, V))
+    one[live] = lo
+    one[live, labels[live]] = hi
+    dz = one * gr[:, None]
+    # fp32: p is off by at most 64 u (lse, two exponentials); everything else is exact
+    off = 0.0 if dtype == "bf16" else 128 * U
+
+    # every product is a multiple of this: 8 bits of lo (hi has a larger last bit), the smallest g
+    last = 2.0 ** (np.floor(np.log2(p)) - 7) * float(gr.min())
+
+    def same(name, got, ref, mags, K):
+        err = np.abs(_np(got, dtype) - ref)
+        sums = (K / 4 + 40) * U * mags
+        assert (err <= RND[dtype] * np.abs(ref) + sums + off * mags).all(), name
+        if dtype == "bf16":
+            exact = mags < 2.0 ** 24 * last
+            assert np.array_equal(_np(got, dtype)[exact], T.round_bf16(ref)[exact]), name
+
+    w, w1z, w2 = small(V, H), zero(V, r) if r else None, small(V, r) if r else None
+    gr1 = _run(dict(base, hidden=zero(N, H), w=w, w1=w1z, w2=w2))[3]
+    Wd, adz = oracle.widen(w, dtype), np.abs(dz)
+    same("hidden", gr1["hidden"], dz @ Wd, adz @ np.abs(Wd), V)
+    if r:
+        d1, a1 = np.zeros((V, r)), np.zeros((V, r))
+        np.add.at(d1, prev, dz @ oracle.widen(w2, dtype))
+        np.add.at(a1, prev, adz @ np.abs(oracle.widen(w2, dtype)))
+        same("markov_w1", gr1["markov_w1"], d1, a1, V + 4 * N)
+        assert not gr1["markov_w2"].any()
+    x, w1 = small(N, H), small(V, r) if r else None
+    gr2 = _run(dict(base, hidden=x, w=zero(V, H), w1=w1, w2=zero(V, r) if r else None))[3]
+    Xd = oracle.widen(x, dtype)
+    same("lm_head_w", gr2["lm_head_w"], dz.T @ Xd, adz.T @ np.abs(Xd), N)
+    if r:
+        Ed = oracle.widen(w1, dtype)[prev]
+        same("markov_w2", gr2["markov_w2"], dz.T @ Ed, adz.T @ np.abs(Ed), N)
+    assert not gr2["hidden"].any()
+
+
+def test_several_pieces_match_one(monkeypatch):
+    """Enough rows that the backward pass walks the vocabulary in pieces: the same gradients as
+    the rows in two halves give, up to the order of sums and the roundings of the halves."""
+    N, H, V, r = 26000, 64, 12000, 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x = rn(N, H).bfloat16()
+    w = (rn(V, H) / 8).bfloat16()
+    w1, w2 = rn(V, r).bfloat16(), (rn(V, r) * 0.3).bfloat16()
+    lab = torch.randint(-1, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    prev = torch.randint(-1, 40, (N,), generator=g, device="cuda", dtype=torch.int32)
+    lg = torch.rand(N, generator=g, device="cuda") / N
+    m = bdr()
+    need = m.lib().dspark_ce_workspace_bytes(N, H, V, r, m.BDR_BF16, 1)
+    assert need < N * V * 2     # less than the logits: pieces
+    mk = dict(markov_w1=w1, markov_w2=w2)
+    loss, lse = m.dspark_ce_loss(x, w, lab, prev_token=prev, **mk)
+    whole = m.dspark_ce_backward(x, w, lab, lse, lg, prev_token=prev, **mk)
+    k = N // 2
+    sl = (slice(0, k), slice(k, N))
+    parts, rows = [], []
+    for s in sl:
+        l2, e2 = m.dspark_ce_loss(x[s], w, lab[s], prev_token=prev[s], **mk)
+        assert torch.equal(l2, loss[s]) and torch.equal(e2, lse[s])
+        parts.append(m.dspark_ce_backward(x[s], w, lab[s], e2, lg[s], prev_token=prev[s], **mk))
+    hid = torch.cat([p["hidden"] for p in parts])
+    # the same d logits; fp32 sums in another order, then one bf16 rounding: at most one step apart
+    assert ((hid.float() - whole["hidden"].float()).abs()
+            <= 2.0 ** -7 * hid.float().abs() + 1e-5 * hid.float().abs().max()).all()
+    for name in ("lm_head_w", "markov_w1", "markov_w2"):
+        a, b = (p[name].float() for p in parts)
+        tol = 2.0 ** -8 * (a.abs() + b.abs() + whole[name].float().abs()) + 1e-5 * whole[name].float().abs().max()
+        assert ((a + b - whole[name].float()).abs() <= tol).all(), name
+
+
+@pytest.mark.parametrize("top", [0, 6])
+def test_rows_left_out_may_hold_anything(top):
+    c = _case(11, 50, 136, 700, 16, "bf16", top=top, empty=0.4)
+    live = _oracle(c)["live"]
+    ref = _run(c)
+    d = dict(c, hidden=c["hidden"].copy(), g=c["g"].copy(), prev=c["prev"].copy())
+    d["hidden"][~live] = 0x7FFF          # NaN
+    d["g"][~live] = np.nan
+    d["prev"][~live] = 2 ** 31 - 1
+    got = _run(d)
+    assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
+    for k in ref[3]:
+        assert torch.equal(ref[3][k], got[3][k]), k
+    # and in other places: rows without a target between the others change nothing
+    keep = np.flatnonzero(live)
+    e = {k: (v[keep] if k in ("hidden", "g", "prev", "labels", "ids", "u") else v) for k, v in c.items()}
+    e["N"] = len(keep)
+    got = _run(e)
+    assert torch.equal(ref[0][torch.from_numpy(live).cuda()], got[0])
+    for k in ("lm_head_w", "markov_w1", "markov_w2"):
+        assert torch.equal(ref[3][k], got[3][k]), k
+
+
+@pytest.mark.parametrize("top", [0, 3])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_no_row_with_a_target_and_no_rows(top, dtype):
+    c = _case(13, 21, 64, 300, 8, dtype, top=top, empty=1.1)
+    if not top:
+        c["labels"][:] = -1
+    loss, lse, picked, grads = _run(c)
+    assert not loss.any() and not lse.any() and (picked is None or not picked.any())
+    for k, v in grads.items():
+        assert not v.any(), k
+    z = {k: (v[:0] if k in ("hidden", "g", "prev", "labels", "ids", "u") else v) for k, v in c.items()}
+    z["N"] = 0
+    loss, lse, picked, grads = _run(z)
+    assert loss.shape == (0,) and grads["hidden"].shape == (0, 64)
+    for k in ("lm_head_w", "markov_w1", "markov_w2"):
+        assert not grads[k].any()
+
+
+def test_single_gradients_equal_the_joint_call():
+    c = _case(15, 90, 200, 900, 24, "bf16")
+    full = _run(c)[3]
+    for k in ALL:
+        assert torch.equal(_run(c, grads=(k,))[3][k], full[k]), k
+    again = _run(c)[3]
+    for k in ALL:
+        assert torch.equal(again[k], full[k]), k
+
+
+def test_every_row_the_same_previous_token():
+    c = _case(16, 600, 64, 150, 40, "f32", empty=0.1)
+    c["prev"][:] = 149
+    _check(c)
+
+
+def test_large_logits_stay_finite():
+    """Logits of +-200: the running maximum keeps every exponential in range."""
+    c = _case(18, 20, 64, 400, 0, "f32", empty=0.0)
+    c["w"] *= np.float32(40)
+    loss, lse, _, grads = _run(c)
+    o = _oracle(c)
+    assert o["zabs"].max() > 300 and torch.isfinite(loss).all()
+    _check(c)
+
+
+def test_captured_and_replayed_on_another_stream():
+    m = bdr()
+    a, b = (_case(s, 70, 136, 1500, 16, "bf16", empty=0.3) for s in (20, 21))
+    d = _case(22, 70, 136, 1500, 16, "bf16", top=5, empty=0.3)
+    x, w, lab, prev, g = (dev(a[k]) for k in ("hidden", "w", "labels", "prev", "g"))
+    ids, u = dev(d["ids"]), dev(d["u"])
+    w1, w2 = dev(a["w1"]), dev(a["w2"])
+    mk = dict(markov_w1=w1, markov_w2=w2, prev_token=prev)
+    L = m.lib()
+    n = max(L.dspark_ce_workspace_bytes(70, 136, 1500, 16, m.BDR_BF16, 1),
+            L.dspark_distill_workspace_bytes(70, 136, 1500, 16, 5, m.BDR_BF16, 1))
+    ws = torch.full((n + 256,), 255, dtype=torch.uint8, device="cuda")
+
+    def step():
+        loss, lse = m.dspark_ce_loss(x, w, lab, workspace=ws, **mk)
+        gr = m.dspark_ce_backward(x, w, lab, lse, g, workspace=ws, **mk)
+        l2, e2, pk = m.dspark_distill_loss(x, w, ids, u, temperature=2.0, workspace=ws, **mk)
+        g2 = m.dspark_distill_backward(x, w, ids, u, e2, pk, g, temperature=2.0, workspace=ws, **mk)
+        return [loss, lse, l2, e2, pk, *(gr[k] for k in ALL), *(g2[k] for k in ALL)]
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        step()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for k, c in enumerate((b, a, b)):
+        x.copy_(dev(c["hidden"]))
+        lab.copy_(dev(c["labels"]))
+        prev.copy_(dev(c["prev"]))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in out]
+        for i, (p, q) in enumerate(zip(got, step())):
+            assert torch.equal(p, q), (k, i)
+
+
+def test_refusals():
+    m = bdr()
+    c = _case(30, 6, 64, 100, 8, "bf16")
+    x, w, lab, mk = dev(c["hidden"]), dev(c["w"]), dev(c["labels"]), _markov(c)
+    with pytest.raises(ValueError):
+        m.dspark_ce_loss(x.t(), w, lab, **mk)
+    with pytest.raises(ValueError):
+        m.dspark_ce_loss(x[:, :32], w, lab, **mk)
+    with pytest.raises(TypeError):
+        m.dspark_ce_loss(x, w, lab.long(), **mk)
+    with pytest.raises(TypeError):
+        m.dspark_ce_loss(x.half(), w.half(), lab)
+    with pytest.raises(ValueError):
+        m.dspark_ce_loss(x, w, lab[:5], **mk)
+    with pytest.raises(ValueError):
+        m.dspark_ce_loss(x, w, lab, markov_w1=mk["markov_w1"])
+    with pytest.raises(ValueError):
+        m.dspark_ce_loss(x, w, lab, markov_w1=mk["markov_w1"], markov_w2=mk["markov_w2"])
+    with pytest.raises(m.BdrError):
+        m.dspark_ce_loss(x, w, lab, workspace=torch.empty(64, dtype=torch.uint8, device="cuda"))
+    loss, lse = m.dspark_ce_loss(x, w, lab, **mk)
+    with pytest.raises(ValueError):
+        m.dspark_ce_backward(x, w, lab, lse, lse, grads=("head",), **mk)
+    with pytest.raises(ValueError):
+        m.dspark_ce_backward(x, w, lab, lse, lse, grads=("markov_w1",))
+    with pytest.raises(m.BdrError):
+        m.dspark_ce_backward(x, w, lab, lse, lse, grads=(), **mk)
+    with pytest.raises(m.BdrError):
+        m.dspark_distill_loss(x, w, lab[:, None].contiguous(), lse[:, None].contiguous(), temperature=0.0)
+
+
+def test_training_step_of_the_readout():
+    """norm -> cross entropy -> backward through both, as a drafter trains them, against
+    differences of the summed loss along random directions (fp32).
+
+    The five-point difference with step h is off by the loss's own error (each value within
+    loss_err of the exact loss) over h and by h^4 |fifth derivative| / 30, which the change
+    from 2 h to h bounds: the sum of both is the tolerance."""
+    m = bdr()
+    N, H, V, r = 24, 64, 500, 8
+    c = _case(40, N, H, V, r, "f32")
+    x, w, lab, g, mk = dev(c["hidden"]), dev(c["w"]), dev(c["labels"]), dev(c["g"]), _markov(c)
+    gn = np.random.default_rng(41)
+    nw, nb = dev((1 + 0.1 * gn.standard_normal(H)).astype(np.float32)), dev((0.1 * gn.standard_normal(H)).astype(np.float32))
+
+    def loss(x, w, nw, nb, w1, w2):
+        y = m.dspark_norm(x, nw, nb, eps=1e-5)
+        l, _ = m.dspark_ce_loss(y, w, lab, markov_w1=w1, markov_w2=w2, prev_token=mk["prev_token"])
+        return float((l.double() * g.double()).sum())
+
+    y, mean, rstd = m.dspark_norm(x, nw, nb, eps=1e-5, stats=True)
+    l, lse = m.dspark_ce_loss(y, w, lab, **mk)
+    gr = m.dspark_ce_backward(y, w, lab, lse, g, **mk)
+    dx, dnw, dnb = m.dspark_norm_backward(gr["hidden"], x, nw, mean, rstd)
+    args = [x, w, nw, nb, mk["markov_w1"], mk["markov_w2"]]
+    zabs = float((y.abs() @ w.abs().t()).max()) + r
+    loss_err = float(g.sum()) * (2 * (H / 4 + 60) * U * zabs + 128 * U * (1 + zabs))
+    for i, d in enumerate((dx, gr["lm_head_w"], dnw, dnb, gr["markov_w1"], gr["markov_w2"])):
+        v = dev(gn.standard_normal(tuple(d.shape)).astype(np.float32))
+        v *= float(d.abs().sum() and 1.0) / float(v.norm())
+
+        def diff(h):
+            f = [loss(*(a + k * h * v if j == i else a for j, a in enumerate(args))) for k in (-2, -1, 1, 2)]
+            return (f[0] - 8 * f[1] + 8 * f[2] - f[3]) / (12 * h)
+
+        h = 0.25
+        d1, d2 = diff(h), diff(2 * h)
+        want = float((d.double() * v.double()).sum())
+        tol = 1.5 * loss_err / h + abs(d1 - d2)
+        log(f"direction {i}: gradient {want:.6f}, difference {d1:.6f}, tolerance {tol:.2e}")
+        assert abs(want - d1) <= tol
