@@ -498,7 +498,7 @@ LossGemm logits_gemm(const LossProblem& p, const LossRows& r, int64_t v0, int64_
   g.M = p.rows;
   g.N = width;
   g.live_m = 1;
-  g.band = 4;
+  g.band = 16;
   g.splits = 1;
   g.scale2 = kLog2e / p.temperature;
   return g;
@@ -570,7 +570,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.M = p.rows;
       d.N = cols;
       d.live_m = 1;
-      d.band = 4;
+      d.band = 16;
       d.splits = splits;
       d.out = part;
       d.ldo = cols;
@@ -591,7 +591,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.splits = 1;
       d.out = static_cast<char*>(out) + v0 * cols * es;
       d.ldo = cols;
-      return launch_loss_dweight(p.dt, p.rows, d, st);
+      return launch_loss_dweight(p.dt, d, st);
     };
     if (o.hidden) BDR_LAUNCH(dfeat(p.w, p.hidden, b.part_x, q.splits_x));
     if (o.w1) BDR_LAUNCH(dfeat(p.w2, p.rank, b.part_e, q.splits_e));

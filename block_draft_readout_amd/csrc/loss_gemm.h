@@ -81,7 +81,8 @@ struct LossTile {
   static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
   static constexpr int LOADS_A = BM / 8 / WAVES, LOADS_B = BN / 8 / WAVES;
   static constexpr int LOADS = LOADS_A + LOADS_B;
-  static constexpr int SLOW_READS = sizeof(S) == 2 ? 2 : 4;
+  // LDS reads the compiler schedules, per half step (the transposing ones are its own block)
+  static constexpr int SLOW_READS = sizeof(S) == 2 ? 0 : 4;
   static constexpr int READS = WTM * (AKS ? SLOW_READS : 1) + WTN * (BKS ? SLOW_READS : 1);
   static constexpr int MFMAS = WTM * WTN * Elem<S>::MFMA_PER16;   // per half step
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "loads split evenly over the waves");
@@ -89,15 +90,14 @@ struct LossTile {
   static_assert(LDS_BYTES <= 160 * 1024, "tile fits");
 };
 
-// XOR of the 32-byte unit index in a reduction-slow bf16 LDS row of ROWB bytes:
-// one transposing read takes the rows {8 g + j : g, j < 4} (or those plus 4), and
-// (row * ROWB + unit * 32) mod 512 has to differ between all 16 of them.
+// XOR of the 32-byte unit index in a reduction-slow bf16 LDS row of ROWB bytes.
+// A transposing read takes 16 pieces of 32 bytes, rows {8 g + j : g, j < 4} (or
+// those plus 4), in two passes of 32 lanes (g = 0, 1, then 2, 3) over 64 banks:
+// (row * ROWB + unit * 32) mod 256 has to differ between the 8 rows of a pass.
 template <int ROWB>
 __device__ __forceinline__ uint32_t slow_swizzle(uint32_t kr) {
-  const uint32_t g = (kr >> 3) & 3u, j = kr & 3u;
-  if constexpr (ROWB % 512 == 0) return g | (j << 2);
-  if constexpr (ROWB % 512 == 256) return g | ((j >> 1) << 2);
-  return g;
+  const uint32_t g = (kr >> 3) & 1u, j = kr & 3u;
+  return ROWB % 256 == 0 ? (j << 1) | g : (j >> 1) | (g << 1);
 }
 
 // 16 bytes per lane, global -> LDS: lane l's land at dst + 16 l (dst uniform)
@@ -106,12 +106,72 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t off, char* dst) {
                                            0, 0, 0);
 }
 
-// four 16-bit values of column lane % 16, from the 4 rows x 16 columns whose
-// 8-byte pieces the 16 lanes of a group name
-__device__ __forceinline__ uint2 lds_read_tr4(const char* p) {
-  typedef short s16x4_t __attribute__((ext_vector_type(4)));
-  return __builtin_bit_cast(
-      uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4_t*)p));
+// Transposing reads of NA operand tiles whose 8-byte pieces this lane names at
+// LDS addresses ad[0 .. NA), and of NB more at ad[NA ..): four 16-bit values of
+// column lane % 16 from 4 k rows (the address's and the next three lanes
+// groups'), and those 4 k rows further on (RA / RB bytes per k row), HALF bytes
+// into the operands' k rows.  One block of assembly with its own wait: the
+// compiler takes the intrinsic for a possible write to LDS and waits for every
+// buffer-to-LDS load in flight before it, which costs the loads' latency once a
+// step (256 x 256 x 64 tiles, 4096 x 30720 x 5120: 1060 -> TR_NEW TFLOP/s).
+#define BDR_TR_READ(i, o0, o1)                                                          \
+  "ds_read_b64_tr_b16 %[l" #i "], %[a" #i "] offset:%c[" #o0 "]\n\t"                     \
+  "ds_read_b64_tr_b16 %[h" #i "], %[a" #i "] offset:%c[" #o1 "]\n\t"
+#define BDR_TR_OUT(i) [l##i] "=&v"(l[i]), [h##i] "=&v"(h[i])
+#define BDR_TR_IN(i) [a##i] "v"(ad[i])
+#define BDR_TR_4(m, i0, i1, i2, i3, ...) \
+  m(i0, ##__VA_ARGS__) m(i1, ##__VA_ARGS__) m(i2, ##__VA_ARGS__) m(i3, ##__VA_ARGS__)
+#define BDR_TR_IMM                                                                       \
+  [p0] "n"(HALF * RA), [p1] "n"((HALF + 4) * RA), [q0] "n"(HALF * RB), [q1] "n"((HALF + 4) * RB)
+template <int NA, int RA, int NB, int RB, int HALF>
+__device__ __forceinline__ void lds_read_tr(const uint32_t (&ad)[NA + NB], u32x4_t (&f)[NA + NB]) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  u32x2_t l[NA + NB], h[NA + NB];
+  if constexpr (NA == 2 && NB == 0) {
+    asm volatile(BDR_TR_READ(0, p0, p1) BDR_TR_READ(1, p0, p1) "s_waitcnt lgkmcnt(0)"
+                 : BDR_TR_OUT(0), BDR_TR_OUT(1)
+                 : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IMM
+                 : "memory");
+  } else if constexpr (NA == 4 && NB == 0) {
+    asm volatile(BDR_TR_4(BDR_TR_READ, 0, 1, 2, 3, p0, p1) "s_waitcnt lgkmcnt(0)"
+                 : BDR_TR_OUT(0), BDR_TR_OUT(1), BDR_TR_OUT(2), BDR_TR_OUT(3)
+                 : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IMM
+                 : "memory");
+  } else if constexpr (NA == 5 && NB == 0) {
+    asm volatile(BDR_TR_4(BDR_TR_READ, 0, 1, 2, 3, p0, p1) BDR_TR_READ(4, p0, p1)
+                 "s_waitcnt lgkmcnt(0)"
+                 : BDR_TR_OUT(0), BDR_TR_OUT(1), BDR_TR_OUT(2), BDR_TR_OUT(3), BDR_TR_OUT(4)
+                 : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IN(4), BDR_TR_IMM
+                 : "memory");
+  } else if constexpr (NA == 4 && NB == 2) {
+    asm volatile(BDR_TR_READ(4, q0, q1) BDR_TR_READ(5, q0, q1)
+                 BDR_TR_4(BDR_TR_READ, 0, 1, 2, 3, p0, p1) "s_waitcnt lgkmcnt(0)"
+                 : BDR_TR_OUT(0), BDR_TR_OUT(1), BDR_TR_OUT(2), BDR_TR_OUT(3), BDR_TR_OUT(4),
+                   BDR_TR_OUT(5)
+                 : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IN(4),
+                   BDR_TR_IN(5), BDR_TR_IMM
+                 : "memory");
+  } else if constexpr (NA == 8 && NB == 5) {
+    asm volatile(BDR_TR_4(BDR_TR_READ, 8, 9, 10, 11, q0, q1) BDR_TR_READ(12, q0, q1)
+                 BDR_TR_4(BDR_TR_READ, 0, 1, 2, 3, p0, p1) BDR_TR_4(BDR_TR_READ, 4, 5, 6, 7, p0, p1)
+                 "s_waitcnt lgkmcnt(0)"
+                 : BDR_TR_OUT(0), BDR_TR_OUT(1), BDR_TR_OUT(2), BDR_TR_OUT(3), BDR_TR_OUT(4),
+                   BDR_TR_OUT(5), BDR_TR_OUT(6), BDR_TR_OUT(7), BDR_TR_OUT(8), BDR_TR_OUT(9),
+                   BDR_TR_OUT(10), BDR_TR_OUT(11), BDR_TR_OUT(12)
+                 : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IN(4),
+                   BDR_TR_IN(5), BDR_TR_IN(6), BDR_TR_IN(7), BDR_TR_IN(8), BDR_TR_IN(9),
+                   BDR_TR_IN(10), BDR_TR_IN(11), BDR_TR_IN(12), BDR_TR_IMM
+                 : "memory");
+  } else {
+    static_assert(NA < 0, "no transposing read of this shape");
+  }
+#pragma unroll
+  for (int i = 0; i < NA + NB; ++i) f[i] = u32x4_t{l[i].x, l[i].y, h[i].x, h[i].y};
+}
+
+// 32-bit LDS address of a pointer into the workgroup's LDS
+__device__ __forceinline__ uint32_t lds_address(const char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
 }
 
 // Joins two running (maximum, sum of 2^(x - maximum)) pairs.
@@ -252,14 +312,6 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
     if constexpr (!decltype(slow)::value) {
       const uint32_t c = (static_cast<uint32_t>(4 * half + grp) ^ static_cast<uint32_t>(lane & 7)) * 16u;
       return *reinterpret_cast<const u32x4_t*>(base + static_cast<uint32_t>(tile * 16 + r16) * 128u + c);
-    } else if constexpr (ES == 2) {
-      constexpr uint32_t ROWB = decltype(rowbytes)::value;
-      const uint32_t kr = static_cast<uint32_t>(8 * grp + (r16 >> 2));
-      const uint32_t off = kr * ROWB + ((static_cast<uint32_t>(tile) ^ slow_swizzle<ROWB>(kr)) << 5) +
-                           static_cast<uint32_t>(lane & 3) * 8u + static_cast<uint32_t>(half) * 32u * ROWB;
-      const uint2 lo = lds_read_tr4(base + off);
-      const uint2 hi = lds_read_tr4(base + off + 4 * ROWB);
-      return u32x4_t{lo.x, lo.y, hi.x, hi.y};
     } else {
       constexpr uint32_t ROWB = decltype(rowbytes)::value;
       const char* p = base + static_cast<uint32_t>(16 * half + 4 * grp) * ROWB +
@@ -270,14 +322,47 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
       return v;
     }
   };
-  auto read_frags = [&](int buf, int half, FragA& a, FragB& b) {
-    const char* base = lds + buf * T::STAGE_BYTES;
-    static_for<T::WTM>([&](auto i) {
-      a[i] = read_op(ASlow{}, ARow{}, base, wm * T::WTM + decltype(i)::value, half);
-    });
+  // LDS address of this lane's piece of slow bf16 tile `tile` at k row 0 of a stage
+  auto slow_at = [&](auto rowbytes, int operand, int tile) -> uint32_t {
+    constexpr uint32_t ROWB = decltype(rowbytes)::value;
+    const uint32_t kr = static_cast<uint32_t>(8 * grp + (r16 >> 2));
+    return lds_address(lds) + static_cast<uint32_t>(operand) + kr * ROWB +
+           ((static_cast<uint32_t>(tile) ^ slow_swizzle<ROWB>(kr)) << 5) +
+           static_cast<uint32_t>(lane & 3) * 8u;
+  };
+  uint32_t at_a[T::WTM], at_b[T::WTN];
+  if constexpr (ES == 2 && T::AKS)
+    static_for<T::WTM>([&](auto i) { at_a[i] = slow_at(ARow{}, 0, wm * T::WTM + decltype(i)::value); });
+  if constexpr (ES == 2 && T::BKS)
     static_for<T::WTN>([&](auto j) {
-      b[j] = read_op(BSlow{}, BRow{}, base + T::A_BYTES, wn * T::WTN + decltype(j)::value, half);
+      at_b[j] = slow_at(BRow{}, T::A_BYTES, wn * T::WTN + decltype(j)::value);
     });
+  auto read_frags = [&](int buf, auto halfc, FragA& a, FragB& b) {
+    constexpr int half = decltype(halfc)::value;
+    const char* base = lds + buf * T::STAGE_BYTES;
+    const uint32_t stage = static_cast<uint32_t>(buf * T::STAGE_BYTES);
+    constexpr bool tr_a = ES == 2 && T::AKS, tr_b = ES == 2 && T::BKS;
+    if constexpr (!tr_a)
+      static_for<T::WTM>([&](auto i) {
+        a[i] = read_op(ASlow{}, ARow{}, base, wm * T::WTM + decltype(i)::value, half);
+      });
+    if constexpr (!tr_b)
+      static_for<T::WTN>([&](auto j) {
+        b[j] = read_op(BSlow{}, BRow{}, base + T::A_BYTES, wn * T::WTN + decltype(j)::value, half);
+      });
+    if constexpr (tr_a && tr_b) {
+      uint32_t ad[T::WTM + T::WTN];
+      u32x4_t f[T::WTM + T::WTN];
+      static_for<T::WTM>([&](auto i) { ad[i] = at_a[i] + stage; });
+      static_for<T::WTN>([&](auto j) { ad[T::WTM + j] = at_b[j] + stage; });
+      lds_read_tr<T::WTM, T::BM * 2, T::WTN, T::BN * 2, 32 * half>(ad, f);
+      static_for<T::WTM>([&](auto i) { a[i] = f[i]; });
+      static_for<T::WTN>([&](auto j) { b[j] = f[T::WTM + j]; });
+    } else if constexpr (tr_b) {
+      uint32_t ad[T::WTN];
+      static_for<T::WTN>([&](auto j) { ad[j] = at_b[j] + stage; });
+      lds_read_tr<T::WTN, T::BN * 2, 0, 0, 32 * half>(ad, b);
+    }
   };
 
   // Per step: wait for its loads, one barrier, then per half the operand reads
@@ -300,7 +385,7 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
     BDR_WAIT_VM_LGKM((T::STAGES - 2) * T::LOADS, 0);
     BDR_WG_BARRIER();
     if constexpr (!kSpread) static_for<T::LOADS>([&](auto q) { dma_one(q); });
-    read_frags(buf, 0, a, b);
+    read_frags(buf, std::integral_constant<int, 0>{}, a, b);
     static_for<NT>([&](auto ec) {
       constexpr int e = decltype(ec)::value;
       constexpr int every = kSpread ? NT / T::LOADS : NT;
@@ -309,7 +394,7 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
       if constexpr (kSpread && e % every == every - 1 && e / every < T::LOADS)
         dma_one(std::integral_constant<int, e / every>{});
     });
-    read_frags(buf, 1, a, b);
+    read_frags(buf, std::integral_constant<int, 1>{}, a, b);
     static_for<NT>([&](auto ec) {
       constexpr int e = decltype(ec)::value;
       acc[e / T::WTN][e % T::WTN] =
@@ -317,14 +402,14 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
     });
     if constexpr (kSpread) {   // keep that order through scheduling
       constexpr int every = NT / T::LOADS * Elem<S>::MFMA_PER16;
-      __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
+      if constexpr (T::READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
       static_for<T::LOADS>([&](auto) {
         __builtin_amdgcn_sched_group_barrier(0x008, every, 0);
         __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
       });
       if constexpr (T::MFMAS - every * T::LOADS > 0)
         __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS - every * T::LOADS, 0);
-      __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
+      if constexpr (T::READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
       __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS, 0);
     }
     buf = buf + 1 == T::STAGES ? 0 : buf + 1;

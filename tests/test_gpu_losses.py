@@ -307,12 +307,13 @@ def test_rows_left_out_may_hold_anything(top):
     assert torch.equal(ref[0], got[0]) and torch.equal(ref[1], got[1])
     for k in ref[3]:
         assert torch.equal(ref[3][k], got[3][k]), k
-    # and in other places: rows without a target between the others change nothing
-    keep = np.flatnonzero(live)
-    e = {k: (v[keep] if k in ("hidden", "g", "prev", "labels", "ids", "u") else v) for k, v in c.items()}
-    e["N"] = len(keep)
+    # and wherever they stand: the rows with a target first, the others after them, is the same
+    # product.  (As many rows in all: the tiles, and so the order of sums, go by that number.)
+    order = np.concatenate([np.flatnonzero(live), np.flatnonzero(~live)])
+    e = {k: (v[order] if k in ("hidden", "g", "prev", "labels", "ids", "u") else v) for k, v in c.items()}
     got = _run(e)
-    assert torch.equal(ref[0][torch.from_numpy(live).cuda()], got[0])
+    back = torch.from_numpy(order).cuda()
+    assert torch.equal(ref[0][back], got[0]) and torch.equal(ref[3]["hidden"][back], got[3]["hidden"])
     for k in ("lm_head_w", "markov_w1", "markov_w2"):
         assert torch.equal(ref[3][k], got[3][k]), k
 
