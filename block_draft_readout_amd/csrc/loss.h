@@ -12,7 +12,7 @@ namespace bdr {
 hipError_t launch_loss_stats(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
 hipError_t launch_loss_dlogits(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
 hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
-hipError_t launch_loss_dweight(bdr_dtype dt, const LossGemm& g, hipStream_t stream);
+hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
 
 // vocabulary columns of one statistics tile
 int loss_stats_cols(bdr_dtype dt, int64_t rows);

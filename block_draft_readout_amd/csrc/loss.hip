@@ -285,29 +285,44 @@ __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, cons
 }
 
 // ---------------------------------------------------------------- gradients out
-// d hidden: the reduction splits added in order, rounded, back at the original
-// rows (zeros for rows without a target).  One workgroup per row.
-template <typename S>
-__global__ __launch_bounds__(256) void loss_dhidden_kernel(const int32_t* pos, const float* part,
-                                                           int splits, int64_t slab, int hidden,
-                                                           S* out) {
+// The reduction splits of a feature gradient added in order.  With `pos`, row n
+// of the output is the compacted row pos[n], or zeros (d hidden, rounded);
+// without, the compacted rows stay where they are (d embedding, fp32).  SL lanes
+// share the splits of four columns and join through LDS: few rows have many
+// splits and few columns to spread over the chip.  Grid (rows, columns / (1024 / SL)).
+template <typename S, int SL>
+__global__ __launch_bounds__(256) void loss_join_kernel(const int32_t* live, const int32_t* pos,
+                                                        const float* part, int splits, int64_t slab,
+                                                        int cols, S* out) {
+  constexpr int QUADS = 256 / SL;
+  __shared__ f32x4_t sums[SL > 1 ? 256 : 1];
   const int64_t n = blockIdx.x;
-  const int p = pos[n];
-  for (int c = static_cast<int>(threadIdx.x) * 4; c < hidden; c += 1024) {
-    f32x4_t v{0.f, 0.f, 0.f, 0.f};
-    if (p >= 0)
-      for (int s = 0; s < splits; ++s)
-        v += *reinterpret_cast<const f32x4_t*>(part + s * slab + static_cast<int64_t>(p) * hidden + c);
-    store4(out + n * hidden + c, v);
+  if (!pos && n >= *live) return;
+  const int p = pos ? pos[n] : static_cast<int>(n);
+  const int q = static_cast<int>(threadIdx.x) % QUADS;
+  const int sl = static_cast<int>(threadIdx.x) / QUADS;
+  const int c = (static_cast<int>(blockIdx.y) * QUADS + q) * 4;
+  f32x4_t v{0.f, 0.f, 0.f, 0.f};
+  if (p >= 0 && c < cols) {
+    const float* src = part + static_cast<int64_t>(p) * cols + c;
+#pragma unroll 4
+    for (int s = sl; s < splits; s += SL) v += *reinterpret_cast<const f32x4_t*>(src + s * slab);
   }
+  if constexpr (SL > 1) {
+    sums[threadIdx.x] = v;
+    __syncthreads();
+    if (sl > 0) return;
+#pragma unroll
+    for (int k = 1; k < SL; ++k) v += sums[k * QUADS + q];
+  }
+  if (c < cols) store4(out + n * cols + c, v);
 }
 
 // d w1[prev] = sum of the embedding gradients of the rows with that previous
 // token, in row order.  One workgroup per compacted row; the first row with a
 // token does the sum for it (d w1 was cleared before).
 template <typename S>
-__global__ __launch_bounds__(256) void loss_dw1_kernel(const LossRows g, const float* part,
-                                                       int splits, int64_t slab, S* out) {
+__global__ __launch_bounds__(256) void loss_dw1_kernel(const LossRows g, const float* de, S* out) {
   __shared__ int first;
   __shared__ int list[256];
   __shared__ int wave_n[4];
@@ -344,12 +359,8 @@ __global__ __launch_bounds__(256) void loss_dw1_kernel(const LossRows g, const f
     if (hit) list[before + __popcll(b & ((1ull << lane) - 1ull))] = i;
     __syncthreads();
     if (gr < groups)
-      for (int q = gr; q < total; q += groups) {
-        const float* src = part + static_cast<int64_t>(list[q]) * r + col;
-        float v = 0.f;
-        for (int s = 0; s < splits; ++s) v += src[s * slab];
-        acc += v;
-      }
+#pragma unroll 4
+      for (int q = gr; q < total; q += groups) acc += de[static_cast<int64_t>(list[q]) * r + col];
     __syncthreads();   // the list is rewritten
   }
   sums[tid] = acc;
@@ -409,6 +420,7 @@ struct LossBuffers {
   char* dz;
   float* part_x;
   float* part_e;
+  float* de;               // [live, r]
 };
 
 size_t lay_out(const LossProblem& p, const LossPlan& q, bool backward, char* base, LossBuffers& b) {
@@ -435,6 +447,7 @@ size_t lay_out(const LossProblem& p, const LossPlan& q, bool backward, char* bas
     b.dz = s.take<char>(p.rows * q.ld * es);
     b.part_x = s.take<float>(q.splits_x * p.rows * p.hidden);
     b.part_e = s.take<float>(q.splits_e * p.rows * p.rank);
+    b.de = s.take<float>(q.splits_e > 1 ? p.rows * p.rank : 0);
   }
   return s.used;
 }
@@ -530,6 +543,23 @@ hipError_t forward(const LossProblem& p, void* workspace, float* loss, float* ls
   return hipGetLastError();
 }
 
+// Many splits with 16 lanes each on four columns, few with one (128 rows of 5120,
+// 16 splits: 54 us with one lane, JOIN_NEW us with 16).
+template <typename S>
+hipError_t join(int64_t rows, const int32_t* live, const int32_t* pos, const float* part, int splits,
+                int cols, S* out, hipStream_t st) {
+  const int64_t slab = rows * cols;
+  if (splits >= 8)
+    hipLaunchKernelGGL((loss_join_kernel<S, 16>),
+                       dim3(static_cast<unsigned>(rows), static_cast<unsigned>((cols + 63) / 64)),
+                       dim3(256), 0, st, live, pos, part, splits, slab, cols, out);
+  else
+    hipLaunchKernelGGL((loss_join_kernel<S, 1>),
+                       dim3(static_cast<unsigned>(rows), static_cast<unsigned>((cols + 1023) / 1024)),
+                       dim3(256), 0, st, live, pos, part, splits, slab, cols, out);
+  return hipGetLastError();
+}
+
 template <typename S>
 hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, const float* lse,
                     const float* picked, const float* loss_grad, hipStream_t st) {
@@ -587,27 +617,29 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.M = width;
       d.N = cols;
       d.live_k = 1;
-      d.band = 4;
+      d.band = p.rows < 1536 ? 16 : 4;
       d.splits = 1;
       d.out = static_cast<char*>(out) + v0 * cols * es;
       d.ldo = cols;
-      return launch_loss_dweight(p.dt, d, st);
+      return launch_loss_dweight(p.dt, p.rows, d, st);
     };
     if (o.hidden) BDR_LAUNCH(dfeat(p.w, p.hidden, b.part_x, q.splits_x));
     if (o.w1) BDR_LAUNCH(dfeat(p.w2, p.rank, b.part_e, q.splits_e));
     if (o.w) BDR_LAUNCH(dweight(b.r.x, p.hidden, o.w));
     if (o.w2) BDR_LAUNCH(dweight(b.r.e, p.rank, o.w2));
   }
-  if (o.hidden) {
-    hipLaunchKernelGGL(loss_dhidden_kernel<S>, dim3(static_cast<unsigned>(p.rows)), dim3(256), 0, st,
-                       b.r.pos, b.part_x, q.splits_x, p.rows * p.hidden, static_cast<int>(p.hidden),
-                       static_cast<S*>(o.hidden));
-    BDR_LAUNCH(hipGetLastError());
-  }
+  if (o.hidden)
+    BDR_LAUNCH(join<S>(p.rows, nullptr, b.r.pos, b.part_x, q.splits_x, static_cast<int>(p.hidden),
+                       static_cast<S*>(o.hidden), st));
   if (o.w1) {
+    const float* de = b.part_e;
+    if (q.splits_e > 1) {
+      BDR_LAUNCH(join<float>(p.rows, b.r.live, nullptr, b.part_e, q.splits_e, p.rank, b.de, st));
+      de = b.de;
+    }
     BDR_LAUNCH(launch_clear(o.w1, p.vocab * p.rank * es, st));
     hipLaunchKernelGGL(loss_dw1_kernel<S>, dim3(static_cast<unsigned>(p.rows)), dim3(256), 0, st,
-                       b.r, b.part_e, q.splits_e, p.rows * p.rank, static_cast<S*>(o.w1));
+                       b.r, de, static_cast<S*>(o.w1));
     BDR_LAUNCH(hipGetLastError());
   }
   return hipSuccess;

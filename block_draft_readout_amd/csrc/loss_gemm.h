@@ -53,7 +53,6 @@ struct LossGemm {
   int64_t M, N;            // extents of C (M: an upper bound where live_m)
   int live_m, live_k;      // the row count is *live / the first segment's extent is *live
   int tiles_n;
-  int tiles;               // grid tiles (all rows)
   int band;                // tile rows per band of the tile order
   int splits;              // reduction splits (LE_PARTIAL)
   // logits epilogues
@@ -69,16 +68,25 @@ struct LossGemm {
   int accumulate;          // LE_PARTIAL: add to what is there
 };
 
-template <typename S_, bool AKS_, bool BKS_, int WM_, int WN_, int WTM_, int WTN_, int STAGES_>
+template <typename S_, bool AKS_, bool BKS_, int WM_, int WN_, int WTM_, int WTN_, int STAGES_,
+          bool LOOP_ = false>
 struct LossTile {
   using S = S_;
   static constexpr bool AKS = AKS_, BKS = BKS_;   // reduction slow
   static constexpr int WM = WM_, WN = WN_, WTM = WTM_, WTN = WTN_, STAGES = STAGES_;
+  static constexpr bool LOOP = LOOP_;             // a workgroup walks several tiles
   static constexpr int WAVES = WM * WN;
   static constexpr int BM = 16 * WM * WTM, BN = 16 * WN * WTN;
   static constexpr int KB = 128 / static_cast<int>(sizeof(S));
   static constexpr int A_BYTES = BM * 128, STAGE_BYTES = (BM + BN) * 128;
-  static constexpr int LDS_BYTES = STAGES * STAGE_BYTES;
+  static constexpr bool STAGED = WTM * WTN <= 32;
+  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  // scratch of the epilogues: row statistics, or a wave's 16 output rows.  A
+  // workgroup with more tiles to come keeps it beside the ring.
+  static constexpr int OUT_ROW = 16 * WTN * static_cast<int>(sizeof(S));
+  static constexpr int SCRATCH = std::max(WN * BM * 8, WAVES * 16 * OUT_ROW);
+  static constexpr int LDS_BYTES = LOOP ? RING_BYTES + SCRATCH : std::max(RING_BYTES, SCRATCH);
+  static constexpr int PER_CU = 160 * 1024 / LDS_BYTES;   // workgroups a compute unit holds
   static constexpr int LOADS_A = BM / 8 / WAVES, LOADS_B = BN / 8 / WAVES;
   static constexpr int LOADS = LOADS_A + LOADS_B;
   // LDS reads the compiler schedules, per half step (the transposing ones are its own block)
@@ -87,7 +95,7 @@ struct LossTile {
   static constexpr int MFMAS = WTM * WTN * Elem<S>::MFMA_PER16;   // per half step
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "loads split evenly over the waves");
   static_assert((!AKS || BM % 64 == 0) && (!BKS || BN % 64 == 0), "slow rows are multiples of 128 bytes");
-  static_assert(LDS_BYTES <= 160 * 1024, "tile fits");
+  static_assert(PER_CU >= 1, "tile fits");
 };
 
 // XOR of the 32-byte unit index in a reduction-slow bf16 LDS row of ROWB bytes.
@@ -108,12 +116,11 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t off, char* dst) {
 
 // Transposing reads of NA operand tiles whose 8-byte pieces this lane names at
 // LDS addresses ad[0 .. NA), and of NB more at ad[NA ..): four 16-bit values of
-// column lane % 16 from 4 k rows (the address's and the next three lanes
-// groups'), and those 4 k rows further on (RA / RB bytes per k row), HALF bytes
-// into the operands' k rows.  One block of assembly with its own wait: the
+// column lane % 16 from 4 k rows, and from the 4 k rows after those (RA / RB bytes
+// per k row), HALF k rows into the stage.  One block of assembly with its own wait: the
 // compiler takes the intrinsic for a possible write to LDS and waits for every
 // buffer-to-LDS load in flight before it, which costs the loads' latency once a
-// step (256 x 256 x 64 tiles, 4096 x 30720 x 5120: 1060 -> TR_NEW TFLOP/s).
+// step (d weight, 256 x 320 tiles, 4096 x 30720 x 5120: 1530 -> 1090 us).
 #define BDR_TR_READ(i, o0, o1)                                                          \
   "ds_read_b64_tr_b16 %[l" #i "], %[a" #i "] offset:%c[" #o0 "]\n\t"                     \
   "ds_read_b64_tr_b16 %[h" #i "], %[a" #i "] offset:%c[" #o1 "]\n\t"
@@ -150,6 +157,22 @@ __device__ __forceinline__ void lds_read_tr(const uint32_t (&ad)[NA + NB], u32x4
                    BDR_TR_OUT(5)
                  : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IN(4),
                    BDR_TR_IN(5), BDR_TR_IMM
+                 : "memory");
+  } else if constexpr (NA == 4 && NB == 4) {
+    asm volatile(BDR_TR_4(BDR_TR_READ, 4, 5, 6, 7, q0, q1)
+                 BDR_TR_4(BDR_TR_READ, 0, 1, 2, 3, p0, p1) "s_waitcnt lgkmcnt(0)"
+                 : BDR_TR_OUT(0), BDR_TR_OUT(1), BDR_TR_OUT(2), BDR_TR_OUT(3), BDR_TR_OUT(4),
+                   BDR_TR_OUT(5), BDR_TR_OUT(6), BDR_TR_OUT(7)
+                 : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IN(4),
+                   BDR_TR_IN(5), BDR_TR_IN(6), BDR_TR_IN(7), BDR_TR_IMM
+                 : "memory");
+  } else if constexpr (NA == 4 && NB == 5) {
+    asm volatile(BDR_TR_4(BDR_TR_READ, 4, 5, 6, 7, q0, q1) BDR_TR_READ(8, q0, q1)
+                 BDR_TR_4(BDR_TR_READ, 0, 1, 2, 3, p0, p1) "s_waitcnt lgkmcnt(0)"
+                 : BDR_TR_OUT(0), BDR_TR_OUT(1), BDR_TR_OUT(2), BDR_TR_OUT(3), BDR_TR_OUT(4),
+                   BDR_TR_OUT(5), BDR_TR_OUT(6), BDR_TR_OUT(7), BDR_TR_OUT(8)
+                 : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IN(4),
+                   BDR_TR_IN(5), BDR_TR_IN(6), BDR_TR_IN(7), BDR_TR_IN(8), BDR_TR_IMM
                  : "memory");
   } else if constexpr (NA == 8 && NB == 5) {
     asm volatile(BDR_TR_4(BDR_TR_READ, 8, 9, 10, 11, q0, q1) BDR_TR_READ(12, q0, q1)
@@ -198,40 +221,45 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   const int wm = wave % T::WM;
   const int wn = wave / T::WM;
 
-  // tile of this workgroup: each XCD (workgroup b runs on XCD b % 8) takes a
-  // contiguous run of the band-ordered tiles, so its workgroups share operand
-  // slices in that XCD's L2
+  // Tiles of this workgroup: each XCD (workgroup b runs on XCD b % 8) takes a
+  // contiguous run of the band-ordered tiles, its workgroups one each or every
+  // wgs-th of the run, so those at work together share slices in that XCD's L2.
   const int live = *g.live;
   const int64_t M = g.live_m ? live : g.M;
   const int tiles_m = static_cast<int>((M + T::BM - 1) / T::BM);
   const int tiles = tiles_m * g.tiles_n;
   const int per_xcd = (tiles + 7) / 8;
-  const int bi = static_cast<int>(blockIdx.x / 8);
-  const int t = static_cast<int>(blockIdx.x % 8) * per_xcd + bi;
-  if (bi >= per_xcd || t >= tiles) return;   // whole workgroup
-  const int band = t / (g.band * g.tiles_n);
-  const int bh = min(g.band, tiles_m - g.band * band);
-  const int bidx = t - g.band * g.tiles_n * band;
-  const int tm = g.band * band + bidx % bh;
-  const int tn = bidx / bh;
-  const int64_t m0 = static_cast<int64_t>(tm) * T::BM;
-  const int64_t n0 = static_cast<int64_t>(tn) * T::BN;
+  const int wgs = static_cast<int>(gridDim.x / 8);
+  if (static_cast<int>(blockIdx.x / 8) >= per_xcd) return;   // whole workgroup
+  const int t_first = static_cast<int>(blockIdx.x % 8) * per_xcd + static_cast<int>(blockIdx.x / 8);
+  const int t_end = T::LOOP ? min(tiles, (static_cast<int>(blockIdx.x % 8) + 1) * per_xcd)
+                            : min(t_first + 1, tiles);
+  if (t_first >= t_end) return;   // whole workgroup
+  auto tile_at = [&](int t, int& tm, int& tn) {
+    const int band = t / (g.band * g.tiles_n);
+    const int bh = min(g.band, tiles_m - g.band * band);
+    const int bidx = t - g.band * g.tiles_n * band;
+    tm = g.band * band + bidx % bh;
+    tn = bidx / bh;
+  };
 
+  constexpr bool kTwo = !T::AKS && !T::BKS;   // two segments may be given
   // reduction steps of this workgroup: the first segment's, then the second's
   const int64_t k0 = g.live_k ? live : g.seg[0].k;
   const int steps0 = static_cast<int>((k0 + T::KB - 1) / T::KB);
-  const int total = steps0 + static_cast<int>((g.seg[1].k + T::KB - 1) / T::KB);
+  const int total = steps0 + (kTwo ? static_cast<int>((g.seg[1].k + T::KB - 1) / T::KB) : 0);
   int s_lo = 0, s_hi = total;
   if constexpr (EPI == LE_PARTIAL) {
     s_lo = static_cast<int>(static_cast<int64_t>(total) * blockIdx.y / g.splits);
     s_hi = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.y + 1) / g.splits);
   }
 
+  const int s_data = s_hi;        // steps from here on read zeros
+  s_hi = max(s_hi, s_lo + 1);     // nothing to reduce: one step of zeros
+
   // per-lane offsets of this wave's loads
   const uint32_t lrow = static_cast<uint32_t>(lane >> 3);
   const uint32_t lchunk = (static_cast<uint32_t>(lane) & 7u) ^ lrow;
-  const int64_t rows_a = min<int64_t>(T::BM, M - m0);
-  const int64_t rows_b = min<int64_t>(T::BN, g.N - n0);
   // byte offset of load q's chunk of this lane inside the step's slice of an
   // operand with row stride ld
   auto lane_off = [&](auto slow, auto rowbytes, int q, uint32_t ld) -> uint32_t {
@@ -252,18 +280,39 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   typedef std::integral_constant<uint32_t, T::BM * ES> ARow;
   typedef std::integral_constant<uint32_t, T::BN * ES> BRow;
 
-  // One step's loads: descriptors prepared once, load q issued by dma_one.  A
-  // step past the end reads zeros (empty descriptors), so that every step
+  // a slow operand has one segment: its loads' offsets never change
+  uint32_t off_a[T::LOADS_A], off_b[T::LOADS_B];
+  if constexpr (T::AKS)
+    static_for<T::LOADS_A>([&](auto q) {
+      off_a[q] = lane_off(ASlow{}, ARow{}, q, static_cast<uint32_t>(g.seg[0].lda));
+    });
+  if constexpr (T::BKS)
+    static_for<T::LOADS_B>([&](auto q) {
+      off_b[q] = lane_off(BSlow{}, BRow{}, q, static_cast<uint32_t>(g.seg[0].ldb));
+    });
+
+  // The loads run STAGES - 1 steps ahead of the MFMAs, with LOOP from one tile's
+  // last step straight into the next tile's first, so a tile's epilogue overlaps
+  // them.  Past the last tile they read zeros (empty descriptors), so that every step
   // issues the same loads and the waits count alike.
+  int ld_t = t_first, ld_s = s_lo;   // tile and step of the next loads
+  int64_t ld_m0 = 0, ld_n0 = 0;
+  auto ld_tile = [&] {
+    int tm, tn;
+    tile_at(ld_t, tm, tn);
+    ld_m0 = static_cast<int64_t>(tm) * T::BM;
+    ld_n0 = static_cast<int64_t>(tn) * T::BN;
+  };
+  ld_tile();
   rsrc_t ra, rb;
   uint32_t ld_a = 0, ld_b = 0, cut = 0;   // cut: kOOB in the lanes past a fast-k tail
   char* ld_dst = lds;
-  auto dma_prep = [&](int step, int buf) {
-    const bool in = step < s_hi;
-    const bool second = step >= steps0;
+  auto dma_prep = [&](int buf) {
+    const bool second = kTwo && ld_s >= steps0;
     const LossSeg& sg = second ? g.seg[1] : g.seg[0];
-    const int64_t kk = static_cast<int64_t>(second ? step - steps0 : step) * T::KB;
+    const int64_t kk = static_cast<int64_t>(second ? ld_s - steps0 : ld_s) * T::KB;
     const int64_t krem = (second ? sg.k : k0) - kk;
+    const bool in = krem > 0 && ld_s < s_data && (!T::LOOP || ld_t < t_end);
     ld_a = static_cast<uint32_t>(sg.lda);
     ld_b = static_cast<uint32_t>(sg.ldb);
     cut = static_cast<int64_t>(lchunk) * Elem<S>::PER16 < krem ? 0u : kOOB;
@@ -272,39 +321,44 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
     const char* pb = static_cast<const char*>(sg.b);
     uint32_t na, nb;
     if constexpr (T::AKS) {
-      pa += (kk * sg.lda + m0) * ES;
-      na = static_cast<uint32_t>((krows * sg.lda - m0) * ES);
+      pa += (kk * sg.lda + ld_m0) * ES;
+      na = static_cast<uint32_t>((krows * sg.lda - ld_m0) * ES);
     } else {
-      pa += (m0 * sg.lda + kk) * ES;
-      na = static_cast<uint32_t>((rows_a * sg.lda - kk) * ES);
+      pa += (ld_m0 * sg.lda + kk) * ES;
+      na = static_cast<uint32_t>((min<int64_t>(T::BM, M - ld_m0) * sg.lda - kk) * ES);
     }
     if constexpr (T::BKS) {
-      pb += (kk * sg.ldb + n0) * ES;
-      nb = static_cast<uint32_t>((krows * sg.ldb - n0) * ES);
+      pb += (kk * sg.ldb + ld_n0) * ES;
+      nb = static_cast<uint32_t>((krows * sg.ldb - ld_n0) * ES);
     } else {
-      pb += (n0 * sg.ldb + kk) * ES;
-      nb = static_cast<uint32_t>((rows_b * sg.ldb - kk) * ES);
+      pb += (ld_n0 * sg.ldb + kk) * ES;
+      nb = static_cast<uint32_t>((min<int64_t>(T::BN, g.N - ld_n0) * sg.ldb - kk) * ES);
     }
     ra = make_rsrc(pa, in ? na : 0u);
     rb = make_rsrc(pb, in ? nb : 0u);
     ld_dst = lds + buf * T::STAGE_BYTES;
+    ++ld_s;
+    if constexpr (T::LOOP) {
+      if (ld_s == s_hi) {
+        ld_s = s_lo;
+        ld_t += wgs;
+        if (ld_t < t_end) ld_tile();
+      }
+    }
   };
   auto dma_one = [&](auto qc) {
     constexpr int q = decltype(qc)::value;
     if constexpr (q < T::LOADS_A) {
-      const uint32_t off = lane_off(ASlow{}, ARow{}, q, ld_a);
-      load_lds16(ra, T::AKS ? off : off | cut, ld_dst + (wave + T::WAVES * q) * 1024);
+      const uint32_t off = T::AKS ? off_a[q] : lane_off(ASlow{}, ARow{}, q, ld_a) | cut;
+      load_lds16(ra, off, ld_dst + (wave + T::WAVES * q) * 1024);
     } else {
       constexpr int p = q - T::LOADS_A;
-      const uint32_t off = lane_off(BSlow{}, BRow{}, p, ld_b);
-      load_lds16(rb, T::BKS ? off : off | cut, ld_dst + T::A_BYTES + (wave + T::WAVES * p) * 1024);
+      const uint32_t off = T::BKS ? off_b[p] : lane_off(BSlow{}, BRow{}, p, ld_b) | cut;
+      load_lds16(rb, off, ld_dst + T::A_BYTES + (wave + T::WAVES * p) * 1024);
     }
   };
 
   f32x4_t acc[T::WTM][T::WTN];
-  static_for<T::WTM>([&](auto i) {
-    static_for<T::WTN>([&](auto j) { acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
-  });
   typedef u32x4_t FragA[T::WTM];
   typedef u32x4_t FragB[T::WTN];
   // operand of MFMA tile `tile` (16 rows of the operand) in half `half` of a step
@@ -369,20 +423,34 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   // and the MFMAs; the loads of step s + STAGES - 1 are spread over the first
   // half's MFMAs (all before them where there are fewer MFMAs than loads).
   static_for<T::STAGES - 1>([&](auto c) {
-    dma_prep(s_lo + decltype(c)::value, decltype(c)::value);
+    dma_prep(decltype(c)::value);
     static_for<T::LOADS>([&](auto q) { dma_one(q); });
   });
-  dma_prep(s_lo + T::STAGES - 1, T::STAGES - 1);
+  dma_prep(T::STAGES - 1);
   constexpr int NT = T::WTM * T::WTN;
   constexpr bool kSpread = NT >= T::LOADS;
+  constexpr int kAhead = (T::STAGES - 2) * T::LOADS;
+  // stores of an epilogue that are younger than the loads the next tile's first
+  // step waits for (memory operations complete in order)
+  constexpr int kStores = T::LOOP && (EPI == LE_DLOGITS || EPI == LE_OUT)
+                              ? T::WTM * ((16 * T::OUT_ROW + 1023) / 1024) : 0;
+  static_assert(!T::LOOP || T::STAGED, "an unstaged epilogue's stores are not counted");
+  static_assert(kAhead + kStores < 64, "waits can count these");
   FragA a;
   FragB b;
   int buf = 0;
+  for (int t = t_first; t < t_end; t += wgs) {
+  static_for<T::WTM>([&](auto i) {
+    static_for<T::WTN>([&](auto j) { acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
+  });
   for (int s = s_lo; s < s_hi; ++s) {
-    // this wave's loads of step s have landed when at most those of the
+    // this wave's loads of the step have landed when at most those of the
     // STAGES - 2 steps after it remain; after the barrier every wave's have,
     // and every wave is done with the stage the next loads overwrite
-    BDR_WAIT_VM_LGKM((T::STAGES - 2) * T::LOADS, 0);
+    if (kStores > 0 && s == s_lo && t != t_first)
+      BDR_WAIT_VM_LGKM(kAhead + kStores, 0);
+    else
+      BDR_WAIT_VM_LGKM(kAhead, 0);
     BDR_WG_BARRIER();
     if constexpr (!kSpread) static_for<T::LOADS>([&](auto q) { dma_one(q); });
     read_frags(buf, std::integral_constant<int, 0>{}, a, b);
@@ -413,19 +481,62 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
       __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS, 0);
     }
     buf = buf + 1 == T::STAGES ? 0 : buf + 1;
-    // where step s + STAGES goes (the stage of step s)
-    dma_prep(s + T::STAGES, buf == 0 ? T::STAGES - 1 : buf - 1);
+    dma_prep(buf == 0 ? T::STAGES - 1 : buf - 1);   // next into the stage of this step
   }
-  BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads
 
+  int tm, tn;
+  tile_at(t, tm, tn);
+  const int64_t m0 = static_cast<int64_t>(tm) * T::BM;
+  const int64_t n0 = static_cast<int64_t>(tn) * T::BN;
   // Lane holds C[m][n .. n + 3] of each of its tiles: rows r16, columns 4 grp ..
   const int64_t mw = m0 + wm * 16 * T::WTM + r16;
   const int64_t nw = n0 + wn * 16 * T::WTN + 4 * grp;
+  char* scratch = lds + (T::LOOP ? T::RING_BYTES : 0);
+  if constexpr (!T::LOOP && (EPI == LE_STATS || (T::STAGED && EPI != LE_PARTIAL))) {
+    BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads
+    BDR_WG_BARRIER();         // and every wave is done with the ring
+  }
+  // A wave's 16 output rows of one A tile through LDS, then 16 bytes per lane
+  // along the rows: whole pieces of OUT_ROW bytes instead of 32-byte ones
+  // (1.56 GB written and nothing else: 284 us against 433 us).  The largest
+  // tiles have no registers for it and few rows to write per product: directly.
+  char* mine = scratch + wave * 16 * T::OUT_ROW;
+  auto put_rows = [&](auto ic, auto&& value) {
+    if constexpr (!T::STAGED) {
+      const int64_t m = mw + decltype(ic)::value * 16;
+      static_for<T::WTN>([&](auto j) {
+        const int64_t n = nw + decltype(j)::value * 16;
+        if (m < M && n < (EPI == LE_DLOGITS ? g.ldo : g.N))
+          store4(static_cast<S*>(g.out) + m * g.ldo + n, value(j));
+      });
+      return;
+    }
+    static_for<T::WTN>([&](auto j) {
+      store4(reinterpret_cast<S*>(mine + r16 * T::OUT_ROW) + decltype(j)::value * 16 + 4 * grp,
+             value(j));
+    });
+    BDR_WAIT_VM_LGKM(63, 0);
+    const rsrc_t out = make_rsrc(static_cast<S*>(g.out) + m0 * g.ldo,
+                                 static_cast<uint32_t>(min<int64_t>(T::BM, M - m0) * g.ldo * ES));
+    const int64_t cols = (EPI == LE_DLOGITS ? g.ldo : g.N) - (n0 + wn * 16 * T::WTN);   // may be <= 0
+#pragma unroll
+    for (int c0 = 0; c0 < 16 * T::OUT_ROW; c0 += 1024) {
+      const int c = c0 + lane * 16;
+      const int row = c / T::OUT_ROW;
+      const int in_row = c % T::OUT_ROW;
+      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + (c < 16 * T::OUT_ROW ? c : 0));
+      const int64_t m = (wm * T::WTM + decltype(ic)::value) * 16 + row;
+      const uint32_t off = static_cast<uint32_t>((m * g.ldo + n0 + wn * 16 * T::WTN) * ES) +
+                           static_cast<uint32_t>(in_row);
+      const bool ok = c < 16 * T::OUT_ROW && in_row < cols * ES;
+      bstore16(__builtin_bit_cast(f32x4_t, v), out, ok ? off : kOOB);
+    }
+    BDR_WAIT_VM_LGKM(63, 0);   // read before the next rows are written
+  };
   if constexpr (EPI == LE_STATS) {
     // maximum and sum of 2^(x scale2 - maximum) over the tile's columns: lanes,
     // then the four lane groups, then the waves side by side through LDS
-    BDR_WG_BARRIER();   // every wave is done with the stages
-    float2* part = reinterpret_cast<float2*>(lds);   // [WN][BM]
+    float2* part = reinterpret_cast<float2*>(scratch);   // [WN][BM]
     static_for<T::WTM>([&](auto i) {
       const int64_t m = mw + decltype(i)::value * 16;
       const bool row_in = m < M;
@@ -437,26 +548,28 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
           const int64_t n = nw + decltype(j)::value * 16 + c;
           const float z = acc[i][j][c];
           if (n == lab) g.picked[m] = z;
-          const float x = n < g.N ? z * g.scale2 : -INFINITY;
-          acc[i][j][c] = x;
-          mx = fmaxf(mx, x);
+          mx = fmaxf(mx, n < g.N ? z : -INFINITY);
         }
       });
       mx = fmaxf(mx, __shfl_xor(mx, 16));
       mx = fmaxf(mx, __shfl_xor(mx, 32));
+      mx *= g.scale2;   // positive
       const float ref = mx == -INFINITY ? 0.f : mx;
       float sum = 0.f;
       static_for<T::WTN>([&](auto j) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) sum += __builtin_amdgcn_exp2f(acc[i][j][c] - ref);
+        for (int c = 0; c < 4; ++c) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -ref));
+          sum += nw + decltype(j)::value * 16 + c < g.N ? p : 0.f;
+        }
       });
       sum += __shfl_xor(sum, 16);
       sum += __shfl_xor(sum, 32);
       if (grp == 0)
         part[wn * T::BM + wm * 16 * T::WTM + decltype(i)::value * 16 + r16] = float2{mx, sum};
     });
-    BDR_WAIT_VM_LGKM(0, 0);
-    BDR_WG_BARRIER();
+    BDR_WAIT_VM_LGKM(63, 0);
+    BDR_WG_BARRIER();   // (the next tile's is behind the barrier of its first step)
     for (int r = static_cast<int>(threadIdx.x); r < T::BM; r += 64 * T::WAVES) {
       if (m0 + r >= M) continue;
       float2 v = part[r];
@@ -466,26 +579,22 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
     }
   } else if constexpr (EPI == LE_DLOGITS) {
     // rounded to the storage type: the operand of two more matrix products,
-    // with as much relative error as their rounded results carry anyway
+    // with as much relative error as their rounded results carry anyway.
+    // Columns from N to the padded width hold zeros.
     static_for<T::WTM>([&](auto i) {
-      const int64_t m = mw + decltype(i)::value * 16;
-      if (m < M) {
-        const int64_t lab = g.label ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
-        const float l2 = g.lse2[m], cf = g.coef[m];
-        S* row = static_cast<S*>(g.out) + m * g.ldo;
-        static_for<T::WTN>([&](auto j) {
-          const int64_t n = nw + decltype(j)::value * 16;
-          if (n < g.ldo) {   // columns from N to the padded width hold zeros
-            f32x4_t v;
+      const int64_t m = min<int64_t>(mw + decltype(i)::value * 16, M - 1);
+      const int64_t lab = g.label ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
+      const float l2 = g.lse2[m], cf = g.coef[m];
+      put_rows(i, [&](auto j) {
+        const int64_t n = nw + decltype(j)::value * 16;
+        f32x4_t v;
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const float p = __builtin_amdgcn_exp2f(acc[i][j][c] * g.scale2 - l2);
-              v[c] = n + c < g.N ? cf * (n + c == lab ? p - 1.f : p) : 0.f;
-            }
-            store4(row + n, v);
-          }
-        });
-      }
+        for (int c = 0; c < 4; ++c) {
+          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -l2));
+          v[c] = n + c < g.N ? cf * (n + c == lab ? p - 1.f : p) : 0.f;
+        }
+        return v;
+      });
     });
   } else if constexpr (EPI == LE_PARTIAL) {
     float* out = static_cast<float*>(g.out) + static_cast<int64_t>(blockIdx.y) * g.slab;
@@ -500,14 +609,10 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
       });
     });
   } else {
-    static_for<T::WTM>([&](auto i) {
-      const int64_t m = mw + decltype(i)::value * 16;
-      static_for<T::WTN>([&](auto j) {
-        const int64_t n = nw + decltype(j)::value * 16;
-        if (m < M && n < g.N) store4(static_cast<S*>(g.out) + m * g.ldo + n, acc[i][j]);
-      });
-    });
+    static_for<T::WTM>([&](auto i) { put_rows(i, [&](auto j) { return acc[i][j]; }); });
   }
+  }
+  BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads
 }
 
 template <typename T, int EPI>
@@ -515,8 +620,9 @@ static hipError_t launch_loss_gemm(LossGemm g, hipStream_t stream) {
   const int64_t tiles_m = (g.M + T::BM - 1) / T::BM;
   g.tiles_n = static_cast<int>((g.N + T::BN - 1) / T::BN);
   const int64_t tiles = tiles_m * g.tiles_n;
-  g.tiles = static_cast<int>(tiles);
-  const dim3 grid(static_cast<unsigned>((tiles + 7) / 8 * 8),
+  int64_t blocks = (tiles + 7) / 8 * 8;
+  if (T::LOOP) blocks = std::min<int64_t>(blocks, 256 * T::PER_CU);
+  const dim3 grid(static_cast<unsigned>(blocks),
                   static_cast<unsigned>(EPI == LE_PARTIAL ? g.splits : 1));
   hipLaunchKernelGGL((loss_gemm_kernel<T, EPI>), grid, dim3(64 * T::WAVES), 0, stream, g);
   return hipGetLastError();

@@ -1,13 +1,17 @@
 // Gradient products of the vocabulary losses: d hidden = d logits W and
 // d weight = d logits^T hidden (and the Markov head's, as narrow as its rank).
 //
-// Measured (bf16, H = 5120):
-//   d hidden, 4096 rows, 30720 entries: 256 x 320 1042 - 1121 us (1237 - 1149 TFLOP/s),
-//     256 x 256 with 4 splits 1203 us, 128 x 128 2059 us
-//   d hidden, 128 rows, 151936 entries: 128 x 320 with 16 splits 321 us, 128 x 128
+// Measured (bf16, H = 5120; "library": its product of the same size, same run):
+//   d hidden, 4096 rows, 30720 entries: 256 x 320 965 us (1335 TFLOP/s; library
+//     1310 - 1460 us), 256 x 256 with 4 splits 1203 us, 128 x 128 2059 us
+//   d hidden, 128 rows, 151936 entries: 128 x 320 with 16 splits 318 us, 128 x 128
 //     with 12 splits 337 us; 7 rows: 32 x 256, 3 stages 292 us
-//   d weight, 4096 rows, 30720 entries: 256 x 320 1090 us (1183 TFLOP/s),
-//     256 x 256 1163 us, 128 x 128 1664 us
+//   d weight, 30720 entries: 4096 rows 256 x 320 1065 us (1209 TFLOP/s; library
+//     1206 - 1380 us), 128 x 320 1188 us; 2048 rows 569 and 611 us; 1024 rows 335
+//     and 308 us; 256 rows 189 and 113 us
+//   d weight, 151936 entries (1.56 GB written): 128 rows 128 x 320 402 us, one
+//     tile per workgroup 504 us; 7 rows 269 - 306 us
+//   d w2, rank 64, 30720 entries, 3072 rows: 3 stages 32 us, 2 stages 39 us
 
 #include "loss.h"
 
@@ -22,10 +26,14 @@ using FeatSome = LossTile<uint16_t, false, true, 2, 4, 4, 5, 2>;     // 128 x 32
 using FeatMany = LossTile<uint16_t, false, true, 2, 4, 8, 5, 2>;     // 256 x 320
 
 using WeightF32 = LossTile<float, true, true, 2, 2, 4, 4, 2>;        // 128 x 128
-using WeightNarrow = LossTile<uint16_t, true, true, 2, 2, 4, 2, 2>;  // 128 x 64
-using WeightWide = LossTile<uint16_t, true, true, 2, 4, 8, 5, 2>;    // 256 x 320
+using WeightNarrow = LossTile<uint16_t, true, true, 2, 2, 4, 2, 3>;  // 128 x 64
+// walks its tiles: with few rows the output's bytes bound it, and its stores
+// overlap the next tile's loads
+using WeightFew = LossTile<uint16_t, true, true, 2, 4, 4, 5, 2, true>;   // 128 x 320
+using WeightMany = LossTile<uint16_t, true, true, 2, 4, 8, 5, 2>;        // 256 x 320
 
 constexpr int64_t kNarrowCols = 128;   // outputs this narrow take the narrow tiles
+constexpr int64_t kManyRows = 1536;    // between the rows measured above
 
 template <typename F>
 auto with_feat_tile(bdr_dtype dt, int64_t rows, int64_t cols, F&& f) {
@@ -44,9 +52,9 @@ int loss_dfeat_splits(bdr_dtype dt, int64_t rows, int64_t cols, int64_t width) {
   return with_feat_tile(dt, rows, cols, [&](auto t) {
     using T = decltype(t);
     const int64_t tiles = (rows + T::BM - 1) / T::BM * ((cols + T::BN - 1) / T::BN);
-    const int64_t slots = 256 * (160 * 1024 / T::LDS_BYTES);
+    const int64_t slots = 256 * T::PER_CU;
     const int64_t steps = (width + T::KB - 1) / T::KB;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 8, 64})));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 8, 256})));
   });
 }
 
@@ -56,10 +64,11 @@ hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, const LossGemm& g, hipS
   });
 }
 
-hipError_t launch_loss_dweight(bdr_dtype dt, const LossGemm& g, hipStream_t stream) {
+hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream) {
   if (dt != BDR_BF16) return launch_loss_gemm<WeightF32, LE_OUT>(g, stream);
   if (g.N <= kNarrowCols) return launch_loss_gemm<WeightNarrow, LE_OUT>(g, stream);
-  return launch_loss_gemm<WeightWide, LE_OUT>(g, stream);
+  if (rows < kManyRows) return launch_loss_gemm<WeightFew, LE_OUT>(g, stream);
+  return launch_loss_gemm<WeightMany, LE_OUT>(g, stream);
 }
 
 }  // namespace bdr

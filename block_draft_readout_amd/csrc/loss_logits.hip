@@ -4,10 +4,12 @@
 // loads of weight rows are in flight per compute unit; many rows by the matrix
 // cores: the largest tile whose accumulators fit two waves per SIMD.  Measured
 // (bf16, H = 5120, V = 151936; statistics):
-//   rows 7:    32 x 128, 3 stages 260 us (6.0 TB/s); 32 x 256, 2 stages 332 us
-//   rows 128:  128 x 320 347 us; 128 x 128 406 us
-//   rows 4096 (30720 entries): 256 x 320 935 us (1378 TFLOP/s); 256 x 256 1092 us;
-//              128 x 128 1735 us
+//   rows 7:    32 x 128, 3 stages 260 us (6.0 TB/s); 32 x 256, 2 stages 332 us;
+//              128 x 320 299 us
+//   rows 128:  128 x 320 319 us; 128 x 128 406 us; 32 x 128 824 us
+//   rows 4096 (30720 entries): 256 x 320 1010 us (1270 TFLOP/s; the library's
+//              product 990 us in the same run); 256 x 256 and 128 x 128 9 % and
+//              75 % slower
 
 #include "loss.h"
 
