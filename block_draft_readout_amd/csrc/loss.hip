@@ -189,17 +189,19 @@ __global__ __launch_bounds__(256) void ce_loss_kernel(const LossRows g, float* l
   }
 }
 
-// logits at the teacher's entries: picked[n, j] = z[n, id_j].  Grid (rows,
-// ceil(top / 16)); each wave takes four entries, so a hidden chunk serves four
-// weight rows.
-template <typename S>
+// logits at the teacher's entries: picked[n, j] = z[n, id_j].  GROUP lanes take
+// four entries of a row, so a hidden chunk serves four weight rows: a wave for
+// short rows, else a workgroup (few rows wait for memory, and 256 lanes have a
+// row's weights in flight at once).  Grid (rows, entries / (1024 / GROUP)).
+template <typename S, int GROUP>
 __global__ __launch_bounds__(256) void distill_pick_kernel(const LossRows g, float* picked) {
   constexpr int PER = Elem<S>::PER16;
-  const int lane = static_cast<int>(threadIdx.x) & 63;
+  __shared__ float part[4][4];
+  const int lane = static_cast<int>(threadIdx.x) % GROUP;
+  const int wave = static_cast<int>(threadIdx.x) >> 6;
   const int64_t n = blockIdx.x;
   const int p = g.pos[n];
-  const int j0 = static_cast<int>(blockIdx.y) * 16 + static_cast<int>(threadIdx.x >> 6) * 4;
-  if (j0 >= g.top) return;
+  const int j0 = (static_cast<int>(blockIdx.y) * (256 / GROUP) + static_cast<int>(threadIdx.x) / GROUP) * 4;
   int id[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) {
@@ -209,32 +211,48 @@ __global__ __launch_bounds__(256) void distill_pick_kernel(const LossRows g, flo
   float s[4] = {0.f, 0.f, 0.f, 0.f};
   auto dots = [&](const void* xv, const void* wv, int len) {
     const S* x = static_cast<const S*>(xv) + static_cast<int64_t>(p) * len;
-    for (int c = lane * PER; c < len; c += 64 * PER) {
+    const S* w = static_cast<const S*>(wv);
+#pragma unroll 2
+    for (int c = lane * PER; c < len; c += GROUP * PER) {
       const u32x4_t xr = load16(x + c);
+      u32x4_t wr[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        if (id[q] < 0) continue;   // uniform over the wave
-        const u32x4_t wr = load16(static_cast<const S*>(wv) + static_cast<int64_t>(id[q]) * len + c);
+      for (int q = 0; q < 4; ++q)   // an entry that is not listed reads row 0 and is dropped
+        wr[q] = load16(w + static_cast<int64_t>(max(id[q], 0)) * len + c);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
           if constexpr (sizeof(S) == 2) {
-            s[q] += __uint_as_float(xr[k] << 16) * __uint_as_float(wr[k] << 16);
-            s[q] += __uint_as_float(xr[k] & 0xFFFF0000u) * __uint_as_float(wr[k] & 0xFFFF0000u);
+            s[q] += __uint_as_float(xr[k] << 16) * __uint_as_float(wr[q][k] << 16);
+            s[q] += __uint_as_float(xr[k] & 0xFFFF0000u) * __uint_as_float(wr[q][k] & 0xFFFF0000u);
           } else {
-            s[q] += __uint_as_float(xr[k]) * __uint_as_float(wr[k]);
+            s[q] += __uint_as_float(xr[k]) * __uint_as_float(wr[q][k]);
           }
         }
-      }
     }
   };
-  if (p >= 0) {
+  if (p >= 0 && (id[0] & id[1] & id[2] & id[3]) != -1) {
     dots(g.x, g.w, g.hidden_size);
     if (g.rank) dots(g.e, g.w2, g.rank);
   }
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    const float v = wave_sum(s[q]);
-    if (lane == 0 && j0 + q < g.top) picked[n * g.top + j0 + q] = v;
+  for (int q = 0; q < 4; ++q) s[q] = wave_sum(s[q]);
+  if constexpr (GROUP > 64) {
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+      for (int q = 0; q < 4; ++q) part[wave][q] = s[q];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int q = 0; q < 4; ++q) s[q] = part[0][q] + part[1][q] + part[2][q] + part[3][q];
+  }
+  if (lane < 4 && j0 + lane < g.top) {
+    float v = 0.f;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+      if (lane == q && id[q] >= 0) v = s[q];
+    picked[n * g.top + j0 + lane] = v;
   }
 }
 
@@ -266,7 +284,7 @@ __global__ __launch_bounds__(256) void distill_loss_kernel(const LossRows g, con
 // at this id).  An id listed twice is written twice with the same value.
 template <typename S>
 __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, const float* picked,
-                                                          S* dz, int64_t ld, int v0, int width,
+                                                          S* dz, int64_t panel, int v0, int width,
                                                           float scale2) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int p = static_cast<int>(i / g.top);
@@ -281,7 +299,8 @@ __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, cons
     if (ids[q] == id) t += g.t[n * g.top + q];
   const float pr = __builtin_amdgcn_exp2f(picked[n * g.top + j] * scale2 - g.lse2[p]);
   const float v = g.coef[p] * (pr - t);
-  dz[p * ld + (id - v0)] = rounded<S>(v);
+  constexpr int KB = 128 / static_cast<int>(sizeof(S));   // d logits lie in panels of KB columns
+  dz[(id - v0) / KB * panel + static_cast<int64_t>(p) * KB + (id - v0) % KB] = rounded<S>(v);
 }
 
 // ---------------------------------------------------------------- gradients out
@@ -531,10 +550,16 @@ hipError_t forward(const LossProblem& p, void* workspace, float* loss, float* ls
   g.stat = b.r.stat;
   BDR_LAUNCH(launch_loss_stats(p.dt, p.rows, g, st));
   if (p.top) {
-    hipLaunchKernelGGL(distill_pick_kernel<S>,
-                       dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.top + 15) / 16)),
-                       dim3(256), 0, st, b.r, picked);
-    BDR_LAUNCH(hipGetLastError());
+    auto pick = [&](auto group) {
+      constexpr int GROUP = decltype(group)::value;
+      const int per = 4 * (256 / GROUP);
+      hipLaunchKernelGGL((distill_pick_kernel<S, GROUP>),
+                         dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.top + per - 1) / per)),
+                         dim3(256), 0, st, b.r, picked);
+      return hipGetLastError();
+    };
+    BDR_LAUNCH(p.hidden / Elem<S>::PER16 <= 128 ? pick(std::integral_constant<int, 64>{})
+                                                : pick(std::integral_constant<int, 256>{}));
     hipLaunchKernelGGL(distill_loss_kernel, dim3(waves4(p.rows)), dim3(256), 0, st, b.r, picked,
                        loss, lse);
   } else {
@@ -574,6 +599,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
   for (int64_t v0 = 0; v0 < p.vocab; v0 += q.piece) {
     const int64_t width = std::min(q.piece, p.vocab - v0);
     const int64_t ld = (width + 63) / 64 * 64;
+    const int64_t panel = p.rows * (128 / es);   // elements of 128-byte columns
     LossGemm g = logits_gemm(p, b.r, v0, width);
     if (!p.top) {
       g.label = b.r.label_c;
@@ -583,19 +609,20 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
     g.coef = b.r.coef;
     g.out = b.dz;
     g.ldo = ld;
+    g.slab = panel;
     BDR_LAUNCH(launch_loss_dlogits(p.dt, p.rows, g, st));
     if (p.top) {
       hipLaunchKernelGGL(distill_fix_kernel<S>,
                          dim3(static_cast<unsigned>((p.rows * p.top + 255) / 256)), dim3(256), 0, st,
-                         b.r, picked, reinterpret_cast<S*>(b.dz), ld, static_cast<int>(v0),
+                         b.r, picked, reinterpret_cast<S*>(b.dz), panel, static_cast<int>(v0),
                          static_cast<int>(width), g.scale2);
       BDR_LAUNCH(hipGetLastError());
     }
     // d hidden and d embedding: reduction over this piece's entries
     auto dfeat = [&](const void* w, int64_t cols, float* part, int splits) {
       LossGemm d{};
-      d.seg[0] = LossSeg{b.dz, static_cast<const char*>(w) + v0 * cols * es, ld, cols, width};
-      d.seg[1] = LossSeg{d.seg[0].a, d.seg[0].b, ld, cols, 0};
+      d.seg[0] = LossSeg{b.dz, static_cast<const char*>(w) + v0 * cols * es, panel, cols, width};
+      d.seg[1] = LossSeg{d.seg[0].a, d.seg[0].b, panel, cols, 0};
       d.live = b.r.live;
       d.M = p.rows;
       d.N = cols;
@@ -611,8 +638,8 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
     // d weight and d w2: reduction over the rows
     auto dweight = [&](const void* feat, int64_t cols, void* out) {
       LossGemm d{};
-      d.seg[0] = LossSeg{b.dz, feat, ld, cols, p.rows};
-      d.seg[1] = LossSeg{d.seg[0].a, d.seg[0].b, ld, cols, 0};
+      d.seg[0] = LossSeg{b.dz, feat, panel, cols, p.rows};
+      d.seg[1] = LossSeg{d.seg[0].a, d.seg[0].b, panel, cols, 0};
       d.live = b.r.live;
       d.M = width;
       d.N = cols;

@@ -40,6 +40,11 @@ enum LossEpilogue {
 };
 
 // One stretch of the reduction: operand bases, row strides (elements) and extent.
+// d logits, operand a of every gradient product (those with slow b), lie in
+// panels of 128 bytes: element (m, v) at a + v / KB * lda + m * KB + v % KB with
+// KB elements in 128 bytes and lda from panel to panel.  A step's slice is then
+// contiguous, where rows of the vocabulary's length would put each of its 128
+// byte pieces into another memory page.
 struct LossSeg {
   const void* a;
   const void* b;
@@ -63,8 +68,9 @@ struct LossGemm {
   float* picked;           // [M] logit of the label
   const float* lse2;       // [M] log2 of the softmax denominator
   const float* coef;       // [M] gradient factor
-  void* out;               // LE_DLOGITS [M, ldo], LE_PARTIAL [splits, slab], LE_OUT [M, ldo]
-  int64_t ldo, slab;
+  void* out;               // LE_DLOGITS panels, LE_PARTIAL [splits, slab], LE_OUT [M, ldo]
+  int64_t ldo;             // LE_DLOGITS: N padded to whole panels
+  int64_t slab;            // elements of a split, or of a panel
   int accumulate;          // LE_PARTIAL: add to what is there
 };
 
@@ -222,19 +228,22 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   const int wn = wave / T::WM;
 
   // Tiles of this workgroup: each XCD (workgroup b runs on XCD b % 8) takes a
-  // contiguous run of the band-ordered tiles, its workgroups one each or every
-  // wgs-th of the run, so those at work together share slices in that XCD's L2.
+  // contiguous run of the work items, its workgroups one each or every wgs-th of
+  // the run, so those at work together share slices in that XCD's L2.
   const int live = *g.live;
   const int64_t M = g.live_m ? live : g.M;
   const int tiles_m = static_cast<int>((M + T::BM - 1) / T::BM);
   const int tiles = tiles_m * g.tiles_n;
-  const int per_xcd = (tiles + 7) / 8;
+  // work items: the tiles of the first reduction split, of the second, ...
+  const int items = EPI == LE_PARTIAL ? tiles * g.splits : tiles;
+  const int per_xcd = (items + 7) / 8;
   const int wgs = static_cast<int>(gridDim.x / 8);
   if (static_cast<int>(blockIdx.x / 8) >= per_xcd) return;   // whole workgroup
-  const int t_first = static_cast<int>(blockIdx.x % 8) * per_xcd + static_cast<int>(blockIdx.x / 8);
-  const int t_end = T::LOOP ? min(tiles, (static_cast<int>(blockIdx.x % 8) + 1) * per_xcd)
-                            : min(t_first + 1, tiles);
-  if (t_first >= t_end) return;   // whole workgroup
+  const int item = static_cast<int>(blockIdx.x % 8) * per_xcd + static_cast<int>(blockIdx.x / 8);
+  if (item >= items) return;
+  const int split = EPI == LE_PARTIAL ? item / tiles : 0;
+  const int t_first = item - split * tiles;
+  const int t_end = T::LOOP ? min(tiles, (static_cast<int>(blockIdx.x % 8) + 1) * per_xcd) : t_first + 1;
   auto tile_at = [&](int t, int& tm, int& tn) {
     const int band = t / (g.band * g.tiles_n);
     const int bh = min(g.band, tiles_m - g.band * band);
@@ -250,8 +259,8 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   const int total = steps0 + (kTwo ? static_cast<int>((g.seg[1].k + T::KB - 1) / T::KB) : 0);
   int s_lo = 0, s_hi = total;
   if constexpr (EPI == LE_PARTIAL) {
-    s_lo = static_cast<int>(static_cast<int64_t>(total) * blockIdx.y / g.splits);
-    s_hi = static_cast<int>(static_cast<int64_t>(total) * (blockIdx.y + 1) / g.splits);
+    s_lo = static_cast<int>(static_cast<int64_t>(total) * split / g.splits);
+    s_hi = static_cast<int>(static_cast<int64_t>(total) * (split + 1) / g.splits);
   }
 
   const int s_data = s_hi;        // steps from here on read zeros
@@ -261,17 +270,18 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   const uint32_t lrow = static_cast<uint32_t>(lane >> 3);
   const uint32_t lchunk = (static_cast<uint32_t>(lane) & 7u) ^ lrow;
   // byte offset of load q's chunk of this lane inside the step's slice of an
-  // operand with row stride ld
-  auto lane_off = [&](auto slow, auto rowbytes, int q, uint32_t ld) -> uint32_t {
+  // operand with row stride ld (panels: with ld from panel to panel)
+  auto lane_off = [&](auto slow, auto rowbytes, auto panels, int q, uint32_t ld) -> uint32_t {
     const uint32_t i = static_cast<uint32_t>(wave + T::WAVES * q);
     if constexpr (!decltype(slow)::value) {
-      return (8u * i + lrow) * ld * ES + lchunk * 16u;
+      return (8u * i + lrow) * (decltype(panels)::value ? 128u : ld * ES) + lchunk * 16u;
     } else {
       constexpr uint32_t ROWB = decltype(rowbytes)::value;
       const uint32_t o = i * 1024u + static_cast<uint32_t>(lane) * 16u;
       const uint32_t kr = o / ROWB;
       uint32_t p = o % ROWB;
       if constexpr (ES == 2) p = (((p >> 5) ^ slow_swizzle<ROWB>(kr)) << 5) | (p & 16u);
+      if constexpr (decltype(panels)::value) return (p >> 7) * ld * ES + kr * 128u + (p & 127u);
       return kr * ld * ES + p;
     }
   };
@@ -280,16 +290,23 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   typedef std::integral_constant<uint32_t, T::BM * ES> ARow;
   typedef std::integral_constant<uint32_t, T::BN * ES> BRow;
 
-  // a slow operand has one segment: its loads' offsets never change
+  // the gradient products have one segment: their loads' offsets never change
+  constexpr bool kPanels = T::BKS;
+  typedef std::integral_constant<bool, kPanels> APanels;
   uint32_t off_a[T::LOADS_A], off_b[T::LOADS_B];
-  if constexpr (T::AKS)
+  if constexpr (kPanels) {
     static_for<T::LOADS_A>([&](auto q) {
-      off_a[q] = lane_off(ASlow{}, ARow{}, q, static_cast<uint32_t>(g.seg[0].lda));
+      off_a[q] = lane_off(ASlow{}, ARow{}, APanels{}, q, static_cast<uint32_t>(g.seg[0].lda));
     });
-  if constexpr (T::BKS)
     static_for<T::LOADS_B>([&](auto q) {
-      off_b[q] = lane_off(BSlow{}, BRow{}, q, static_cast<uint32_t>(g.seg[0].ldb));
+      off_b[q] = lane_off(BSlow{}, BRow{}, std::false_type{}, q, static_cast<uint32_t>(g.seg[0].ldb));
     });
+  }
+  // slow panels: LDS row of this lane in load 0, and how many rows further each
+  // load is (rows past the reduction's end are cut per lane)
+  constexpr uint32_t kLoadRows = T::WAVES * 1024u / (T::BM * ES);
+  const uint32_t kr0 = (static_cast<uint32_t>(wave) * 1024u + static_cast<uint32_t>(lane) * 16u) / (T::BM * ES);
+  static_assert(!T::AKS || T::WAVES * 1024 % (T::BM * ES) == 0, "loads step by whole rows");
 
   // The loads run STAGES - 1 steps ahead of the MFMAs, with LOOP from one tile's
   // last step straight into the next tile's first, so a tile's epilogue overlaps
@@ -306,6 +323,7 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   ld_tile();
   rsrc_t ra, rb;
   uint32_t ld_a = 0, ld_b = 0, cut = 0;   // cut: kOOB in the lanes past a fast-k tail
+  uint32_t ld_rows = 0;                   // slow panels: k rows of the step
   char* ld_dst = lds;
   auto dma_prep = [&](int buf) {
     const bool second = kTwo && ld_s >= steps0;
@@ -321,8 +339,13 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
     const char* pb = static_cast<const char*>(sg.b);
     uint32_t na, nb;
     if constexpr (T::AKS) {
-      pa += (kk * sg.lda + ld_m0) * ES;
-      na = static_cast<uint32_t>((krows * sg.lda - ld_m0) * ES);
+      const int64_t left = min<int64_t>(T::BM / T::KB, (M + T::KB - 1) / T::KB - ld_m0 / T::KB);
+      pa += (ld_m0 / T::KB * sg.lda + kk * T::KB) * ES;
+      na = static_cast<uint32_t>((left * sg.lda - kk * T::KB) * ES);
+      ld_rows = static_cast<uint32_t>(krows);
+    } else if constexpr (kPanels) {
+      pa += (kk / T::KB * sg.lda + ld_m0 * T::KB) * ES;
+      na = static_cast<uint32_t>(min<int64_t>(T::BM, M - ld_m0) * 128);
     } else {
       pa += (ld_m0 * sg.lda + kk) * ES;
       na = static_cast<uint32_t>((min<int64_t>(T::BM, M - ld_m0) * sg.lda - kk) * ES);
@@ -349,11 +372,18 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   auto dma_one = [&](auto qc) {
     constexpr int q = decltype(qc)::value;
     if constexpr (q < T::LOADS_A) {
-      const uint32_t off = T::AKS ? off_a[q] : lane_off(ASlow{}, ARow{}, q, ld_a) | cut;
+      uint32_t off;
+      if constexpr (T::AKS)
+        off = kr0 + q * kLoadRows < ld_rows ? off_a[q] : kOOB;
+      else if constexpr (kPanels)
+        off = off_a[q];   // a panel's columns past the reduction's end are zeros
+      else
+        off = lane_off(ASlow{}, ARow{}, APanels{}, q, ld_a) | cut;
       load_lds16(ra, off, ld_dst + (wave + T::WAVES * q) * 1024);
     } else {
       constexpr int p = q - T::LOADS_A;
-      const uint32_t off = T::BKS ? off_b[p] : lane_off(BSlow{}, BRow{}, p, ld_b) | cut;
+      const uint32_t off =
+          T::BKS ? off_b[p] : lane_off(BSlow{}, BRow{}, std::false_type{}, p, ld_b) | cut;
       load_lds16(rb, off, ld_dst + T::A_BYTES + (wave + T::WAVES * p) * 1024);
     }
   };
@@ -506,8 +536,13 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
       const int64_t m = mw + decltype(ic)::value * 16;
       static_for<T::WTN>([&](auto j) {
         const int64_t n = nw + decltype(j)::value * 16;
-        if (m < M && n < (EPI == LE_DLOGITS ? g.ldo : g.N))
+        if (m >= M) return;
+        if constexpr (EPI == LE_DLOGITS) {
+          if (n < g.ldo)
+            store4(static_cast<S*>(g.out) + n / T::KB * g.slab + m * T::KB + n % T::KB, value(j));
+        } else if (n < g.N) {
           store4(static_cast<S*>(g.out) + m * g.ldo + n, value(j));
+        }
       });
       return;
     }
@@ -516,19 +551,26 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
              value(j));
     });
     BDR_WAIT_VM_LGKM(63, 0);
-    const rsrc_t out = make_rsrc(static_cast<S*>(g.out) + m0 * g.ldo,
-                                 static_cast<uint32_t>(min<int64_t>(T::BM, M - m0) * g.ldo * ES));
-    const int64_t cols = (EPI == LE_DLOGITS ? g.ldo : g.N) - (n0 + wn * 16 * T::WTN);   // may be <= 0
+    constexpr bool kOutPanels = EPI == LE_DLOGITS;
+    const int64_t left = min<int64_t>(T::BM, M - m0);
+    const rsrc_t out =
+        kOutPanels
+            ? make_rsrc(static_cast<S*>(g.out) + n0 / T::KB * g.slab + m0 * T::KB,
+                        static_cast<uint32_t>((T::BN / T::KB - 1) * g.slab * ES + left * 128))
+            : make_rsrc(static_cast<S*>(g.out) + m0 * g.ldo, static_cast<uint32_t>(left * g.ldo * ES));
+    const int64_t cols = (kOutPanels ? g.ldo : g.N) - (n0 + wn * 16 * T::WTN);   // may be <= 0
 #pragma unroll
     for (int c0 = 0; c0 < 16 * T::OUT_ROW; c0 += 1024) {
       const int c = c0 + lane * 16;
       const int row = c / T::OUT_ROW;
       const int in_row = c % T::OUT_ROW;
       const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + (c < 16 * T::OUT_ROW ? c : 0));
-      const int64_t m = (wm * T::WTM + decltype(ic)::value) * 16 + row;
-      const uint32_t off = static_cast<uint32_t>((m * g.ldo + n0 + wn * 16 * T::WTN) * ES) +
-                           static_cast<uint32_t>(in_row);
-      const bool ok = c < 16 * T::OUT_ROW && in_row < cols * ES;
+      const int m = (wm * T::WTM + decltype(ic)::value) * 16 + row;
+      const int nb = wn * T::OUT_ROW + in_row;   // byte of the tile's row
+      const uint32_t off =
+          kOutPanels ? static_cast<uint32_t>((nb / 128) * g.slab * ES + m * 128 + nb % 128)
+                     : static_cast<uint32_t>((m * g.ldo + n0) * ES + nb);
+      const bool ok = c < 16 * T::OUT_ROW && in_row < cols * ES && m < left;
       bstore16(__builtin_bit_cast(f32x4_t, v), out, ok ? off : kOOB);
     }
     BDR_WAIT_VM_LGKM(63, 0);   // read before the next rows are written
@@ -597,7 +639,7 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
       });
     });
   } else if constexpr (EPI == LE_PARTIAL) {
-    float* out = static_cast<float*>(g.out) + static_cast<int64_t>(blockIdx.y) * g.slab;
+    float* out = static_cast<float*>(g.out) + static_cast<int64_t>(split) * g.slab;
     static_for<T::WTM>([&](auto i) {
       const int64_t m = mw + decltype(i)::value * 16;
       static_for<T::WTN>([&](auto j) {
@@ -619,11 +661,10 @@ template <typename T, int EPI>
 static hipError_t launch_loss_gemm(LossGemm g, hipStream_t stream) {
   const int64_t tiles_m = (g.M + T::BM - 1) / T::BM;
   g.tiles_n = static_cast<int>((g.N + T::BN - 1) / T::BN);
-  const int64_t tiles = tiles_m * g.tiles_n;
-  int64_t blocks = (tiles + 7) / 8 * 8;
+  const int64_t items = tiles_m * g.tiles_n * (EPI == LE_PARTIAL ? g.splits : 1);
+  int64_t blocks = (items + 7) / 8 * 8;
   if (T::LOOP) blocks = std::min<int64_t>(blocks, 256 * T::PER_CU);
-  const dim3 grid(static_cast<unsigned>(blocks),
-                  static_cast<unsigned>(EPI == LE_PARTIAL ? g.splits : 1));
+  const dim3 grid(static_cast<unsigned>(blocks));
   hipLaunchKernelGGL((loss_gemm_kernel<T, EPI>), grid, dim3(64 * T::WAVES), 0, stream, g);
   return hipGetLastError();
 }

@@ -2,14 +2,16 @@
 // d weight = d logits^T hidden (and the Markov head's, as narrow as its rank).
 //
 // Measured (bf16, H = 5120; "library": its product of the same size, same run):
-//   d hidden, 4096 rows, 30720 entries: 256 x 320 965 us (1335 TFLOP/s; library
+//   d hidden, 4096 rows, 30720 entries: 256 x 320 918 us (1404 TFLOP/s; library
 //     1310 - 1460 us), 256 x 256 with 4 splits 1203 us, 128 x 128 2059 us
-//   d hidden, 128 rows, 151936 entries: 128 x 320 with 16 splits 318 us, 128 x 128
-//     with 12 splits 337 us; 7 rows: 32 x 256, 3 stages 292 us
-//   d weight, 30720 entries: 4096 rows 256 x 320 1065 us (1209 TFLOP/s; library
-//     1206 - 1380 us), 128 x 320 1188 us; 2048 rows 569 and 611 us; 1024 rows 335
+//   d hidden, 151936 entries: 128 rows 128 x 320 with 16 splits 318 us, 128 x 128
+//     with 12 splits 337 us; 7 rows 32 x 256 with 12 splits 271 us, 128 x 320 276 us
+//   d embedding, rank 64: 128 rows, 151936 entries, 256 splits 15 us, 32 splits
+//     36 us; 4096 rows, 30720 entries, 16 splits 43 us, 64 splits 73 us
+//   d weight, 30720 entries: 4096 rows 256 x 320 1014 us (1270 TFLOP/s; library
+//     1206 - 1380 us), 128 x 320 1183 us; 2048 rows 569 and 611 us; 1024 rows 335
 //     and 308 us; 256 rows 189 and 113 us
-//   d weight, 151936 entries (1.56 GB written): 128 rows 128 x 320 402 us, one
+//   d weight, 151936 entries (1.56 GB written): 128 rows 128 x 320 379 us, one
 //     tile per workgroup 504 us; 7 rows 269 - 306 us
 //   d w2, rank 64, 30720 entries, 3072 rows: 3 stages 32 us, 2 stages 39 us
 
@@ -19,13 +21,13 @@ namespace bdr {
 
 namespace {
 
-using FeatF32 = LossTile<float, false, true, 2, 2, 4, 4, 2>;         // 128 x 128
-using FeatNarrow = LossTile<uint16_t, false, true, 2, 2, 4, 2, 2>;   // 128 x 64
+using FeatF32 = LossTile<float, false, true, 2, 2, 2, 2, 2>;         // 64 x 64
+using FeatNarrow = LossTile<uint16_t, false, true, 2, 2, 4, 2, 3>;   // 128 x 64
 using FeatFew = LossTile<uint16_t, false, true, 1, 4, 2, 4, 3>;      // 32 x 256
 using FeatSome = LossTile<uint16_t, false, true, 2, 4, 4, 5, 2>;     // 128 x 320
 using FeatMany = LossTile<uint16_t, false, true, 2, 4, 8, 5, 2>;     // 256 x 320
 
-using WeightF32 = LossTile<float, true, true, 2, 2, 4, 4, 2>;        // 128 x 128
+using WeightF32 = LossTile<float, true, true, 2, 2, 2, 2, 2>;        // 64 x 64
 using WeightNarrow = LossTile<uint16_t, true, true, 2, 2, 4, 2, 3>;  // 128 x 64
 // walks its tiles: with few rows the output's bytes bound it, and its stores
 // overlap the next tile's loads
@@ -47,14 +49,14 @@ auto with_feat_tile(bdr_dtype dt, int64_t rows, int64_t cols, F&& f) {
 }  // namespace
 
 // As many reduction splits as fill the compute units once (a workgroup's LDS
-// sets how many share one), each with at least 8 steps.
+// sets how many share one), each with at least 4 steps.
 int loss_dfeat_splits(bdr_dtype dt, int64_t rows, int64_t cols, int64_t width) {
   return with_feat_tile(dt, rows, cols, [&](auto t) {
     using T = decltype(t);
     const int64_t tiles = (rows + T::BM - 1) / T::BM * ((cols + T::BN - 1) / T::BN);
     const int64_t slots = 256 * T::PER_CU;
     const int64_t steps = (width + T::KB - 1) / T::KB;
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 8, 256})));
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 4, 256})));
   });
 }
 

@@ -17,7 +17,7 @@ namespace bdr {
 
 namespace {
 
-using LogitsF32 = LossTile<float, false, false, 2, 2, 4, 4, 2>;          // 128 x 128
+using LogitsF32 = LossTile<float, false, false, 2, 2, 2, 2, 2>;          // 64 x 64
 using LogitsFew = LossTile<uint16_t, false, false, 1, 4, 2, 2, 3>;       // 32 x 128
 using LogitsSome = LossTile<uint16_t, false, false, 2, 4, 4, 5, 2>;      // 128 x 320
 using LogitsMany = LossTile<uint16_t, false, false, 2, 4, 8, 5, 2>;      // 256 x 320
