@@ -189,19 +189,37 @@ __global__ __launch_bounds__(kBwdThreads) void norm_backward_kernel(const NormAr
     for (int e = 0; e < PER; ++e) dw[c][e] = db[c][e] = 0.f;
   }
   const int64_t stride = static_cast<int64_t>(gridDim.x) * GROUPS;
-  // every group walks the same number of rounds: the joins below hold barriers
-  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * GROUPS; r0 < g.rows; r0 += stride) {
-    const int64_t row = r0 + group;
+  // A group of several waves holds the next row's chunks while it works on one
+  // (its joins are barriers, and few rows are in flight); waves by themselves
+  // cover each other.
+  constexpr bool kAhead = LANES > 64;
+  u32x4_t rx[CH], rd[CH], nx[kAhead ? CH : 1], nd[kAhead ? CH : 1];
+  auto load_row = [&](int64_t row, u32x4_t* vx, u32x4_t* vd) {
     const bool live = row < g.rows;
     const S* x = static_cast<const S*>(g.x) + (live ? row : 0) * g.x_stride;
     const S* dy = static_cast<const S*>(g.dy) + (live ? row : 0) * g.dy_stride;
-    u32x4_t rx[CH], rd[CH];
 #pragma unroll
     for (int c = 0; c < CH; ++c) {
       const int col = (c * LANES + lane) * PER;
       const bool in = live && col < g.hidden;
-      rx[c] = in ? load16(x + col) : u32x4_t{0, 0, 0, 0};
-      rd[c] = in ? load16(dy + col) : u32x4_t{0, 0, 0, 0};
+      vx[c] = in ? load16(x + col) : u32x4_t{0, 0, 0, 0};
+      vd[c] = in ? load16(dy + col) : u32x4_t{0, 0, 0, 0};
+    }
+  };
+  if constexpr (kAhead) load_row(static_cast<int64_t>(blockIdx.x) * GROUPS + group, nx, nd);
+  // every group walks the same number of rounds: the joins below hold barriers
+  for (int64_t r0 = static_cast<int64_t>(blockIdx.x) * GROUPS; r0 < g.rows; r0 += stride) {
+    const int64_t row = r0 + group;
+    const bool live = row < g.rows;
+    if constexpr (kAhead) {
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        rx[c] = nx[c];
+        rd[c] = nd[c];
+      }
+      load_row(row + stride, nx, nd);
+    } else {
+      load_row(row, rx, rd);
     }
     const float mean = g.mean && live ? g.mean[row] : 0.f;
     const float rstd = live ? g.rstd[row] : 0.f;
@@ -302,29 +320,24 @@ __global__ __launch_bounds__(1024) void norm_vector_grad_kernel(const float* par
 
 // Workgroups of the backward pass: one per compute unit; each writes a partial row.
 static int64_t norm_backward_blocks(int64_t rows) {
-  return std::max<int64_t>(1, std::min<int64_t>(256, (rows + 1) / 2));
+  return std::max<int64_t>(1, std::min<int64_t>(256, (rows + 3) / 4));
 }
 
 size_t norm_workspace(int64_t rows, int64_t hidden) {
   return align256(static_cast<size_t>(norm_backward_blocks(rows)) * 2 * hidden * sizeof(float));
 }
 
-// Lanes that hold a row and 16-byte chunks per lane.  A wave holds a row of up
-// to 256 chunks by itself (no barrier); a longer row is spread over 256 lanes,
-// and past that over as many lanes as keep it in registers (backward holds x,
-// dy and two column sums per element).
-template <int LANES, int MOST, typename F>
+// f(integral_constant CH) for the smallest of the listed chunk counts that holds ch
+template <int FIRST, int... REST, typename F>
 static hipError_t by_chunks(int64_t ch, F&& f) {
-  using std::integral_constant;
-  integral_constant<int, LANES> lanes;
-  if constexpr (LANES == 64)
-    if (ch <= 1) return f(lanes, integral_constant<int, 1>{});
-  if (ch <= 2) return f(lanes, integral_constant<int, 2>{});
-  if (ch <= 3) return f(lanes, integral_constant<int, 3>{});
-  if (MOST == 4 || ch <= 4) return f(lanes, integral_constant<int, 4>{});
-  return f(lanes, integral_constant<int, MOST>{});
+  if constexpr (sizeof...(REST) == 0)
+    return f(std::integral_constant<int, FIRST>{});
+  else
+    return ch <= FIRST ? f(std::integral_constant<int, FIRST>{}) : by_chunks<REST...>(ch, f);
 }
 
+// A wave holds a row of up to 256 chunks of 16 bytes by itself, 256 lanes a
+// longer one.
 template <typename S>
 static hipError_t norm_forward(const NormArgs& g, hipStream_t stream) {
   const int64_t chunks = g.hidden / Elem<S>::PER16;
@@ -337,13 +350,19 @@ static hipError_t norm_forward(const NormArgs& g, hipStream_t stream) {
                        stream, g);
     return hipGetLastError();
   };
-  if (chunks <= 4 * 64) return by_chunks<64, 4>((chunks + 63) / 64, run);
+  std::integral_constant<int, 64> wave;
+  std::integral_constant<int, 256> wide;
+  if (chunks <= 4 * 64)
+    return by_chunks<1, 2, 3, 4>((chunks + 63) / 64, [&](auto ch) { return run(wave, ch); });
   if constexpr (sizeof(S) == 4)   // rows over 8192
-    if (chunks > 8 * 256)
-      return run(std::integral_constant<int, 256>{}, std::integral_constant<int, 16>{});
-  return by_chunks<256, 8>((chunks + 255) / 256, run);
+    if (chunks > 8 * 256) return run(wide, std::integral_constant<int, 16>{});
+  return by_chunks<2, 3, 4, 8>((chunks + 255) / 256, [&](auto ch) { return run(wide, ch); });
 }
 
+// A wave walks rows of up to 2560 features (fp32: 2048) by itself: no barriers,
+// and a workgroup's eight waves have as many rows in flight (16381 x 2560 bf16:
+// 50 us, 256 lanes a row 68 us).  Longer rows, whose column sums would not
+// fit a wave's registers, are spread over 256 or 512 lanes.
 template <typename S>
 static hipError_t norm_backward(const NormArgs& g, void* dw, void* db, hipStream_t stream) {
   const int64_t chunks = g.hidden / Elem<S>::PER16;
@@ -354,13 +373,27 @@ static hipError_t norm_backward(const NormArgs& g, void* dw, void* db, hipStream
                        dim3(blocks), dim3(kBwdThreads), lds, stream, g);
     return hipGetLastError();
   };
+  std::integral_constant<int, 64> wave;
+  std::integral_constant<int, 256> wide;
+  std::integral_constant<int, 512> whole;
+  const int64_t ch = (chunks + 63) / 64;
+  auto wide_run = [&](auto c) { return run(wide, c); };
   hipError_t e;
-  if (chunks <= 4 * 64)
-    e = by_chunks<64, 4>((chunks + 63) / 64, run);
-  else if (chunks <= 4 * 256)
-    e = by_chunks<256, 4>((chunks + 255) / 256, run);
-  else   // rows over 8192 (bf16) or 4096 (fp32)
-    e = run(std::integral_constant<int, 512>{}, std::integral_constant<int, sizeof(S) == 2 ? 4 : 8>{});
+  if constexpr (sizeof(S) == 2) {
+    if (ch <= 5)
+      e = by_chunks<1, 2, 3, 4, 5>(ch, [&](auto c) { return run(wave, c); });
+    else if (chunks <= 4 * 256)
+      e = by_chunks<2, 3, 4>((chunks + 255) / 256, wide_run);
+    else
+      e = run(whole, std::integral_constant<int, 4>{});
+  } else {
+    if (ch <= 8)
+      e = by_chunks<1, 2, 3, 4, 6, 8>(ch, [&](auto c) { return run(wave, c); });
+    else if (chunks <= 6 * 256)
+      e = by_chunks<3, 4, 5, 6>((chunks + 255) / 256, wide_run);
+    else
+      e = by_chunks<4, 8>((chunks + 511) / 512, [&](auto c) { return run(whole, c); });
+  }
   if (e != hipSuccess || !(dw || db)) return e;
   hipLaunchKernelGGL(norm_vector_grad_kernel<S>, dim3(static_cast<unsigned>((g.hidden + 63) / 64), 2),
                      dim3(1024), 0, stream, g.partial, static_cast<int>(blocks), g.hidden,

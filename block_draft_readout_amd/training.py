@@ -42,7 +42,7 @@ def _need(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
         raise ValueError(f"{name} must be a tensor on {device}")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
@@ -51,6 +51,12 @@ def _need(t: torch.Tensor, name: str, shape, dtype, device) -> torch.Tensor:
 
 def _ptr(t: Optional[torch.Tensor]):
     return None if t is None else t.data_ptr()
+
+
+def _stream(device: torch.device) -> int:
+    """Handle of the device's current stream (torch.cuda.current_stream without the object,
+    whose construction costs as much as a small kernel's launch)."""
+    return torch._C._cuda_getCurrentRawStream(device.index)
 
 
 def _space(nbytes: int, device, ws: Optional[torch.Tensor]):
@@ -97,17 +103,16 @@ def dspark_norm(x: torch.Tensor, weight: torch.Tensor, bias: Optional[torch.Tens
     if bias is not None:
         _need(bias, "bias", (h,), x.dtype, dev)
     if out is None:
-        out = torch.empty(x.shape, dtype=x.dtype, device=dev)
+        out = torch.empty_like(x, memory_format=torch.contiguous_format)
     else:
         _need(out, "out", x.shape, x.dtype, dev)
     st = torch.empty((1 if rms else 2, rows), dtype=torch.float32, device=dev)
-    rstd = st[0]
-    mean = None if rms else st[1]
+    at = st.data_ptr()   # rstd, then the means
     with _on(dev):
         _abi.check("dspark_norm", L.dspark_norm(
             x.data_ptr(), rows, h, stride, dt, weight.data_ptr(), _ptr(bias), eps, out.data_ptr(),
-            _ptr(mean), rstd.data_ptr(), torch.cuda.current_stream(dev).cuda_stream))
-    return (out, mean, rstd) if stats else out
+            None if rms else at + 4 * rows, at, _stream(dev)))
+    return (out, None if rms else st[1], st[0]) if stats else out
 
 
 def dspark_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tensor,
@@ -128,7 +133,7 @@ def dspark_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tens
     _need(rstd, "rstd", (rows,), torch.float32, dev)
     if mean is not None:
         _need(mean, "mean", (rows,), torch.float32, dev)
-    dx = torch.empty(x.shape, dtype=x.dtype, device=dev) if want_x else None
+    dx = torch.empty_like(x, memory_format=torch.contiguous_format) if want_x else None
     dw = torch.empty(h, dtype=x.dtype, device=dev) if want_weight else None
     db = torch.empty(h, dtype=x.dtype, device=dev) if bias else None
     need = L.dspark_norm_backward_workspace_bytes(rows, h) if want_weight or bias else 0
@@ -136,8 +141,7 @@ def dspark_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tens
     with _on(dev):
         _abi.check("dspark_norm_backward", L.dspark_norm_backward(
             grad.data_ptr(), gs, x.data_ptr(), xs, rows, h, dt, weight.data_ptr(), _ptr(mean),
-            rstd.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), wp, wn,
-            torch.cuda.current_stream(dev).cuda_stream))
+            rstd.data_ptr(), _ptr(dx), _ptr(dw), _ptr(db), wp, wn, _stream(dev)))
     return dx, dw, db
 
 
@@ -184,7 +188,7 @@ class _Readout:
         return torch.empty(self.lead + tail, dtype=torch.float32, device=self.device)
 
     def stream(self):
-        return torch.cuda.current_stream(self.device).cuda_stream
+        return _stream(self.device)
 
     def gradients(self, names: Optional[Sequence[str]]) -> Dict[str, torch.Tensor]:
         shapes = {"hidden": self.lead + (self.h,), "lm_head_w": (self.vocab, self.h)}
