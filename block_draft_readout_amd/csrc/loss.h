@@ -14,8 +14,14 @@ hipError_t launch_loss_dlogits(bdr_dtype dt, int64_t rows, const LossGemm& g, hi
 hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
 hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
 
+// output tiles of tile shape T
+template <typename T>
+int64_t loss_tiles(int64_t rows, int64_t cols) {
+  return (rows + T::BM - 1) / T::BM * ((cols + T::BN - 1) / T::BN);
+}
+
 // vocabulary columns of one statistics tile
-int loss_stats_cols(bdr_dtype dt, int64_t rows);
+int loss_stats_cols(bdr_dtype dt, int64_t rows, int64_t cols);
 // reduction splits of a d hidden product over `width` vocabulary entries
 int loss_dfeat_splits(bdr_dtype dt, int64_t rows, int64_t cols, int64_t width);
 

@@ -116,9 +116,15 @@ __global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, i
 // before the row again in every workgroup is cheaper than a scan in a launch of
 // its own: 4 bytes a row from L2 against 2 H bytes copied.
 template <typename S, bool BACKWARD>
-__global__ __launch_bounds__(256) void loss_gather_kernel(const LossRows g) {
+__global__ __launch_bounds__(256) void loss_gather_kernel(const LossRows g, u32x4_t* clear,
+                                                          int64_t clear16) {
   __shared__ int counts[4];
   const int64_t n = blockIdx.x;
+  if (BACKWARD && n >= g.rows) {   // workgroups past the rows clear d w1
+    for (int64_t i = (n - g.rows) * 256 + threadIdx.x; i < clear16; i += (gridDim.x - g.rows) * 256)
+      clear[i] = u32x4_t{0, 0, 0, 0};
+    return;
+  }
   const uint32_t V = static_cast<uint32_t>(g.vocab);
   int c = 0;
   for (int64_t i = threadIdx.x; i < n; i += 256) c += static_cast<uint32_t>(g.label[i]) < V;
@@ -339,7 +345,7 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const int32_t* live, con
 
 // d w1[prev] = sum of the embedding gradients of the rows with that previous
 // token, in row order.  One workgroup per compacted row; the first row with a
-// token does the sum for it (d w1 was cleared before).
+// token does the sum for it (d w1 was cleared with the compaction).
 template <typename S>
 __global__ __launch_bounds__(256) void loss_dw1_kernel(const LossRows g, const float* de, S* out) {
   __shared__ int first;
@@ -408,7 +414,7 @@ struct LossPlan {
 LossPlan plan_loss(const LossProblem& p) {
   LossPlan q{};
   const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
-  const int cols = loss_stats_cols(p.dt, p.rows);
+  const int cols = loss_stats_cols(p.dt, p.rows, p.vocab);
   q.stat_tiles = static_cast<int>((p.vocab + cols - 1) / cols);
   // whole vocabulary where its d logits fit, else equal pieces
   int64_t most = kPieceBytes / (p.rows * es) / kPieceCols * kPieceCols;
@@ -501,17 +507,21 @@ void fill_rows(const LossProblem& p, const LossPlan& q, LossBuffers& b) {
 unsigned waves4(int64_t rows) { return static_cast<unsigned>((rows + 3) / 4); }
 
 template <typename S>
-hipError_t gather(const LossProblem& p, const LossBuffers& b, bool backward, hipStream_t st) {
+hipError_t gather(const LossProblem& p, const LossBuffers& b, bool backward, void* dw1,
+                  hipStream_t st) {
   if (p.top) {
     hipLaunchKernelGGL(distill_target_kernel, dim3(waves4(p.rows)), dim3(256), 0, st, b.r, b.has);
     BDR_LAUNCH(hipGetLastError());
   }
-  if (backward)
-    hipLaunchKernelGGL((loss_gather_kernel<S, true>), dim3(static_cast<unsigned>(p.rows)), dim3(256),
-                       0, st, b.r);
-  else
+  if (backward) {
+    const int64_t n16 = dw1 ? p.vocab * p.rank * static_cast<int64_t>(sizeof(S)) / 16 : 0;
+    const int64_t blocks = p.rows + std::min<int64_t>((n16 + 255) / 256, 2048);
+    hipLaunchKernelGGL((loss_gather_kernel<S, true>), dim3(static_cast<unsigned>(blocks)), dim3(256),
+                       0, st, b.r, static_cast<u32x4_t*>(dw1), n16);
+  } else {
     hipLaunchKernelGGL((loss_gather_kernel<S, false>), dim3(static_cast<unsigned>(p.rows)),
-                       dim3(256), 0, st, b.r);
+                       dim3(256), 0, st, b.r, nullptr, 0);
+  }
   return hipGetLastError();
 }
 
@@ -543,7 +553,7 @@ hipError_t forward(const LossProblem& p, void* workspace, float* loss, float* ls
   LossBuffers b{};
   lay_out(p, q, false, static_cast<char*>(workspace), b);
   fill_rows(p, q, b);
-  BDR_LAUNCH(gather<S>(p, b, false, st));
+  BDR_LAUNCH(gather<S>(p, b, false, nullptr, st));
   LossGemm g = logits_gemm(p, b.r, 0, p.vocab);
   g.label = p.top ? nullptr : b.r.label_c;
   g.picked = b.r.z_label;
@@ -595,7 +605,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
   fill_rows(p, q, b);
   b.r.lse = lse;
   b.r.loss_grad = loss_grad;
-  BDR_LAUNCH(gather<S>(p, b, true, st));
+  BDR_LAUNCH(gather<S>(p, b, true, o.w1, st));
   for (int64_t v0 = 0; v0 < p.vocab; v0 += q.piece) {
     const int64_t width = std::min(q.piece, p.vocab - v0);
     const int64_t ld = (width + 63) / 64 * 64;
@@ -664,7 +674,6 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       BDR_LAUNCH(join<float>(p.rows, b.r.live, nullptr, b.part_e, q.splits_e, p.rank, b.de, st));
       de = b.de;
     }
-    BDR_LAUNCH(launch_clear(o.w1, p.vocab * p.rank * es, st));
     hipLaunchKernelGGL(loss_dw1_kernel<S>, dim3(static_cast<unsigned>(p.rows)), dim3(256), 0, st,
                        b.r, de, static_cast<S*>(o.w1));
     BDR_LAUNCH(hipGetLastError());

@@ -75,12 +75,13 @@ struct LossGemm {
 };
 
 template <typename S_, bool AKS_, bool BKS_, int WM_, int WN_, int WTM_, int WTN_, int STAGES_,
-          bool LOOP_ = false>
+          bool LOOP_ = false, bool NT_B_ = false>
 struct LossTile {
   using S = S_;
   static constexpr bool AKS = AKS_, BKS = BKS_;   // reduction slow
   static constexpr int WM = WM_, WN = WN_, WTM = WTM_, WTN = WTN_, STAGES = STAGES_;
   static constexpr bool LOOP = LOOP_;             // a workgroup walks several tiles
+  static constexpr bool NT_B = NT_B_;             // B is streamed once: non-temporal loads
   static constexpr int WAVES = WM * WN;
   static constexpr int BM = 16 * WM * WTM, BN = 16 * WN * WTN;
   static constexpr int KB = 128 / static_cast<int>(sizeof(S));
@@ -115,9 +116,10 @@ __device__ __forceinline__ uint32_t slow_swizzle(uint32_t kr) {
 }
 
 // 16 bytes per lane, global -> LDS: lane l's land at dst + 16 l (dst uniform)
+template <int AUX>
 __device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t off, char* dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)dst, 16, off,
-                                           0, 0, 0);
+                                           0, 0, AUX);
 }
 
 // Transposing reads of NA operand tiles whose 8-byte pieces this lane names at
@@ -379,12 +381,12 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
         off = off_a[q];   // a panel's columns past the reduction's end are zeros
       else
         off = lane_off(ASlow{}, ARow{}, APanels{}, q, ld_a) | cut;
-      load_lds16(ra, off, ld_dst + (wave + T::WAVES * q) * 1024);
+      load_lds16<0>(ra, off, ld_dst + (wave + T::WAVES * q) * 1024);
     } else {
       constexpr int p = q - T::LOADS_A;
       const uint32_t off =
           T::BKS ? off_b[p] : lane_off(BSlow{}, BRow{}, std::false_type{}, p, ld_b) | cut;
-      load_lds16(rb, off, ld_dst + T::A_BYTES + (wave + T::WAVES * p) * 1024);
+      load_lds16<T::NT_B ? 2 : 0>(rb, off, ld_dst + T::A_BYTES + (wave + T::WAVES * p) * 1024);
     }
   };
 

@@ -4,8 +4,9 @@
 // Measured (bf16, H = 5120; "library": its product of the same size, same run):
 //   d hidden, 4096 rows, 30720 entries: 256 x 320 918 us (1404 TFLOP/s; library
 //     1310 - 1460 us), 256 x 256 with 4 splits 1203 us, 128 x 128 2059 us
-//   d hidden, 151936 entries: 128 rows 128 x 320 with 16 splits 318 us, 128 x 128
-//     with 12 splits 337 us; 7 rows 32 x 256 with 12 splits 271 us, 128 x 320 276 us
+//   d hidden, 151936 entries, 16 splits: 7 rows 64 x 320 225 us (6.9 TB/s; 258 us
+//     with temporal loads), 128 x 320 250 us; 64 rows 239 and 265 us; 128 rows
+//     128 x 320 295 us (315 us temporal); 256 rows 256 x 320 376 us, 128 x 320 512 us
 //   d embedding, rank 64: 128 rows, 151936 entries, 256 splits 15 us, 32 splits
 //     36 us; 4096 rows, 30720 entries, 16 splits 43 us, 64 splits 73 us
 //   d weight, 30720 entries: 4096 rows 256 x 320 1014 us (1270 TFLOP/s; library
@@ -23,9 +24,9 @@ namespace {
 
 using FeatF32 = LossTile<float, false, true, 2, 2, 2, 2, 2>;         // 64 x 64
 using FeatNarrow = LossTile<uint16_t, false, true, 2, 2, 4, 2, 3>;   // 128 x 64
-using FeatFew = LossTile<uint16_t, false, true, 1, 4, 2, 4, 3>;      // 32 x 256
-using FeatSome = LossTile<uint16_t, false, true, 2, 4, 4, 5, 2>;     // 128 x 320
-using FeatMany = LossTile<uint16_t, false, true, 2, 4, 8, 5, 2>;     // 256 x 320
+using FeatFew = LossTile<uint16_t, false, true, 2, 4, 2, 5, 3, false, true>;    // 64 x 320
+using FeatSome = LossTile<uint16_t, false, true, 2, 4, 4, 5, 2, false, true>;   // 128 x 320
+using FeatMany = LossTile<uint16_t, false, true, 2, 4, 8, 5, 2>;                // 256 x 320
 
 using WeightF32 = LossTile<float, true, true, 2, 2, 2, 2, 2>;        // 64 x 64
 using WeightNarrow = LossTile<uint16_t, true, true, 2, 2, 4, 2, 3>;  // 128 x 64
@@ -53,7 +54,7 @@ auto with_feat_tile(bdr_dtype dt, int64_t rows, int64_t cols, F&& f) {
 int loss_dfeat_splits(bdr_dtype dt, int64_t rows, int64_t cols, int64_t width) {
   return with_feat_tile(dt, rows, cols, [&](auto t) {
     using T = decltype(t);
-    const int64_t tiles = (rows + T::BM - 1) / T::BM * ((cols + T::BN - 1) / T::BN);
+    const int64_t tiles = loss_tiles<T>(rows, cols);
     const int64_t slots = 256 * T::PER_CU;
     const int64_t steps = (width + T::KB - 1) / T::KB;
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>({slots / tiles, steps / 4, 256})));
@@ -68,7 +69,9 @@ hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, const LossGemm& g, hipS
 
 hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream) {
   if (dt != BDR_BF16) return launch_loss_gemm<WeightF32, LE_OUT>(g, stream);
-  if (g.N <= kNarrowCols) return launch_loss_gemm<WeightNarrow, LE_OUT>(g, stream);
+  // narrow outputs, and small ones whose wide tiles would leave half the chip idle
+  if (g.N <= kNarrowCols || loss_tiles<WeightFew>(g.M, g.N) < 128)
+    return launch_loss_gemm<WeightNarrow, LE_OUT>(g, stream);
   if (rows < kManyRows) return launch_loss_gemm<WeightFew, LE_OUT>(g, stream);
   return launch_loss_gemm<WeightMany, LE_OUT>(g, stream);
 }

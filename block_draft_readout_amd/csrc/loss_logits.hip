@@ -1,15 +1,20 @@
 // Logits products of the vocabulary losses: softmax statistics and d logits.
 //
-// Few rows are bound by streaming the weight: small row tiles, so that several
-// loads of weight rows are in flight per compute unit; many rows by the matrix
-// cores: the largest tile whose accumulators fit two waves per SIMD.  Measured
-// (bf16, H = 5120, V = 151936; statistics):
-//   rows 7:    32 x 128, 3 stages 260 us (6.0 TB/s); 32 x 256, 2 stages 332 us;
-//              128 x 320 299 us
-//   rows 128:  128 x 320 319 us; 128 x 128 406 us; 32 x 128 824 us
-//   rows 4096 (30720 entries): 256 x 320 1010 us (1270 TFLOP/s; the library's
-//              product 990 us in the same run); 256 x 256 and 128 x 128 9 % and
-//              75 % slower
+// Few rows are bound by streaming the weight, which one row of tiles reads once:
+// row tiles no taller than needed, non-temporal loads, as many stages as fit.
+// Many rows are bound by the matrix cores: the largest tile whose accumulators
+// fit two waves per SIMD.  Where those tiles are too few to occupy the chip (a
+// small vocabulary), smaller ones.  Measured (bf16, statistics):
+//   H = 5120, V = 151936:
+//     rows 7    64 x 320 228 us (6.8 TB/s; 257 us with temporal loads),
+//               32 x 128 229 us, 128 x 320 282 us
+//     rows 64   64 x 320 239 us, 128 x 320 287 us, 32 x 128 479 us
+//     rows 128  128 x 320 298 us (317 us temporal), 64 x 320 438 us
+//     rows 256  256 x 320 395 us, 128 x 320 552 us
+//     rows 4096, 30720 entries: 256 x 320 1010 us (1270 TFLOP/s; the library's
+//               product 990 us in the same run), 256 x 256 and 128 x 128 9 % and
+//               75 % slower
+//   H = 1024, V = 16384, rows 64: 32 x 128 13.7 us, 64 x 320 20.1 us
 
 #include "loss.h"
 
@@ -17,33 +22,44 @@ namespace bdr {
 
 namespace {
 
-using LogitsF32 = LossTile<float, false, false, 2, 2, 2, 2, 2>;          // 64 x 64
-using LogitsFew = LossTile<uint16_t, false, false, 1, 4, 2, 2, 3>;       // 32 x 128
-using LogitsSome = LossTile<uint16_t, false, false, 2, 4, 4, 5, 2>;      // 128 x 320
-using LogitsMany = LossTile<uint16_t, false, false, 2, 4, 8, 5, 2>;      // 256 x 320
+using LogitsF32 = LossTile<float, false, false, 2, 2, 2, 2, 2>;                       // 64 x 64
+using LogitsSmall = LossTile<uint16_t, false, false, 1, 4, 2, 2, 4, false, true>;     // 32 x 128
+using LogitsMid = LossTile<uint16_t, false, false, 2, 2, 4, 4, 2>;                    // 128 x 128
+using LogitsFew = LossTile<uint16_t, false, false, 2, 4, 2, 5, 3, false, true>;       // 64 x 320
+using LogitsSome = LossTile<uint16_t, false, false, 2, 4, 4, 5, 2, false, true>;      // 128 x 320
+using LogitsMany = LossTile<uint16_t, false, false, 2, 4, 8, 5, 2>;                   // 256 x 320
 
-template <int EPI>
-hipError_t logits(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream) {
-  if (dt != BDR_BF16) return launch_loss_gemm<LogitsF32, EPI>(g, stream);
-  if (rows <= LogitsFew::BM) return launch_loss_gemm<LogitsFew, EPI>(g, stream);
-  if (rows <= LogitsSome::BM) return launch_loss_gemm<LogitsSome, EPI>(g, stream);
-  return launch_loss_gemm<LogitsMany, EPI>(g, stream);
+template <typename F>
+auto with_logits_tile(bdr_dtype dt, int64_t rows, int64_t cols, F&& f) {
+  if (dt != BDR_BF16) return f(LogitsF32{});
+  // the tile fit for the rows, where it leaves at most a quarter of the compute units idle
+  if (rows <= LogitsFew::BM ? loss_tiles<LogitsFew>(rows, cols) >= 192
+      : rows <= LogitsSome::BM ? loss_tiles<LogitsSome>(rows, cols) >= 192
+                               : loss_tiles<LogitsMany>(rows, cols) >= 192) {
+    if (rows <= LogitsFew::BM) return f(LogitsFew{});
+    if (rows <= LogitsSome::BM) return f(LogitsSome{});
+    return f(LogitsMany{});
+  }
+  if (loss_tiles<LogitsMid>(rows, cols) >= 64 && rows > 64) return f(LogitsMid{});
+  return f(LogitsSmall{});
 }
 
 }  // namespace
 
-int loss_stats_cols(bdr_dtype dt, int64_t rows) {
-  if (dt != BDR_BF16) return LogitsF32::BN;
-  if (rows <= LogitsFew::BM) return LogitsFew::BN;
-  return rows <= LogitsSome::BM ? LogitsSome::BN : LogitsMany::BN;
+int loss_stats_cols(bdr_dtype dt, int64_t rows, int64_t cols) {
+  return with_logits_tile(dt, rows, cols, [](auto t) { return decltype(t)::BN; });
 }
 
 hipError_t launch_loss_stats(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream) {
-  return logits<LE_STATS>(dt, rows, g, stream);
+  return with_logits_tile(dt, rows, g.N, [&](auto t) {
+    return launch_loss_gemm<decltype(t), LE_STATS>(g, stream);
+  });
 }
 
 hipError_t launch_loss_dlogits(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream) {
-  return logits<LE_DLOGITS>(dt, rows, g, stream);
+  return with_logits_tile(dt, rows, g.N, [&](auto t) {
+    return launch_loss_gemm<decltype(t), LE_DLOGITS>(g, stream);
+  });
 }
 
 }  // namespace bdr
