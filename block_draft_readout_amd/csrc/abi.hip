@@ -787,6 +787,8 @@ int dflash_fuse_fc_rows_fp8(const void* const* taps, int n_taps, int64_t rows, i
 // ---------------------------------------------------------------------------- training: row norm
 namespace {
 
+constexpr int64_t kMaxNormRows = int64_t(1) << 24;   // 256 work-items each in a 32-bit grid
+
 int norm_shape(int64_t rows, int64_t hidden, int dt) {
   if (!valid_dtype(dt)) return fail(BDR_EINVAL, "unknown dtype %d", dt);
   if (rows < 0) return fail(BDR_EINVAL, "rows must be >= 0");
@@ -798,7 +800,7 @@ int norm_shape(int64_t rows, int64_t hidden, int dt) {
   if (hidden % e)
     return fail(BDR_EUNSUPPORTED, "hidden %lld must be a multiple of %d for this dtype",
                 static_cast<long long>(hidden), e);
-  if (rows > kMaxVocab) return fail(BDR_EUNSUPPORTED, "rows must be < 2^31 - 1");
+  if (rows >= kMaxNormRows) return fail(BDR_EUNSUPPORTED, "rows must be < 2^24");
   return BDR_OK;
 }
 
@@ -895,6 +897,8 @@ namespace {
 
 constexpr int64_t kMaxLossRows = int64_t(1) << 20;
 constexpr int64_t kMaxLossHidden = int64_t(1) << 20;
+constexpr int64_t kMaxLossElems = int64_t(1) << 35;   // of each product: grids stay in 32 bits
+constexpr float kMinLossTemperature = 1e-4f, kMaxLossTemperature = 1e4f;
 
 // the sizes of a loss call (top == 0: cross entropy)
 int loss_shape(int64_t rows, int64_t hidden, int64_t vocab, int rank, int dt, int top, bool distill) {
@@ -905,6 +909,9 @@ int loss_shape(int64_t rows, int64_t hidden, int64_t vocab, int rank, int dt, in
   if (rank < 0) return fail(BDR_EINVAL, "rank must be >= 0");
   if (rows > kMaxLossRows || hidden > kMaxLossHidden || vocab > kMaxMarkovVocab)
     return fail(BDR_EUNSUPPORTED, "rows and hidden must be <= 2^20 and vocab <= 2^21 here");
+  if (rows > kMaxLossElems / vocab || hidden > kMaxLossElems / vocab ||
+      (rows > 0 && hidden > kMaxLossElems / rows))
+    return fail(BDR_EUNSUPPORTED, "rows * vocab, vocab * hidden and rows * hidden must be <= 2^35");
   if (rank > BDR_MAX_RANK) return fail(BDR_EUNSUPPORTED, "rank %d > %d", rank, BDR_MAX_RANK);
   const int e = dt == BDR_BF16 ? 8 : 4;
   if (hidden % e || rank % e)
@@ -978,6 +985,16 @@ int loss_run_backward(const LossProblem& p, const LossGrads& o, const float* lse
   }
   if (!o.hidden && !o.w && !o.w1 && !o.w2) return fail(BDR_EINVAL, "no gradient is wanted");
   BDR_TRY(loss_inputs(p));
+  const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
+  const int64_t bytes[4] = {p.rows * p.hidden * es, p.vocab * p.hidden * es, p.vocab * p.rank * es,
+                            p.vocab * p.rank * es};
+  const void* in[4] = {p.x, p.w, p.rank ? p.w1 : nullptr, p.rank ? p.w2 : nullptr};
+  const void* out[4] = {o.hidden, o.w, o.w1, o.w2};
+  for (int i = 0; i < 4; ++i)
+    for (int j = 0; j < 4; ++j)
+      if (out[i] && ((in[j] && overlap(out[i], bytes[i], in[j], bytes[j])) ||
+                     (j > i && out[j] && overlap(out[i], bytes[i], out[j], bytes[j]))))
+        return fail(BDR_EINVAL, "a gradient overlaps an input or another gradient");
   BDR_TRY(need_ptr(lse, "lse", 4));
   if (p.top) BDR_TRY(need_ptr(picked, "picked", 4));
   BDR_TRY(need_ptr(loss_grad, "loss_grad", 4));
@@ -1051,8 +1068,8 @@ namespace {
 int distill_problem(LossProblem& p, const void* hidden, const void* lm_head_w,
                     const int32_t* ids, const void* logits, int teacher_dt, float temperature) {
   if (!valid_dtype(teacher_dt)) return fail(BDR_EINVAL, "unknown teacher dtype %d", teacher_dt);
-  if (!(temperature > 0.f) || !std::isfinite(temperature))
-    return fail(BDR_EINVAL, "temperature must be finite and > 0");
+  if (!(temperature >= kMinLossTemperature && temperature <= kMaxLossTemperature))
+    return fail(BDR_EINVAL, "temperature must be in [1e-4, 1e4]");
   p.x = hidden;
   p.w = lm_head_w;
   p.ids = ids;

@@ -4,9 +4,10 @@
 // Measured (bf16, H = 5120; "library": its product of the same size, same run):
 //   d hidden, 4096 rows, 30720 entries: 256 x 320 918 us (1404 TFLOP/s; library
 //     1310 - 1460 us), 256 x 256 with 4 splits 1203 us, 128 x 128 2059 us
-//   d hidden, 151936 entries, 16 splits: 7 rows 64 x 320 225 us (6.9 TB/s; 258 us
-//     with temporal loads), 128 x 320 250 us; 64 rows 239 and 265 us; 128 rows
-//     128 x 320 295 us (315 us temporal); 256 rows 256 x 320 376 us, 128 x 320 512 us
+//   d hidden, 151936 entries: 7 rows 64 x 320 225 us (6.9 TB/s; 258 us with temporal
+//     loads), 128 x 320 250 us; 64 rows 239 and 265 us; 128 rows 128 x 256 with
+//     three stages 267 us, 128 x 320 286 us (315 us temporal); 256 rows 256 x 320
+//     376 us, 128 x 320 512 us
 //   d embedding, rank 64: 128 rows, 151936 entries, 256 splits 15 us, 32 splits
 //     36 us; 4096 rows, 30720 entries, 16 splits 43 us, 64 splits 73 us
 //   d weight, 30720 entries: 4096 rows 256 x 320 1014 us (1270 TFLOP/s; library
@@ -25,7 +26,7 @@ namespace {
 using FeatF32 = LossTile<float, false, true, 2, 2, 2, 2, 2>;         // 64 x 64
 using FeatNarrow = LossTile<uint16_t, false, true, 2, 2, 4, 2, 3>;   // 128 x 64
 using FeatFew = LossTile<uint16_t, false, true, 2, 4, 2, 5, 3, false, true>;    // 64 x 320
-using FeatSome = LossTile<uint16_t, false, true, 2, 4, 4, 5, 2, false, true>;   // 128 x 320
+using FeatSome = LossTile<uint16_t, false, true, 2, 4, 4, 4, 3, false, true>;   // 128 x 256
 using FeatMany = LossTile<uint16_t, false, true, 2, 4, 8, 5, 2>;                // 256 x 320
 
 using WeightF32 = LossTile<float, true, true, 2, 2, 2, 2, 2>;        // 64 x 64

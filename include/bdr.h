@@ -607,7 +607,8 @@ int dflash_fuse_fc_rows_fp8(const void* const* taps, int n_taps, int64_t rows,
  *
  *   x        [rows, H] dtype, row m at x + m * x_stride elements (x_stride >= H,
  *            rows 16-byte aligned: a multiple of 8 (bf16) or 4 (f32))
- *   rows     >= 0; 0 < H <= BDR_MAX_NORM_HIDDEN, H % 8 == 0 (bf16) or H % 4 == 0
+ *   rows     0 <= rows < 2^24; 0 < H <= BDR_MAX_NORM_HIDDEN, H % 8 == 0 (bf16) or
+ *            H % 4 == 0 (f32)
  *   weight   [H] dtype; bias [H] dtype or NULL
  *   eps      finite, >= 0
  *   y        [rows, H] dtype, contiguous; may be x itself where x_stride == H
@@ -651,7 +652,7 @@ int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64
  *
  *   hidden     [rows, H] dtype; 0 <= rows <= 2^20; 0 < H <= 2^20, H % 8 == 0
  *              (bf16) or H % 4 == 0 (f32)
- *   lm_head_w  [V, H] dtype; 0 < V <= 2^21
+ *   lm_head_w  [V, H] dtype; 0 < V <= 2^21; rows * V, V * H and rows * H <= 2^35
  *   markov_w1, markov_w2 [V, r] dtype, prev_token [rows] int32; both matrices
  *              NULL or rank == 0: no bias; rank as in dspark_markov_argmax
  *   labels     [rows] int32
@@ -668,7 +669,8 @@ int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64
  *   lse        [rows] as written by dspark_ce_loss for the same inputs
  *   loss_grad  [rows] fp32
  *   d_hidden [rows, H], d_lm_head_w [V, H], d_markov_w1, d_markov_w2 [V, r]:
- *              dtype, each may be NULL (a frozen head costs nothing)
+ *              dtype, each may be NULL (a frozen head costs nothing); none may
+ *              overlap an input or another gradient
  *   workspace  >= dspark_ce_workspace_bytes(rows, H, V, rank, dt, 1)
  * rows == 0 clears the weight gradients that are given.
  */
@@ -702,7 +704,7 @@ int dspark_ce_backward(const void* hidden, int64_t rows, int64_t hidden_size, in
  *
  *   teacher_ids    [rows, top] int32; 1 <= top <= BDR_MAX_TEACHER
  *   teacher_logits [rows, top] teacher_dt (BDR_F32 or BDR_BF16)
- *   temperature    finite, > 0
+ *   temperature    1e-4 .. 1e4
  *   loss, lse      [rows] fp32 out; picked [rows, top] fp32 out (0 for entries
  *                  that are not listed and rows that are left out)
  *   workspace      >= dspark_distill_workspace_bytes(rows, H, V, rank, top, dt, 0)

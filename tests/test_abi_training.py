@@ -30,7 +30,7 @@ def _norm(A, **k):
 def test_norm_refusals(A):
     E, U = A.BDR_EINVAL, A.BDR_EUNSUPPORTED
     assert _norm(A, dt=7) == E and _norm(A, dt=A.BDR_BF16_PACKED) == E
-    assert _norm(A, rows=-1) == E
+    assert _norm(A, rows=-1) == E and _norm(A, rows=1 << 24) == U
     assert _norm(A, hidden=0) == E
     assert _norm(A, hidden=68, stride=72) == U
     assert _norm(A, hidden=A.MAX_NORM_HIDDEN + 8, stride=A.MAX_NORM_HIDDEN + 8) == U
@@ -71,7 +71,7 @@ def test_norm_backward_refusals(A):
 def _loss(A, distill=False, backward=False, **k):
     a = dict(x=P, rows=5, hidden=64, vocab=1000, dt=A.BDR_BF16, w=P, w1=P, w2=P, rank=8, prev=P,
              labels=P, ids=P, u=P, top=4, udt=A.BDR_F32, T=1.0, loss=P, lse=P, picked=P, g=P,
-             dh=P, dw=P, d1=P, d2=P, ws=P, n=1 << 40)
+             dh=2 * P, dw=3 * P, d1=5 * P, d2=6 * P, ws=P, n=1 << 40)
     a.update(k)
     L = A.load()
     head = (a["x"], a["rows"], a["hidden"], a["vocab"], a["dt"], a["w"], a["w1"], a["w2"], a["rank"],
@@ -95,6 +95,7 @@ def test_loss_refusals(A, distill, backward):
     assert f(dt=A.BDR_BF16_PACKED) == E and f(dt=9) == E
     assert f(rows=-1) == E and f(hidden=0) == E and f(vocab=0) == E and f(rank=-8) == E
     assert f(rows=(1 << 20) + 1) == U and f(hidden=(1 << 20) + 8) == U and f(vocab=(1 << 21) + 1) == U
+    assert f(rows=1 << 20, vocab=1 << 16) == U and f(hidden=1 << 18, vocab=1 << 18) == U
     assert f(hidden=68) == U and f(rank=12) == U and f(rank=136) == U
     assert f(dt=A.BDR_F32, hidden=66) == U
     assert f(x=None) == E and f(x=P + 8) == E and f(w=None) == E
@@ -103,7 +104,7 @@ def test_loss_refusals(A, distill, backward):
     assert f(lse=None) == E
     if distill:
         assert f(top=0) == E and f(top=A.MAX_TEACHER + 1) == U and f(udt=5) == E
-        assert f(T=0.0) == E and f(T=-1.0) == E and f(T=float("inf")) == E and f(T=float("nan")) == E
+        assert f(T=0.0) == E and f(T=-1.0) == E and f(T=9e-5) == E and f(T=1.1e4) == E and f(T=float("inf")) == E and f(T=float("nan")) == E
         assert f(ids=None) == E and f(u=None) == E and f(u=P + 2) == E and f(picked=None) == E
     else:
         assert f(labels=None) == E and f(labels=P + 2) == E
@@ -111,6 +112,7 @@ def test_loss_refusals(A, distill, backward):
         assert f(g=None) == E
         assert f(dh=None, dw=None, d1=None, d2=None) == E
         assert f(dh=P + 8) == E and f(dw=P + 8) == E
+        assert f(dh=P) == E and f(dw=P + 1024) == E and f(d1=3 * P + 16) == E   # overlaps
         assert f(rank=0) == E                            # Markov gradients without a head
         assert f(rows=0, dw=None, d1=None, d2=None) == A.BDR_OK
     else:

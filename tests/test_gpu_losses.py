@@ -344,6 +344,15 @@ def test_no_row_with_a_target_and_no_rows(top, dtype):
         assert not grads[k].any()
 
 
+def test_nothing_to_learn_in_the_large_tiles():
+    """No row with a target where the weight gradient's workgroups walk their tiles."""
+    c = _case(14, 21, 640, 20011, 32, "bf16", empty=1.1)
+    c["labels"][:] = -1
+    _, _, _, grads = _run(c)
+    for k, v in grads.items():
+        assert not v.any(), k
+
+
 def test_single_gradients_equal_the_joint_call():
     c = _case(15, 90, 200, 900, 24, "bf16")
     full = _run(c)[3]
