@@ -11,8 +11,12 @@ namespace bdr {
 // (d logits fast, weights slow) and d weight (both slow).
 hipError_t launch_loss_stats(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
 hipError_t launch_loss_dlogits(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
-hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
-hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream);
+// the gradients of hidden and embedding, or of W and w2 (either may be NULL), in
+// one launch where they take the same tiles
+hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, bool small, const LossGemm* x,
+                             const LossGemm* e, hipStream_t stream);
+hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, bool small, const LossGemm* x,
+                               const LossGemm* e, hipStream_t stream);
 
 // output tiles of tile shape T
 template <typename T>
@@ -23,6 +27,6 @@ int64_t loss_tiles(int64_t rows, int64_t cols) {
 // vocabulary columns of one statistics tile
 int loss_stats_cols(bdr_dtype dt, int64_t rows, int64_t cols);
 // reduction splits of a d hidden product over `width` vocabulary entries
-int loss_dfeat_splits(bdr_dtype dt, int64_t rows, int64_t cols, int64_t width);
+int loss_dfeat_splits(bdr_dtype dt, int64_t rows, bool small, int64_t cols, int64_t width);
 
 }  // namespace bdr

@@ -36,6 +36,7 @@ namespace {
 
 constexpr int64_t kPieceBytes = int64_t(512) << 20;   // d logits of one piece
 constexpr int64_t kPieceCols = 2560;                  // pieces are multiples of this
+constexpr int64_t kSmallProduct = int64_t(1) << 30;   // rows * hidden * vocab
 
 // What the row kernels read and write, besides the products.
 struct LossRows {
@@ -310,26 +311,41 @@ __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, cons
 }
 
 // ---------------------------------------------------------------- gradients out
-// The reduction splits of a feature gradient added in order.  With `pos`, row n
-// of the output is the compacted row pos[n], or zeros (d hidden, rounded);
-// without, the compacted rows stay where they are (d embedding, fp32).  SL lanes
-// share the splits of four columns and join through LDS: few rows have many
-// splits and few columns to spread over the chip.  Grid (rows, columns / (1024 / SL)).
+// The reduction splits of the feature gradients added in order: d hidden rounded
+// and back at the original rows (zeros for rows without a target), d embedding
+// fp32 at the compacted rows.  SL lanes share the splits of four columns and join
+// through LDS: few rows have many splits and few columns to spread over the chip.
+// Grid (rows, column blocks of d hidden, then of d embedding), 1024 / SL columns
+// in a block.
+template <typename S>
+struct JoinArgs {
+  const int32_t* live;
+  const int32_t* pos;
+  const float* part_x;
+  const float* part_e;
+  int splits_x, splits_e, hidden, rank, blocks_x;
+  int64_t rows;
+  S* dx;
+  float* de;
+};
+
 template <typename S, int SL>
-__global__ __launch_bounds__(256) void loss_join_kernel(const int32_t* live, const int32_t* pos,
-                                                        const float* part, int splits, int64_t slab,
-                                                        int cols, S* out) {
+__global__ __launch_bounds__(256) void loss_join_kernel(const JoinArgs<S> g) {
   constexpr int QUADS = 256 / SL;
   __shared__ f32x4_t sums[SL > 1 ? 256 : 1];
   const int64_t n = blockIdx.x;
-  if (!pos && n >= *live) return;
-  const int p = pos ? pos[n] : static_cast<int>(n);
+  const bool emb = static_cast<int>(blockIdx.y) >= g.blocks_x;   // uniform
+  if (emb && n >= *g.live) return;
+  const int p = emb ? static_cast<int>(n) : g.pos[n];
   const int q = static_cast<int>(threadIdx.x) % QUADS;
   const int sl = static_cast<int>(threadIdx.x) / QUADS;
-  const int c = (static_cast<int>(blockIdx.y) * QUADS + q) * 4;
+  const int cols = emb ? g.rank : g.hidden;
+  const int splits = emb ? g.splits_e : g.splits_x;
+  const int c = ((static_cast<int>(blockIdx.y) - (emb ? g.blocks_x : 0)) * QUADS + q) * 4;
   f32x4_t v{0.f, 0.f, 0.f, 0.f};
   if (p >= 0 && c < cols) {
-    const float* src = part + static_cast<int64_t>(p) * cols + c;
+    const float* src = (emb ? g.part_e : g.part_x) + static_cast<int64_t>(p) * cols + c;
+    const int64_t slab = g.rows * cols;
 #pragma unroll 4
     for (int s = sl; s < splits; s += SL) v += *reinterpret_cast<const f32x4_t*>(src + s * slab);
   }
@@ -340,7 +356,11 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const int32_t* live, con
 #pragma unroll
     for (int k = 1; k < SL; ++k) v += sums[k * QUADS + q];
   }
-  if (c < cols) store4(out + n * cols + c, v);
+  if (c >= cols) return;
+  if (emb)
+    store4(g.de + n * cols + c, v);
+  else
+    store4(g.dx + n * cols + c, v);
 }
 
 // d w1[prev] = sum of the embedding gradients of the rows with that previous
@@ -407,6 +427,7 @@ __global__ __launch_bounds__(256) void clear_kernel(u32x4_t* p, int64_t n16) {
 struct LossPlan {
   int64_t piece;       // vocabulary entries per piece (backward)
   int64_t ld;          // row length of the piece's d logits buffer
+  bool small;          // narrow tiles, fewer launches
   int splits_x, splits_e;
   int stat_tiles;
 };
@@ -423,8 +444,9 @@ LossPlan plan_loss(const LossProblem& p) {
   q.piece = ((p.vocab + pieces - 1) / pieces + kPieceCols - 1) / kPieceCols * kPieceCols;
   q.piece = std::min(q.piece, p.vocab);
   q.ld = (q.piece + 63) / 64 * 64;
-  q.splits_x = loss_dfeat_splits(p.dt, p.rows, p.hidden, q.piece);
-  q.splits_e = p.rank ? loss_dfeat_splits(p.dt, p.rows, p.rank, q.piece) : 0;
+  q.small = p.rows * p.hidden <= kSmallProduct / p.vocab;
+  q.splits_x = loss_dfeat_splits(p.dt, p.rows, q.small, p.hidden, q.piece);
+  q.splits_e = p.rank ? loss_dfeat_splits(p.dt, p.rows, q.small, p.rank, q.piece) : 0;
   return q;
 }
 
@@ -581,18 +603,20 @@ hipError_t forward(const LossProblem& p, void* workspace, float* loss, float* ls
 // Many splits with 16 lanes each on four columns, few with one (128 rows of 5120,
 // 16 splits: 54 us with one lane, 20 us with 16).
 template <typename S>
-hipError_t join(int64_t rows, const int32_t* live, const int32_t* pos, const float* part, int splits,
-                int cols, S* out, hipStream_t st) {
-  const int64_t slab = rows * cols;
-  if (splits >= 8)
-    hipLaunchKernelGGL((loss_join_kernel<S, 16>),
-                       dim3(static_cast<unsigned>(rows), static_cast<unsigned>((cols + 63) / 64)),
-                       dim3(256), 0, st, live, pos, part, splits, slab, cols, out);
-  else
-    hipLaunchKernelGGL((loss_join_kernel<S, 1>),
-                       dim3(static_cast<unsigned>(rows), static_cast<unsigned>((cols + 1023) / 1024)),
-                       dim3(256), 0, st, live, pos, part, splits, slab, cols, out);
-  return hipGetLastError();
+hipError_t join(JoinArgs<S> g, hipStream_t st) {
+  auto run = [&](auto lanes) {
+    constexpr int SL = decltype(lanes)::value;
+    constexpr int COLS = 1024 / SL;
+    g.blocks_x = g.dx ? (g.hidden + COLS - 1) / COLS : 0;
+    const int blocks_e = g.de ? (g.rank + COLS - 1) / COLS : 0;
+    hipLaunchKernelGGL((loss_join_kernel<S, SL>),
+                       dim3(static_cast<unsigned>(g.rows), static_cast<unsigned>(g.blocks_x + blocks_e)),
+                       dim3(256), 0, st, g);
+    return hipGetLastError();
+  };
+  if (g.dx ? g.splits_x >= 8 : g.splits_e >= 8)
+    return run(std::integral_constant<int, 16>{});
+  return run(std::integral_constant<int, 1>{});
 }
 
 template <typename S>
@@ -643,7 +667,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.ldo = cols;
       d.slab = p.rows * cols;
       d.accumulate = v0 > 0;
-      return launch_loss_dfeat(p.dt, p.rows, d, st);
+      return d;
     };
     // d weight and d w2: reduction over the rows
     auto dweight = [&](const void* feat, int64_t cols, void* out) {
@@ -658,22 +682,26 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.splits = 1;
       d.out = static_cast<char*>(out) + v0 * cols * es;
       d.ldo = cols;
-      return launch_loss_dweight(p.dt, p.rows, d, st);
+      return d;
     };
-    if (o.hidden) BDR_LAUNCH(dfeat(p.w, p.hidden, b.part_x, q.splits_x));
-    if (o.w1) BDR_LAUNCH(dfeat(p.w2, p.rank, b.part_e, q.splits_e));
-    if (o.w) BDR_LAUNCH(dweight(b.r.x, p.hidden, o.w));
-    if (o.w2) BDR_LAUNCH(dweight(b.r.e, p.rank, o.w2));
+    LossGemm gx, ge;
+    if (o.hidden) gx = dfeat(p.w, p.hidden, b.part_x, q.splits_x);
+    if (o.w1) ge = dfeat(p.w2, p.rank, b.part_e, q.splits_e);
+    BDR_LAUNCH(launch_loss_dfeat(p.dt, p.rows, q.small, o.hidden ? &gx : nullptr,
+                                 o.w1 ? &ge : nullptr, st));
+    if (o.w) gx = dweight(b.r.x, p.hidden, o.w);
+    if (o.w2) ge = dweight(b.r.e, p.rank, o.w2);
+    BDR_LAUNCH(launch_loss_dweight(p.dt, p.rows, q.small, o.w ? &gx : nullptr,
+                                   o.w2 ? &ge : nullptr, st));
   }
-  if (o.hidden)
-    BDR_LAUNCH(join<S>(p.rows, nullptr, b.r.pos, b.part_x, q.splits_x, static_cast<int>(p.hidden),
-                       static_cast<S*>(o.hidden), st));
+  const bool join_e = o.w1 && q.splits_e > 1;
+  if (o.hidden || join_e)
+    BDR_LAUNCH(join(JoinArgs<S>{b.r.live, b.r.pos, b.part_x, b.part_e, q.splits_x, q.splits_e,
+                                static_cast<int>(p.hidden), p.rank, 0, p.rows,
+                                static_cast<S*>(o.hidden), join_e ? b.de : nullptr},
+                    st));
   if (o.w1) {
-    const float* de = b.part_e;
-    if (q.splits_e > 1) {
-      BDR_LAUNCH(join<float>(p.rows, b.r.live, nullptr, b.part_e, q.splits_e, p.rank, b.de, st));
-      de = b.de;
-    }
+    const float* de = join_e ? b.de : b.part_e;
     hipLaunchKernelGGL(loss_dw1_kernel<S>, dim3(static_cast<unsigned>(p.rows)), dim3(256), 0, st,
                        b.r, de, static_cast<S*>(o.w1));
     BDR_LAUNCH(hipGetLastError());

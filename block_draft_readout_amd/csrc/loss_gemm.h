@@ -217,8 +217,9 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4_t v) {
 }
 __device__ __forceinline__ void store4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
 
+// Workgroup `block` of `blocks` (a multiple of 8) of one product.
 template <typename T, int EPI>
-__global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm g) {
+__device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int blocks) {
   using S = typename T::S;
   constexpr int ES = static_cast<int>(sizeof(S));
   __shared__ __attribute__((aligned(16))) char lds[T::LDS_BYTES];
@@ -229,7 +230,7 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   const int wm = wave % T::WM;
   const int wn = wave / T::WM;
 
-  // Tiles of this workgroup: each XCD (workgroup b runs on XCD b % 8) takes a
+  // Tiles of this workgroup: each XCD takes a
   // contiguous run of the work items, its workgroups one each or every wgs-th of
   // the run, so those at work together share slices in that XCD's L2.
   const int live = *g.live;
@@ -239,13 +240,14 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
   // work items: the tiles of the first reduction split, of the second, ...
   const int items = EPI == LE_PARTIAL ? tiles * g.splits : tiles;
   const int per_xcd = (items + 7) / 8;
-  const int wgs = static_cast<int>(gridDim.x / 8);
-  if (static_cast<int>(blockIdx.x / 8) >= per_xcd) return;   // whole workgroup
-  const int item = static_cast<int>(blockIdx.x % 8) * per_xcd + static_cast<int>(blockIdx.x / 8);
+  const int wgs = blocks / 8;
+  const int xcd = block % 8, in_xcd = block / 8;   // workgroup b runs on XCD b % 8
+  if (in_xcd >= per_xcd) return;   // whole workgroup
+  const int item = xcd * per_xcd + in_xcd;
   if (item >= items) return;
   const int split = EPI == LE_PARTIAL ? item / tiles : 0;
   const int t_first = item - split * tiles;
-  const int t_end = T::LOOP ? min(tiles, (static_cast<int>(blockIdx.x % 8) + 1) * per_xcd) : t_first + 1;
+  const int t_end = T::LOOP ? min(tiles, (xcd + 1) * per_xcd) : t_first + 1;
   auto tile_at = [&](int t, int& tm, int& tn) {
     const int band = t / (g.band * g.tiles_n);
     const int bh = min(g.band, tiles_m - g.band * band);
@@ -660,14 +662,44 @@ __global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm
 }
 
 template <typename T, int EPI>
-static hipError_t launch_loss_gemm(LossGemm g, hipStream_t stream) {
+__global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm g) {
+  loss_gemm_body<T, EPI>(g, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
+}
+
+// Two products in one launch, the second one's workgroups after the first's.
+template <typename T, int EPI>
+__global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_pair_kernel(const LossGemm g0,
+                                                                       const LossGemm g1,
+                                                                       int blocks0) {
+  const int b = static_cast<int>(blockIdx.x);
+  const bool second = b >= blocks0;
+  loss_gemm_body<T, EPI>(second ? g1 : g0, second ? b - blocks0 : b,
+                         second ? static_cast<int>(gridDim.x) - blocks0 : blocks0);
+}
+
+// Fills in the tile grid and returns the workgroups of a product.
+template <typename T, int EPI>
+static int64_t loss_gemm_blocks(LossGemm& g) {
   const int64_t tiles_m = (g.M + T::BM - 1) / T::BM;
   g.tiles_n = static_cast<int>((g.N + T::BN - 1) / T::BN);
   const int64_t items = tiles_m * g.tiles_n * (EPI == LE_PARTIAL ? g.splits : 1);
-  int64_t blocks = (items + 7) / 8 * 8;
-  if (T::LOOP) blocks = std::min<int64_t>(blocks, 256 * T::PER_CU);
-  const dim3 grid(static_cast<unsigned>(blocks));
-  hipLaunchKernelGGL((loss_gemm_kernel<T, EPI>), grid, dim3(64 * T::WAVES), 0, stream, g);
+  const int64_t blocks = (items + 7) / 8 * 8;
+  return T::LOOP ? std::min<int64_t>(blocks, 256 * T::PER_CU) : blocks;
+}
+
+template <typename T, int EPI>
+static hipError_t launch_loss_gemm(LossGemm g, hipStream_t stream) {
+  const unsigned blocks = static_cast<unsigned>(loss_gemm_blocks<T, EPI>(g));
+  hipLaunchKernelGGL((loss_gemm_kernel<T, EPI>), dim3(blocks), dim3(64 * T::WAVES), 0, stream, g);
+  return hipGetLastError();
+}
+
+template <typename T, int EPI>
+static hipError_t launch_loss_gemm_pair(LossGemm g0, LossGemm g1, hipStream_t stream) {
+  const unsigned b0 = static_cast<unsigned>(loss_gemm_blocks<T, EPI>(g0));
+  const unsigned b1 = static_cast<unsigned>(loss_gemm_blocks<T, EPI>(g1));
+  hipLaunchKernelGGL((loss_gemm_pair_kernel<T, EPI>), dim3(b0 + b1), dim3(64 * T::WAVES), 0, stream,
+                     g0, g1, static_cast<int>(b0));
   return hipGetLastError();
 }
 

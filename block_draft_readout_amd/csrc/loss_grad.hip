@@ -39,21 +39,32 @@ using WeightMany = LossTile<uint16_t, true, true, 2, 4, 8, 5, 2>;        // 256 
 constexpr int64_t kNarrowCols = 128;   // outputs this narrow take the narrow tiles
 constexpr int64_t kManyRows = 1536;    // between the rows measured above
 
+// `small`: a product of a few billion operations at most, where the launches
+// count: narrow tiles, so that both gradients of a kind go into one launch.
 template <typename F>
-auto with_feat_tile(bdr_dtype dt, int64_t rows, int64_t cols, F&& f) {
+auto with_feat_tile(bdr_dtype dt, int64_t rows, bool small, int64_t cols, F&& f) {
   if (dt != BDR_BF16) return f(FeatF32{});
-  if (cols <= kNarrowCols) return f(FeatNarrow{});
+  if (small || cols <= kNarrowCols) return f(FeatNarrow{});
   if (rows <= FeatFew::BM) return f(FeatFew{});
   if (rows <= FeatSome::BM) return f(FeatSome{});
   return f(FeatMany{});
+}
+
+template <typename F>
+auto with_weight_tile(bdr_dtype dt, int64_t rows, bool small, const LossGemm& g, F&& f) {
+  if (dt != BDR_BF16) return f(WeightF32{});
+  // narrow outputs, and ones whose wide tiles would leave half the chip idle
+  if (small || g.N <= kNarrowCols || loss_tiles<WeightFew>(g.M, g.N) < 128) return f(WeightNarrow{});
+  if (rows < kManyRows) return f(WeightFew{});
+  return f(WeightMany{});
 }
 
 }  // namespace
 
 // As many reduction splits as fill the compute units once (a workgroup's LDS
 // sets how many share one), each with at least 4 steps.
-int loss_dfeat_splits(bdr_dtype dt, int64_t rows, int64_t cols, int64_t width) {
-  return with_feat_tile(dt, rows, cols, [&](auto t) {
+int loss_dfeat_splits(bdr_dtype dt, int64_t rows, bool small, int64_t cols, int64_t width) {
+  return with_feat_tile(dt, rows, small, cols, [&](auto t) {
     using T = decltype(t);
     const int64_t tiles = loss_tiles<T>(rows, cols);
     const int64_t slots = 256 * T::PER_CU;
@@ -62,19 +73,32 @@ int loss_dfeat_splits(bdr_dtype dt, int64_t rows, int64_t cols, int64_t width) {
   });
 }
 
-hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream) {
-  return with_feat_tile(dt, rows, g.N, [&](auto t) {
-    return launch_loss_gemm<decltype(t), LE_PARTIAL>(g, stream);
-  });
+hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, bool small, const LossGemm* x,
+                             const LossGemm* e, hipStream_t stream) {
+  if (x && e && dt != BDR_BF16) return launch_loss_gemm_pair<FeatF32, LE_PARTIAL>(*x, *e, stream);
+  if (x && e && small) return launch_loss_gemm_pair<FeatNarrow, LE_PARTIAL>(*x, *e, stream);
+  for (const LossGemm* g : {x, e}) {
+    if (!g) continue;
+    const hipError_t err = with_feat_tile(dt, rows, small, g->N, [&](auto t) {
+      return launch_loss_gemm<decltype(t), LE_PARTIAL>(*g, stream);
+    });
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
-hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, const LossGemm& g, hipStream_t stream) {
-  if (dt != BDR_BF16) return launch_loss_gemm<WeightF32, LE_OUT>(g, stream);
-  // narrow outputs, and small ones whose wide tiles would leave half the chip idle
-  if (g.N <= kNarrowCols || loss_tiles<WeightFew>(g.M, g.N) < 128)
-    return launch_loss_gemm<WeightNarrow, LE_OUT>(g, stream);
-  if (rows < kManyRows) return launch_loss_gemm<WeightFew, LE_OUT>(g, stream);
-  return launch_loss_gemm<WeightMany, LE_OUT>(g, stream);
+hipError_t launch_loss_dweight(bdr_dtype dt, int64_t rows, bool small, const LossGemm* x,
+                               const LossGemm* e, hipStream_t stream) {
+  if (x && e && dt != BDR_BF16) return launch_loss_gemm_pair<WeightF32, LE_OUT>(*x, *e, stream);
+  if (x && e && small) return launch_loss_gemm_pair<WeightNarrow, LE_OUT>(*x, *e, stream);
+  for (const LossGemm* g : {x, e}) {
+    if (!g) continue;
+    const hipError_t err = with_weight_tile(dt, rows, small, *g, [&](auto t) {
+      return launch_loss_gemm<decltype(t), LE_OUT>(*g, stream);
+    });
+    if (err != hipSuccess) return err;
+  }
+  return hipSuccess;
 }
 
 }  // namespace bdr
