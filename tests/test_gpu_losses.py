@@ -418,6 +418,66 @@ def test_captured_and_replayed_on_another_stream():
             assert torch.equal(p, q), (k, i)
 
 
+def test_two_streams_at_once():
+    """Calls that share inputs but no workspace, in flight together."""
+    m = bdr()
+    c = _case(24, 400, 264, 30011, 16, "bf16", empty=0.2)
+    d = _case(25, 50, 264, 30011, 16, "bf16", top=8, empty=0.2)
+    serial = [_run(c), _run(d, 2.0)]
+    torch.cuda.synchronize()
+    s = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(3):
+        both = []
+        for st, (k, t) in zip(s, ((c, 1.0), (d, 2.0))):
+            with torch.cuda.stream(st):
+                both.append(_run(k, t))
+        torch.cuda.synchronize()
+        for a, b in zip(serial, both):
+            assert torch.equal(a[0], b[0])
+            for n in a[3]:
+                assert torch.equal(a[3][n], b[3][n]), n
+    assert m is not None
+
+
+def test_weights_beyond_32_bit_offsets():
+    """2^21 entries of 1032 features: 4.3 GB of weight and as much gradient.  The loss and the rows
+    of d W that the last entries get, against float64 on the device."""
+    m = bdr()
+    N, H, V = 3, 1032, 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(3)
+    w = torch.empty(V, H, dtype=torch.bfloat16, device="cuda")
+    for a in range(0, V, 1 << 18):
+        w[a:a + (1 << 18)] = torch.randn(1 << 18, H, generator=g, device="cuda") / 32
+    x = torch.randn(N, H, generator=g, device="cuda").bfloat16()
+    lab = torch.tensor([V - 1, 0, V - 2], dtype=torch.int32, device="cuda")
+    one = torch.tensor([1.0, 0.5, 2.0], device="cuda")
+    loss, lse = m.dspark_ce_loss(x, w, lab)
+    gr = m.dspark_ce_backward(x, w, lab, lse, one)
+    z = torch.cat([x.double() @ w[a:a + (1 << 18)].double().t() for a in range(0, V, 1 << 18)], dim=1)
+    ref = torch.logsumexp(z, dim=1)
+    zabs = max(float((x.double().abs() @ w[a:a + (1 << 18)].double().abs().t()).max())
+               for a in range(0, V, 1 << 18))
+    zerr = (H / 4 + 40) * U * zabs
+    assert (lse.double() - ref).abs().max() <= zerr + 64 * U * (1 + float(ref.abs().max()))
+    pick = z.gather(1, lab.long()[:, None])[:, 0]
+    assert (loss.double() - (ref - pick)).abs().max() <= 2 * zerr + 64 * U * (1 + float(ref.abs().max()))
+    dz = (z - ref[:, None]).exp_()
+    dz[torch.arange(N), lab.long()] -= 1
+    dz *= one.double()[:, None]
+    for lo, hi in ((0, 4), (V - 1000, V)):
+        want = dz[:, lo:hi].t() @ x.double()
+        mags = dz[:, lo:hi].abs().t() @ x.double().abs()
+        p = dz[:, lo:hi].abs() + torch.where(dz[:, lo:hi] < 0, one.double()[:, None], 0.0)
+        ep = 2 * zerr + 64 * U * (1 + float(ref.abs().max()) + zabs)
+        tol = (ep * p.t() @ x.double().abs()) + 2.0 ** -8 * (mags + want.abs()) + TINY * N
+        assert ((gr["lm_head_w"][lo:hi].double() - want).abs() <= tol).all()
+    dh = sum(dz[:, a:a + (1 << 18)] @ w[a:a + (1 << 18)].double() for a in range(0, V, 1 << 18))
+    ah = sum(dz[:, a:a + (1 << 18)].abs() @ w[a:a + (1 << 18)].double().abs() for a in range(0, V, 1 << 18))
+    # d logits' rounding and the softmax's error against the sum of magnitudes, V / 4 fp32 additions
+    tol = (2.0 ** -8 + 2 * zerr + (V / 4 + 40) * U) * ah + 2.0 ** -8 * dh.abs()
+    assert ((gr["hidden"].double() - dh).abs() <= tol).all()
+
+
 def test_refusals():
     m = bdr()
     c = _case(30, 6, 64, 100, 8, "bf16")
