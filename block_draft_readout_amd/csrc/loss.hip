@@ -38,6 +38,9 @@ constexpr int64_t kPieceBytes = int64_t(512) << 20;   // d logits of one piece
 constexpr int64_t kPieceCols = 2560;                  // pieces are multiples of this
 constexpr int64_t kSmallProduct = int64_t(1) << 30;   // rows * hidden * vocab
 
+constexpr int64_t kCountRows = 1024;                  // rows of a block of the compaction
+constexpr int64_t kManyRows = 4096;                   // more take a count of the blocks first
+
 // What the row kernels read and write, besides the products.
 struct LossRows {
   const void* hidden;
@@ -56,6 +59,7 @@ struct LossRows {
   const float* loss_grad;
   // workspace
   int32_t* live;           // [1]
+  int32_t* counts;         // [blocks of kCountRows rows] rows with a target, or NULL
   int32_t* pos;            // [rows] compacted row or -1
   int32_t* row_of;         // [live] original row
   int32_t* label_c;        // [live]
@@ -72,7 +76,8 @@ struct LossRows {
 
 // ---------------------------------------------------------------- targets of the distillation
 // t = softmax of a row's valid teacher logits over T, and whether it has any
-// mass; one wave per row.
+// mass; one wave per row.  The maximum is taken off before the division: the
+// difference of two close logits is exact, their quotients by a small T are not.
 __global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, int32_t* has) {
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
@@ -86,9 +91,8 @@ __global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, i
     const int j = c * 64 + lane;
     v[c] = -INFINITY;
     if (j < g.top && static_cast<uint32_t>(ids[j]) < static_cast<uint32_t>(g.vocab)) {
-      const float u = g.u_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(g.u)[n * g.top + j])
-                               : static_cast<const float*>(g.u)[n * g.top + j];
-      v[c] = u / g.temperature;
+      v[c] = g.u_bf16 ? bf16_to_f32(static_cast<const uint16_t*>(g.u)[n * g.top + j])
+                      : static_cast<const float*>(g.u)[n * g.top + j];
     }
     mx = fmaxf(mx, v[c]);
     any |= !(v[c] == -INFINITY);
@@ -99,7 +103,7 @@ __global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, i
   float sum = 0.f;
 #pragma unroll
   for (int c = 0; c < BDR_MAX_TEACHER / 64; ++c) {
-    v[c] = v[c] == -INFINITY ? 0.f : expf(v[c] - mx);
+    v[c] = v[c] == -INFINITY ? 0.f : expf((v[c] - mx) / g.temperature);
     sum += v[c];
   }
   sum = wave_sum(sum);
@@ -112,10 +116,28 @@ __global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, i
 }
 
 // ---------------------------------------------------------------- compaction
+// Rows with a target in each block of rows.
+__global__ __launch_bounds__(256) void loss_count_kernel(const LossRows g) {
+  __shared__ int counts[4];
+  const int64_t n0 = static_cast<int64_t>(blockIdx.x) * kCountRows;
+  int c = 0;
+  for (int64_t n = n0 + threadIdx.x; n < min(n0 + kCountRows, g.rows); n += 256)
+    c += static_cast<uint32_t>(g.label[n]) < static_cast<uint32_t>(g.vocab);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) c += __shfl_xor(c, m);
+  if ((threadIdx.x & 63) == 0) counts[threadIdx.x >> 6] = c;
+  __syncthreads();
+  if (threadIdx.x == 0) g.counts[blockIdx.x] = counts[0] + counts[1] + counts[2] + counts[3];
+}
+
 // One workgroup per row: counts the rows with a target before it (its place),
 // copies its hidden state and its Markov embedding there.  Reading the labels
 // before the row again in every workgroup is cheaper than a scan in a launch of
-// its own: 4 bytes a row from L2 against 2 H bytes copied.
+// its own (4 bytes a row from L2 against 2 H bytes copied) up to some thousand
+// rows; with more, a launch counts each block of rows first, and a workgroup reads
+// the blocks' counts and the labels of its own block only (forward call, H = 64,
+// 1000 entries: 65536 rows 619 -> 145 us, 16384 rows 70 -> 44 us, 8191 rows 36 -> 31
+// us; 4096 rows take the 21 us of 2048 rows without it).
 template <typename S, bool BACKWARD>
 __global__ __launch_bounds__(256) void loss_gather_kernel(const LossRows g, u32x4_t* clear,
                                                           int64_t clear16) {
@@ -128,7 +150,12 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(const LossRows g, u32x
   }
   const uint32_t V = static_cast<uint32_t>(g.vocab);
   int c = 0;
-  for (int64_t i = threadIdx.x; i < n; i += 256) c += static_cast<uint32_t>(g.label[i]) < V;
+  int64_t first = 0;   // rows before it are in the counts
+  if (g.counts) {
+    first = n / kCountRows * kCountRows;
+    for (int64_t i = threadIdx.x; i < n / kCountRows; i += 256) c += g.counts[i];
+  }
+  for (int64_t i = first + threadIdx.x; i < n; i += 256) c += static_cast<uint32_t>(g.label[i]) < V;
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1) c += __shfl_xor(c, m);
   if ((threadIdx.x & 63) == 0) counts[threadIdx.x >> 6] = c;
@@ -368,7 +395,6 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const JoinArgs<S> g) {
 // token does the sum for it (d w1 was cleared with the compaction).
 template <typename S>
 __global__ __launch_bounds__(256) void loss_dw1_kernel(const LossRows g, const float* de, S* out) {
-  __shared__ int first;
   __shared__ int list[256];
   __shared__ int wave_n[4];
   __shared__ float sums[256];
@@ -378,12 +404,15 @@ __global__ __launch_bounds__(256) void loss_dw1_kernel(const LossRows g, const f
   const int tok = g.prev_c[p];
   if (tok < 0) return;
   const int tid = static_cast<int>(threadIdx.x);
-  if (tid == 0) first = 1;
-  __syncthreads();
-  for (int i = tid; i < p; i += 256)
-    if (g.prev_c[i] == tok) first = 0;
-  __syncthreads();
-  if (!first) return;
+  for (int base = 0; base < p; base += 2048) {   // most rows of a common token end here early
+    int seen = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      const int i = base + k * 256 + tid;
+      if (i < p) seen |= g.prev_c[i] == tok;
+    }
+    if (__syncthreads_or(seen)) return;
+  }
   // column r of group gr of the workgroup: rows of the list strided by groups
   const int r = g.rank;
   const int groups = 256 / r;
@@ -475,6 +504,8 @@ size_t lay_out(const LossProblem& p, const LossPlan& q, bool backward, char* bas
   const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
   LossRows& r = b.r;
   r.live = s.take<int32_t>(1);
+  r.counts = s.take<int32_t>(p.rows > kManyRows ? (p.rows + kCountRows - 1) / kCountRows : 0);
+  if (p.rows <= kManyRows) r.counts = nullptr;
   r.pos = s.take<int32_t>(p.rows);
   r.row_of = s.take<int32_t>(p.rows);
   r.label_c = s.take<int32_t>(p.rows);
@@ -533,6 +564,12 @@ hipError_t gather(const LossProblem& p, const LossBuffers& b, bool backward, voi
                   hipStream_t st) {
   if (p.top) {
     hipLaunchKernelGGL(distill_target_kernel, dim3(waves4(p.rows)), dim3(256), 0, st, b.r, b.has);
+    BDR_LAUNCH(hipGetLastError());
+  }
+  if (b.r.counts) {
+    hipLaunchKernelGGL(loss_count_kernel,
+                       dim3(static_cast<unsigned>((p.rows + kCountRows - 1) / kCountRows)), dim3(256),
+                       0, st, b.r);
     BDR_LAUNCH(hipGetLastError());
   }
   if (backward) {
@@ -678,6 +715,9 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.M = width;
       d.N = cols;
       d.live_k = 1;
+      // many rows: taller bands push the step's d logits out of an XCD's L2 (256 x 320
+      // tiles, 4096 rows: 4 rows of tiles a band 1718 us, 16 1887 us; 1000 rows: 849 and
+      // 798 us; 128 x 320 tiles, 128 rows: 464 and 388 us)
       d.band = p.rows < 1536 ? 16 : 4;
       d.splits = 1;
       d.out = static_cast<char*>(out) + v0 * cols * es;

@@ -128,7 +128,8 @@ __device__ __forceinline__ void load_lds16(rsrc_t r, uint32_t off, char* dst) {
 // per k row), HALF k rows into the stage.  One block of assembly with its own wait: the
 // compiler takes the intrinsic for a possible write to LDS and waits for every
 // buffer-to-LDS load in flight before it, which costs the loads' latency once a
-// step (d weight, 256 x 320 tiles, 4096 x 30720 x 5120: 1530 -> 1090 us).
+// step (d weight of 12 x 2560 entries, 4096 rows of 5120, 256 x 320 tiles: 1530 ->
+// 1090 us).
 #define BDR_TR_READ(i, o0, o1)                                                          \
   "ds_read_b64_tr_b16 %[l" #i "], %[a" #i "] offset:%c[" #o0 "]\n\t"                     \
   "ds_read_b64_tr_b16 %[h" #i "], %[a" #i "] offset:%c[" #o1 "]\n\t"
@@ -165,14 +166,6 @@ __device__ __forceinline__ void lds_read_tr(const uint32_t (&ad)[NA + NB], u32x4
                    BDR_TR_OUT(5)
                  : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IN(4),
                    BDR_TR_IN(5), BDR_TR_IMM
-                 : "memory");
-  } else if constexpr (NA == 4 && NB == 4) {
-    asm volatile(BDR_TR_4(BDR_TR_READ, 4, 5, 6, 7, q0, q1)
-                 BDR_TR_4(BDR_TR_READ, 0, 1, 2, 3, p0, p1) "s_waitcnt lgkmcnt(0)"
-                 : BDR_TR_OUT(0), BDR_TR_OUT(1), BDR_TR_OUT(2), BDR_TR_OUT(3), BDR_TR_OUT(4),
-                   BDR_TR_OUT(5), BDR_TR_OUT(6), BDR_TR_OUT(7)
-                 : BDR_TR_IN(0), BDR_TR_IN(1), BDR_TR_IN(2), BDR_TR_IN(3), BDR_TR_IN(4),
-                   BDR_TR_IN(5), BDR_TR_IN(6), BDR_TR_IN(7), BDR_TR_IMM
                  : "memory");
   } else if constexpr (NA == 4 && NB == 5) {
     asm volatile(BDR_TR_4(BDR_TR_READ, 4, 5, 6, 7, q0, q1) BDR_TR_READ(8, q0, q1)
@@ -230,9 +223,9 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   const int wm = wave % T::WM;
   const int wn = wave / T::WM;
 
-  // Tiles of this workgroup: each XCD takes a
-  // contiguous run of the work items, its workgroups one each or every wgs-th of
-  // the run, so those at work together share slices in that XCD's L2.
+  // Tiles of this workgroup: each XCD takes a contiguous run of the work items, its
+  // workgroups one each or every wgs-th of the run, so those at work together share
+  // slices in that XCD's L2.
   const int live = *g.live;
   const int64_t M = g.live_m ? live : g.M;
   const int tiles_m = static_cast<int>((M + T::BM - 1) / T::BM);
@@ -474,189 +467,189 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   FragB b;
   int buf = 0;
   for (int t = t_first; t < t_end; t += wgs) {
-  static_for<T::WTM>([&](auto i) {
-    static_for<T::WTN>([&](auto j) { acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
-  });
-  for (int s = s_lo; s < s_hi; ++s) {
-    // this wave's loads of the step have landed when at most those of the
-    // STAGES - 2 steps after it remain; after the barrier every wave's have,
-    // and every wave is done with the stage the next loads overwrite
-    if (kStores > 0 && s == s_lo && t != t_first)
-      BDR_WAIT_VM_LGKM(kAhead + kStores, 0);
-    else
-      BDR_WAIT_VM_LGKM(kAhead, 0);
-    BDR_WG_BARRIER();
-    if constexpr (!kSpread) static_for<T::LOADS>([&](auto q) { dma_one(q); });
-    read_frags(buf, std::integral_constant<int, 0>{}, a, b);
-    static_for<NT>([&](auto ec) {
-      constexpr int e = decltype(ec)::value;
-      constexpr int every = kSpread ? NT / T::LOADS : NT;
-      acc[e / T::WTN][e % T::WTN] =
-          mma16(b[e % T::WTN], a[e / T::WTN], acc[e / T::WTN][e % T::WTN], S());
-      if constexpr (kSpread && e % every == every - 1 && e / every < T::LOADS)
-        dma_one(std::integral_constant<int, e / every>{});
+    static_for<T::WTM>([&](auto i) {
+      static_for<T::WTN>([&](auto j) { acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
     });
-    read_frags(buf, std::integral_constant<int, 1>{}, a, b);
-    static_for<NT>([&](auto ec) {
-      constexpr int e = decltype(ec)::value;
-      acc[e / T::WTN][e % T::WTN] =
-          mma16(b[e % T::WTN], a[e / T::WTN], acc[e / T::WTN][e % T::WTN], S());
-    });
-    if constexpr (kSpread) {   // keep that order through scheduling
-      constexpr int every = NT / T::LOADS * Elem<S>::MFMA_PER16;
-      if constexpr (T::READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
-      static_for<T::LOADS>([&](auto) {
-        __builtin_amdgcn_sched_group_barrier(0x008, every, 0);
-        __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+    for (int s = s_lo; s < s_hi; ++s) {
+      // this wave's loads of the step have landed when at most those of the
+      // STAGES - 2 steps after it remain; after the barrier every wave's have,
+      // and every wave is done with the stage the next loads overwrite
+      if (kStores > 0 && s == s_lo && t != t_first)
+        BDR_WAIT_VM_LGKM(kAhead + kStores, 0);
+      else
+        BDR_WAIT_VM_LGKM(kAhead, 0);
+      BDR_WG_BARRIER();
+      if constexpr (!kSpread) static_for<T::LOADS>([&](auto q) { dma_one(q); });
+      read_frags(buf, std::integral_constant<int, 0>{}, a, b);
+      static_for<NT>([&](auto ec) {
+        constexpr int e = decltype(ec)::value;
+        constexpr int every = kSpread ? NT / T::LOADS : NT;
+        acc[e / T::WTN][e % T::WTN] =
+            mma16(b[e % T::WTN], a[e / T::WTN], acc[e / T::WTN][e % T::WTN], S());
+        if constexpr (kSpread && e % every == every - 1 && e / every < T::LOADS)
+          dma_one(std::integral_constant<int, e / every>{});
       });
-      if constexpr (T::MFMAS - every * T::LOADS > 0)
-        __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS - every * T::LOADS, 0);
-      if constexpr (T::READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS, 0);
+      read_frags(buf, std::integral_constant<int, 1>{}, a, b);
+      static_for<NT>([&](auto ec) {
+        constexpr int e = decltype(ec)::value;
+        acc[e / T::WTN][e % T::WTN] =
+            mma16(b[e % T::WTN], a[e / T::WTN], acc[e / T::WTN][e % T::WTN], S());
+      });
+      if constexpr (kSpread) {   // keep that order through scheduling
+        constexpr int every = NT / T::LOADS * Elem<S>::MFMA_PER16;
+        if constexpr (T::READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
+        static_for<T::LOADS>([&](auto) {
+          __builtin_amdgcn_sched_group_barrier(0x008, every, 0);
+          __builtin_amdgcn_sched_group_barrier(0x020, 1, 0);
+        });
+        if constexpr (T::MFMAS - every * T::LOADS > 0)
+          __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS - every * T::LOADS, 0);
+        if constexpr (T::READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS, 0);
+      }
+      buf = buf + 1 == T::STAGES ? 0 : buf + 1;
+      dma_prep(buf == 0 ? T::STAGES - 1 : buf - 1);   // next into the stage of this step
     }
-    buf = buf + 1 == T::STAGES ? 0 : buf + 1;
-    dma_prep(buf == 0 ? T::STAGES - 1 : buf - 1);   // next into the stage of this step
-  }
 
-  int tm, tn;
-  tile_at(t, tm, tn);
-  const int64_t m0 = static_cast<int64_t>(tm) * T::BM;
-  const int64_t n0 = static_cast<int64_t>(tn) * T::BN;
-  // Lane holds C[m][n .. n + 3] of each of its tiles: rows r16, columns 4 grp ..
-  const int64_t mw = m0 + wm * 16 * T::WTM + r16;
-  const int64_t nw = n0 + wn * 16 * T::WTN + 4 * grp;
-  char* scratch = lds + (T::LOOP ? T::RING_BYTES : 0);
-  if constexpr (!T::LOOP && (EPI == LE_STATS || (T::STAGED && EPI != LE_PARTIAL))) {
-    BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads
-    BDR_WG_BARRIER();         // and every wave is done with the ring
-  }
-  // A wave's 16 output rows of one A tile through LDS, then 16 bytes per lane
-  // along the rows: whole pieces of OUT_ROW bytes instead of 32-byte ones
-  // (1.56 GB written and nothing else: 284 us against 433 us).  The largest
-  // tiles have no registers for it and few rows to write per product: directly.
-  char* mine = scratch + wave * 16 * T::OUT_ROW;
-  auto put_rows = [&](auto ic, auto&& value) {
-    if constexpr (!T::STAGED) {
-      const int64_t m = mw + decltype(ic)::value * 16;
-      static_for<T::WTN>([&](auto j) {
-        const int64_t n = nw + decltype(j)::value * 16;
-        if (m >= M) return;
-        if constexpr (EPI == LE_DLOGITS) {
-          if (n < g.ldo)
-            store4(static_cast<S*>(g.out) + n / T::KB * g.slab + m * T::KB + n % T::KB, value(j));
-        } else if (n < g.N) {
-          store4(static_cast<S*>(g.out) + m * g.ldo + n, value(j));
-        }
-      });
-      return;
+    int tm, tn;
+    tile_at(t, tm, tn);
+    const int64_t m0 = static_cast<int64_t>(tm) * T::BM;
+    const int64_t n0 = static_cast<int64_t>(tn) * T::BN;
+    // Lane holds C[m][n .. n + 3] of each of its tiles: rows r16, columns 4 grp ..
+    const int64_t mw = m0 + wm * 16 * T::WTM + r16;
+    const int64_t nw = n0 + wn * 16 * T::WTN + 4 * grp;
+    char* scratch = lds + (T::LOOP ? T::RING_BYTES : 0);
+    if constexpr (!T::LOOP && (EPI == LE_STATS || (T::STAGED && EPI != LE_PARTIAL))) {
+      BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads
+      BDR_WG_BARRIER();         // and every wave is done with the ring
     }
-    static_for<T::WTN>([&](auto j) {
-      store4(reinterpret_cast<S*>(mine + r16 * T::OUT_ROW) + decltype(j)::value * 16 + 4 * grp,
-             value(j));
-    });
-    BDR_WAIT_VM_LGKM(63, 0);
-    constexpr bool kOutPanels = EPI == LE_DLOGITS;
-    const int64_t left = min<int64_t>(T::BM, M - m0);
-    const rsrc_t out =
-        kOutPanels
-            ? make_rsrc(static_cast<S*>(g.out) + n0 / T::KB * g.slab + m0 * T::KB,
-                        static_cast<uint32_t>((T::BN / T::KB - 1) * g.slab * ES + left * 128))
-            : make_rsrc(static_cast<S*>(g.out) + m0 * g.ldo, static_cast<uint32_t>(left * g.ldo * ES));
-    const int64_t cols = (kOutPanels ? g.ldo : g.N) - (n0 + wn * 16 * T::WTN);   // may be <= 0
+    // A wave's 16 output rows of one A tile through LDS, then 16 bytes per lane
+    // along the rows: whole pieces of OUT_ROW bytes instead of 32-byte ones
+    // (1.56 GB written and nothing else: 284 us against 433 us).  The largest
+    // tiles have no registers for it and few rows to write per product: directly.
+    char* mine = scratch + wave * 16 * T::OUT_ROW;
+    auto put_rows = [&](auto ic, auto&& value) {
+      if constexpr (!T::STAGED) {
+        const int64_t m = mw + decltype(ic)::value * 16;
+        static_for<T::WTN>([&](auto j) {
+          const int64_t n = nw + decltype(j)::value * 16;
+          if (m >= M) return;
+          if constexpr (EPI == LE_DLOGITS) {
+            if (n < g.ldo)
+              store4(static_cast<S*>(g.out) + n / T::KB * g.slab + m * T::KB + n % T::KB, value(j));
+          } else if (n < g.N) {
+            store4(static_cast<S*>(g.out) + m * g.ldo + n, value(j));
+          }
+        });
+        return;
+      }
+      static_for<T::WTN>([&](auto j) {
+        store4(reinterpret_cast<S*>(mine + r16 * T::OUT_ROW) + decltype(j)::value * 16 + 4 * grp,
+               value(j));
+      });
+      BDR_WAIT_VM_LGKM(63, 0);
+      constexpr bool kOutPanels = EPI == LE_DLOGITS;
+      const int64_t left = min<int64_t>(T::BM, M - m0);
+      const rsrc_t out =
+          kOutPanels
+              ? make_rsrc(static_cast<S*>(g.out) + n0 / T::KB * g.slab + m0 * T::KB,
+                          static_cast<uint32_t>((T::BN / T::KB - 1) * g.slab * ES + left * 128))
+              : make_rsrc(static_cast<S*>(g.out) + m0 * g.ldo, static_cast<uint32_t>(left * g.ldo * ES));
+      const int64_t cols = (kOutPanels ? g.ldo : g.N) - (n0 + wn * 16 * T::WTN);   // may be <= 0
 #pragma unroll
-    for (int c0 = 0; c0 < 16 * T::OUT_ROW; c0 += 1024) {
-      const int c = c0 + lane * 16;
-      const int row = c / T::OUT_ROW;
-      const int in_row = c % T::OUT_ROW;
-      const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + (c < 16 * T::OUT_ROW ? c : 0));
-      const int m = (wm * T::WTM + decltype(ic)::value) * 16 + row;
-      const int nb = wn * T::OUT_ROW + in_row;   // byte of the tile's row
-      const uint32_t off =
-          kOutPanels ? static_cast<uint32_t>((nb / 128) * g.slab * ES + m * 128 + nb % 128)
-                     : static_cast<uint32_t>((m * g.ldo + n0) * ES + nb);
-      const bool ok = c < 16 * T::OUT_ROW && in_row < cols * ES && m < left;
-      bstore16(__builtin_bit_cast(f32x4_t, v), out, ok ? off : kOOB);
+      for (int c0 = 0; c0 < 16 * T::OUT_ROW; c0 += 1024) {
+        const int c = c0 + lane * 16;
+        const int row = c / T::OUT_ROW;
+        const int in_row = c % T::OUT_ROW;
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + (c < 16 * T::OUT_ROW ? c : 0));
+        const int m = (wm * T::WTM + decltype(ic)::value) * 16 + row;
+        const int nb = wn * T::OUT_ROW + in_row;   // byte of the tile's row
+        const uint32_t off =
+            kOutPanels ? static_cast<uint32_t>((nb / 128) * g.slab * ES + m * 128 + nb % 128)
+                       : static_cast<uint32_t>((m * g.ldo + n0) * ES + nb);
+        const bool ok = c < 16 * T::OUT_ROW && in_row < cols * ES && m < left;
+        bstore16(__builtin_bit_cast(f32x4_t, v), out, ok ? off : kOOB);
+      }
+      BDR_WAIT_VM_LGKM(63, 0);   // read before the next rows are written
+    };
+    if constexpr (EPI == LE_STATS) {
+      // maximum and sum of 2^(x scale2 - maximum) over the tile's columns: lanes,
+      // then the four lane groups, then the waves side by side through LDS
+      float2* part = reinterpret_cast<float2*>(scratch);   // [WN][BM]
+      static_for<T::WTM>([&](auto i) {
+        const int64_t m = mw + decltype(i)::value * 16;
+        const bool row_in = m < M;
+        const int64_t lab = g.label && row_in ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
+        float mx = -INFINITY;
+        static_for<T::WTN>([&](auto j) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int64_t n = nw + decltype(j)::value * 16 + c;
+            const float z = acc[i][j][c];
+            if (n == lab) g.picked[m] = z;
+            mx = fmaxf(mx, n < g.N ? z : -INFINITY);
+          }
+        });
+        mx = fmaxf(mx, __shfl_xor(mx, 16));
+        mx = fmaxf(mx, __shfl_xor(mx, 32));
+        mx *= g.scale2;   // positive
+        const float ref = mx == -INFINITY ? 0.f : mx;
+        float sum = 0.f;
+        static_for<T::WTN>([&](auto j) {
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -ref));
+            sum += nw + decltype(j)::value * 16 + c < g.N ? p : 0.f;
+          }
+        });
+        sum += __shfl_xor(sum, 16);
+        sum += __shfl_xor(sum, 32);
+        if (grp == 0)
+          part[wn * T::BM + wm * 16 * T::WTM + decltype(i)::value * 16 + r16] = float2{mx, sum};
+      });
+      BDR_WAIT_VM_LGKM(63, 0);
+      BDR_WG_BARRIER();   // (the next tile's is behind the barrier of its first step)
+      for (int r = static_cast<int>(threadIdx.x); r < T::BM; r += 64 * T::WAVES) {
+        if (m0 + r >= M) continue;
+        float2 v = part[r];
+#pragma unroll
+        for (int w = 1; w < T::WN; ++w) v = merge_stat(v, part[w * T::BM + r]);
+        g.stat[(m0 + r) * g.tiles_n + tn] = v;
+      }
+    } else if constexpr (EPI == LE_DLOGITS) {
+      // rounded to the storage type: the operand of two more matrix products,
+      // with as much relative error as their rounded results carry anyway.
+      // Columns from N to the padded width hold zeros.
+      static_for<T::WTM>([&](auto i) {
+        const int64_t m = min<int64_t>(mw + decltype(i)::value * 16, M - 1);
+        const int64_t lab = g.label ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
+        const float l2 = g.lse2[m], cf = g.coef[m];
+        put_rows(i, [&](auto j) {
+          const int64_t n = nw + decltype(j)::value * 16;
+          f32x4_t v;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -l2));
+            v[c] = n + c < g.N ? cf * (n + c == lab ? p - 1.f : p) : 0.f;
+          }
+          return v;
+        });
+      });
+    } else if constexpr (EPI == LE_PARTIAL) {
+      float* out = static_cast<float*>(g.out) + static_cast<int64_t>(split) * g.slab;
+      static_for<T::WTM>([&](auto i) {
+        const int64_t m = mw + decltype(i)::value * 16;
+        static_for<T::WTN>([&](auto j) {
+          const int64_t n = nw + decltype(j)::value * 16;
+          if (m < M && n < g.N) {
+            f32x4_t* p = reinterpret_cast<f32x4_t*>(out + m * g.ldo + n);
+            *p = g.accumulate ? *p + acc[i][j] : acc[i][j];
+          }
+        });
+      });
+    } else {
+      static_for<T::WTM>([&](auto i) { put_rows(i, [&](auto j) { return acc[i][j]; }); });
     }
-    BDR_WAIT_VM_LGKM(63, 0);   // read before the next rows are written
-  };
-  if constexpr (EPI == LE_STATS) {
-    // maximum and sum of 2^(x scale2 - maximum) over the tile's columns: lanes,
-    // then the four lane groups, then the waves side by side through LDS
-    float2* part = reinterpret_cast<float2*>(scratch);   // [WN][BM]
-    static_for<T::WTM>([&](auto i) {
-      const int64_t m = mw + decltype(i)::value * 16;
-      const bool row_in = m < M;
-      const int64_t lab = g.label && row_in ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
-      float mx = -INFINITY;
-      static_for<T::WTN>([&](auto j) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const int64_t n = nw + decltype(j)::value * 16 + c;
-          const float z = acc[i][j][c];
-          if (n == lab) g.picked[m] = z;
-          mx = fmaxf(mx, n < g.N ? z : -INFINITY);
-        }
-      });
-      mx = fmaxf(mx, __shfl_xor(mx, 16));
-      mx = fmaxf(mx, __shfl_xor(mx, 32));
-      mx *= g.scale2;   // positive
-      const float ref = mx == -INFINITY ? 0.f : mx;
-      float sum = 0.f;
-      static_for<T::WTN>([&](auto j) {
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -ref));
-          sum += nw + decltype(j)::value * 16 + c < g.N ? p : 0.f;
-        }
-      });
-      sum += __shfl_xor(sum, 16);
-      sum += __shfl_xor(sum, 32);
-      if (grp == 0)
-        part[wn * T::BM + wm * 16 * T::WTM + decltype(i)::value * 16 + r16] = float2{mx, sum};
-    });
-    BDR_WAIT_VM_LGKM(63, 0);
-    BDR_WG_BARRIER();   // (the next tile's is behind the barrier of its first step)
-    for (int r = static_cast<int>(threadIdx.x); r < T::BM; r += 64 * T::WAVES) {
-      if (m0 + r >= M) continue;
-      float2 v = part[r];
-#pragma unroll
-      for (int w = 1; w < T::WN; ++w) v = merge_stat(v, part[w * T::BM + r]);
-      g.stat[(m0 + r) * g.tiles_n + tn] = v;
-    }
-  } else if constexpr (EPI == LE_DLOGITS) {
-    // rounded to the storage type: the operand of two more matrix products,
-    // with as much relative error as their rounded results carry anyway.
-    // Columns from N to the padded width hold zeros.
-    static_for<T::WTM>([&](auto i) {
-      const int64_t m = min<int64_t>(mw + decltype(i)::value * 16, M - 1);
-      const int64_t lab = g.label ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
-      const float l2 = g.lse2[m], cf = g.coef[m];
-      put_rows(i, [&](auto j) {
-        const int64_t n = nw + decltype(j)::value * 16;
-        f32x4_t v;
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -l2));
-          v[c] = n + c < g.N ? cf * (n + c == lab ? p - 1.f : p) : 0.f;
-        }
-        return v;
-      });
-    });
-  } else if constexpr (EPI == LE_PARTIAL) {
-    float* out = static_cast<float*>(g.out) + static_cast<int64_t>(split) * g.slab;
-    static_for<T::WTM>([&](auto i) {
-      const int64_t m = mw + decltype(i)::value * 16;
-      static_for<T::WTN>([&](auto j) {
-        const int64_t n = nw + decltype(j)::value * 16;
-        if (m < M && n < g.N) {
-          f32x4_t* p = reinterpret_cast<f32x4_t*>(out + m * g.ldo + n);
-          *p = g.accumulate ? *p + acc[i][j] : acc[i][j];
-        }
-      });
-    });
-  } else {
-    static_for<T::WTM>([&](auto i) { put_rows(i, [&](auto j) { return acc[i][j]; }); });
-  }
   }
   BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads
 }

@@ -2,20 +2,22 @@
 // d weight = d logits^T hidden (and the Markov head's, as narrow as its rank).
 //
 // Measured (bf16, H = 5120; "library": its product of the same size, same run):
-//   d hidden, 4096 rows, 30720 entries: 256 x 320 918 us (1404 TFLOP/s; library
+//   d hidden, 4096 rows, 12 x 2560 entries: 256 x 320 918 us (1404 TFLOP/s; library
 //     1310 - 1460 us), 256 x 256 with 4 splits 1203 us, 128 x 128 2059 us
 //   d hidden, 151936 entries: 7 rows 64 x 320 225 us (6.9 TB/s; 258 us with temporal
 //     loads), 128 x 320 250 us; 64 rows 239 and 265 us; 128 rows 128 x 256 with
 //     three stages 267 us, 128 x 320 286 us (315 us temporal); 256 rows 256 x 320
 //     376 us, 128 x 320 512 us
 //   d embedding, rank 64: 128 rows, 151936 entries, 256 splits 15 us, 32 splits
-//     36 us; 4096 rows, 30720 entries, 16 splits 43 us, 64 splits 73 us
-//   d weight, 30720 entries: 4096 rows 256 x 320 1014 us (1270 TFLOP/s; library
-//     1206 - 1380 us), 128 x 320 1183 us; 2048 rows 569 and 611 us; 1024 rows 335
-//     and 308 us; 256 rows 189 and 113 us
-//   d weight, 151936 entries (1.56 GB written): 128 rows 128 x 320 379 us, one
+//     36 us; 4096 rows, 12 x 2560 entries, 16 splits 43 us, 64 splits 73 us
+//   d weight, 20 x 2560 entries: 4096 rows 256 x 320 1718 us (1250 TFLOP/s), 128 x 320
+//     2000 us; 2048 rows 902 and 1052 us; 30 x 2560 entries: 1280 rows 934 and 1010
+//     us, 1000 rows 794 and 815 us, 768 rows 657 and 646 us, 512 rows 512 and 473 us
+//     (H = 2560: 490 and 526, 420 and 435, 351 and 348, 268 and 255 us)
+//   d weight, 151936 entries (1.56 GB written): 128 rows 128 x 320 388 us, one
 //     tile per workgroup 504 us; 7 rows 269 - 306 us
-//   d w2, rank 64, 30720 entries, 3072 rows: 3 stages 32 us, 2 stages 39 us
+//   d w2, rank 64, 151936 entries: 4096 rows 231 us (5.4 TB/s of d logits; 2 stages
+//     231 us), 1000 rows 62 us (2 stages 65 us), 128 rows 15.7 us (14.8 us)
 
 #include "loss.h"
 
@@ -37,7 +39,7 @@ using WeightFew = LossTile<uint16_t, true, true, 2, 4, 4, 5, 2, true>;   // 128 
 using WeightMany = LossTile<uint16_t, true, true, 2, 4, 8, 5, 2>;        // 256 x 320
 
 constexpr int64_t kNarrowCols = 128;   // outputs this narrow take the narrow tiles
-constexpr int64_t kManyRows = 1536;    // between the rows measured above
+constexpr int64_t kManyRows = 896;     // between the rows measured above
 
 // `small`: a product of a few billion operations at most, where the launches
 // count: narrow tiles, so that both gradients of a kind go into one launch.

@@ -12,7 +12,7 @@
 //     rows 128  128 x 320 298 us (317 us temporal), 64 x 320 438 us
 //     rows 256  256 x 320 395 us, 128 x 320 552 us (non-temporal 598 us), 64 x 320
 //               952 us, 32 x 128 1795 us
-//     rows 4096, 30720 entries: 256 x 320 1010 us (1270 TFLOP/s; the library's
+//     rows 4096, 12 x 2560 entries: 256 x 320 1010 us (1270 TFLOP/s; the library's
 //               product 990 us in the same run), 256 x 256 and 128 x 128 9 % and
 //               75 % slower
 //   H = 1024, V = 16384, rows 64: 32 x 128 13.7 us, 64 x 320 20.1 us

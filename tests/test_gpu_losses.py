@@ -509,6 +509,50 @@ def test_refusals():
         m.dspark_distill_loss(x, w, lab[:, None].contiguous(), lse[:, None].contiguous(), temperature=0.0)
 
 
+@pytest.mark.parametrize("dtype,top", [("f32", 0), ("bf16", 0), ("f32", 3), ("bf16", 3)])
+def test_many_rows(dtype, top):
+    """Rows counted block by block before the compaction (the last block ends inside), and a
+    previous token that first appears thousands of rows in."""
+    c = _case(60 + top, 9001, 8, 130, 8, dtype, top=top)
+    c["prev"][c["prev"] == 77] = 0
+    for n, tok in ((7000, 77), (8990, 77)):
+        c["prev"][n] = tok
+        if top:
+            c["ids"][n, 0], c["u"][n, 0] = 5, 0.5
+        else:
+            c["labels"][n] = 5
+    _check(c, 1.5 if top else 1.0)
+
+
+def test_small_temperature_keeps_close_teacher_logits_apart():
+    """hidden = 0 and W = 1 on the diagonal: d hidden is d logits itself, g T (1 / V - t).  The
+    teacher's logits differ by a few steps of fp32, which T = 1e-4 makes differences of up to
+    19 in the exponent.
+
+    t: the division's rounding and that of the sum add at most u (2 d / T + top) and the
+    exponential a few u; the other factors a few u each: 64 u (1 + max d / T) covers them
+    (u top = 40 u).  The product only adds zeros."""
+    m = bdr()
+    V = H = 128
+    N, top, temp = 33, 40, float(np.float32(1e-4))
+    gn = np.random.default_rng(8)
+    step = gn.integers(0, 2001, (N, top))
+    u = (8.0 + step * 2.0 ** -20).astype(np.float32)
+    ids = np.stack([gn.permutation(V)[:top] for _ in range(N)]).astype(np.int32)
+    gr = (gn.random(N) + 0.5).astype(np.float32)
+    x = torch.zeros((N, H), dtype=torch.float32, device="cuda")
+    w = torch.eye(V, dtype=torch.float32, device="cuda")
+    _, lse, picked = m.dspark_distill_loss(x, w, dev(ids), dev(u), temperature=temp)
+    got = _np(m.dspark_distill_backward(x, w, dev(ids), dev(u), lse, picked, dev(gr), temperature=temp,
+                                        grads=("hidden",))["hidden"])
+    t = T.teacher_targets(ids, u, V, temp)
+    target = np.zeros((N, V))
+    np.put_along_axis(target, ids.astype(np.int64), t, axis=1)
+    scale = gr.astype(np.float64)[:, None] * temp
+    big = 64 * U * (1 + 2000 * 2.0 ** -20 / temp)
+    _within("d hidden", got, scale * (1 / V - target), scale * big * (1 / V + target) + TINY)
+
+
 def test_training_step_of_the_readout():
     """norm -> cross entropy -> backward through both, as a drafter trains them, against
     differences of the summed loss along random directions (fp32).
