@@ -91,7 +91,10 @@ struct LossTile {
   // scratch of the epilogues: row statistics, or a wave's 16 output rows.  A
   // workgroup with more tiles to come keeps it beside the ring.
   static constexpr int OUT_ROW = 16 * WTN * static_cast<int>(sizeof(S));
-  static constexpr int SCRATCH = std::max(WN * BM * 8, WAVES * 16 * OUT_ROW);
+  // 16 bytes between the rows: the 16 rows a store instruction reaches then start in
+  // 16 different groups of four banks (an odd multiple of 16 bytes, over 256)
+  static constexpr int OUT_PITCH = OUT_ROW + 16;
+  static constexpr int SCRATCH = std::max(WN * BM * 8, WAVES * 16 * OUT_PITCH);
   static constexpr int LDS_BYTES = LOOP ? RING_BYTES + SCRATCH : std::max(RING_BYTES, SCRATCH);
   static constexpr int PER_CU = 160 * 1024 / LDS_BYTES;   // workgroups a compute unit holds
   static constexpr int LOADS_A = BM / 8 / WAVES, LOADS_B = BN / 8 / WAVES;
@@ -527,7 +530,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
     // along the rows: whole pieces of OUT_ROW bytes instead of 32-byte ones
     // (1.56 GB written and nothing else: 284 us against 433 us).  The largest
     // tiles have no registers for it and few rows to write per product: directly.
-    char* mine = scratch + wave * 16 * T::OUT_ROW;
+    char* mine = scratch + wave * 16 * T::OUT_PITCH;
     auto put_rows = [&](auto ic, auto&& value) {
       if constexpr (!T::STAGED) {
         const int64_t m = mw + decltype(ic)::value * 16;
@@ -544,7 +547,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         return;
       }
       static_for<T::WTN>([&](auto j) {
-        store4(reinterpret_cast<S*>(mine + r16 * T::OUT_ROW) + decltype(j)::value * 16 + 4 * grp,
+        store4(reinterpret_cast<S*>(mine + r16 * T::OUT_PITCH) + decltype(j)::value * 16 + 4 * grp,
                value(j));
       });
       BDR_WAIT_VM_LGKM(63, 0);
@@ -561,7 +564,8 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         const int c = c0 + lane * 16;
         const int row = c / T::OUT_ROW;
         const int in_row = c % T::OUT_ROW;
-        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(mine + (c < 16 * T::OUT_ROW ? c : 0));
+        const u32x4_t v = *reinterpret_cast<const u32x4_t*>(
+            mine + (c < 16 * T::OUT_ROW ? row * T::OUT_PITCH + in_row : 0));
         const int m = (wm * T::WTM + decltype(ic)::value) * 16 + row;
         const int nb = wn * T::OUT_ROW + in_row;   // byte of the tile's row
         const uint32_t off =
