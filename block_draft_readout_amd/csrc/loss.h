@@ -24,8 +24,12 @@ int64_t loss_tiles(int64_t rows, int64_t cols) {
   return (rows + T::BM - 1) / T::BM * ((cols + T::BN - 1) / T::BN);
 }
 
+// Weights larger than the last-level cache (256 MiB) stay in HBM between the products
+// that read them: bytes of `n` bf16 entries above that.
+inline bool beyond_cache(int64_t n) { return n * 2 > (int64_t(256) << 20); }
+
 // vocabulary columns of one statistics tile
-int loss_stats_cols(bdr_dtype dt, int64_t rows, int64_t cols);
+int loss_stats_cols(bdr_dtype dt, int64_t rows, int64_t cols, int64_t hidden);
 // reduction splits of a d hidden product over `width` vocabulary entries
 int loss_dfeat_splits(bdr_dtype dt, int64_t rows, bool small, int64_t cols, int64_t width);
 

@@ -464,7 +464,7 @@ struct LossPlan {
 LossPlan plan_loss(const LossProblem& p) {
   LossPlan q{};
   const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
-  const int cols = loss_stats_cols(p.dt, p.rows, p.vocab);
+  const int cols = loss_stats_cols(p.dt, p.rows, p.vocab, p.hidden);
   q.stat_tiles = static_cast<int>((p.vocab + cols - 1) / cols);
   // whole vocabulary where its d logits fit, else equal pieces
   int64_t most = kPieceBytes / (p.rows * es) / kPieceCols * kPieceCols;

@@ -75,19 +75,25 @@ struct LossGemm {
 };
 
 template <typename S_, bool AKS_, bool BKS_, int WM_, int WN_, int WTM_, int WTN_, int STAGES_,
-          bool LOOP_ = false, bool NT_B_ = false>
+          bool LOOP_ = false, bool NT_B_ = false, int STAGES_A_ = STAGES_>
 struct LossTile {
   using S = S_;
   static constexpr bool AKS = AKS_, BKS = BKS_;   // reduction slow
   static constexpr int WM = WM_, WN = WN_, WTM = WTM_, WTN = WTN_, STAGES = STAGES_;
   static constexpr bool LOOP = LOOP_;             // a workgroup walks several tiles
   static constexpr bool NT_B = NT_B_;             // B is streamed once: non-temporal loads
+  static constexpr int STAGES_A = STAGES_A_;      // stages of A where it has fewer (it comes from L2)
   static constexpr int WAVES = WM * WN;
   static constexpr int BM = 16 * WM * WTM, BN = 16 * WN * WTN;
   static constexpr int KB = 128 / static_cast<int>(sizeof(S));
-  static constexpr int A_BYTES = BM * 128, STAGE_BYTES = (BM + BN) * 128;
+  static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
   static constexpr bool STAGED = WTM * WTN <= 32;
-  static constexpr int RING_BYTES = STAGES * STAGE_BYTES;
+  static constexpr int RING_BYTES = STAGES_A * A_BYTES + STAGES * B_BYTES;
+  // a stage's A and B lie side by side, or in rings of their own
+  static constexpr int LAG = STAGES - STAGES_A;   // steps by which A's loads trail B's
+  static constexpr int A_STEP = LAG ? A_BYTES : A_BYTES + B_BYTES;
+  static constexpr int B_STEP = LAG ? B_BYTES : A_BYTES + B_BYTES;
+  static constexpr int B_BASE = LAG ? STAGES_A * A_BYTES : A_BYTES;
   // scratch of the epilogues: row statistics, or a wave's 16 output rows.  A
   // workgroup with more tiles to come keeps it beside the ring.
   static constexpr int OUT_ROW = 16 * WTN * static_cast<int>(sizeof(S));
@@ -97,6 +103,10 @@ struct LossTile {
   static constexpr int SCRATCH = std::max(WN * BM * 8, WAVES * 16 * OUT_PITCH);
   static constexpr int LDS_BYTES = LOOP ? RING_BYTES + SCRATCH : std::max(RING_BYTES, SCRATCH);
   static constexpr int PER_CU = 160 * 1024 / LDS_BYTES;   // workgroups a compute unit holds
+  // waves of a SIMD to leave registers for: the workgroups LDS has room for, up to two
+  // waves (without it 128 x 128 d logits took 268 registers, so one workgroup of two
+  // ran: 4258 us instead of 2260, 4096 rows of 5120, 20 x 2560 entries)
+  static constexpr int SIMD_WAVES = std::max(1, std::min(2, PER_CU * WAVES / 4));
   static constexpr int LOADS_A = BM / 8 / WAVES, LOADS_B = BN / 8 / WAVES;
   static constexpr int LOADS = LOADS_A + LOADS_B;
   // LDS reads the compiler schedules, per half step (the transposing ones are its own block)
@@ -105,6 +115,7 @@ struct LossTile {
   static constexpr int MFMAS = WTM * WTN * Elem<S>::MFMA_PER16;   // per half step
   static_assert(BM % (8 * WAVES) == 0 && BN % (8 * WAVES) == 0, "loads split evenly over the waves");
   static_assert((!AKS || BM % 64 == 0) && (!BKS || BN % 64 == 0), "slow rows are multiples of 128 bytes");
+  static_assert(LAG == 0 || (STAGES_A == 2 && !LOOP), "A in two stages, B in more");
   static_assert(PER_CU >= 1, "tile fits");
 };
 
@@ -322,44 +333,62 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   };
   ld_tile();
   rsrc_t ra, rb;
-  uint32_t ld_a = 0, ld_b = 0, cut = 0;   // cut: kOOB in the lanes past a fast-k tail
+  uint32_t ld_a = 0, ld_b = 0;
+  uint32_t cut_a = 0, cut_b = 0;          // kOOB in the lanes past a fast-k tail
   uint32_t ld_rows = 0;                   // slow panels: k rows of the step
-  char* ld_dst = lds;
-  auto dma_prep = [&](int buf) {
-    const bool second = kTwo && ld_s >= steps0;
-    const LossSeg& sg = second ? g.seg[1] : g.seg[0];
-    const int64_t kk = static_cast<int64_t>(second ? ld_s - steps0 : ld_s) * T::KB;
-    const int64_t krem = (second ? sg.k : k0) - kk;
-    const bool in = krem > 0 && ld_s < s_data && (!T::LOOP || ld_t < t_end);
-    ld_a = static_cast<uint32_t>(sg.lda);
-    ld_b = static_cast<uint32_t>(sg.ldb);
-    cut = static_cast<int64_t>(lchunk) * Elem<S>::PER16 < krem ? 0u : kOOB;
-    const int64_t krows = min<int64_t>(T::KB, krem);
-    const char* pa = static_cast<const char*>(sg.a);
-    const char* pb = static_cast<const char*>(sg.b);
+  char *dst_a = lds, *dst_b = lds;
+  // Step `s` of the reduction: its segment, its first k there and how many are left
+  // (none past the end).
+  auto at_step = [&](int s, const LossSeg*& sg, int64_t& kk, int64_t& krem) {
+    const bool second = kTwo && s >= steps0;
+    sg = second ? &g.seg[1] : &g.seg[0];
+    kk = static_cast<int64_t>(second ? s - steps0 : s) * T::KB;
+    krem = (second ? sg->k : k0) - kk;
+    if (s >= s_data || (T::LOOP && ld_t >= t_end)) krem = 0;
+  };
+  // descriptors of B's step ld_s into stage buf_b and A's LAG steps before it into buf_a
+  auto dma_prep = [&](int buf_a, int buf_b) {
+    const LossSeg *sb, *sa;
+    int64_t kb, kb_rem, ka, ka_rem;
+    at_step(ld_s, sb, kb, kb_rem);
+    if constexpr (T::LAG > 0) {
+      at_step(ld_s - T::LAG, sa, ka, ka_rem);
+    } else {
+      sa = sb;
+      ka = kb;
+      ka_rem = kb_rem;
+    }
+    ld_a = static_cast<uint32_t>(sa->lda);
+    ld_b = static_cast<uint32_t>(sb->ldb);
+    cut_a = static_cast<int64_t>(lchunk) * Elem<S>::PER16 < ka_rem ? 0u : kOOB;
+    cut_b = static_cast<int64_t>(lchunk) * Elem<S>::PER16 < kb_rem ? 0u : kOOB;
+    const int64_t krows = min<int64_t>(T::KB, kb_rem);
+    const char* pa = static_cast<const char*>(sa->a);
+    const char* pb = static_cast<const char*>(sb->b);
     uint32_t na, nb;
     if constexpr (T::AKS) {
       const int64_t left = min<int64_t>(T::BM / T::KB, (M + T::KB - 1) / T::KB - ld_m0 / T::KB);
-      pa += (ld_m0 / T::KB * sg.lda + kk * T::KB) * ES;
-      na = static_cast<uint32_t>((left * sg.lda - kk * T::KB) * ES);
-      ld_rows = static_cast<uint32_t>(krows);
+      pa += (ld_m0 / T::KB * sa->lda + ka * T::KB) * ES;
+      na = static_cast<uint32_t>((left * sa->lda - ka * T::KB) * ES);
+      ld_rows = static_cast<uint32_t>(min<int64_t>(T::KB, ka_rem));
     } else if constexpr (kPanels) {
-      pa += (kk / T::KB * sg.lda + ld_m0 * T::KB) * ES;
+      pa += (ka / T::KB * sa->lda + ld_m0 * T::KB) * ES;
       na = static_cast<uint32_t>(min<int64_t>(T::BM, M - ld_m0) * 128);
     } else {
-      pa += (ld_m0 * sg.lda + kk) * ES;
-      na = static_cast<uint32_t>((min<int64_t>(T::BM, M - ld_m0) * sg.lda - kk) * ES);
+      pa += (ld_m0 * sa->lda + ka) * ES;
+      na = static_cast<uint32_t>((min<int64_t>(T::BM, M - ld_m0) * sa->lda - ka) * ES);
     }
     if constexpr (T::BKS) {
-      pb += (kk * sg.ldb + ld_n0) * ES;
-      nb = static_cast<uint32_t>((krows * sg.ldb - ld_n0) * ES);
+      pb += (kb * sb->ldb + ld_n0) * ES;
+      nb = static_cast<uint32_t>((krows * sb->ldb - ld_n0) * ES);
     } else {
-      pb += (ld_n0 * sg.ldb + kk) * ES;
-      nb = static_cast<uint32_t>((min<int64_t>(T::BN, g.N - ld_n0) * sg.ldb - kk) * ES);
+      pb += (ld_n0 * sb->ldb + kb) * ES;
+      nb = static_cast<uint32_t>((min<int64_t>(T::BN, g.N - ld_n0) * sb->ldb - kb) * ES);
     }
-    ra = make_rsrc(pa, in ? na : 0u);
-    rb = make_rsrc(pb, in ? nb : 0u);
-    ld_dst = lds + buf * T::STAGE_BYTES;
+    ra = make_rsrc(pa, ka_rem > 0 ? na : 0u);
+    rb = make_rsrc(pb, kb_rem > 0 ? nb : 0u);
+    dst_a = lds + buf_a * T::A_STEP;
+    dst_b = lds + T::B_BASE + buf_b * T::B_STEP;
     ++ld_s;
     if constexpr (T::LOOP) {
       if (ld_s == s_hi) {
@@ -378,13 +407,13 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       else if constexpr (kPanels)
         off = off_a[q];   // a panel's columns past the reduction's end are zeros
       else
-        off = lane_off(ASlow{}, ARow{}, APanels{}, q, ld_a) | cut;
-      load_lds16<0>(ra, off, ld_dst + (wave + T::WAVES * q) * 1024);
+        off = lane_off(ASlow{}, ARow{}, APanels{}, q, ld_a) | cut_a;
+      load_lds16<0>(ra, off, dst_a + (wave + T::WAVES * q) * 1024);
     } else {
       constexpr int p = q - T::LOADS_A;
       const uint32_t off =
-          T::BKS ? off_b[p] : lane_off(BSlow{}, BRow{}, std::false_type{}, p, ld_b) | cut;
-      load_lds16<T::NT_B ? 2 : 0>(rb, off, ld_dst + T::A_BYTES + (wave + T::WAVES * p) * 1024);
+          T::BKS ? off_b[p] : lane_off(BSlow{}, BRow{}, std::false_type{}, p, ld_b) | cut_b;
+      load_lds16<T::NT_B ? 2 : 0>(rb, off, dst_b + (wave + T::WAVES * p) * 1024);
     }
   };
 
@@ -419,32 +448,32 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
     static_for<T::WTM>([&](auto i) { at_a[i] = slow_at(ARow{}, 0, wm * T::WTM + decltype(i)::value); });
   if constexpr (ES == 2 && T::BKS)
     static_for<T::WTN>([&](auto j) {
-      at_b[j] = slow_at(BRow{}, T::A_BYTES, wn * T::WTN + decltype(j)::value);
+      at_b[j] = slow_at(BRow{}, T::B_BASE, wn * T::WTN + decltype(j)::value);
     });
-  auto read_frags = [&](int buf, auto halfc, FragA& a, FragB& b) {
+  auto read_frags = [&](int buf_a, int buf_b, auto halfc, FragA& a, FragB& b) {
     constexpr int half = decltype(halfc)::value;
-    const char* base = lds + buf * T::STAGE_BYTES;
-    const uint32_t stage = static_cast<uint32_t>(buf * T::STAGE_BYTES);
+    const uint32_t stage_a = static_cast<uint32_t>(buf_a * T::A_STEP);
+    const uint32_t stage_b = static_cast<uint32_t>(buf_b * T::B_STEP);
     constexpr bool tr_a = ES == 2 && T::AKS, tr_b = ES == 2 && T::BKS;
     if constexpr (!tr_a)
       static_for<T::WTM>([&](auto i) {
-        a[i] = read_op(ASlow{}, ARow{}, base, wm * T::WTM + decltype(i)::value, half);
+        a[i] = read_op(ASlow{}, ARow{}, lds + stage_a, wm * T::WTM + decltype(i)::value, half);
       });
     if constexpr (!tr_b)
       static_for<T::WTN>([&](auto j) {
-        b[j] = read_op(BSlow{}, BRow{}, base + T::A_BYTES, wn * T::WTN + decltype(j)::value, half);
+        b[j] = read_op(BSlow{}, BRow{}, lds + T::B_BASE + stage_b, wn * T::WTN + decltype(j)::value, half);
       });
     if constexpr (tr_a && tr_b) {
       uint32_t ad[T::WTM + T::WTN];
       u32x4_t f[T::WTM + T::WTN];
-      static_for<T::WTM>([&](auto i) { ad[i] = at_a[i] + stage; });
-      static_for<T::WTN>([&](auto j) { ad[T::WTM + j] = at_b[j] + stage; });
+      static_for<T::WTM>([&](auto i) { ad[i] = at_a[i] + stage_a; });
+      static_for<T::WTN>([&](auto j) { ad[T::WTM + j] = at_b[j] + stage_b; });
       lds_read_tr<T::WTM, T::BM * 2, T::WTN, T::BN * 2, 32 * half>(ad, f);
       static_for<T::WTM>([&](auto i) { a[i] = f[i]; });
       static_for<T::WTN>([&](auto j) { b[j] = f[T::WTM + j]; });
     } else if constexpr (tr_b) {
       uint32_t ad[T::WTN];
-      static_for<T::WTN>([&](auto j) { ad[j] = at_b[j] + stage; });
+      static_for<T::WTN>([&](auto j) { ad[j] = at_b[j] + stage_b; });
       lds_read_tr<T::WTN, T::BN * 2, 0, 0, 32 * half>(ad, b);
     }
   };
@@ -453,13 +482,18 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   // and the MFMAs; the loads of step s + STAGES - 1 are spread over the first
   // half's MFMAs (all before them where there are fewer MFMAs than loads).
   static_for<T::STAGES - 1>([&](auto c) {
-    dma_prep(decltype(c)::value);
-    static_for<T::LOADS>([&](auto q) { dma_one(q); });
+    constexpr int step_a = decltype(c)::value - T::LAG;   // A's: nothing before its first
+    dma_prep(step_a < 0 ? 0 : step_a, decltype(c)::value);
+    static_for<T::LOADS>([&](auto q) {
+      if constexpr (decltype(q)::value >= T::LOADS_A || step_a >= 0) dma_one(q);
+    });
   });
-  dma_prep(T::STAGES - 1);
+  dma_prep(T::STAGES_A - 1, T::STAGES - 1);
   constexpr int NT = T::WTM * T::WTN;
   constexpr bool kSpread = NT >= T::LOADS;
-  constexpr int kAhead = (T::STAGES - 2) * T::LOADS;
+  // loads younger than a step's own when it begins: those of the STAGES - 2 steps after
+  // it; with LAG B's of the step before, which that step issued after this step's A
+  constexpr int kAhead = T::LAG ? T::LOADS_B : (T::STAGES - 2) * T::LOADS;
   // stores of an epilogue that are younger than the loads the next tile's first
   // step waits for (memory operations complete in order)
   constexpr int kStores = T::LOOP && (EPI == LE_DLOGITS || EPI == LE_OUT)
@@ -468,7 +502,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   static_assert(kAhead + kStores < 64, "waits can count these");
   FragA a;
   FragB b;
-  int buf = 0;
+  int buf = 0, buf_a = 0;   // stages of B and A
   for (int t = t_first; t < t_end; t += wgs) {
     static_for<T::WTM>([&](auto i) {
       static_for<T::WTN>([&](auto j) { acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
@@ -483,7 +517,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         BDR_WAIT_VM_LGKM(kAhead, 0);
       BDR_WG_BARRIER();
       if constexpr (!kSpread) static_for<T::LOADS>([&](auto q) { dma_one(q); });
-      read_frags(buf, std::integral_constant<int, 0>{}, a, b);
+      read_frags(buf_a, buf, std::integral_constant<int, 0>{}, a, b);
       static_for<NT>([&](auto ec) {
         constexpr int e = decltype(ec)::value;
         constexpr int every = kSpread ? NT / T::LOADS : NT;
@@ -492,7 +526,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         if constexpr (kSpread && e % every == every - 1 && e / every < T::LOADS)
           dma_one(std::integral_constant<int, e / every>{});
       });
-      read_frags(buf, std::integral_constant<int, 1>{}, a, b);
+      read_frags(buf_a, buf, std::integral_constant<int, 1>{}, a, b);
       static_for<NT>([&](auto ec) {
         constexpr int e = decltype(ec)::value;
         acc[e / T::WTN][e % T::WTN] =
@@ -511,7 +545,10 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS, 0);
       }
       buf = buf + 1 == T::STAGES ? 0 : buf + 1;
-      dma_prep(buf == 0 ? T::STAGES - 1 : buf - 1);   // next into the stage of this step
+      if constexpr (T::LAG > 0) buf_a ^= 1; else buf_a = buf;
+      // next into the stages of this step
+      dma_prep(T::LAG ? buf_a ^ 1 : (buf == 0 ? T::STAGES - 1 : buf - 1),
+               buf == 0 ? T::STAGES - 1 : buf - 1);
     }
 
     int tm, tn;
@@ -521,6 +558,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
     // Lane holds C[m][n .. n + 3] of each of its tiles: rows r16, columns 4 grp ..
     const int64_t mw = m0 + wm * 16 * T::WTM + r16;
     const int64_t nw = n0 + wn * 16 * T::WTN + 4 * grp;
+    const int n_in = static_cast<int>(g.N - nw);   // columns from this lane's first; may be <= 0
     char* scratch = lds + (T::LOOP ? T::RING_BYTES : 0);
     if constexpr (!T::LOOP && (EPI == LE_STATS || (T::STAGED && EPI != LE_PARTIAL))) {
       BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads
@@ -580,18 +618,21 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       // maximum and sum of 2^(x scale2 - maximum) over the tile's columns: lanes,
       // then the four lane groups, then the waves side by side through LDS
       float2* part = reinterpret_cast<float2*>(scratch);   // [WN][BM]
+      int lab[T::WTM];   // column of the label, from this lane's first
       static_for<T::WTM>([&](auto i) {
         const int64_t m = mw + decltype(i)::value * 16;
-        const bool row_in = m < M;
-        const int64_t lab = g.label && row_in ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
+        lab[i] = g.label && m < M ? g.label[m] - g.label0 - static_cast<int>(nw) : -1;
+      });
+      static_for<T::WTM>([&](auto i) {
+        const int64_t m = mw + decltype(i)::value * 16;
         float mx = -INFINITY;
         static_for<T::WTN>([&](auto j) {
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const int64_t n = nw + decltype(j)::value * 16 + c;
+            const int n = decltype(j)::value * 16 + c;
             const float z = acc[i][j][c];
-            if (n == lab) g.picked[m] = z;
-            mx = fmaxf(mx, n < g.N ? z : -INFINITY);
+            if (n == lab[i]) g.picked[m] = z;
+            mx = fmaxf(mx, n < n_in ? z : -INFINITY);
           }
         });
         mx = fmaxf(mx, __shfl_xor(mx, 16));
@@ -603,7 +644,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -ref));
-            sum += nw + decltype(j)::value * 16 + c < g.N ? p : 0.f;
+            sum += decltype(j)::value * 16 + c < n_in ? p : 0.f;
           }
         });
         sum += __shfl_xor(sum, 16);
@@ -624,17 +665,22 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       // rounded to the storage type: the operand of two more matrix products,
       // with as much relative error as their rounded results carry anyway.
       // Columns from N to the padded width hold zeros.
-      static_for<T::WTM>([&](auto i) {
+      float l2[T::WTM], cf[T::WTM];
+      int lab[T::WTM];   // column of the label, from this lane's first
+      static_for<T::WTM>([&](auto i) {   // all before the stores' waits
         const int64_t m = min<int64_t>(mw + decltype(i)::value * 16, M - 1);
-        const int64_t lab = g.label ? static_cast<int64_t>(g.label[m]) - g.label0 : -1;
-        const float l2 = g.lse2[m], cf = g.coef[m];
+        lab[i] = g.label ? g.label[m] - g.label0 - static_cast<int>(nw) : -1;
+        l2[i] = g.lse2[m];
+        cf[i] = g.coef[m];
+      });
+      static_for<T::WTM>([&](auto i) {
         put_rows(i, [&](auto j) {
-          const int64_t n = nw + decltype(j)::value * 16;
           f32x4_t v;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
-            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -l2));
-            v[c] = n + c < g.N ? cf * (n + c == lab ? p - 1.f : p) : 0.f;
+            const int n = decltype(j)::value * 16 + c;
+            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -l2[i]));
+            v[c] = n < n_in ? cf[i] * (n == lab[i] ? p - 1.f : p) : 0.f;
           }
           return v;
         });
@@ -659,13 +705,13 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
 }
 
 template <typename T, int EPI>
-__global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_kernel(const LossGemm g) {
+__global__ __launch_bounds__(64 * T::WAVES, T::SIMD_WAVES) void loss_gemm_kernel(const LossGemm g) {
   loss_gemm_body<T, EPI>(g, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x));
 }
 
 // Two products in one launch, the second one's workgroups after the first's.
 template <typename T, int EPI>
-__global__ __launch_bounds__(64 * T::WAVES) void loss_gemm_pair_kernel(const LossGemm g0,
+__global__ __launch_bounds__(64 * T::WAVES, T::SIMD_WAVES) void loss_gemm_pair_kernel(const LossGemm g0,
                                                                        const LossGemm g1,
                                                                        int blocks0) {
   const int b = static_cast<int>(blockIdx.x);

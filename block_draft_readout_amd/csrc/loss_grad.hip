@@ -5,9 +5,11 @@
 //   d hidden, 4096 rows, 12 x 2560 entries: 256 x 320 918 us (1404 TFLOP/s; library
 //     1310 - 1460 us), 256 x 256 with 4 splits 1203 us, 128 x 128 2059 us
 //   d hidden, 151936 entries: 7 rows 64 x 320 225 us (6.9 TB/s; 258 us with temporal
-//     loads), 128 x 320 250 us; 64 rows 239 and 265 us; 128 rows 128 x 256 with
-//     three stages 267 us, 128 x 320 286 us (315 us temporal); 256 rows 256 x 320
-//     376 us, 128 x 320 512 us
+//     loads), 128 x 320 250 us; 64 rows 239 and 265 us; 128 rows 128 x 256 with three
+//     stages 266 us, 128 x 320 260 us with three of the weight's and 286 us with two;
+//     256 rows 256 x 320 376 us, 128 x 320 512 us
+//   d hidden, H = 2560, 26455 entries (in the last-level cache), 128 rows: 128 x 256
+//     34 us (39 us non-temporal); H = 1024, 32000 entries: 24 us, 128 x 320 26 us
 //   d embedding, rank 64: 128 rows, 151936 entries, 256 splits 15 us, 32 splits
 //     36 us; 4096 rows, 12 x 2560 entries, 16 splits 43 us, 64 splits 73 us
 //   d weight, 20 x 2560 entries: 4096 rows 256 x 320 1718 us (1250 TFLOP/s), 128 x 320
@@ -27,9 +29,11 @@ namespace {
 
 using FeatF32 = LossTile<float, false, true, 2, 2, 2, 2, 2>;         // 64 x 64
 using FeatNarrow = LossTile<uint16_t, false, true, 2, 2, 4, 2, 3>;   // 128 x 64
-using FeatFew = LossTile<uint16_t, false, true, 2, 4, 2, 5, 3, false, true>;    // 64 x 320
-using FeatSome = LossTile<uint16_t, false, true, 2, 4, 4, 4, 3, false, true>;   // 128 x 256
-using FeatMany = LossTile<uint16_t, false, true, 2, 4, 8, 5, 2>;                // 256 x 320
+using FeatFew = LossTile<uint16_t, false, true, 2, 4, 2, 5, 3>;      // 64 x 320
+using FeatFewOnce = LossTile<uint16_t, false, true, 2, 4, 2, 5, 3, false, true>;
+using FeatSome = LossTile<uint16_t, false, true, 2, 4, 4, 4, 3>;     // 128 x 256
+using FeatSomeOnce = LossTile<uint16_t, false, true, 2, 4, 4, 4, 3, false, true>;
+using FeatMany = LossTile<uint16_t, false, true, 2, 4, 8, 5, 2>;     // 256 x 320
 
 using WeightF32 = LossTile<float, true, true, 2, 2, 2, 2, 2>;        // 64 x 64
 using WeightNarrow = LossTile<uint16_t, true, true, 2, 2, 4, 2, 3>;  // 128 x 64
@@ -44,11 +48,13 @@ constexpr int64_t kManyRows = 896;     // between the rows measured above
 // `small`: a product of a few billion operations at most, where the launches
 // count: narrow tiles, so that both gradients of a kind go into one launch.
 template <typename F>
-auto with_feat_tile(bdr_dtype dt, int64_t rows, bool small, int64_t cols, F&& f) {
+auto with_feat_tile(bdr_dtype dt, int64_t rows, bool small, int64_t cols, int64_t width, F&& f) {
   if (dt != BDR_BF16) return f(FeatF32{});
   if (small || cols <= kNarrowCols) return f(FeatNarrow{});
-  if (rows <= FeatFew::BM) return f(FeatFew{});
-  if (rows <= FeatSome::BM) return f(FeatSome{});
+  // one row of tiles reads the weight once: non-temporal where no cache would keep it
+  const bool once = beyond_cache(cols * width);
+  if (rows <= FeatFew::BM) return once ? f(FeatFewOnce{}) : f(FeatFew{});
+  if (rows <= FeatSome::BM) return once ? f(FeatSomeOnce{}) : f(FeatSome{});
   return f(FeatMany{});
 }
 
@@ -66,7 +72,7 @@ auto with_weight_tile(bdr_dtype dt, int64_t rows, bool small, const LossGemm& g,
 // As many reduction splits as fill the compute units once (a workgroup's LDS
 // sets how many share one), each with at least 4 steps.
 int loss_dfeat_splits(bdr_dtype dt, int64_t rows, bool small, int64_t cols, int64_t width) {
-  return with_feat_tile(dt, rows, small, cols, [&](auto t) {
+  return with_feat_tile(dt, rows, small, cols, width, [&](auto t) {
     using T = decltype(t);
     const int64_t tiles = loss_tiles<T>(rows, cols);
     const int64_t slots = 256 * T::PER_CU;
@@ -81,7 +87,7 @@ hipError_t launch_loss_dfeat(bdr_dtype dt, int64_t rows, bool small, const LossG
   if (x && e && small) return launch_loss_gemm_pair<FeatNarrow, LE_PARTIAL>(*x, *e, stream);
   for (const LossGemm* g : {x, e}) {
     if (!g) continue;
-    const hipError_t err = with_feat_tile(dt, rows, small, g->N, [&](auto t) {
+    const hipError_t err = with_feat_tile(dt, rows, small, g->N, g->seg[0].k, [&](auto t) {
       return launch_loss_gemm<decltype(t), LE_PARTIAL>(*g, stream);
     });
     if (err != hipSuccess) return err;

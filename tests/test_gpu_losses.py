@@ -439,6 +439,63 @@ def test_two_streams_at_once():
     assert m is not None
 
 
+@pytest.mark.parametrize("N,H,V,r", [(5, 2560, 60001, 16), (60, 2560, 60001, 32), (100, 2560, 60001, 0),
+                                     (60, 2568, 60001, 0), (100, 2568, 60001, 8), (128, 2624, 60033, 8)])
+def test_one_row_of_tiles_over_a_large_weight(N, H, V, r):
+    """Few rows and a weight larger than the caches, with rows of whole cache lines and rows that
+    end inside one: the float64 reference and the tolerances of _check, on the device."""
+    m = bdr()
+    g = torch.Generator(device="cuda").manual_seed(N + H)
+    rn = lambda *s: torch.randn(*s, generator=g, device="cuda")
+    x, w = rn(N, H).bfloat16(), (rn(V, H) * 2 / H ** 0.5).bfloat16()
+    lab = torch.randint(-V // 5, V, (N,), generator=g, device="cuda", dtype=torch.int32)
+    lab[0] = V - 1
+    gr = torch.rand(N, generator=g, device="cuda") + 0.2
+    mk = {}
+    if r:
+        mk = dict(markov_w1=rn(V, r).bfloat16(), markov_w2=(rn(V, r) * 0.3).bfloat16(),
+                  prev_token=torch.randint(-1, 40, (N,), generator=g, device="cuda", dtype=torch.int32))
+    loss, lse = m.dspark_ce_loss(x, w, lab, **mk)
+    got = m.dspark_ce_backward(x, w, lab, lse, gr, **mk)
+    live = lab >= 0
+    X, W = x.double() * live[:, None], w.double()
+    z, zabs = X @ W.t(), X.abs() @ W.abs().t()
+    if r:
+        prev = mk["prev_token"].long()
+        has = (prev >= 0) & live
+        e = mk["markov_w1"].double()[prev.clamp(min=0)] * has[:, None]
+        W2 = mk["markov_w2"].double()
+        z, zabs = z + e @ W2.t(), zabs + e.abs() @ W2.abs().t()
+    zabs = zabs.max(dim=1).values
+    ref = torch.logsumexp(z, dim=1)
+    at = lab.long().clamp(min=0)[:, None]
+    zerr = ((H + r) / 4 + 40) * U * zabs
+    mag = 1 + ref.abs() + zabs
+    ep = 2 * zerr + 64 * U * mag
+    assert ((lse.double() - ref * live).abs() <= (zerr + 64 * U * mag) * live).all()
+    assert ((loss.double() - (ref - z.gather(1, at)[:, 0]) * live).abs() <= (ep + 64 * U * mag) * live).all()
+    gp = (z - ref[:, None]).exp() * (gr.double() * live)[:, None]
+    dz = gp.clone()
+    dz.scatter_add_(1, at, -(gr.double() * live)[:, None])
+    E = gp * ep[:, None] + (RND["bf16"] + 4 * U) * dz.abs() + TINY * live[:, None]
+
+    def near(name, want, moved, mags, K):
+        tol = moved + (K / 4 + 40) * U * mags + RND["bf16"] * want.abs() + TINY * K
+        assert ((got[name].double() - want).abs() <= tol).all(), name
+
+    near("hidden", dz @ W, E @ W.abs(), dz.abs() @ W.abs(), V)
+    assert not got["hidden"][~live].any()
+    near("lm_head_w", dz.t() @ X, E.t() @ X.abs(), dz.abs().t() @ X.abs(), N)
+    if r:
+        near("markov_w2", dz.t() @ e, E.t() @ e.abs(), dz.abs().t() @ e.abs(), N)
+        rows = prev.clamp(min=0)
+
+        def d1(a):
+            return torch.zeros(V, r, dtype=torch.float64, device="cuda").index_add_(0, rows, a * has[:, None])
+
+        near("markov_w1", d1(dz @ W2), d1(E @ W2.abs()), d1(dz.abs() @ W2.abs()), V + 4 * N)
+
+
 def test_weights_beyond_32_bit_offsets():
     """2^21 entries of 1032 features: 4.3 GB of weight and as much gradient.  The loss and the rows
     of d W that the last entries get, against float64 on the device."""
