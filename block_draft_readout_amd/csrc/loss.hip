@@ -717,8 +717,9 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.live_k = 1;
       // many rows: taller bands push the step's d logits out of an XCD's L2 (256 x 320
       // tiles, 4096 rows: 4 rows of tiles a band 1718 us, 16 1887 us; 1000 rows: 849 and
-      // 798 us; 128 x 320 tiles, 128 rows: 464 and 388 us)
-      d.band = p.rows < 1536 ? 16 : 4;
+      // 798 us; 128 x 320 tiles, 768 rows: 16 646 us, 24 669 us; 128 rows: 4 464 us, 16
+      // 373 us, 24 358 us)
+      d.band = p.rows <= 512 ? 24 : p.rows < 1536 ? 16 : 4;
       d.splits = 1;
       d.out = static_cast<char*>(out) + v0 * cols * es;
       d.ldo = cols;
