@@ -22,7 +22,8 @@
 // backward pass walks the vocabulary in pieces and recomputes a piece's logits
 // straight into d z (the only logits-sized buffer, one piece wide).  Per-row
 // values, softmax sums and d hidden across pieces are fp32; d z is rounded to
-// the storage type, as an operand of matrix products has to be.
+// the storage type, as an operand of matrix products has to be (for up to 64 rows
+// of bf16 kept as two such terms).
 //
 // Every sum has a fixed order: the same inputs give the same bits.
 
@@ -319,7 +320,7 @@ __global__ __launch_bounds__(256) void distill_loss_kernel(const LossRows g, con
 template <typename S>
 __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, const float* picked,
                                                           S* dz, int64_t panel, int v0, int width,
-                                                          float scale2) {
+                                                          float scale2, int two) {
   const int64_t i = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x;
   const int p = static_cast<int>(i / g.top);
   if (p >= *g.live) return;
@@ -334,7 +335,11 @@ __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, cons
   const float pr = __builtin_amdgcn_exp2f(picked[n * g.top + j] * scale2 - g.lse2[p]);
   const float v = g.coef[p] * (pr - t);
   constexpr int KB = 128 / static_cast<int>(sizeof(S));   // d logits lie in panels of KB columns
-  dz[(id - v0) / KB * panel + static_cast<int64_t>(p) * KB + (id - v0) % KB] = rounded<S>(v);
+  S* at = dz + (id - v0) / KB * panel + (static_cast<int64_t>(p) << two) * KB + (id - v0) % KB;
+  *at = rounded<S>(v);
+  if constexpr (sizeof(S) == 2) {
+    if (two) at[KB] = rounded<S>(left_over(v));
+  }
 }
 
 // ---------------------------------------------------------------- gradients out
@@ -350,7 +355,7 @@ struct JoinArgs {
   const int32_t* pos;
   const float* part_x;
   const float* part_e;
-  int splits_x, splits_e, hidden, rank, blocks_x;
+  int splits_x, splits_e, hidden, rank, blocks_x, two;
   int64_t rows;
   S* dx;
   float* de;
@@ -367,14 +372,15 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const JoinArgs<S> g) {
   const int q = static_cast<int>(threadIdx.x) % QUADS;
   const int sl = static_cast<int>(threadIdx.x) / QUADS;
   const int cols = emb ? g.rank : g.hidden;
-  const int splits = emb ? g.splits_e : g.splits_x;
+  const int parts = (emb ? g.splits_e : g.splits_x) << g.two;   // splits, the terms of each
   const int c = ((static_cast<int>(blockIdx.y) - (emb ? g.blocks_x : 0)) * QUADS + q) * 4;
   f32x4_t v{0.f, 0.f, 0.f, 0.f};
   if (p >= 0 && c < cols) {
-    const float* src = (emb ? g.part_e : g.part_x) + static_cast<int64_t>(p) * cols + c;
-    const int64_t slab = g.rows * cols;
+    const float* src = (emb ? g.part_e : g.part_x) + (static_cast<int64_t>(p) << g.two) * cols + c;
+    const int64_t slab = (g.rows << g.two) * cols;
 #pragma unroll 4
-    for (int s = sl; s < splits; s += SL) v += *reinterpret_cast<const f32x4_t*>(src + s * slab);
+    for (int s = sl; s < parts; s += SL)
+      v += *reinterpret_cast<const f32x4_t*>(src + (s >> g.two) * slab + (s & g.two) * cols);
   }
   if constexpr (SL > 1) {
     sums[threadIdx.x] = v;
@@ -456,6 +462,7 @@ __global__ __launch_bounds__(256) void clear_kernel(u32x4_t* p, int64_t n16) {
 struct LossPlan {
   int64_t piece;       // vocabulary entries per piece (backward)
   int64_t ld;          // row length of the piece's d logits buffer
+  int two;             // d logits in two terms (stored rows = rows << two)
   bool small;          // narrow tiles, fewer launches
   int splits_x, splits_e;
   int stat_tiles;
@@ -467,15 +474,17 @@ LossPlan plan_loss(const LossProblem& p) {
   const int cols = loss_stats_cols(p.dt, p.rows, p.vocab, p.hidden);
   q.stat_tiles = static_cast<int>((p.vocab + cols - 1) / cols);
   // whole vocabulary where its d logits fit, else equal pieces
-  int64_t most = kPieceBytes / (p.rows * es) / kPieceCols * kPieceCols;
+  q.two = p.dt == BDR_BF16 && p.rows <= kTwoTermRows;
+  const int64_t rows = p.rows << q.two;
+  int64_t most = kPieceBytes / (rows * es) / kPieceCols * kPieceCols;
   most = std::max<int64_t>(most, kPieceCols);
   const int64_t pieces = (p.vocab + most - 1) / most;
   q.piece = ((p.vocab + pieces - 1) / pieces + kPieceCols - 1) / kPieceCols * kPieceCols;
   q.piece = std::min(q.piece, p.vocab);
   q.ld = (q.piece + 63) / 64 * 64;
   q.small = p.rows * p.hidden <= kSmallProduct / p.vocab;
-  q.splits_x = loss_dfeat_splits(p.dt, p.rows, q.small, p.hidden, q.piece);
-  q.splits_e = p.rank ? loss_dfeat_splits(p.dt, p.rows, q.small, p.rank, q.piece) : 0;
+  q.splits_x = loss_dfeat_splits(p.dt, rows, q.small, p.hidden, q.piece);
+  q.splits_e = p.rank ? loss_dfeat_splits(p.dt, rows, q.small, p.rank, q.piece) : 0;
   return q;
 }
 
@@ -522,10 +531,11 @@ size_t lay_out(const LossProblem& p, const LossPlan& q, bool backward, char* bas
   } else {
     r.lse2 = s.take<float>(p.rows);
     r.coef = s.take<float>(p.rows);
-    b.dz = s.take<char>(p.rows * q.ld * es);
-    b.part_x = s.take<float>(q.splits_x * p.rows * p.hidden);
-    b.part_e = s.take<float>(q.splits_e * p.rows * p.rank);
-    b.de = s.take<float>(q.splits_e > 1 ? p.rows * p.rank : 0);
+    const int64_t rows = p.rows << q.two;
+    b.dz = s.take<char>(rows * q.ld * es);
+    b.part_x = s.take<float>(q.splits_x * rows * p.hidden);
+    b.part_e = s.take<float>(q.splits_e * rows * p.rank);
+    b.de = s.take<float>(q.splits_e > 1 || q.two ? p.rows * p.rank : 0);
   }
   return s.used;
 }
@@ -661,6 +671,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
                     const float* picked, const float* loss_grad, hipStream_t st) {
   const LossPlan q = plan_loss(p);
   const int64_t es = sizeof(S);
+  const int64_t rows = p.rows << q.two;   // of d logits as stored
   LossBuffers b{};
   lay_out(p, q, true, static_cast<char*>(workspace), b);
   fill_rows(p, q, b);
@@ -670,7 +681,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
   for (int64_t v0 = 0; v0 < p.vocab; v0 += q.piece) {
     const int64_t width = std::min(q.piece, p.vocab - v0);
     const int64_t ld = (width + 63) / 64 * 64;
-    const int64_t panel = p.rows * (128 / es);   // elements of 128-byte columns
+    const int64_t panel = rows * (128 / es);   // elements of 128-byte columns
     LossGemm g = logits_gemm(p, b.r, v0, width);
     if (!p.top) {
       g.label = b.r.label_c;
@@ -681,12 +692,13 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
     g.out = b.dz;
     g.ldo = ld;
     g.slab = panel;
+    g.two = q.two;
     BDR_LAUNCH(launch_loss_dlogits(p.dt, p.rows, g, st));
     if (p.top) {
       hipLaunchKernelGGL(distill_fix_kernel<S>,
                          dim3(static_cast<unsigned>((p.rows * p.top + 255) / 256)), dim3(256), 0, st,
                          b.r, picked, reinterpret_cast<S*>(b.dz), panel, static_cast<int>(v0),
-                         static_cast<int>(width), g.scale2);
+                         static_cast<int>(width), g.scale2, q.two);
       BDR_LAUNCH(hipGetLastError());
     }
     // d hidden and d embedding: reduction over this piece's entries
@@ -695,26 +707,28 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.seg[0] = LossSeg{b.dz, static_cast<const char*>(w) + v0 * cols * es, panel, cols, width};
       d.seg[1] = LossSeg{d.seg[0].a, d.seg[0].b, panel, cols, 0};
       d.live = b.r.live;
-      d.M = p.rows;
+      d.M = rows;
       d.N = cols;
       d.live_m = 1;
       d.band = 16;
       d.splits = splits;
+      d.two = q.two;
       d.out = part;
       d.ldo = cols;
-      d.slab = p.rows * cols;
+      d.slab = rows * cols;
       d.accumulate = v0 > 0;
       return d;
     };
     // d weight and d w2: reduction over the rows
     auto dweight = [&](const void* feat, int64_t cols, void* out) {
       LossGemm d{};
-      d.seg[0] = LossSeg{b.dz, feat, panel, cols, p.rows};
+      d.seg[0] = LossSeg{b.dz, feat, panel, cols, rows};
       d.seg[1] = LossSeg{d.seg[0].a, d.seg[0].b, panel, cols, 0};
       d.live = b.r.live;
       d.M = width;
       d.N = cols;
       d.live_k = 1;
+      d.two = q.two;
       // many rows: taller bands push the step's d logits out of an XCD's L2 (256 x 320
       // tiles, 4096 rows: 4 rows of tiles a band 1718 us, 16 1887 us; 1000 rows: 849 and
       // 798 us; 128 x 320 tiles, 768 rows: 16 646 us, 24 669 us; 128 rows: 4 464 us, 16
@@ -728,17 +742,17 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
     LossGemm gx, ge;
     if (o.hidden) gx = dfeat(p.w, p.hidden, b.part_x, q.splits_x);
     if (o.w1) ge = dfeat(p.w2, p.rank, b.part_e, q.splits_e);
-    BDR_LAUNCH(launch_loss_dfeat(p.dt, p.rows, q.small, o.hidden ? &gx : nullptr,
+    BDR_LAUNCH(launch_loss_dfeat(p.dt, rows, q.small, o.hidden ? &gx : nullptr,
                                  o.w1 ? &ge : nullptr, st));
     if (o.w) gx = dweight(b.r.x, p.hidden, o.w);
     if (o.w2) ge = dweight(b.r.e, p.rank, o.w2);
-    BDR_LAUNCH(launch_loss_dweight(p.dt, p.rows, q.small, o.w ? &gx : nullptr,
+    BDR_LAUNCH(launch_loss_dweight(p.dt, rows, q.small, o.w ? &gx : nullptr,
                                    o.w2 ? &ge : nullptr, st));
   }
-  const bool join_e = o.w1 && q.splits_e > 1;
+  const bool join_e = o.w1 && (q.splits_e > 1 || q.two);
   if (o.hidden || join_e)
     BDR_LAUNCH(join(JoinArgs<S>{b.r.live, b.r.pos, b.part_x, b.part_e, q.splits_x, q.splits_e,
-                                static_cast<int>(p.hidden), p.rank, 0, p.rows,
+                                static_cast<int>(p.hidden), p.rank, 0, q.two, p.rows,
                                 static_cast<S*>(o.hidden), join_e ? b.de : nullptr},
                     st));
   if (o.w1) {

@@ -60,6 +60,7 @@ struct LossGemm {
   int tiles_n;
   int band;                // tile rows per band of the tile order
   int splits;              // reduction splits (LE_PARTIAL)
+  int two;                 // 1: row m of d logits is the sum of rows 2 m and 2 m + 1 as stored (0: row m)
   // logits epilogues
   float scale2;            // log2(e) / temperature
   const int32_t* label;    // [M] target entry or NULL
@@ -103,6 +104,8 @@ struct LossTile {
   static constexpr int SCRATCH = std::max(WN * BM * 8, WAVES * 16 * OUT_PITCH);
   static constexpr int LDS_BYTES = LOOP ? RING_BYTES + SCRATCH : std::max(RING_BYTES, SCRATCH);
   static constexpr int PER_CU = 160 * 1024 / LDS_BYTES;   // workgroups a compute unit holds
+  // may meet d logits in two terms, which only few rows have (they take no larger tiles)
+  static constexpr bool TWO = sizeof(S) == 2 && BM <= 128;
   // waves of a SIMD to leave registers for: the workgroups LDS has room for, up to two
   // waves (without it 128 x 128 d logits took 268 registers, so one workgroup of two
   // ran: 4258 us instead of 2260, 4096 rows of 5120, 20 x 2560 entries)
@@ -224,6 +227,12 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4_t v) {
 }
 __device__ __forceinline__ void store4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
 
+// what rounding x to bf16 leaves (nothing of an infinity)
+__device__ __forceinline__ float left_over(float x) {
+  const float hi = bf16_to_f32(rounded<uint16_t>(x));
+  return fabsf(hi) == INFINITY ? 0.f : x - hi;
+}
+
 // Workgroup `block` of `blocks` (a multiple of 8) of one product.
 template <typename T, int EPI>
 __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int blocks) {
@@ -240,7 +249,8 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   // Tiles of this workgroup: each XCD takes a contiguous run of the work items, its
   // workgroups one each or every wgs-th of the run, so those at work together share
   // slices in that XCD's L2.
-  const int live = *g.live;
+  const int two = T::TWO ? g.two : 0;
+  const int live = *g.live << (EPI == LE_PARTIAL || EPI == LE_OUT ? two : 0);   // rows as stored
   const int64_t M = g.live_m ? live : g.M;
   const int tiles_m = static_cast<int>((M + T::BM - 1) / T::BM);
   const int tiles = tiles_m * g.tiles_n;
@@ -282,7 +292,9 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   const uint32_t lchunk = (static_cast<uint32_t>(lane) & 7u) ^ lrow;
   // byte offset of load q's chunk of this lane inside the step's slice of an
   // operand with row stride ld (panels: with ld from panel to panel)
-  auto lane_off = [&](auto slow, auto rowbytes, auto panels, int q, uint32_t ld) -> uint32_t {
+  // (two rows of A's reduction to one of B's where d logits come in two terms)
+  auto lane_off = [&](auto slow, auto rowbytes, auto panels, int q, uint32_t ld,
+                      int two = 0) -> uint32_t {
     const uint32_t i = static_cast<uint32_t>(wave + T::WAVES * q);
     if constexpr (!decltype(slow)::value) {
       return (8u * i + lrow) * (decltype(panels)::value ? 128u : ld * ES) + lchunk * 16u;
@@ -293,7 +305,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       uint32_t p = o % ROWB;
       if constexpr (ES == 2) p = (((p >> 5) ^ slow_swizzle<ROWB>(kr)) << 5) | (p & 16u);
       if constexpr (decltype(panels)::value) return (p >> 7) * ld * ES + kr * 128u + (p & 127u);
-      return kr * ld * ES + p;
+      return (kr >> two) * ld * ES + p;
     }
   };
   typedef std::integral_constant<bool, T::AKS> ASlow;
@@ -304,13 +316,15 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   // the gradient products have one segment: their loads' offsets never change
   constexpr bool kPanels = T::BKS;
   typedef std::integral_constant<bool, kPanels> APanels;
+  const int two_b = EPI == LE_OUT ? two : 0;
   uint32_t off_a[T::LOADS_A], off_b[T::LOADS_B];
   if constexpr (kPanels) {
     static_for<T::LOADS_A>([&](auto q) {
       off_a[q] = lane_off(ASlow{}, ARow{}, APanels{}, q, static_cast<uint32_t>(g.seg[0].lda));
     });
     static_for<T::LOADS_B>([&](auto q) {
-      off_b[q] = lane_off(BSlow{}, BRow{}, std::false_type{}, q, static_cast<uint32_t>(g.seg[0].ldb));
+      off_b[q] = lane_off(BSlow{}, BRow{}, std::false_type{}, q, static_cast<uint32_t>(g.seg[0].ldb),
+                          two_b);
     });
   }
   // slow panels: LDS row of this lane in load 0, and how many rows further each
@@ -379,8 +393,8 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       na = static_cast<uint32_t>((min<int64_t>(T::BM, M - ld_m0) * sa->lda - ka) * ES);
     }
     if constexpr (T::BKS) {
-      pb += (kb * sb->ldb + ld_n0) * ES;
-      nb = static_cast<uint32_t>((krows * sb->ldb - ld_n0) * ES);
+      pb += ((kb >> two_b) * sb->ldb + ld_n0) * ES;
+      nb = static_cast<uint32_t>(((krows >> two_b) * sb->ldb - ld_n0) * ES);
     } else {
       pb += (ld_n0 * sb->ldb + kb) * ES;
       nb = static_cast<uint32_t>((min<int64_t>(T::BN, g.N - ld_n0) * sb->ldb - kb) * ES);
@@ -569,7 +583,9 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
     // (1.56 GB written and nothing else: 284 us against 433 us).  The largest
     // tiles have no registers for it and few rows to write per product: directly.
     char* mine = scratch + wave * 16 * T::OUT_PITCH;
-    auto put_rows = [&](auto ic, auto&& value) {
+    // (d logits: term `term` of the rows)
+    const int terms = EPI == LE_DLOGITS ? two : 0;
+    auto put_rows = [&](auto ic, int term, auto&& value) {
       if constexpr (!T::STAGED) {
         const int64_t m = mw + decltype(ic)::value * 16;
         static_for<T::WTN>([&](auto j) {
@@ -577,7 +593,9 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
           if (m >= M) return;
           if constexpr (EPI == LE_DLOGITS) {
             if (n < g.ldo)
-              store4(static_cast<S*>(g.out) + n / T::KB * g.slab + m * T::KB + n % T::KB, value(j));
+              store4(static_cast<S*>(g.out) + n / T::KB * g.slab + ((m << terms) + term) * T::KB +
+                         n % T::KB,
+                     value(j));
           } else if (n < g.N) {
             store4(static_cast<S*>(g.out) + m * g.ldo + n, value(j));
           }
@@ -593,8 +611,8 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       const int64_t left = min<int64_t>(T::BM, M - m0);
       const rsrc_t out =
           kOutPanels
-              ? make_rsrc(static_cast<S*>(g.out) + n0 / T::KB * g.slab + m0 * T::KB,
-                          static_cast<uint32_t>((T::BN / T::KB - 1) * g.slab * ES + left * 128))
+              ? make_rsrc(static_cast<S*>(g.out) + n0 / T::KB * g.slab + (m0 << terms) * T::KB,
+                          static_cast<uint32_t>((T::BN / T::KB - 1) * g.slab * ES + (left << terms) * 128))
               : make_rsrc(static_cast<S*>(g.out) + m0 * g.ldo, static_cast<uint32_t>(left * g.ldo * ES));
       const int64_t cols = (kOutPanels ? g.ldo : g.N) - (n0 + wn * 16 * T::WTN);   // may be <= 0
 #pragma unroll
@@ -607,7 +625,8 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         const int m = (wm * T::WTM + decltype(ic)::value) * 16 + row;
         const int nb = wn * T::OUT_ROW + in_row;   // byte of the tile's row
         const uint32_t off =
-            kOutPanels ? static_cast<uint32_t>((nb / 128) * g.slab * ES + m * 128 + nb % 128)
+            kOutPanels ? static_cast<uint32_t>((nb / 128) * g.slab * ES + ((m << terms) + term) * 128 +
+                                              nb % 128)
                        : static_cast<uint32_t>((m * g.ldo + n0) * ES + nb);
         const bool ok = c < 16 * T::OUT_ROW && in_row < cols * ES && m < left;
         bstore16(__builtin_bit_cast(f32x4_t, v), out, ok ? off : kOOB);
@@ -662,8 +681,11 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         g.stat[(m0 + r) * g.tiles_n + tn] = v;
       }
     } else if constexpr (EPI == LE_DLOGITS) {
-      // rounded to the storage type: the operand of two more matrix products,
-      // with as much relative error as their rounded results carry anyway.
+      // rounded to the storage type: the operand of two more matrix products, with as
+      // much relative error as their rounded results carry anyway.  That holds for the
+      // sum of many rows' roundings; few rows' may all fall on one side, so a second
+      // term takes what the first one's rounding left (16 bits in all), which costs
+      // little where the products wait for the weight.
       // Columns from N to the padded width hold zeros.
       float l2[T::WTM], cf[T::WTM];
       int lab[T::WTM];   // column of the label, from this lane's first
@@ -674,7 +696,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         cf[i] = g.coef[m];
       });
       static_for<T::WTM>([&](auto i) {
-        put_rows(i, [&](auto j) {
+        auto value = [&](auto j) {
           f32x4_t v;
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
@@ -683,7 +705,17 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
             v[c] = n < n_in ? cf[i] * (n == lab[i] ? p - 1.f : p) : 0.f;
           }
           return v;
-        });
+        };
+        put_rows(i, 0, value);
+        if constexpr (T::TWO) {
+          if (two)
+            put_rows(i, 1, [&](auto j) {
+              f32x4_t v = value(j);
+#pragma unroll
+              for (int c = 0; c < 4; ++c) v[c] = left_over(v[c]);
+              return v;
+            });
+        }
       });
     } else if constexpr (EPI == LE_PARTIAL) {
       float* out = static_cast<float*>(g.out) + static_cast<int64_t>(split) * g.slab;
@@ -698,7 +730,7 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         });
       });
     } else {
-      static_for<T::WTM>([&](auto i) { put_rows(i, [&](auto j) { return acc[i][j]; }); });
+      static_for<T::WTM>([&](auto i) { put_rows(i, 0, [&](auto j) { return acc[i][j]; }); });
     }
   }
   BDR_WAIT_VM_LGKM(0, 0);   // the trailing zero-filling loads

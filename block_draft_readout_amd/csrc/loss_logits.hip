@@ -58,7 +58,8 @@ auto with_logits_tile(bdr_dtype dt, int64_t rows, int64_t cols, int64_t hidden, 
   const bool few_once = stream && rows <= LogitsFew::BM, some_once = stream && rows <= LogitsSome::BM;
   const double t[5] = {logits_us<LogitsFew>(rows, cols, hidden, 1.2, few_once),
                        logits_us<LogitsSome>(rows, cols, hidden, 1.3, some_once),
-                       logits_us<LogitsMany>(rows, cols, hidden, 2.1, false),
+                       // (its d logits have no second term, which few rows need)
+                       rows <= kTwoTermRows ? 1e30 : logits_us<LogitsMany>(rows, cols, hidden, 2.1, false),
                        logits_us<LogitsMid>(rows, cols, hidden, 1.15, false),
                        logits_us<LogitsSmall>(rows, cols, hidden, 0.85, false)};
   const int best = static_cast<int>(std::min_element(t, t + 5) - t);
