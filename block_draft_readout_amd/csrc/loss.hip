@@ -23,7 +23,8 @@
 // straight into d z (the only logits-sized buffer, one piece wide).  Per-row
 // values, softmax sums and d hidden across pieces are fp32; d z is rounded to
 // the storage type, as an operand of matrix products has to be (for up to 64 rows
-// of bf16 kept as two such terms).
+// of bf16 kept as two such terms; with more, what the label's entry loses is added to
+// the gradients apart, to the weights' for up to 512 rows).
 //
 // Every sum has a fixed order: the same inputs give the same bits.
 
@@ -69,6 +70,7 @@ struct LossRows {
   void* e;                 // [live, r]
   float* lse2;             // [live]
   float* coef;             // [live]
+  float* resid;            // [live] what rounding d logits left at label_c, or NULL
   float* t;                // [rows, top]
   float2* stat;            // [live, tiles]
   int tiles;
@@ -79,7 +81,8 @@ struct LossRows {
 // t = softmax of a row's valid teacher logits over T, and whether it has any
 // mass; one wave per row.  The maximum is taken off before the division: the
 // difference of two close logits is exact, their quotients by a small T are not.
-__global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, int32_t* has) {
+// `label` gets the row's heaviest entry, or -1.
+__global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, int32_t* label) {
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int64_t n = static_cast<int64_t>(blockIdx.x) * 4 + (threadIdx.x >> 6);
   if (n >= g.rows) return;
@@ -108,12 +111,27 @@ __global__ __launch_bounds__(256) void distill_target_kernel(const LossRows g, i
     sum += v[c];
   }
   sum = wave_sum(sum);
+  float top_weight = 0.f;
+#pragma unroll
+  for (int c = 0; c < BDR_MAX_TEACHER / 64; ++c) top_weight = fmaxf(top_weight, v[c]);
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) top_weight = fmaxf(top_weight, __shfl_xor(top_weight, m));
 #pragma unroll
   for (int c = 0; c < BDR_MAX_TEACHER / 64; ++c) {
     const int j = c * 64 + lane;
     if (j < g.top) g.t[n * g.top + j] = row_any ? v[c] / sum : 0.f;
   }
-  if (lane == 0) has[n] = row_any ? 0 : -1;
+  // the largest id among the entries of the largest weight (NaN weights: any listed id)
+  int best = -1;
+#pragma unroll
+  for (int c = 0; c < BDR_MAX_TEACHER / 64; ++c) {
+    const int j = c * 64 + lane;
+    if (j < g.top && !(v[c] < top_weight) && static_cast<uint32_t>(ids[j]) < static_cast<uint32_t>(g.vocab))
+      best = max(best, ids[j]);
+  }
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) best = max(best, __shfl_xor(best, m));
+  if (lane == 0) label[n] = row_any ? best : -1;
 }
 
 // ---------------------------------------------------------------- compaction
@@ -339,6 +357,7 @@ __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, cons
   *at = rounded<S>(v);
   if constexpr (sizeof(S) == 2) {
     if (two) at[KB] = rounded<S>(left_over(v));
+    if (g.resid && id == g.label_c[p]) g.resid[p] = left_over(v);
   }
 }
 
@@ -359,6 +378,10 @@ struct JoinArgs {
   int64_t rows;
   S* dx;
   float* de;
+  const float* resid;      // [live] d logits' rounding at label, or NULL
+  const int32_t* label;    // [live]
+  const S* w;              // [V, hidden]
+  const S* w2;             // [V, rank]
 };
 
 template <typename S, int SL>
@@ -390,6 +413,8 @@ __global__ __launch_bounds__(256) void loss_join_kernel(const JoinArgs<S> g) {
     for (int k = 1; k < SL; ++k) v += sums[k * QUADS + q];
   }
   if (c >= cols) return;
+  if (g.resid && p >= 0)
+    v += g.resid[p] * load4((emb ? g.w2 : g.w) + static_cast<int64_t>(g.label[p]) * cols + c);
   if (emb)
     store4(g.de + n * cols + c, v);
   else
@@ -463,6 +488,7 @@ struct LossPlan {
   int64_t piece;       // vocabulary entries per piece (backward)
   int64_t ld;          // row length of the piece's d logits buffer
   int two;             // d logits in two terms (stored rows = rows << two)
+  bool resid;          // what their rounding leaves at the label is added
   bool small;          // narrow tiles, fewer launches
   int splits_x, splits_e;
   int stat_tiles;
@@ -475,6 +501,7 @@ LossPlan plan_loss(const LossProblem& p) {
   q.stat_tiles = static_cast<int>((p.vocab + cols - 1) / cols);
   // whole vocabulary where its d logits fit, else equal pieces
   q.two = p.dt == BDR_BF16 && p.rows <= kTwoTermRows;
+  q.resid = p.dt == BDR_BF16 && !q.two;
   const int64_t rows = p.rows << q.two;
   int64_t most = kPieceBytes / (rows * es) / kPieceCols * kPieceCols;
   most = std::max<int64_t>(most, kPieceCols);
@@ -535,7 +562,9 @@ size_t lay_out(const LossProblem& p, const LossPlan& q, bool backward, char* bas
     b.dz = s.take<char>(rows * q.ld * es);
     b.part_x = s.take<float>(q.splits_x * rows * p.hidden);
     b.part_e = s.take<float>(q.splits_e * rows * p.rank);
-    b.de = s.take<float>(q.splits_e > 1 || q.two ? p.rows * p.rank : 0);
+    b.de = s.take<float>(q.splits_e > 1 || q.two || q.resid ? p.rows * p.rank : 0);
+    r.resid = s.take<float>(q.resid ? p.rows : 0);
+    if (!q.resid) r.resid = nullptr;
   }
   return s.used;
 }
@@ -693,6 +722,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
     g.ldo = ld;
     g.slab = panel;
     g.two = q.two;
+    g.resid = p.top ? nullptr : b.r.resid;   // (distillation: written with the teacher's entries)
     BDR_LAUNCH(launch_loss_dlogits(p.dt, p.rows, g, st));
     if (p.top) {
       hipLaunchKernelGGL(distill_fix_kernel<S>,
@@ -729,6 +759,9 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       d.N = cols;
       d.live_k = 1;
       d.two = q.two;
+      d.label = b.r.label_c;
+      d.label0 = static_cast<int>(v0);
+      d.resid = p.rows <= kHeldRows ? b.r.resid : nullptr;
       // many rows: taller bands push the step's d logits out of an XCD's L2 (256 x 320
       // tiles, 4096 rows: 4 rows of tiles a band 1718 us, 16 1887 us; 1000 rows: 849 and
       // 798 us; 128 x 320 tiles, 768 rows: 16 646 us, 24 669 us; 128 rows: 4 464 us, 16
@@ -749,11 +782,12 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
     BDR_LAUNCH(launch_loss_dweight(p.dt, rows, q.small, o.w ? &gx : nullptr,
                                    o.w2 ? &ge : nullptr, st));
   }
-  const bool join_e = o.w1 && (q.splits_e > 1 || q.two);
+  const bool join_e = o.w1 && (q.splits_e > 1 || q.two || q.resid);
   if (o.hidden || join_e)
     BDR_LAUNCH(join(JoinArgs<S>{b.r.live, b.r.pos, b.part_x, b.part_e, q.splits_x, q.splits_e,
                                 static_cast<int>(p.hidden), p.rank, 0, q.two, p.rows,
-                                static_cast<S*>(o.hidden), join_e ? b.de : nullptr},
+                                static_cast<S*>(o.hidden), join_e ? b.de : nullptr, b.r.resid,
+                                b.r.label_c, static_cast<const S*>(p.w), static_cast<const S*>(p.w2)},
                     st));
   if (o.w1) {
     const float* de = join_e ? b.de : b.part_e;

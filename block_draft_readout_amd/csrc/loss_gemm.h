@@ -52,6 +52,9 @@ struct LossSeg {
   int64_t k;
 };
 
+// rows whose labels a wave of a weight gradient holds
+constexpr int kHeldRows = 512;
+
 struct LossGemm {
   LossSeg seg[2];          // the second one with the reduction fast on both sides only
   const int32_t* live;     // device: rows that take part
@@ -63,10 +66,12 @@ struct LossGemm {
   int two;                 // 1: row m of d logits is the sum of rows 2 m and 2 m + 1 as stored (0: row m)
   // logits epilogues
   float scale2;            // log2(e) / temperature
-  const int32_t* label;    // [M] target entry or NULL
+  const int32_t* label;    // [M] target entry or NULL (LE_OUT: of the reduction's rows)
   int label0;              // vocabulary entry of column 0
   float2* stat;            // [M, tiles_n] (maximum, sum) in units of log2
   float* picked;           // [M] logit of the label
+  float* resid;            // [M] what rounding d logits left at the label, or NULL (LE_OUT: added, up to
+                           // kHeldRows rows)
   const float* lse2;       // [M] log2 of the softmax denominator
   const float* coef;       // [M] gradient factor
   void* out;               // LE_DLOGITS panels, LE_PARTIAL [splits, slab], LE_OUT [M, ldo]
@@ -226,6 +231,15 @@ __device__ __forceinline__ void store4(uint16_t* p, f32x4_t v) {
   *reinterpret_cast<uint2*>(p) = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 __device__ __forceinline__ void store4(float* p, f32x4_t v) { *reinterpret_cast<f32x4_t*>(p) = v; }
+
+__device__ __forceinline__ f32x4_t load4(const uint16_t* p) {
+  const uint2 v = *reinterpret_cast<const uint2*>(p);
+  return f32x4_t{__uint_as_float(v.x << 16), __uint_as_float(v.x & 0xFFFF0000u),
+                 __uint_as_float(v.y << 16), __uint_as_float(v.y & 0xFFFF0000u)};
+}
+__device__ __forceinline__ f32x4_t load4(const float* p) {
+  return *reinterpret_cast<const f32x4_t*>(p);
+}
 
 // what rounding x to bf16 leaves (nothing of an infinity)
 __device__ __forceinline__ float left_over(float x) {
@@ -492,6 +506,18 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
     }
   };
 
+  // the rows' labels stay in registers (a load in a tile's epilogue would wait for the
+  // next tile's operands, which are on their way before it)
+  constexpr int kHeld = EPI == LE_OUT && T::TWO ? kHeldRows / 64 : 1;
+  int held[kHeld];
+  if constexpr (EPI == LE_OUT && T::TWO) {
+    static_for<kHeld>([&](auto c) {
+      const int p = 64 * decltype(c)::value + lane;
+      held[c] = g.resid && p < live ? g.label[p] : -1;
+      asm volatile("" : "+v"(held[c]));   // loaded from here on
+    });
+  }
+
   // Per step: wait for its loads, one barrier, then per half the operand reads
   // and the MFMAs; the loads of step s + STAGES - 1 are spread over the first
   // half's MFMAs (all before them where there are fewer MFMAs than loads).
@@ -683,9 +709,11 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
     } else if constexpr (EPI == LE_DLOGITS) {
       // rounded to the storage type: the operand of two more matrix products, with as
       // much relative error as their rounded results carry anyway.  That holds for the
-      // sum of many rows' roundings; few rows' may all fall on one side, so a second
-      // term takes what the first one's rounding left (16 bits in all), which costs
-      // little where the products wait for the weight.
+      // sum of many roundings; a few rows' may all fall on one side, so a second term
+      // takes what the first one's rounding left (16 bits in all), which costs little
+      // where the products wait for the weight.  With more rows what is left at the
+      // label, by far the largest entry as a rule, is added in fp32 to d hidden and d
+      // embedding, and up to kHeldRows rows to the weights' gradients.
       // Columns from N to the padded width hold zeros.
       float l2[T::WTM], cf[T::WTM];
       int lab[T::WTM];   // column of the label, from this lane's first
@@ -706,7 +734,16 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
           }
           return v;
         };
-        put_rows(i, 0, value);
+        put_rows(i, 0, [&](auto j) {
+          const f32x4_t v = value(j);
+          if constexpr (sizeof(S) == 2) {
+            const int c = lab[i] - decltype(j)::value * 16;
+            const int64_t m = mw + decltype(i)::value * 16;
+            if (g.resid && static_cast<unsigned>(c) < 4u && m < M && lab[i] < n_in)
+              g.resid[m] = left_over(c == 0 ? v[0] : c == 1 ? v[1] : c == 2 ? v[2] : v[3]);
+          }
+          return v;
+        });
         if constexpr (T::TWO) {
           if (two)
             put_rows(i, 1, [&](auto j) {
@@ -730,6 +767,31 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         });
       });
     } else {
+      if constexpr (T::TWO) {
+        if (g.resid) {   // rows with their label in this wave's rows of C: resid * operand b
+          const int row0 = static_cast<int>(m0) + wm * 16 * T::WTM + g.label0;
+          for (int p0 = 0; p0 < live; p0 += 64) {
+            int at = -1;
+            static_for<kHeld>([&](auto c) { at = p0 == 64 * decltype(c)::value ? held[c] : at; });
+            at = at < 0 ? -1 : at - row0;
+            unsigned long long hits = __ballot(static_cast<unsigned>(at) < 16u * T::WTM);
+            while (hits) {
+              const int b = __ffsll(hits) - 1;
+              hits &= hits - 1;
+              const int rel = __builtin_amdgcn_readlane(at, b);
+              const float r = g.resid[p0 + b];
+              const S* x = static_cast<const S*>(g.seg[0].b) + static_cast<int64_t>(p0 + b) * g.seg[0].ldb + nw;
+              static_for<T::WTM>([&](auto i) {
+                if (rel >> 4 == decltype(i)::value && r16 == (rel & 15))
+                  static_for<T::WTN>([&](auto j) {
+                    if (decltype(j)::value * 16 < n_in)
+                      acc[i][j] += r * load4(x + decltype(j)::value * 16);
+                  });
+              });
+            }
+          }
+        }
+      }
       static_for<T::WTM>([&](auto i) { put_rows(i, 0, [&](auto j) { return acc[i][j]; }); });
     }
   }

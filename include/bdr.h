@@ -665,7 +665,9 @@ int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64
  *   d_markov_w2 = dz^T markov_w1[prev], d_markov_w1[p] = sum_{m: prev[m] = p} dz[m] markov_w2
  * dz is recomputed a piece of the vocabulary at a time and rounded to the dtype
  * as an operand of these products (bf16 of up to 64 rows: kept as two such terms,
- * 16 bits), which sum in fp32; each gradient is rounded once more, on output.  Rows of the weight gradients that no row reaches are 0.
+ * 16 bits; of more: what the rounding takes from the label's entry -- of a teacher's
+ * list, the heaviest -- is given back in fp32, to the weights' gradients for up to 512
+ * rows), which sum in fp32; each gradient is rounded once more, on output.  Rows of the weight gradients that no row reaches are 0.
  *   lse        [rows] as written by dspark_ce_loss for the same inputs
  *   loss_grad  [rows] fp32
  *   d_hidden [rows, H], d_lm_head_w [V, H], d_markov_w1, d_markov_w2 [V, r]:
