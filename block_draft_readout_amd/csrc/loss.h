@@ -29,8 +29,8 @@ int64_t loss_tiles(int64_t rows, int64_t cols) {
 // bound them (a step of 128 rows of 5120 would go from 1287 to 1581 us).  One term's
 // rounding adds to a gradient about the error of its own rounding (1.4 times in all,
 // relative to the norm); over a few dozen rows it scatters, 1.0 to 1.9 times.  More rows
-// get back in fp32 what the rounding takes from the label's entry (1.0 to 1.2 times; a
-// step of 128 rows of 5120 1283 -> 1307 us).
+// get back in fp32 what the rounding takes from the label's entry (at most 1.5 times over
+// 78 drawn problems; a step of 128 rows of 5120 1283 -> 1307 us).
 constexpr int64_t kTwoTermRows = 64;
 
 // Weights larger than the last-level cache (256 MiB) stay in HBM between the products
