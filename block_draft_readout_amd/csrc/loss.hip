@@ -362,10 +362,11 @@ __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, cons
 }
 
 // ---------------------------------------------------------------- gradients out
-// The reduction splits of the feature gradients added in order: d hidden rounded
-// and back at the original rows (zeros for rows without a target), d embedding
-// fp32 at the compacted rows.  SL lanes share the splits of four columns and join
-// through LDS: few rows have many splits and few columns to spread over the chip.
+// The reduction splits (and terms) of the feature gradients added in order, and what
+// rounding d logits left at the label: d hidden rounded and back at the original rows
+// (zeros for rows without a target), d embedding fp32 at the compacted rows.  SL lanes
+// share the splits of four columns and join through LDS: few rows have many splits and
+// few columns to spread over the chip.
 // Grid (rows, column blocks of d hidden, then of d embedding), 1024 / SL columns
 // in a block.
 template <typename S>
