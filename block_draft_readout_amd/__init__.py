@@ -120,7 +120,8 @@ def _ws_ptr(ws: Optional[torch.Tensor]):
         return None, 0
     p = ws.data_ptr()
     al = (p + 255) & ~255
-    return C.c_void_p(al), ws.numel() * ws.element_size() - (al - p)
+    # (none where the tensor ends before the first aligned byte: the C ABI's size is unsigned)
+    return C.c_void_p(al), max(0, ws.numel() * ws.element_size() - (al - p))
 
 
 def workspace_bytes(kind: str, **kw) -> int:

@@ -60,7 +60,9 @@ def _stream(device: torch.device) -> int:
 
 
 def _space(nbytes: int, device, ws: Optional[torch.Tensor]):
-    """(aligned pointer, bytes, tensor) of a workspace; these calls keep no state in it."""
+    """(aligned pointer, bytes, tensor) of a workspace; these calls keep no state in it.  A
+    tensor that ends before the first aligned byte has no bytes (the C ABI's size is unsigned
+    and takes one that is too small for the refusal)."""
     if ws is None:
         if nbytes == 0:
             return None, 0, None
@@ -69,7 +71,7 @@ def _space(nbytes: int, device, ws: Optional[torch.Tensor]):
         raise ValueError(f"workspace must be a contiguous tensor on {device}")
     p = ws.data_ptr()
     al = (p + 255) & ~255
-    return al, ws.numel() * ws.element_size() - (al - p), ws
+    return al, max(0, ws.numel() * ws.element_size() - (al - p)), ws
 
 
 # ----------------------------------------------------------------------------- row norm
