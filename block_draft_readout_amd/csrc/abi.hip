@@ -9,6 +9,7 @@
 #include <cstdarg>
 #include <cstdio>
 #include <cstring>
+#include <initializer_list>
 #include <mutex>
 
 #include "bdr_internal.h"
@@ -818,6 +819,27 @@ bool overlap(const void* p, int64_t bytes, const void* q, int64_t qbytes) {
   return a < b + static_cast<uintptr_t>(qbytes) && b < a + static_cast<uintptr_t>(bytes);
 }
 
+// An argument's memory; p NULL: not given.
+struct Span {
+  const void* p;
+  int64_t bytes;
+  const char* name;
+};
+
+// No output (the workspace is one) shares memory with an input or another output.
+int no_overlap(std::initializer_list<Span> outs, std::initializer_list<Span> ins) {
+  auto meet = [](const Span& a, const Span& b) {
+    return a.p && b.p && overlap(a.p, a.bytes, b.p, b.bytes);
+  };
+  for (auto o = outs.begin(); o != outs.end(); ++o) {
+    for (const Span& i : ins)
+      if (meet(*o, i)) return fail(BDR_EINVAL, "%s overlaps %s", o->name, i.name);
+    for (auto q = o + 1; q != outs.end(); ++q)
+      if (meet(*o, *q)) return fail(BDR_EINVAL, "%s overlaps %s", o->name, q->name);
+  }
+  return BDR_OK;
+}
+
 }  // namespace
 
 int dspark_norm(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, bdr_dtype dt,
@@ -834,9 +856,13 @@ int dspark_norm(const void* x, int64_t rows, int64_t hidden, int64_t x_stride, b
   if (mean) BDR_TRY(need_ptr(mean, "mean", 4));
   BDR_TRY(need_ptr(rstd, "rstd", 4));
   const int64_t es = dt == BDR_BF16 ? 2 : 4;
-  if (!(x == y && x_stride == hidden) &&
-      overlap(x, ((rows - 1) * x_stride + hidden) * es, y, rows * hidden * es))
+  const Span sx{x, ((rows - 1) * x_stride + hidden) * es, "x"};
+  const Span sy{y, rows * hidden * es, "y"};
+  const Span sm{mean, rows * 4, "mean"}, sr{rstd, rows * 4, "rstd"};
+  if (!(x == y && x_stride == hidden) && overlap(x, sx.bytes, y, sy.bytes))
     return fail(BDR_EINVAL, "y overlaps x (only y == x with x_stride == hidden may)");
+  BDR_TRY(no_overlap({sy, sm, sr}, {{weight, hidden * es, "weight"}, {bias, hidden * es, "bias"}}));
+  BDR_TRY(no_overlap({sm, sr}, {sx}));
   BDR_TRY(check_device());
   const hipError_t e = launch_norm(x, rows, hidden, x_stride, dt, weight, bias, eps, y, mean, rstd,
                                    as_stream(stream));
@@ -875,15 +901,20 @@ int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64
   BDR_TRY(need_ptr(weight, "weight"));
   if (mean) BDR_TRY(need_ptr(mean, "mean", 4));
   BDR_TRY(need_ptr(rstd, "rstd", 4));
-  if (dx) {
-    BDR_TRY(need_ptr(dx, "dx"));
-    const int64_t out = rows * hidden * es;
-    if ((!(dx == dy && dy_stride == hidden) &&
-         overlap(dy, ((rows - 1) * dy_stride + hidden) * es, dx, out)) ||
-        overlap(x, ((rows - 1) * x_stride + hidden) * es, dx, out))
-      return fail(BDR_EINVAL, "dx overlaps dy or x (only dx == dy with dy_stride == hidden may)");
-  }
-  if (dweight || dbias) BDR_TRY(need_ws(workspace, workspace_bytes, norm_workspace(rows, hidden)));
+  if (dx) BDR_TRY(need_ptr(dx, "dx"));
+  const size_t need = dweight || dbias ? norm_workspace(rows, hidden) : 0;
+  BDR_TRY(need_ws(workspace, workspace_bytes, need));
+  const Span sdy{dy, ((rows - 1) * dy_stride + hidden) * es, "dy"};
+  const Span sdx{dx, rows * hidden * es, "dx"};
+  const Span sdw{dweight, hidden * es, "dweight"}, sdb{dbias, hidden * es, "dbias"};
+  const Span sws{need ? workspace : nullptr, static_cast<int64_t>(need), "workspace"};
+  if (dx && !(dx == dy && dy_stride == hidden) && overlap(dy, sdy.bytes, dx, sdx.bytes))
+    return fail(BDR_EINVAL, "dx overlaps dy (only dx == dy with dy_stride == hidden may)");
+  BDR_TRY(no_overlap({sdx, sdw, sdb, sws}, {{x, ((rows - 1) * x_stride + hidden) * es, "x"},
+                                            {weight, hidden * es, "weight"},
+                                            {mean, rows * 4, "mean"},
+                                            {rstd, rows * 4, "rstd"}}));
+  BDR_TRY(no_overlap({sdw, sdb, sws}, {sdy}));
   BDR_TRY(check_device());
   const hipError_t e = launch_norm_backward(dy, dy_stride, x, x_stride, rows, hidden, dt, weight,
                                             mean, rstd, dx, dweight, dbias, workspace,
@@ -953,6 +984,25 @@ int loss_inputs(const LossProblem& p) {
   return BDR_OK;
 }
 
+// No output of a loss call shares memory with what it reads, or with another output.  lse,
+// picked and loss_grad are inputs of the backward call (NULL: outputs, or not given).
+int loss_overlaps(const LossProblem& p, std::initializer_list<Span> outs, const float* lse,
+                  const float* picked, const float* loss_grad) {
+  const int64_t es = p.dt == BDR_BF16 ? 2 : 4, us = p.u_dt == BDR_BF16 ? 2 : 4;
+  const int64_t head = p.vocab * p.rank * es, list = p.rows * p.top;
+  return no_overlap(outs, {{p.x, p.rows * p.hidden * es, "hidden"},
+                           {p.w, p.vocab * p.hidden * es, "lm_head_w"},
+                           {p.rank ? p.w1 : nullptr, head, "markov_w1"},
+                           {p.rank ? p.w2 : nullptr, head, "markov_w2"},
+                           {p.rank ? p.prev : nullptr, p.rows * 4, "prev_token"},
+                           {p.top ? nullptr : p.labels, p.rows * 4, "labels"},
+                           {p.top ? p.ids : nullptr, list * 4, "teacher_ids"},
+                           {p.top ? p.u : nullptr, list * us, "teacher_logits"},
+                           {lse, p.rows * 4, "lse"},
+                           {picked, list * 4, "picked"},
+                           {loss_grad, p.rows * 4, "loss_grad"}});
+}
+
 int loss_run_forward(const LossProblem& p, float* loss, float* lse, float* picked, void* workspace,
                      size_t workspace_bytes, void* stream, const char* name) {
   if (p.rows == 0) return BDR_OK;
@@ -960,7 +1010,13 @@ int loss_run_forward(const LossProblem& p, float* loss, float* lse, float* picke
   BDR_TRY(need_ptr(loss, "loss", 4));
   BDR_TRY(need_ptr(lse, "lse", 4));
   if (p.top) BDR_TRY(need_ptr(picked, "picked", 4));
-  BDR_TRY(need_ws(workspace, workspace_bytes, loss_workspace(p, false)));
+  const size_t need = loss_workspace(p, false);
+  BDR_TRY(need_ws(workspace, workspace_bytes, need));
+  BDR_TRY(loss_overlaps(p, {{loss, p.rows * 4, "loss"},
+                            {lse, p.rows * 4, "lse"},
+                            {p.top ? picked : nullptr, p.rows * p.top * 4, "picked"},
+                            {workspace, static_cast<int64_t>(need), "workspace"}},
+                        nullptr, nullptr, nullptr));
   BDR_TRY(check_device());
   const hipError_t e = launch_loss_forward(p, workspace, loss, lse, picked, as_stream(stream));
   if (e != hipSuccess) return hip_fail(e, name);
@@ -985,20 +1041,18 @@ int loss_run_backward(const LossProblem& p, const LossGrads& o, const float* lse
   }
   if (!o.hidden && !o.w && !o.w1 && !o.w2) return fail(BDR_EINVAL, "no gradient is wanted");
   BDR_TRY(loss_inputs(p));
-  const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
-  const int64_t bytes[4] = {p.rows * p.hidden * es, p.vocab * p.hidden * es, p.vocab * p.rank * es,
-                            p.vocab * p.rank * es};
-  const void* in[4] = {p.x, p.w, p.rank ? p.w1 : nullptr, p.rank ? p.w2 : nullptr};
-  const void* out[4] = {o.hidden, o.w, o.w1, o.w2};
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j)
-      if (out[i] && ((in[j] && overlap(out[i], bytes[i], in[j], bytes[j])) ||
-                     (j > i && out[j] && overlap(out[i], bytes[i], out[j], bytes[j]))))
-        return fail(BDR_EINVAL, "a gradient overlaps an input or another gradient");
   BDR_TRY(need_ptr(lse, "lse", 4));
   if (p.top) BDR_TRY(need_ptr(picked, "picked", 4));
   BDR_TRY(need_ptr(loss_grad, "loss_grad", 4));
-  BDR_TRY(need_ws(workspace, workspace_bytes, loss_workspace(p, true)));
+  const size_t need = loss_workspace(p, true);
+  BDR_TRY(need_ws(workspace, workspace_bytes, need));
+  const int64_t es = p.dt == BDR_BF16 ? 2 : 4;
+  BDR_TRY(loss_overlaps(p, {{o.hidden, p.rows * p.hidden * es, "d_hidden"},
+                            {o.w, p.vocab * p.hidden * es, "d_lm_head_w"},
+                            {o.w1, p.vocab * p.rank * es, "d_markov_w1"},
+                            {o.w2, p.vocab * p.rank * es, "d_markov_w2"},
+                            {workspace, static_cast<int64_t>(need), "workspace"}},
+                        lse, p.top ? picked : nullptr, loss_grad));
   BDR_TRY(check_device());
   const hipError_t e = launch_loss_backward(p, o, workspace, lse, picked, loss_grad,
                                             as_stream(stream));

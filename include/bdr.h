@@ -595,6 +595,9 @@ int dflash_fuse_fc_rows_fp8(const void* const* taps, int n_taps, int64_t rows,
  * that is NULL is not computed; gradients overwrite their output.  Every sum
  * has a fixed order, so the same inputs give the same bits.  The workspaces of
  * these calls hold no state: any contents will do, nothing needs clearing.
+ * No output, and no byte of the workspace, may lie between the first and the
+ * last element of an input or of another output (BDR_EINVAL), except where an
+ * output "may be" an input below.
  * ------------------------------------------------------------------------- */
 
 /* dspark_norm -- normalise each row (layer norm, or root-mean-square norm).
@@ -671,8 +674,7 @@ int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64
  *   lse        [rows] as written by dspark_ce_loss for the same inputs
  *   loss_grad  [rows] fp32
  *   d_hidden [rows, H], d_lm_head_w [V, H], d_markov_w1, d_markov_w2 [V, r]:
- *              dtype, each may be NULL (a frozen head costs nothing); none may
- *              overlap an input or another gradient
+ *              dtype, each may be NULL (a frozen head costs nothing)
  *   workspace  >= dspark_ce_workspace_bytes(rows, H, V, rank, dt, 1)
  * rows == 0 clears the weight gradients that are given.
  */
