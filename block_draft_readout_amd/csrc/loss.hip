@@ -56,7 +56,7 @@ struct LossRows {
   int u_bf16;
   int64_t rows;
   int hidden_size, vocab, rank, top;
-  float inv_t, temperature;
+  float scale2, temperature;   // log2(e) / temperature
   const float* lse;        // backward inputs
   const float* loss_grad;
   // workspace
@@ -215,14 +215,21 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(const LossRows g, u32x
 }
 
 // ---------------------------------------------------------------- loss values
-// log2 of the softmax denominator of one compacted row, in every lane of a wave
-__device__ __forceinline__ float row_lse2(const float2* stat, int tiles, int lane) {
+// One compacted row's reference m and log2 of its sum of 2^(z scale2 - m), in every lane of a
+// wave.  log2 of the softmax denominator is their sum, but a loss takes the label's logit from m
+// first: logits that share a large offset (2^20: half a step of the sum is 0.06) leave it whole.
+__device__ __forceinline__ float2 row_stat(const float2* stat, int tiles, int lane) {
   float2 v{-INFINITY, 0.f};
   for (int i = lane; i < tiles; i += 64) v = merge_stat(v, stat[i]);
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1)
     v = merge_stat(v, float2{__shfl_xor(v.x, m), __shfl_xor(v.y, m)});
-  return v.x + __builtin_amdgcn_logf(v.y);
+  return float2{v.x, __builtin_amdgcn_logf(v.y)};
+}
+
+// lse - z / T, z of the row that st is of: the product is not rounded before it is taken off
+__device__ __forceinline__ float less_logit(float2 st, float z, float scale2) {
+  return (__builtin_fmaf(-z, scale2, st.x) + st.y) * kLn2;
 }
 
 // one wave per original row
@@ -233,8 +240,9 @@ __global__ __launch_bounds__(256) void ce_loss_kernel(const LossRows g, float* l
   const int p = g.pos[n];
   float l = 0.f, out = 0.f;
   if (p >= 0) {
-    l = row_lse2(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane) * kLn2;
-    out = l - g.z_label[p];
+    const float2 st = row_stat(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane);
+    l = (st.x + st.y) * kLn2;
+    out = less_logit(st, g.z_label[p], g.scale2);
   }
   if (lane == 0) {
     loss[n] = out;
@@ -318,10 +326,11 @@ __global__ __launch_bounds__(256) void distill_loss_kernel(const LossRows g, con
   const int p = g.pos[n];
   float l = 0.f, out = 0.f;
   if (p >= 0) {
-    l = row_lse2(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane) * kLn2;
+    const float2 st = row_stat(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane);
+    l = (st.x + st.y) * kLn2;
     for (int j = lane; j < g.top; j += 64) {
       const float t = g.t[n * g.top + j];
-      if (t != 0.f) out += t * (logf(t) - (picked[n * g.top + j] * g.inv_t - l));
+      if (t != 0.f) out += t * (logf(t) + less_logit(st, picked[n * g.top + j], g.scale2));
     }
     out = wave_sum(out) * (g.temperature * g.temperature);
   }
@@ -587,7 +596,7 @@ void fill_rows(const LossProblem& p, const LossPlan& q, LossBuffers& b) {
   r.rank = p.rank;
   r.top = p.top;
   r.temperature = p.temperature;
-  r.inv_t = 1.0f / p.temperature;
+  r.scale2 = kLog2e / p.temperature;   // as the products' epilogues take it
   r.tiles = q.stat_tiles;
 }
 

@@ -651,7 +651,9 @@ int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64
  * label outside [0, V) leaves its row out: loss and lse are 0, every gradient
  * of the row is 0, and its hidden state, previous token and loss_grad are not
  * used (they may hold anything, NaN too).  The product takes the dtype's
- * operands and sums in fp32; lse and loss are fp32.
+ * operands and sums in fp32; lse and loss are fp32.  (loss is not the difference
+ * of the rounded lse: the label's logit is taken off the row's maximum first, so
+ * logits with a large common offset lose no digits of it.)
  *
  *   hidden     [rows, H] dtype; 0 <= rows <= 2^20; 0 < H <= 2^20, H % 8 == 0
  *              (bf16) or H % 4 == 0 (f32)
