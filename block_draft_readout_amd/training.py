@@ -24,6 +24,11 @@ _DT = {torch.bfloat16: BDR_BF16, torch.float32: BDR_F32}
 _NO_GUARD = contextlib.nullcontext()
 
 
+def _tensor(t, name: str) -> None:
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a tensor, got {type(t).__name__}")
+
+
 def _dtype(t: torch.Tensor, name: str) -> int:
     try:
         return _DT[t.dtype]
@@ -77,6 +82,7 @@ def _space(nbytes: int, device, ws: Optional[torch.Tensor]):
 # ----------------------------------------------------------------------------- row norm
 def _rows(t: torch.Tensor, name: str) -> Tuple[torch.Tensor, int, int, int]:
     """[..., H] as (tensor, rows, H, row stride): contiguous, or 2-D with a unit last stride."""
+    _tensor(t, name)
     if not t.is_cuda:
         raise ValueError(f"{name} must be a device tensor")
     if t.dim() < 1:
@@ -125,6 +131,7 @@ def dspark_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tens
     None for the root-mean-square form.  bias=False: no bias gradient (None);
     want_x / want_weight=False likewise."""
     L = _abi.load()
+    _tensor(grad, "grad")
     x, rows, h, xs = _rows(x, "x")
     dt = _dtype(x, "x")
     dev = x.device
@@ -151,7 +158,13 @@ def dspark_norm_backward(grad: torch.Tensor, x: torch.Tensor, weight: torch.Tens
 class _Readout:
     """Checked arguments that every loss call shares."""
 
-    def __init__(self, hidden, lm_head_w, markov_w1, markov_w2, prev_token):
+    def __init__(self, hidden, lm_head_w, markov_w1, markov_w2, prev_token, teacher=()):
+        _tensor(hidden, "hidden")
+        _tensor(lm_head_w, "lm_head_w")   # (a PackedWeight is none)
+        if markov_w1 is not None:
+            _tensor(markov_w1, "markov_w1")
+        for name, t in zip(("teacher_ids", "teacher_logits"), teacher):
+            _tensor(t, name)
         if not hidden.is_cuda:
             raise ValueError("hidden must be a device tensor")
         if hidden.dim() < 1 or lm_head_w.dim() != 2:
@@ -273,7 +286,7 @@ def dspark_distill_loss(hidden: torch.Tensor, lm_head_w: torch.Tensor, teacher_i
     [..., top] int32 and teacher_logits [..., top] fp32 or bf16, at temperature T.  An id
     outside [0, V) is not listed; a row without listed mass is left out (loss and lse 0)."""
     L = _abi.load()
-    r = _Readout(hidden, lm_head_w, markov_w1, markov_w2, prev_token)
+    r = _Readout(hidden, lm_head_w, markov_w1, markov_w2, prev_token, (teacher_ids, teacher_logits))
     top, targs = _teacher(r, teacher_ids, teacher_logits)
     loss, lse, picked = r.new_rows(), r.new_rows(), r.new_rows(top)
     wp, wn, _keep = _space(
@@ -297,7 +310,7 @@ def dspark_distill_backward(hidden: torch.Tensor, lm_head_w: torch.Tensor,
     """Gradients of sum(loss_grad * loss) for the loss, lse and picked of dspark_distill_loss on
     the same inputs, as dspark_ce_backward returns them."""
     L = _abi.load()
-    r = _Readout(hidden, lm_head_w, markov_w1, markov_w2, prev_token)
+    r = _Readout(hidden, lm_head_w, markov_w1, markov_w2, prev_token, (teacher_ids, teacher_logits))
     top, targs = _teacher(r, teacher_ids, teacher_logits)
     r.per_row(lse, "lse", torch.float32)
     r.per_row(picked, "picked", torch.float32, (top,))
