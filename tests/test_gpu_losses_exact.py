@@ -16,7 +16,6 @@ import numpy as np
 import pytest
 
 from oracle import training as T
-from workloads import synth
 
 # rows, features, entries, rank: two terms in narrow tiles and in tiles of 64 and 128 rows, weights
 # within and beyond the caches; one term in narrow tiles, tiles of 128 and of 256 rows, a weight
