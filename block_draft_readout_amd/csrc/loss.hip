@@ -69,6 +69,7 @@ struct LossRows {
   void* x;                 // [live, H]
   void* e;                 // [live, r]
   float* lse2;             // [live]
+  float* lse_corr;         // [live] 2^-(what rounding lse2 left), fp32 tensors only
   float* coef;             // [live]
   float* resid;            // [live] what rounding d logits left at label_c, or NULL
   float* t;                // [rows, top]
@@ -192,7 +193,13 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(const LossRows g, u32x
       g.row_of[at] = static_cast<int32_t>(n);
       if (g.rank) g.prev_c[at] = has_prev ? p : -1;
       if (BACKWARD) {
-        g.lse2[at] = g.lse[n] * kLog2e;
+        // lse in units of log2: rounded to fp32, it would move every probability of the row by up
+        // to 7e-7.  bf16 d logits have 2^-8; fp32's get the rounding back as a factor.
+        const double l2 = static_cast<double>(g.lse[n]) * 1.4426950408889634;
+        const float hi = static_cast<float>(l2);
+        g.lse2[at] = hi;
+        if (sizeof(S) == 4)
+          g.lse_corr[at] = __builtin_amdgcn_exp2f(fabsf(hi) < INFINITY ? static_cast<float>(hi - l2) : 0.f);
         g.coef[at] = g.loss_grad[n] * g.temperature;
       }
     }
@@ -215,21 +222,27 @@ __global__ __launch_bounds__(256) void loss_gather_kernel(const LossRows g, u32x
 }
 
 // ---------------------------------------------------------------- loss values
-// One compacted row's reference m and log2 of its sum of 2^(z scale2 - m), in every lane of a
-// wave.  log2 of the softmax denominator is their sum, but a loss takes the label's logit from m
-// first: logits that share a large offset (2^20: half a step of the sum is 0.06) leave it whole.
-__device__ __forceinline__ float2 row_stat(const float2* stat, int tiles, int lane) {
+// A softmax denominator: exp(lse) = 2^m s, s the row's sum of 2^(z scale2 - m), kept apart and in
+// 64 bits until a result is rounded once.  A loss takes the label's logit from m first: logits that
+// share a large offset (2^20: half a step of lse in fp32 is 0.06) leave it whole.
+struct RowLse {
+  double m, log_s;
+  __device__ float lse() const { return static_cast<float>(m * kLn2d + log_s); }
+  // lse - z / T
+  __device__ double less(float z, float scale2) const {
+    return (m - static_cast<double>(z) * scale2) * kLn2d + log_s;
+  }
+  static constexpr double kLn2d = 0.69314718055994530942;
+};
+
+// one compacted row's, in every lane of a wave
+__device__ __forceinline__ RowLse row_lse(const float2* stat, int tiles, int lane) {
   float2 v{-INFINITY, 0.f};
   for (int i = lane; i < tiles; i += 64) v = merge_stat(v, stat[i]);
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1)
     v = merge_stat(v, float2{__shfl_xor(v.x, m), __shfl_xor(v.y, m)});
-  return float2{v.x, __builtin_amdgcn_logf(v.y)};
-}
-
-// lse - z / T, z of the row that st is of: the product is not rounded before it is taken off
-__device__ __forceinline__ float less_logit(float2 st, float z, float scale2) {
-  return (__builtin_fmaf(-z, scale2, st.x) + st.y) * kLn2;
+  return RowLse{v.x, log(static_cast<double>(v.y))};
 }
 
 // one wave per original row
@@ -240,9 +253,9 @@ __global__ __launch_bounds__(256) void ce_loss_kernel(const LossRows g, float* l
   const int p = g.pos[n];
   float l = 0.f, out = 0.f;
   if (p >= 0) {
-    const float2 st = row_stat(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane);
-    l = (st.x + st.y) * kLn2;
-    out = less_logit(st, g.z_label[p], g.scale2);
+    const RowLse d = row_lse(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane);
+    l = d.lse();
+    out = static_cast<float>(d.less(g.z_label[p], g.scale2));
   }
   if (lane == 0) {
     loss[n] = out;
@@ -326,11 +339,11 @@ __global__ __launch_bounds__(256) void distill_loss_kernel(const LossRows g, con
   const int p = g.pos[n];
   float l = 0.f, out = 0.f;
   if (p >= 0) {
-    const float2 st = row_stat(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane);
-    l = (st.x + st.y) * kLn2;
+    const RowLse d = row_lse(g.stat + static_cast<int64_t>(p) * g.tiles, g.tiles, lane);
+    l = d.lse();
     for (int j = lane; j < g.top; j += 64) {
       const float t = g.t[n * g.top + j];
-      if (t != 0.f) out += t * (logf(t) + less_logit(st, picked[n * g.top + j], g.scale2));
+      if (t != 0.f) out += t * (logf(t) + static_cast<float>(d.less(picked[n * g.top + j], g.scale2)));
     }
     out = wave_sum(out) * (g.temperature * g.temperature);
   }
@@ -359,7 +372,8 @@ __global__ __launch_bounds__(256) void distill_fix_kernel(const LossRows g, cons
   float t = 0.f;
   for (int q = 0; q < g.top; ++q)
     if (ids[q] == id) t += g.t[n * g.top + q];
-  const float pr = __builtin_amdgcn_exp2f(picked[n * g.top + j] * scale2 - g.lse2[p]);
+  float pr = __builtin_amdgcn_exp2f(__builtin_fmaf(picked[n * g.top + j], scale2, -g.lse2[p]));
+  if constexpr (sizeof(S) == 4) pr *= g.lse_corr[p];
   const float v = g.coef[p] * (pr - t);
   constexpr int KB = 128 / static_cast<int>(sizeof(S));   // d logits lie in panels of KB columns
   S* at = dz + (id - v0) / KB * panel + (static_cast<int64_t>(p) << two) * KB + (id - v0) % KB;
@@ -567,6 +581,7 @@ size_t lay_out(const LossProblem& p, const LossPlan& q, bool backward, char* bas
     r.stat = s.take<float2>(p.rows * q.stat_tiles);
   } else {
     r.lse2 = s.take<float>(p.rows);
+    r.lse_corr = s.take<float>(p.dt == BDR_F32 ? p.rows : 0);
     r.coef = s.take<float>(p.rows);
     const int64_t rows = p.rows << q.two;
     b.dz = s.take<char>(rows * q.ld * es);
@@ -727,6 +742,7 @@ hipError_t backward(const LossProblem& p, const LossGrads& o, void* workspace, c
       g.label0 = static_cast<int>(v0);
     }
     g.lse2 = b.r.lse2;
+    g.lse_corr = b.r.lse_corr;
     g.coef = b.r.coef;
     g.out = b.dz;
     g.ldo = ld;

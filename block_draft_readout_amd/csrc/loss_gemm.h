@@ -73,6 +73,7 @@ struct LossGemm {
   float* resid;            // [M] what rounding d logits left at the label, or NULL (LE_OUT: added, up to
                            // kHeldRows rows)
   const float* lse2;       // [M] log2 of the softmax denominator
+  const float* lse_corr;   // [M] fp32: factor of the probabilities, what rounding lse2 left
   const float* coef;       // [M] gradient factor
   void* out;               // LE_DLOGITS panels, LE_PARTIAL [splits, slab], LE_OUT [M, ldo]
   int64_t ldo;             // LE_DLOGITS: N padded to whole panels
@@ -715,13 +716,14 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       // label, by far the largest entry as a rule, is added in fp32 to d hidden and d
       // embedding, and up to kHeldRows rows to the weights' gradients.
       // Columns from N to the padded width hold zeros.
-      float l2[T::WTM], cf[T::WTM];
+      float l2[T::WTM], cf[T::WTM], corr[T::WTM];
       int lab[T::WTM];   // column of the label, from this lane's first
       static_for<T::WTM>([&](auto i) {   // all before the stores' waits
         const int64_t m = min<int64_t>(mw + decltype(i)::value * 16, M - 1);
         lab[i] = g.label ? g.label[m] - g.label0 - static_cast<int>(nw) : -1;
         l2[i] = g.lse2[m];
         cf[i] = g.coef[m];
+        if constexpr (ES == 4) corr[i] = g.lse_corr[m];
       });
       static_for<T::WTM>([&](auto i) {
         auto value = [&](auto j) {
@@ -729,7 +731,8 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
 #pragma unroll
           for (int c = 0; c < 4; ++c) {
             const int n = decltype(j)::value * 16 + c;
-            const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -l2[i]));
+            float p = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][c], g.scale2, -l2[i]));
+            if constexpr (ES == 4) p *= corr[i];
             v[c] = n < n_in ? cf[i] * (n == lab[i] ? p - 1.f : p) : 0.f;
           }
           return v;
