@@ -242,7 +242,8 @@ __device__ __forceinline__ RowLse row_lse(const float2* stat, int tiles, int lan
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1)
     v = merge_stat(v, float2{__shfl_xor(v.x, m), __shfl_xor(v.y, m)});
-  return RowLse{v.x, log(static_cast<double>(v.y))};
+  // (a join of two pairs is not the same bits from both sides: the first lane's counts)
+  return RowLse{__shfl(v.x, 0), log(static_cast<double>(__shfl(v.y, 0)))};
 }
 
 // one wave per original row
@@ -263,70 +264,76 @@ __global__ __launch_bounds__(256) void ce_loss_kernel(const LossRows g, float* l
   }
 }
 
-// logits at the teacher's entries: picked[n, j] = z[n, id_j].  GROUP lanes take
-// four entries of a row, so a hidden chunk serves four weight rows: a wave for
-// short rows, else a workgroup (few rows wait for memory, and 256 lanes have a
-// row's weights in flight at once).  Grid (rows, entries / (1024 / GROUP)).
-template <typename S, int GROUP>
-__global__ __launch_bounds__(256) void distill_pick_kernel(const LossRows g, float* picked) {
+// logits at the teacher's entries: picked[n, j] = z[n, id_j], bit for bit those that the softmax is
+// made of, so that what summing them lost cancels in lse - z (a dot product in another order left
+// 5e-5 of a confident row's loss).  A matrix product's element is one chain of MFMAs along the
+// reduction, whatever the tile: this one walks that chain with sixteen entries' weight rows as one
+// operand and the row's hidden state, in all sixteen columns, as the other, in pieces of 64 bytes of
+// every row, a batch of pieces on its way while another is multiplied (1 row of 5120, 20 entries: 12
+// us, bound by latency; dot products by whole workgroups took 5, twelve waves handing the chain on
+// take 10; 4096 rows of 5120, 64 entries: 440 us, 6 TB/s; the dot products took 480).
+// Grid (rows, entries / 16), a wave each.
+constexpr int kPickAhead = 8;     // pieces of a batch
+
+template <typename S>
+__global__ __launch_bounds__(64) void distill_pick_kernel(const LossRows g, float* picked) {
   constexpr int PER = Elem<S>::PER16;
-  __shared__ float part[4][4];
-  const int lane = static_cast<int>(threadIdx.x) % GROUP;
-  const int wave = static_cast<int>(threadIdx.x) >> 6;
+  const int lane = static_cast<int>(threadIdx.x);
+  const int r16 = lane & 15, grp = lane >> 4;
   const int64_t n = blockIdx.x;
+  const int j0 = static_cast<int>(blockIdx.y) * 16;
   const int p = g.pos[n];
-  const int j0 = (static_cast<int>(blockIdx.y) * (256 / GROUP) + static_cast<int>(threadIdx.x) / GROUP) * 4;
-  int id[4];
+  int id = p >= 0 && j0 + r16 < g.top ? g.ids[n * g.top + j0 + r16] : -1;
+  if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(g.vocab)) id = -1;
+  // pieces of the hidden state, then of the embedding
+  const int first = (g.hidden_size + 4 * PER - 1) / (4 * PER);
+  const int pieces = __ballot(id >= 0) == 0ull ? 0 : first + (g.rank + 4 * PER - 1) / (4 * PER);
+  const int64_t row = max(p, 0), entry = max(id, 0);
+  const S* x = static_cast<const S*>(g.x) + row * g.hidden_size;
+  const S* w = static_cast<const S*>(g.w) + entry * g.hidden_size;
+  const S* e = static_cast<const S*>(g.e) + row * g.rank;
+  const S* w2 = static_cast<const S*>(g.w2) + entry * g.rank;
+  typedef u32x4_t Batch[kPickAhead];
+  auto load = [&](int c0, Batch& a, Batch& b) {   // zeros past a stretch's end, and past the last piece
+    if (c0 < pieces && (c0 + kPickAhead) * 4 * PER <= g.hidden_size) {
+      // whole pieces (an entry that is not listed reads row 0 and is dropped)
+      const S* xc = x + (c0 * 4 + grp) * PER;
+      const S* wc = w + (c0 * 4 + grp) * PER;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    id[q] = p >= 0 && j0 + q < g.top ? g.ids[n * g.top + j0 + q] : -1;
-    if (static_cast<uint32_t>(id[q]) >= static_cast<uint32_t>(g.vocab)) id[q] = -1;
-  }
-  float s[4] = {0.f, 0.f, 0.f, 0.f};
-  auto dots = [&](const void* xv, const void* wv, int len) {
-    const S* x = static_cast<const S*>(xv) + static_cast<int64_t>(p) * len;
-    const S* w = static_cast<const S*>(wv);
-#pragma unroll 2
-    for (int c = lane * PER; c < len; c += GROUP * PER) {
-      const u32x4_t xr = load16(x + c);
-      u32x4_t wr[4];
+      for (int q = 0; q < kPickAhead; ++q) {
+        a[q] = load16(xc + q * 4 * PER);
+        b[q] = load16(wc + q * 4 * PER);
+      }
+      return;
+    }
 #pragma unroll
-      for (int q = 0; q < 4; ++q)   // an entry that is not listed reads row 0 and is dropped
-        wr[q] = load16(w + static_cast<int64_t>(max(id[q], 0)) * len + c);
-#pragma unroll
-      for (int q = 0; q < 4; ++q)
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          if constexpr (sizeof(S) == 2) {
-            s[q] += __uint_as_float(xr[k] << 16) * __uint_as_float(wr[q][k] << 16);
-            s[q] += __uint_as_float(xr[k] & 0xFFFF0000u) * __uint_as_float(wr[q][k] & 0xFFFF0000u);
-          } else {
-            s[q] += __uint_as_float(xr[k]) * __uint_as_float(wr[q][k]);
-          }
-        }
+    for (int q = 0; q < kPickAhead; ++q) {
+      const bool second = c0 + q >= first;
+      const int col = ((second ? c0 + q - first : c0 + q) * 4 + grp) * PER;
+      const bool in = c0 + q < pieces && col < (second ? g.rank : g.hidden_size);
+      a[q] = in ? load16((second ? e : x) + col) : u32x4_t{0, 0, 0, 0};
+      b[q] = in && id >= 0 ? load16((second ? w2 : w) + col) : u32x4_t{0, 0, 0, 0};
     }
   };
-  if (p >= 0 && (id[0] & id[1] & id[2] & id[3]) != -1) {
-    dots(g.x, g.w, g.hidden_size);
-    if (g.rank) dots(g.e, g.w2, g.rank);
+  f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+  auto multiply = [&](const Batch& a, const Batch& b) {
+#pragma unroll
+    for (int q = 0; q < kPickAhead; ++q) acc = mma16(b[q], a[q], acc, S());
+  };
+  Batch a0, b0, a1, b1;
+  load(0, a0, b0);
+  for (int c = 0; c < pieces; c += 2 * kPickAhead) {
+    load(c + kPickAhead, a1, b1);
+    multiply(a0, b0);
+    load(c + 2 * kPickAhead, a0, b0);
+    multiply(a1, b1);
   }
+  // a lane holds entries 4 grp .. + 3 in every column
 #pragma unroll
-  for (int q = 0; q < 4; ++q) s[q] = wave_sum(s[q]);
-  if constexpr (GROUP > 64) {
-    if ((threadIdx.x & 63) == 0) {
-#pragma unroll
-      for (int q = 0; q < 4; ++q) part[wave][q] = s[q];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int q = 0; q < 4; ++q) s[q] = part[0][q] + part[1][q] + part[2][q] + part[3][q];
-  }
-  if (lane < 4 && j0 + lane < g.top) {
-    float v = 0.f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q)
-      if (lane == q && id[q] >= 0) v = s[q];
-    picked[n * g.top + j0 + lane] = v;
+  for (int c = 0; c < 4; ++c) {
+    const int j = 4 * grp + c;
+    const bool listed = __shfl(id, j) >= 0;
+    if (r16 == 0 && j0 + j < g.top) picked[n * g.top + j0 + j] = listed ? acc[c] : 0.f;
   }
 }
 
@@ -683,16 +690,10 @@ hipError_t forward(const LossProblem& p, void* workspace, float* loss, float* ls
   g.stat = b.r.stat;
   BDR_LAUNCH(launch_loss_stats(p.dt, p.rows, g, st));
   if (p.top) {
-    auto pick = [&](auto group) {
-      constexpr int GROUP = decltype(group)::value;
-      const int per = 4 * (256 / GROUP);
-      hipLaunchKernelGGL((distill_pick_kernel<S, GROUP>),
-                         dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.top + per - 1) / per)),
-                         dim3(256), 0, st, b.r, picked);
-      return hipGetLastError();
-    };
-    BDR_LAUNCH(p.hidden / Elem<S>::PER16 <= 128 ? pick(std::integral_constant<int, 64>{})
-                                                : pick(std::integral_constant<int, 256>{}));
+    hipLaunchKernelGGL(distill_pick_kernel<S>,
+                       dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.top + 15) / 16)),
+                       dim3(64), 0, st, b.r, picked);
+    BDR_LAUNCH(hipGetLastError());
     hipLaunchKernelGGL(distill_loss_kernel, dim3(waves4(p.rows)), dim3(256), 0, st, b.r, picked,
                        loss, lse);
   } else {
