@@ -285,8 +285,9 @@ __global__ __launch_bounds__(64) void distill_pick_kernel(const LossRows g, floa
   const int p = g.pos[n];
   int id = p >= 0 && j0 + r16 < g.top ? g.ids[n * g.top + j0 + r16] : -1;
   if (static_cast<uint32_t>(id) >= static_cast<uint32_t>(g.vocab)) id = -1;
-  // pieces of the hidden state, then of the embedding
-  const int first = (g.hidden_size + 4 * PER - 1) / (4 * PER);
+  // pieces of the hidden state, then of the embedding; two are a step of the product, and the
+  // embedding starts a step
+  const int first = (g.hidden_size + 8 * PER - 1) / (8 * PER) * 2;
   const int pieces = __ballot(id >= 0) == 0ull ? 0 : first + (g.rank + 4 * PER - 1) / (4 * PER);
   const int64_t row = max(p, 0), entry = max(id, 0);
   const S* x = static_cast<const S*>(g.x) + row * g.hidden_size;
@@ -318,7 +319,13 @@ __global__ __launch_bounds__(64) void distill_pick_kernel(const LossRows g, floa
   f32x4_t acc{0.f, 0.f, 0.f, 0.f};
   auto multiply = [&](const Batch& a, const Batch& b) {
 #pragma unroll
-    for (int q = 0; q < kPickAhead; ++q) acc = mma16(b[q], a[q], acc, S());
+    for (int q = 0; q < kPickAhead; q += 2) {
+      f32x4_t s{0.f, 0.f, 0.f, 0.f};
+      if constexpr (sizeof(S) == 2) s = acc;   // (fp32: a step is summed by itself)
+      s = mma16(b[q], a[q], s, S());
+      s = mma16(b[q + 1], a[q + 1], s, S());
+      if constexpr (sizeof(S) == 2) acc = s; else acc += s;
+    }
   };
   Batch a0, b0, a1, b1;
   load(0, a0, b0);

@@ -447,6 +447,13 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   };
 
   f32x4_t acc[T::WTM][T::WTN];
+  // fp32 tensors: a step's products are summed by themselves before they join the running sum, an
+  // eighth of the roundings at its size (bf16 tiles have no registers for it, and their operands'
+  // roundings are larger)
+  f32x4_t part[T::WTM][T::WTN];
+  auto& sum = [&]() -> auto& {
+    if constexpr (ES == 4) return part; else return acc;
+  }();
   typedef u32x4_t FragA[T::WTM];
   typedef u32x4_t FragB[T::WTN];
   // operand of MFMA tile `tile` (16 rows of the operand) in half `half` of a step
@@ -549,6 +556,10 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       static_for<T::WTN>([&](auto j) { acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
     });
     for (int s = s_lo; s < s_hi; ++s) {
+      if constexpr (ES == 4)
+        static_for<T::WTM>([&](auto i) {
+          static_for<T::WTN>([&](auto j) { part[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
+        });
       // this wave's loads of the step have landed when at most those of the
       // STAGES - 2 steps after it remain; after the barrier every wave's have,
       // and every wave is done with the stage the next loads overwrite
@@ -562,16 +573,16 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
       static_for<NT>([&](auto ec) {
         constexpr int e = decltype(ec)::value;
         constexpr int every = kSpread ? NT / T::LOADS : NT;
-        acc[e / T::WTN][e % T::WTN] =
-            mma16(b[e % T::WTN], a[e / T::WTN], acc[e / T::WTN][e % T::WTN], S());
+        sum[e / T::WTN][e % T::WTN] =
+            mma16(b[e % T::WTN], a[e / T::WTN], sum[e / T::WTN][e % T::WTN], S());
         if constexpr (kSpread && e % every == every - 1 && e / every < T::LOADS)
           dma_one(std::integral_constant<int, e / every>{});
       });
       read_frags(buf_a, buf, std::integral_constant<int, 1>{}, a, b);
       static_for<NT>([&](auto ec) {
         constexpr int e = decltype(ec)::value;
-        acc[e / T::WTN][e % T::WTN] =
-            mma16(b[e % T::WTN], a[e / T::WTN], acc[e / T::WTN][e % T::WTN], S());
+        sum[e / T::WTN][e % T::WTN] =
+            mma16(b[e % T::WTN], a[e / T::WTN], sum[e / T::WTN][e % T::WTN], S());
       });
       if constexpr (kSpread) {   // keep that order through scheduling
         constexpr int every = NT / T::LOADS * Elem<S>::MFMA_PER16;
@@ -585,6 +596,10 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         if constexpr (T::READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
         __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS, 0);
       }
+      if constexpr (ES == 4)
+        static_for<T::WTM>([&](auto i) {
+          static_for<T::WTN>([&](auto j) { acc[i][j] += part[i][j]; });
+        });
       buf = buf + 1 == T::STAGES ? 0 : buf + 1;
       if constexpr (T::LAG > 0) buf_a ^= 1; else buf_a = buf;
       // next into the stages of this step
