@@ -33,6 +33,13 @@ int64_t loss_tiles(int64_t rows, int64_t cols) {
 // 78 drawn problems; a step of 128 rows of 5120 1283 -> 1307 us).
 constexpr int64_t kTwoTermRows = 64;
 
+// Logits of up to this many bf16 rows are summed in blocks of kJoinSteps steps (fp32's of one): the
+// loss of a confident row is a small difference, and a few rows' errors do not average out (one row
+// of 3528: 3.3e-6 of its loss as a chain of MFMAs, a vector product in fp32 5e-7).  Tiles for more
+// rows have no registers for it.
+constexpr int64_t kJoinRows = kTwoTermRows;
+constexpr int kJoinSteps = 4;
+
 // Weights larger than the last-level cache (256 MiB) stay in HBM between the products
 // that read them: bytes of `n` bf16 entries above that.
 inline bool beyond_cache(int64_t n) { return n * 2 > (int64_t(256) << 20); }

@@ -270,12 +270,13 @@ __global__ __launch_bounds__(256) void ce_loss_kernel(const LossRows g, float* l
 // reduction, whatever the tile: this one walks that chain with sixteen entries' weight rows as one
 // operand and the row's hidden state, in all sixteen columns, as the other, in pieces of 64 bytes of
 // every row, a batch of pieces on its way while another is multiplied (1 row of 5120, 20 entries: 12
-// us, bound by latency; dot products by whole workgroups took 5, twelve waves handing the chain on
+// us, bound by latency; dot products by whole workgroups took 5, twelve waves handing the sums on
 // take 10; 4096 rows of 5120, 64 entries: 440 us, 6 TB/s; the dot products took 480).
 // Grid (rows, entries / 16), a wave each.
 constexpr int kPickAhead = 8;     // pieces of a batch
 
-template <typename S>
+// JOIN: steps of two pieces that are summed by themselves, as the product's tiles do
+template <typename S, int JOIN>
 __global__ __launch_bounds__(64) void distill_pick_kernel(const LossRows g, float* picked) {
   constexpr int PER = Elem<S>::PER16;
   const int lane = static_cast<int>(threadIdx.x);
@@ -316,15 +317,18 @@ __global__ __launch_bounds__(64) void distill_pick_kernel(const LossRows g, floa
       b[q] = in && id >= 0 ? load16((second ? w2 : w) + col) : u32x4_t{0, 0, 0, 0};
     }
   };
-  f32x4_t acc{0.f, 0.f, 0.f, 0.f};
+  static_assert(kPickAhead % 2 == 0 && (JOIN == 0 || kPickAhead % (2 * JOIN) == 0), "whole blocks");
+  f32x4_t acc{0.f, 0.f, 0.f, 0.f}, part;
   auto multiply = [&](const Batch& a, const Batch& b) {
 #pragma unroll
-    for (int q = 0; q < kPickAhead; q += 2) {
-      f32x4_t s{0.f, 0.f, 0.f, 0.f};
-      if constexpr (sizeof(S) == 2) s = acc;   // (fp32: a step is summed by itself)
-      s = mma16(b[q], a[q], s, S());
-      s = mma16(b[q + 1], a[q + 1], s, S());
-      if constexpr (sizeof(S) == 2) acc = s; else acc += s;
+    for (int q = 0; q < kPickAhead; ++q) {
+      if constexpr (JOIN > 0) {
+        if (q % (2 * JOIN) == 0) part = f32x4_t{0.f, 0.f, 0.f, 0.f};
+        part = mma16(b[q], a[q], part, S());
+        if (q % (2 * JOIN) == 2 * JOIN - 1) acc += part;
+      } else {
+        acc = mma16(b[q], a[q], acc, S());
+      }
     }
   };
   Batch a0, b0, a1, b1;
@@ -697,10 +701,17 @@ hipError_t forward(const LossProblem& p, void* workspace, float* loss, float* ls
   g.stat = b.r.stat;
   BDR_LAUNCH(launch_loss_stats(p.dt, p.rows, g, st));
   if (p.top) {
-    hipLaunchKernelGGL(distill_pick_kernel<S>,
-                       dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.top + 15) / 16)),
-                       dim3(64), 0, st, b.r, picked);
-    BDR_LAUNCH(hipGetLastError());
+    auto pick = [&](auto join) {
+      hipLaunchKernelGGL((distill_pick_kernel<S, decltype(join)::value>),
+                         dim3(static_cast<unsigned>(p.rows), static_cast<unsigned>((p.top + 15) / 16)),
+                         dim3(64), 0, st, b.r, picked);
+      return hipGetLastError();
+    };
+    if constexpr (sizeof(S) == 4)
+      BDR_LAUNCH(pick(std::integral_constant<int, 1>{}));
+    else
+      BDR_LAUNCH(p.rows <= kJoinRows ? pick(std::integral_constant<int, kJoinSteps>{})
+                                     : pick(std::integral_constant<int, 0>{}));
     hipLaunchKernelGGL(distill_loss_kernel, dim3(waves4(p.rows)), dim3(256), 0, st, b.r, picked,
                        loss, lse);
   } else {

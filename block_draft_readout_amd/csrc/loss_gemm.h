@@ -82,7 +82,7 @@ struct LossGemm {
 };
 
 template <typename S_, bool AKS_, bool BKS_, int WM_, int WN_, int WTM_, int WTN_, int STAGES_,
-          bool LOOP_ = false, bool NT_B_ = false, int STAGES_A_ = STAGES_>
+          bool LOOP_ = false, bool NT_B_ = false, int STAGES_A_ = STAGES_, int JOIN_ = 0>
 struct LossTile {
   using S = S_;
   static constexpr bool AKS = AKS_, BKS = BKS_;   // reduction slow
@@ -90,6 +90,10 @@ struct LossTile {
   static constexpr bool LOOP = LOOP_;             // a workgroup walks several tiles
   static constexpr bool NT_B = NT_B_;             // B is streamed once: non-temporal loads
   static constexpr int STAGES_A = STAGES_A_;      // stages of A where it has fewer (it comes from L2)
+  // Steps whose products are summed by themselves before they join the running sum (0: a chain
+  // of MFMAs on the running sum).  An eighth of the roundings at its size, for as many registers
+  // again: in fp32 a step (8 MFMAs), in bf16 four (8), where the tile has them.
+  static constexpr int JOIN = sizeof(S) == 4 ? 1 : JOIN_;
   static constexpr int WAVES = WM * WN;
   static constexpr int BM = 16 * WM * WTM, BN = 16 * WN * WTN;
   static constexpr int KB = 128 / static_cast<int>(sizeof(S));
@@ -447,12 +451,9 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   };
 
   f32x4_t acc[T::WTM][T::WTN];
-  // fp32 tensors: a step's products are summed by themselves before they join the running sum, an
-  // eighth of the roundings at its size (bf16 tiles have no registers for it, and their operands'
-  // roundings are larger)
-  f32x4_t part[T::WTM][T::WTN];
+  f32x4_t part[T::WTM][T::WTN];   // JOIN: what has not joined acc
   auto& sum = [&]() -> auto& {
-    if constexpr (ES == 4) return part; else return acc;
+    if constexpr (T::JOIN > 0) return part; else return acc;
   }();
   typedef u32x4_t FragA[T::WTM];
   typedef u32x4_t FragB[T::WTN];
@@ -553,13 +554,9 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
   int buf = 0, buf_a = 0;   // stages of B and A
   for (int t = t_first; t < t_end; t += wgs) {
     static_for<T::WTM>([&](auto i) {
-      static_for<T::WTN>([&](auto j) { acc[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
+      static_for<T::WTN>([&](auto j) { acc[i][j] = part[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
     });
     for (int s = s_lo; s < s_hi; ++s) {
-      if constexpr (ES == 4)
-        static_for<T::WTM>([&](auto i) {
-          static_for<T::WTN>([&](auto j) { part[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f}; });
-        });
       // this wave's loads of the step have landed when at most those of the
       // STAGES - 2 steps after it remain; after the barrier every wave's have,
       // and every wave is done with the stage the next loads overwrite
@@ -596,10 +593,15 @@ __device__ __forceinline__ void loss_gemm_body(const LossGemm& g, int block, int
         if constexpr (T::READS > 0) __builtin_amdgcn_sched_group_barrier(0x100, T::READS, 0);
         __builtin_amdgcn_sched_group_barrier(0x008, T::MFMAS, 0);
       }
-      if constexpr (ES == 4)
-        static_for<T::WTM>([&](auto i) {
-          static_for<T::WTN>([&](auto j) { acc[i][j] += part[i][j]; });
-        });
+      if constexpr (T::JOIN > 0) {
+        if (T::JOIN == 1 || (s - s_lo) % T::JOIN == T::JOIN - 1 || s == s_hi - 1)
+          static_for<T::WTM>([&](auto i) {
+            static_for<T::WTN>([&](auto j) {
+              acc[i][j] += part[i][j];
+              part[i][j] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+            });
+          });
+      }
       buf = buf + 1 == T::STAGES ? 0 : buf + 1;
       if constexpr (T::LAG > 0) buf_a ^= 1; else buf_a = buf;
       // next into the stages of this step

@@ -34,10 +34,16 @@ using LogitsF32 = LossTile<float, false, false, 2, 2, 2, 2, 2>;            // 64
 using LogitsSmall = LossTile<uint16_t, false, false, 1, 4, 2, 2, 4>;       // 32 x 128
 using LogitsMid = LossTile<uint16_t, false, false, 2, 2, 4, 4, 2>;         // 128 x 128
 using LogitsFew = LossTile<uint16_t, false, false, 2, 4, 2, 5, 3>;         // 64 x 320
-using LogitsFewOnce = LossTile<uint16_t, false, false, 2, 4, 2, 5, 3, false, true>;
 using LogitsSome = LossTile<uint16_t, false, false, 2, 4, 4, 5, 3, false, false, 2>;   // 128 x 320
 using LogitsSomeOnce = LossTile<uint16_t, false, false, 2, 4, 4, 5, 3, false, true, 2>;
 using LogitsMany = LossTile<uint16_t, false, false, 2, 4, 8, 5, 2>;        // 256 x 320
+
+static_assert(kJoinRows == 64, "the rows of one FewRowsOnce tile");
+// up to kJoinRows rows
+using FewRowsSmall = LossTile<uint16_t, false, false, 1, 4, 2, 2, 4, false, false, 4, kJoinSteps>;
+using FewRowsMid = LossTile<uint16_t, false, false, 2, 2, 4, 4, 2, false, false, 2, kJoinSteps>;
+using FewRowsFew = LossTile<uint16_t, false, false, 2, 4, 2, 5, 3, false, false, 3, kJoinSteps>;
+using FewRowsOnce = LossTile<uint16_t, false, false, 2, 4, 2, 5, 3, false, true, 3, kJoinSteps>;
 
 // Microseconds of a product on tiles T: rounds of workgroups over the chip times its
 // steps of 64 elements times `step` (of a full chip, from the times above), and no
@@ -55,15 +61,21 @@ template <typename F>
 auto with_logits_tile(bdr_dtype dt, int64_t rows, int64_t cols, int64_t hidden, F&& f) {
   if (dt != BDR_BF16) return f(LogitsF32{});
   const bool stream = beyond_cache(cols * hidden) && hidden % 64 == 0;
-  const bool few_once = stream && rows <= LogitsFew::BM, some_once = stream && rows <= LogitsSome::BM;
+  const bool few_rows = rows <= kJoinRows;
+  const bool few_once = stream && few_rows, some_once = stream && rows <= LogitsSome::BM;
+  // (few rows are summed in blocks and have d logits of two terms, which the tall tiles do not)
   const double t[5] = {logits_us<LogitsFew>(rows, cols, hidden, 1.2, few_once),
-                       logits_us<LogitsSome>(rows, cols, hidden, 1.3, some_once),
-                       // (its d logits have no second term, which few rows need)
-                       rows <= kTwoTermRows ? 1e30 : logits_us<LogitsMany>(rows, cols, hidden, 2.1, false),
+                       few_rows ? 1e30 : logits_us<LogitsSome>(rows, cols, hidden, 1.3, some_once),
+                       few_rows ? 1e30 : logits_us<LogitsMany>(rows, cols, hidden, 2.1, false),
                        logits_us<LogitsMid>(rows, cols, hidden, 1.15, false),
                        logits_us<LogitsSmall>(rows, cols, hidden, 0.85, false)};
   const int best = static_cast<int>(std::min_element(t, t + 5) - t);
-  if (best == 0) return few_once ? f(LogitsFewOnce{}) : f(LogitsFew{});
+  if (few_rows) {
+    if (best == 0) return few_once ? f(FewRowsOnce{}) : f(FewRowsFew{});
+    if (best == 3) return f(FewRowsMid{});
+    return f(FewRowsSmall{});
+  }
+  if (best == 0) return f(LogitsFew{});
   if (best == 1) return some_once ? f(LogitsSomeOnce{}) : f(LogitsSome{});
   if (best == 2) return f(LogitsMany{});
   if (best == 3) return f(LogitsMid{});
