@@ -16,8 +16,8 @@
 //     2000 us; 2048 rows 902 and 1052 us; 30 x 2560 entries: 1280 rows 934 and 1010
 //     us, 1000 rows 794 and 815 us, 768 rows 657 and 646 us, 512 rows 512 and 473 us
 //     (H = 2560: 490 and 526, 420 and 435, 351 and 348, 268 and 255 us)
-//   d weight, 151936 entries (1.56 GB written): 128 rows 128 x 320 358 us, one
-//     tile per workgroup 504 us; 7 rows 269 - 311 us
+//   d weight, 151936 entries (1.56 GB written): 128 rows 128 x 320 376 us by itself and
+//     444 us in a traced step, where one tile per workgroup takes 579 us; 7 rows 269 - 311 us
 //   d w2, rank 64, 151936 entries: 4096 rows 231 us (5.4 TB/s of d logits; 2 stages
 //     231 us), 1000 rows 62 us (2 stages 65 us), 128 rows 15.7 us (14.8 us)
 

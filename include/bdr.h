@@ -15,14 +15,14 @@
  *     by the caller, 16-byte aligned; workspaces are 256-byte aligned.  The
  *     library never allocates or frees device memory and never synchronises.
  *   - Workspaces hold cross-workgroup counters and argmax keys (those of the
- *     training calls at the end hold none): a workspace
- *     must be zero-filled once before its first use, and every call that
- *     completes leaves its counters and hand-off slots zero-filled again (the
- *     Markov error word too when the call is given a status word), so it can
- *     be reused by later calls and by graph replays.  Other workspace bytes
- *     (argmax keys and log-sum-exp partials of verification) are scratch that every
- *     call rewrites before reading.  One workspace must not be used by two
- *     calls that can run concurrently.
+ *     training calls at the end hold none): a workspace must be zero-filled
+ *     once before its first use, and every call that completes leaves its
+ *     counters and hand-off slots zero-filled again (the Markov error word too
+ *     when the call is given a status word), so it can be reused by later calls
+ *     and by graph replays.  Other workspace bytes (argmax keys and log-sum-exp
+ *     partials of verification) are scratch that every call rewrites before
+ *     reading.  One workspace must not be used by two calls that can run
+ *     concurrently.
  *   - `stream` is a hipStream_t (NULL = the legacy default stream); all work is
  *     enqueued on it in order, so calls on one stream see each other's results.
  *   - A call with no work (rows == 0 or batch == 0) returns BDR_OK after
@@ -33,10 +33,12 @@
  *     (thread-local text).
  *   - Values that live on the device (token ids, logits) are not checked: a
  *     draft token outside [0, V) never matches, and a previous token outside
- *     [0, V) contributes no Markov bias.  Floating inputs must be finite.
+ *     [0, V) contributes no Markov bias.  Floating inputs must be finite (the
+ *     training calls say which may hold anything).
  *   - Operands are read with 32-bit-offset buffer loads: each tap / hidden
  *     tensor, each 64-row slab of a weight and each Markov matrix must be
- *     under 2^31 bytes (BDR_EUNSUPPORTED otherwise).
+ *     under 2^31 bytes (BDR_EUNSUPPORTED otherwise).  The training calls give
+ *     their own, larger limits.
  *   - Token ids are int32, counters int64.  dtype selects the storage of
  *     weights and activations (BDR_BF16 or BDR_F32); accumulation is fp32.
  *     BDR_BF16_PACKED is bf16 storage with the GEMM weight (fc_w, lm_head_w)
@@ -669,10 +671,12 @@ int dspark_norm_backward(const void* dy, int64_t dy_stride, const void* x, int64
  *   d_hidden = dz lm_head_w,            d_lm_head_w = dz^T hidden
  *   d_markov_w2 = dz^T markov_w1[prev], d_markov_w1[p] = sum_{m: prev[m] = p} dz[m] markov_w2
  * dz is recomputed a piece of the vocabulary at a time and rounded to the dtype
- * as an operand of these products (bf16 of up to 64 rows: kept as two such terms,
- * 16 bits; of more: what the rounding takes from the label's entry -- of a teacher's
- * list, the heaviest -- is given back in fp32, to the weights' gradients for up to 512
- * rows), which sum in fp32; each gradient is rounded once more, on output.  Rows of the weight gradients that no row reaches are 0.
+ * as an operand of these products, which sum in fp32.  bf16 of up to 64 rows is
+ * kept as two such terms, 16 bits.  Of more rows, what the rounding takes from
+ * the label's entry -- of a teacher's list, the heaviest -- is given back in
+ * fp32: to d_hidden and d_markov_w1, and for up to 512 rows to the weights'
+ * gradients d_lm_head_w and d_markov_w2.  Each gradient is rounded once more, on
+ * output.  Rows of the weight gradients that no row reaches are 0.
  *   lse        [rows] as written by dspark_ce_loss for the same inputs
  *   loss_grad  [rows] fp32
  *   d_hidden [rows, H], d_lm_head_w [V, H], d_markov_w1, d_markov_w2 [V, r]:
