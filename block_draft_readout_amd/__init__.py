@@ -17,6 +17,7 @@ import torch
 
 from . import _abi
 from ._abi import BdrError, BDR_BF16, BDR_BF16_PACKED, BDR_F32  # noqa: F401
+from .paged import dflash_paged_attention, dspark_qk_norm_rope, spec_slots
 from .training import (dspark_ce_backward, dspark_ce_loss, dspark_distill_backward,
                        dspark_distill_loss, dspark_norm, dspark_norm_backward)
 
@@ -28,6 +29,7 @@ __all__ = [
     "dflash_hc_average", "dflash_fuse_fc_rows_fp8", "PackedWeight", "pack_weight",
     "dspark_norm", "dspark_norm_backward", "dspark_ce_loss", "dspark_ce_backward",
     "dspark_distill_loss", "dspark_distill_backward",
+    "spec_slots", "dspark_qk_norm_rope", "dflash_paged_attention",
     "workspace_bytes", "lib", "BdrError", "set_markov_poll_timeout_us",
     "set_markov_forced_time_out", "MARKOV_TIMED_OUT",
 ]

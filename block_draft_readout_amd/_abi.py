@@ -89,6 +89,17 @@ SIGNATURES = {
     "dspark_distill_backward": (_int, [_vp, _i64, _i64, _i64, _int, _vp, _vp, _vp, _int, _vp, _vp,
                                        _vp, _int, _int, C.c_float, _vp, _vp, _vp, _vp, _vp, _vp,
                                        _vp, _vp, _sz, _vp]),
+    "spec_slots": (_int, [_vp, _vp, _i64, _i64, _int, _vp, _vp, _vp, _i64, _vp, _i64, _vp, _vp, _vp,
+                          _vp, _vp, _vp, _vp, _vp]),
+    "dspark_qk_norm_rope": (_int, [_vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _i64, _i64, _int,
+                                   _int, _int, _int, _vp, _vp, _int, _int, _vp, _vp, C.c_float,
+                                   _vp, _vp, _vp, _vp, _vp, _i64, _int, _i64, _i64, _i64, _vp,
+                                   _vp, _vp]),
+    "dflash_paged_attention_workspace_bytes": (_sz, [_i64, _int, _int, _int, _int, _i64, _i64,
+                                                     _int]),
+    "dflash_paged_attention": (_int, [_vp, _i64, _i64, _i64, _int, _int, _int, _int, _vp, _vp, _i64,
+                                      _int, _i64, _i64, _i64, _vp, _vp, _vp, _i64, _i64, _vp, _vp,
+                                      C.c_float, _int, _int, _vp, _vp, _vp, _sz, _vp]),
 }
 
 _lib = None

@@ -1166,4 +1166,390 @@ int dspark_distill_backward(const void* hidden, int64_t rows, int64_t hidden_siz
                            "dspark_distill_backward launch");
 }
 
+// ---------------------------------------------------------------------------- paged attention
+namespace {
+
+constexpr int64_t kMaxRequests = int64_t(1) << 20;
+constexpr int64_t kMaxContext = int64_t(1) << 30;    // positions of a block table's row
+constexpr int64_t kMaxSlotRows = int64_t(1) << 24;
+constexpr int64_t kMaxQueryVectors = int64_t(1) << 30;
+constexpr int kMaxHeads = 1024;
+
+int table_shape(int64_t batch, int64_t max_pages, int64_t page_size) {
+  if (batch < 0) return fail(BDR_EINVAL, "batch must be >= 0");
+  if (max_pages < 1) return fail(BDR_EINVAL, "max_pages must be >= 1");
+  if (page_size < 1) return fail(BDR_EINVAL, "page_size must be >= 1");
+  if (batch > kMaxRequests) return fail(BDR_EUNSUPPORTED, "batch must be <= 2^20");
+  if (max_pages > kMaxContext / page_size)
+    return fail(BDR_EUNSUPPORTED, "max_pages * page_size must be <= 2^30");
+  return BDR_OK;
+}
+
+int head_shape(int q_heads, int kv_heads, int head_dim, int dt, bool queries) {
+  if (!valid_dtype(dt)) return fail(BDR_EINVAL, "unknown dtype %d", dt);
+  if (kv_heads < 1 || q_heads < (queries ? 1 : 0))
+    return fail(BDR_EINVAL, "kv_heads must be >= 1 and q_heads >= %d", queries ? 1 : 0);
+  if (q_heads > kMaxHeads || kv_heads > kMaxHeads || q_heads + kv_heads > kMaxHeads)
+    return fail(BDR_EUNSUPPORTED, "q_heads + kv_heads must be <= %d", kMaxHeads);
+  if (head_dim != 64 && head_dim != 128 && head_dim != 256)
+    return fail(BDR_EUNSUPPORTED, "head_dim %d must be 64, 128 or 256", head_dim);
+  return BDR_OK;
+}
+
+// elements from the first to the last of [n, heads, dim] at these strides
+int64_t head_span(int64_t n, int64_t row, int heads, int64_t head, int dim) {
+  return (n - 1) * row + (heads - 1) * head + dim;
+}
+
+int head_strides(int64_t rows, int64_t row, int heads, int64_t head, int dt, const char* name) {
+  const int e = dt == BDR_BF16 ? 8 : 4;
+  if (row < 0 || head < 0 || row % e || head % e)
+    return fail(BDR_EINVAL, "the strides of %s must be multiples of %d and >= 0", name, e);
+  if ((rows > 0 && row > kMaxElems / rows) || head > kMaxElems / kMaxHeads)
+    return fail(BDR_EUNSUPPORTED, "the strides of %s are too large", name);
+  return BDR_OK;
+}
+
+struct Cache {
+  const void *k, *v;
+  int64_t pages;
+  int page;
+  int64_t page_stride, token_stride, head_stride;
+  const float *k_scale, *v_scale;
+};
+
+int cache_elem(const Cache& c, int dt) { return c.k_scale ? 1 : dt == BDR_BF16 ? 2 : 4; }
+
+int64_t cache_bytes(const Cache& c, int kv_heads, int head_dim, int dt) {
+  return ((c.pages - 1) * c.page_stride + (c.page - 1) * c.token_stride +
+          (kv_heads - 1) * c.head_stride + head_dim) * cache_elem(c, dt);
+}
+
+int cache_shape(const Cache& c, int kv_heads, int dt) {
+  if (c.pages < 1) return fail(BDR_EINVAL, "pages must be >= 1");
+  if (c.page < 1) return fail(BDR_EINVAL, "page_size must be >= 1");
+  if (c.pages > 0x7FFFFFFFLL / c.page)
+    return fail(BDR_EUNSUPPORTED, "pages * page_size must be < 2^31");
+  if ((c.k_scale == nullptr) != (c.v_scale == nullptr))
+    return fail(BDR_EINVAL, "k_scale and v_scale must both be given or both be NULL");
+  if (c.k_scale && dt != BDR_BF16) return fail(BDR_EINVAL, "an E4M3 cache goes with bf16 tensors");
+  if (c.k_scale) {
+    BDR_TRY(need_ptr(c.k_scale, "k_scale", 4));
+    BDR_TRY(need_ptr(c.v_scale, "v_scale", 4));
+  }
+  const int e = 16 / cache_elem(c, dt);
+  if (c.page_stride < 0 || c.token_stride < 0 || c.head_stride < 0 || c.page_stride % e ||
+      c.token_stride % e || c.head_stride % e)
+    return fail(BDR_EINVAL, "the cache's strides must be multiples of 16 bytes and >= 0");
+  if (c.page_stride > kMaxElems / c.pages || c.token_stride > kMaxElems / c.page ||
+      c.head_stride > kMaxElems / kv_heads)
+    return fail(BDR_EUNSUPPORTED, "the cache's strides are too large");
+  return BDR_OK;
+}
+
+// a written cache's elements lie apart, and its keys apart from its values
+int cache_apart(const Cache& c, int kv_heads, int head_dim, int dt) {
+  struct Axis {
+    int64_t stride, n;
+  };
+  const int64_t e = cache_elem(c, dt);
+  const intptr_t d = static_cast<const char*>(c.v) - static_cast<const char*>(c.k);
+  Axis a[4] = {{c.page_stride * e, c.pages}, {c.token_stride * e, c.page},
+               {c.head_stride * e, kv_heads}, {d < 0 ? -d : d, 2}};
+  std::sort(a, a + 4, [](const Axis& x, const Axis& y) { return x.stride < y.stride; });
+  int64_t reach = head_dim * e;   // bytes that the axes so far span
+  for (const Axis& x : a) {
+    if (x.n == 1) continue;
+    if (x.stride < reach) return fail(BDR_EINVAL, "elements of the cache overlap");
+    reach += (x.n - 1) * x.stride;
+  }
+  return BDR_OK;
+}
+
+}  // namespace
+
+int spec_slots(const int32_t* cached, const int32_t* new_tokens, int64_t batch, int64_t max_pages,
+               int page_size, int32_t* block_table, const int32_t* page_count,
+               int32_t* free_pages, int64_t free_capacity, const int32_t* free_count,
+               int64_t max_rows, int32_t* query_offsets, int32_t* kv_len, int32_t* positions,
+               int32_t* slots, int32_t* page_count_out, int32_t* free_count_out, int32_t* status,
+               void* stream) {
+  BDR_TRY(table_shape(batch, max_pages, page_size));
+  if (free_capacity < 0) return fail(BDR_EINVAL, "free_capacity must be >= 0");
+  if (free_capacity > 0x7FFFFFFFLL) return fail(BDR_EUNSUPPORTED, "free_capacity must be < 2^31");
+  if (max_rows < 0) return fail(BDR_EINVAL, "max_rows must be >= 0");
+  if (max_rows > kMaxSlotRows) return fail(BDR_EUNSUPPORTED, "max_rows must be <= 2^24");
+  if (batch > 0) {
+    BDR_TRY(need_ptr(cached, "cached", 4));
+    BDR_TRY(need_ptr(new_tokens, "new_tokens", 4));
+    BDR_TRY(need_ptr(block_table, "block_table", 4));
+    BDR_TRY(need_ptr(page_count, "page_count", 4));
+    BDR_TRY(need_ptr(kv_len, "kv_len", 4));
+    BDR_TRY(need_ptr(page_count_out, "page_count_out", 4));
+  }
+  if (free_capacity > 0) BDR_TRY(need_ptr(free_pages, "free_pages", 4));
+  BDR_TRY(need_ptr(free_count, "free_count", 4));
+  BDR_TRY(need_ptr(query_offsets, "query_offsets", 4));
+  if (max_rows > 0) {
+    BDR_TRY(need_ptr(positions, "positions", 4));
+    BDR_TRY(need_ptr(slots, "slots", 4));
+  }
+  BDR_TRY(need_ptr(free_count_out, "free_count_out", 4));
+  BDR_TRY(need_ptr(status, "status", 4));
+  auto given = [](const void* p, int64_t n) { return n > 0 ? p : nullptr; };
+  const Span in_count{given(page_count, batch), batch * 4, "page_count"};
+  const Span in_free{free_count, 4, "free_count"};
+  const Span out_count{given(page_count_out, batch), batch * 4, "page_count_out"};
+  const Span out_free{free_count_out, 4, "free_count_out"};
+  const std::initializer_list<Span> outs = {
+      {given(block_table, batch), batch * max_pages * 4, "block_table"},
+      {given(free_pages, free_capacity), free_capacity * 4, "free_pages"},
+      {query_offsets, (batch + 1) * 4, "query_offsets"},
+      {given(kv_len, batch), batch * 4, "kv_len"},
+      {given(positions, max_rows), max_rows * 4, "positions"},
+      {given(slots, max_rows), max_rows * 4, "slots"},
+      {status, 4, "status"}};
+  const Span in_cached{given(cached, batch), batch * 4, "cached"};
+  const Span in_new{given(new_tokens, batch), batch * 4, "new_tokens"};
+  BDR_TRY(no_overlap(outs, {in_cached, in_new, in_count, in_free, out_count, out_free}));
+  BDR_TRY(no_overlap({out_count, out_free}, {in_cached, in_new}));
+  if (page_count_out != page_count) BDR_TRY(no_overlap({out_count}, {in_count}));
+  if (free_count_out != free_count) BDR_TRY(no_overlap({out_free}, {in_free}));
+  BDR_TRY(no_overlap({out_count}, {in_free}));
+  BDR_TRY(no_overlap({out_free}, {in_count}));
+  BDR_TRY(check_device());
+  const SlotProblem p{cached, new_tokens, static_cast<int32_t>(batch), static_cast<int32_t>(max_pages),
+                      page_size, static_cast<int32_t>(free_capacity), static_cast<int32_t>(max_rows),
+                      block_table, page_count, free_pages, free_count, query_offsets, kv_len, positions,
+                      slots, page_count_out, free_count_out, status};
+  const hipError_t e = launch_slots(p, as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "spec_slots launch");
+  return BDR_OK;
+}
+
+int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k,
+                        int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                        int64_t v_row_stride, int64_t v_head_stride, int64_t rows, int q_heads,
+                        int kv_heads, int head_dim, bdr_dtype dt, const int32_t* positions,
+                        const float* inv_freq, int rot_dim, int interleaved, const void* q_weight,
+                        const void* k_weight, float eps, void* q_out, void* k_out,
+                        const int32_t* slots, void* k_cache, void* v_cache, int64_t pages,
+                        int page_size, int64_t page_stride, int64_t token_stride,
+                        int64_t head_stride, const float* k_scale, const float* v_scale,
+                        void* stream) {
+  BDR_TRY(head_shape(q_heads, kv_heads, head_dim, dt, false));
+  if (rows < 0) return fail(BDR_EINVAL, "rows must be >= 0");
+  if (rows >= kMaxSlotRows) return fail(BDR_EUNSUPPORTED, "rows must be < 2^24");
+  if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16)
+    return fail(BDR_EINVAL, "rot_dim %d must be a multiple of 16 in 16 .. head_dim", rot_dim);
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(BDR_EINVAL, "eps must be finite and >= 0");
+  if ((q_weight == nullptr) != (k_weight == nullptr))
+    return fail(BDR_EINVAL, "q_weight and k_weight must both be given or both be NULL");
+  if ((k_cache == nullptr) != (v_cache == nullptr))
+    return fail(BDR_EINVAL, "k_cache and v_cache must both be given or both be NULL");
+  const bool cached = k_cache != nullptr;
+  const Cache c{k_cache, v_cache, pages, page_size, page_stride, token_stride, head_stride, k_scale, v_scale};
+  if (cached) {
+    BDR_TRY(need_ptr(k_cache, "k_cache"));
+    BDR_TRY(need_ptr(v_cache, "v_cache"));
+    BDR_TRY(cache_shape(c, kv_heads, dt));
+    BDR_TRY(cache_apart(c, kv_heads, head_dim, dt));
+  } else if (k_scale || v_scale) {
+    return fail(BDR_EINVAL, "scales are given without a cache");
+  }
+  BDR_TRY(head_strides(rows, q_row_stride, q_heads, q_head_stride, dt, "q"));
+  BDR_TRY(head_strides(rows, k_row_stride, kv_heads, k_head_stride, dt, "k"));
+  BDR_TRY(head_strides(rows, v_row_stride, kv_heads, v_head_stride, dt, "v"));
+  if (rows == 0) return BDR_OK;
+  if (q_heads) {
+    BDR_TRY(need_ptr(q, "q"));
+    BDR_TRY(need_ptr(q_out, "q_out"));
+  }
+  BDR_TRY(need_ptr(k, "k"));
+  if (k_out) BDR_TRY(need_ptr(k_out, "k_out"));
+  if (cached) {
+    BDR_TRY(need_ptr(v, "v"));
+    BDR_TRY(need_ptr(slots, "slots", 4));
+  } else if (!k_out) {
+    return fail(BDR_EINVAL, "keys go nowhere: k_out or a cache is needed");
+  }
+  BDR_TRY(need_ptr(positions, "positions", 4));
+  BDR_TRY(need_ptr(inv_freq, "inv_freq", 4));
+  if (q_weight) {
+    BDR_TRY(need_ptr(q_weight, "q_weight"));
+    BDR_TRY(need_ptr(k_weight, "k_weight"));
+  }
+  const int64_t es = dt == BDR_BF16 ? 2 : 4;
+  const Span sq{q_heads ? q : nullptr, q_heads ? head_span(rows, q_row_stride, q_heads, q_head_stride, head_dim) * es : 0, "q"};
+  const Span sk{k, head_span(rows, k_row_stride, kv_heads, k_head_stride, head_dim) * es, "k"};
+  const Span sv{cached ? v : nullptr, head_span(rows, v_row_stride, kv_heads, v_head_stride, head_dim) * es, "v"};
+  const Span oq{q_heads ? q_out : nullptr, rows * q_heads * head_dim * es, "q_out"};
+  const Span ok{k_out, rows * kv_heads * head_dim * es, "k_out"};
+  const int64_t cb = cached ? cache_bytes(c, kv_heads, head_dim, dt) : 0;
+  const Span ck{k_cache, cb, "k_cache"}, cv{v_cache, cb, "v_cache"};
+  const std::initializer_list<Span> rest = {{positions, rows * 4, "positions"},
+                                            {inv_freq, rot_dim * 2, "inv_freq"},
+                                            {q_weight, head_dim * es, "q_weight"},
+                                            {k_weight, head_dim * es, "k_weight"},
+                                            {cached ? slots : nullptr, rows * 4, "slots"},
+                                            {k_scale, kv_heads * 4, "k_scale"},
+                                            {v_scale, kv_heads * 4, "v_scale"}};
+  BDR_TRY(no_overlap({oq, ok}, rest));
+  BDR_TRY(no_overlap({ck}, rest));
+  BDR_TRY(no_overlap({cv}, rest));
+  BDR_TRY(no_overlap({ck}, {sq, sk, sv, oq, ok}));   // (keys and values may interleave)
+  BDR_TRY(no_overlap({cv}, {sq, sk, sv, oq, ok}));
+  auto in_place = [&](const void* in, const void* out, int64_t row, int64_t head, int heads) {
+    return in == out && head == head_dim && row == static_cast<int64_t>(heads) * head_dim;
+  };
+  if (!(q_heads && in_place(q, q_out, q_row_stride, q_head_stride, q_heads))) BDR_TRY(no_overlap({oq}, {sq}));
+  if (!(k_out && in_place(k, k_out, k_row_stride, k_head_stride, kv_heads))) BDR_TRY(no_overlap({ok}, {sk}));
+  BDR_TRY(no_overlap({oq}, {sk, sv}));
+  BDR_TRY(no_overlap({ok}, {sq, sv}));
+  BDR_TRY(check_device());
+  QkProblem p{};
+  p.q = q;
+  p.k = k;
+  p.v = v;
+  p.q_row = q_row_stride;
+  p.q_head = q_head_stride;
+  p.k_row = k_row_stride;
+  p.k_head = k_head_stride;
+  p.v_row = v_row_stride;
+  p.v_head = v_head_stride;
+  p.rows = rows;
+  p.hq = q_heads;
+  p.hkv = kv_heads;
+  p.dim = head_dim;
+  p.half = rot_dim / 2;
+  p.interleaved = interleaved != 0;
+  p.fp8 = k_scale != nullptr;
+  p.dt = dt;
+  p.positions = positions;
+  p.inv_freq = inv_freq;
+  p.wq = q_weight;
+  p.wk = k_weight;
+  p.eps = eps;
+  p.q_out = q_out;
+  p.k_out = k_out;
+  p.slots = slots;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.page = cached ? page_size : 1;
+  p.slots_held = cached ? static_cast<int32_t>(pages * page_size) : 0;
+  p.page_stride = page_stride;
+  p.token_stride = token_stride;
+  p.head_stride = head_stride;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  const hipError_t e = launch_qk(p, as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "dspark_qk_norm_rope launch");
+  return BDR_OK;
+}
+
+namespace {
+
+int attn_shape(int64_t rows, int q_heads, int kv_heads, int head_dim, int dt, int64_t batch,
+               int64_t max_pages, int64_t page_size) {
+  BDR_TRY(head_shape(q_heads, kv_heads, head_dim, dt, true));
+  if (q_heads % kv_heads)
+    return fail(BDR_EINVAL, "q_heads %d must be a multiple of kv_heads %d", q_heads, kv_heads);
+  if (rows < 0) return fail(BDR_EINVAL, "rows must be >= 0");
+  if (rows > kMaxQueryVectors / q_heads)
+    return fail(BDR_EUNSUPPORTED, "rows * q_heads must be <= 2^30");
+  return table_shape(batch, max_pages, page_size);
+}
+
+AttnProblem attn_sizes(int64_t rows, int q_heads, int kv_heads, int head_dim, bdr_dtype dt,
+                       int64_t batch, int64_t max_pages, int page_size) {
+  AttnProblem p{};
+  p.rows = rows;
+  p.hq = q_heads;
+  p.hkv = kv_heads;
+  p.group = q_heads / kv_heads;
+  p.dim = head_dim;
+  p.dt = dt;
+  p.batch = static_cast<int>(batch);
+  p.width = static_cast<int>(max_pages);
+  p.page = page_size;
+  return p;
+}
+
+}  // namespace
+
+size_t dflash_paged_attention_workspace_bytes(int64_t rows, int q_heads, int kv_heads, int head_dim,
+                                              bdr_dtype dt, int64_t batch, int64_t max_pages,
+                                              int page_size) {
+  if (attn_shape(rows, q_heads, kv_heads, head_dim, dt, batch, max_pages, page_size) != BDR_OK ||
+      rows == 0 || batch == 0)
+    return 0;
+  return attn_workspace(attn_sizes(rows, q_heads, kv_heads, head_dim, dt, batch, max_pages, page_size));
+}
+
+int dflash_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, int64_t rows,
+                           int q_heads, int kv_heads, int head_dim, bdr_dtype dt,
+                           const void* k_cache, const void* v_cache, int64_t pages, int page_size,
+                           int64_t page_stride, int64_t token_stride, int64_t head_stride,
+                           const float* k_scale, const float* v_scale, const int32_t* block_table,
+                           int64_t batch, int64_t max_pages, const int32_t* query_offsets,
+                           const int32_t* kv_len, float scale, int causal, int window, void* out,
+                           float* lse, void* workspace, size_t workspace_bytes, void* stream) {
+  BDR_TRY(attn_shape(rows, q_heads, kv_heads, head_dim, dt, batch, max_pages, page_size));
+  const Cache c{k_cache, v_cache, pages, page_size, page_stride, token_stride, head_stride, k_scale, v_scale};
+  BDR_TRY(cache_shape(c, kv_heads, dt));
+  BDR_TRY(head_strides(rows, q_row_stride, q_heads, q_head_stride, dt, "q"));
+  if (!(scale > 0.f) || !std::isfinite(scale)) return fail(BDR_EINVAL, "scale must be finite and > 0");
+  if (window < 0) return fail(BDR_EINVAL, "window must be >= 0");
+  if (rows == 0 || batch == 0) return BDR_OK;
+  BDR_TRY(need_ptr(q, "q"));
+  BDR_TRY(need_ptr(k_cache, "k_cache"));
+  BDR_TRY(need_ptr(v_cache, "v_cache"));
+  BDR_TRY(need_ptr(block_table, "block_table", 4));
+  BDR_TRY(need_ptr(query_offsets, "query_offsets", 4));
+  BDR_TRY(need_ptr(kv_len, "kv_len", 4));
+  BDR_TRY(need_ptr(out, "out"));
+  if (lse) BDR_TRY(need_ptr(lse, "lse", 4));
+  AttnProblem p = attn_sizes(rows, q_heads, kv_heads, head_dim, dt, batch, max_pages, page_size);
+  const size_t need = attn_workspace(p);
+  BDR_TRY(need_ws(workspace, workspace_bytes, need));
+  const int64_t es = dt == BDR_BF16 ? 2 : 4;
+  const int64_t cb = cache_bytes(c, kv_heads, head_dim, dt);
+  BDR_TRY(no_overlap({{out, rows * q_heads * head_dim * es, "out"},
+                      {lse, rows * q_heads * 4, "lse"},
+                      {need ? workspace : nullptr, static_cast<int64_t>(need), "workspace"}},
+                     {{q, head_span(rows, q_row_stride, q_heads, q_head_stride, head_dim) * es, "q"},
+                      {k_cache, cb, "k_cache"},
+                      {v_cache, cb, "v_cache"},
+                      {k_scale, kv_heads * 4, "k_scale"},
+                      {v_scale, kv_heads * 4, "v_scale"},
+                      {block_table, batch * max_pages * 4, "block_table"},
+                      {query_offsets, (batch + 1) * 4, "query_offsets"},
+                      {kv_len, batch * 4, "kv_len"}}));
+  BDR_TRY(check_device());
+  p.q = q;
+  p.q_row = q_row_stride;
+  p.q_head = q_head_stride;
+  p.fp8 = k_scale != nullptr;
+  p.k_cache = k_cache;
+  p.v_cache = v_cache;
+  p.pages = static_cast<int>(pages);
+  p.page_stride = page_stride;
+  p.token_stride = token_stride;
+  p.head_stride = head_stride;
+  p.k_scale = k_scale;
+  p.v_scale = v_scale;
+  p.table = block_table;
+  p.offsets = query_offsets;
+  p.kv_len = kv_len;
+  p.scale = scale;
+  p.causal = causal != 0;
+  // a window past every context is none
+  p.window = window >= max_pages * page_size ? 0 : window;
+  p.out = out;
+  p.lse = lse;
+  const hipError_t e = launch_attn(p, workspace, as_stream(stream));
+  if (e != hipSuccess) return hip_fail(e, "dflash_paged_attention launch");
+  return BDR_OK;
+}
+
 }  // extern "C"

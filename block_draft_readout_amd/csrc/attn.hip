@@ -1,0 +1,70 @@
+// Host side of the attention over a paged cache: which variant, how many
+// workgroups, and the workspace of its partials.
+
+#include <algorithm>
+
+#include "attn_run.h"
+
+namespace bdr {
+
+namespace {
+
+constexpr int64_t kCus = 256;   // compute units of an MI355X
+
+struct Choice {
+  int which;          // 0 few, 1 some, 2 many rows
+  int bm;             // rows of a row tile
+  int64_t slabs, min_share;
+  int whole;
+};
+
+Choice choose(const AttnProblem& p) {
+  Choice c{};
+  // rows of a request and kv head on average
+  const int64_t rows = (p.rows * p.group + p.batch - 1) / p.batch;
+  const bool wide = p.dim == 256;
+  c.which = rows <= 32 ? 0 : rows <= 64 ? 1 : 2;
+  if (p.dt == BDR_F32 && (wide || c.which == 1)) c.which = 2;
+  if (wide && c.which == 1) c.which = 2;
+  c.bm = c.which == 0 ? 32 : c.which == 1 ? 64 : 128;
+  // row tiles at most
+  const int64_t tiles = ((p.rows * p.group + c.bm - 1) / c.bm + p.batch) * p.hkv;
+  const int64_t longest = static_cast<int64_t>(p.width) * p.page;
+  c.whole = longest <= 256;
+  c.slabs = c.whole ? tiles : 2 * kCus;
+  c.min_share = 8;
+  return c;
+}
+
+}  // namespace
+
+size_t attn_workspace(const AttnProblem& p) {
+  const Choice c = choose(p);
+  if (c.whole) return 0;
+  const size_t slots = 2 * static_cast<size_t>(c.slabs) * c.bm;
+  return align256(slots * p.dim * sizeof(float)) + align256(slots * sizeof(float2)) +
+         align256(static_cast<size_t>(c.slabs) * kRecord * sizeof(int32_t));
+}
+
+hipError_t launch_attn(const AttnProblem& p, void* workspace, hipStream_t stream) {
+  const Choice c = choose(p);
+  AttnArgs g{};
+  g.p = p;
+  g.slabs = c.slabs;
+  g.min_share = c.min_share;
+  g.whole = c.whole;
+  g.scale2 = p.scale * kLog2e;
+  if (!c.whole) {
+    const size_t slots = 2 * static_cast<size_t>(c.slabs) * c.bm;
+    char* at = static_cast<char*>(workspace);
+    g.part_o = reinterpret_cast<float*>(at);
+    at += align256(slots * p.dim * sizeof(float));
+    g.part_ml = reinterpret_cast<float2*>(at);
+    at += align256(slots * sizeof(float2));
+    g.record = reinterpret_cast<int32_t*>(at);
+  }
+  if (p.dt == BDR_F32) return launch_attn_f32(g, c.which, stream);
+  return p.fp8 ? launch_attn_fp8(g, c.which, stream) : launch_attn_bf16(g, c.which, stream);
+}
+
+}  // namespace bdr

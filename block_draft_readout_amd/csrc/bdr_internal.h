@@ -118,6 +118,69 @@ hipError_t launch_clear(void* p, int64_t bytes, hipStream_t stream);
 // the gradients of a call without rows: zeros
 hipError_t launch_loss_clear(const LossProblem& p, const LossGrads& out, hipStream_t stream);
 
+// ----------------------------------------------------------------------------
+// The drafter's attention over its paged cache.
+// ----------------------------------------------------------------------------
+struct SlotProblem {
+  const int32_t* cached;   // [batch] tokens in the cache, negative: the request is over
+  const int32_t* fresh;    // [batch] new tokens
+  int32_t batch, width, page, capacity, rows;
+  int32_t* table;          // [batch, width]
+  const int32_t* count;    // [batch] pages held
+  int32_t* free_pages;     // [capacity] stack
+  const int32_t* free_count;
+  int32_t* offsets;        // [batch + 1]
+  int32_t* kv_len;         // [batch]
+  int32_t* positions;      // [rows]
+  int32_t* slots;          // [rows]
+  int32_t* count_out;      // [batch], may be count
+  int32_t* free_out;       // may be free_count
+  int32_t* status;
+};
+hipError_t launch_slots(const SlotProblem& p, hipStream_t stream);
+
+struct QkProblem {
+  const void *q, *k, *v;   // rows and heads at these strides (elements)
+  int64_t q_row, q_head, k_row, k_head, v_row, v_head;
+  int64_t rows;
+  int hq, hkv, dim, half, interleaved, fp8;
+  bdr_dtype dt;
+  const int32_t* positions;
+  const float* inv_freq;   // [half]
+  const void *wq, *wk;     // [dim], both or neither
+  float eps;
+  void *q_out, *k_out;     // contiguous; k_out may be NULL
+  const int32_t* slots;    // [rows] with a cache
+  void *k_cache, *v_cache;
+  int32_t page, slots_held;
+  int64_t page_stride, token_stride, head_stride;
+  const float *k_scale, *v_scale;
+};
+hipError_t launch_qk(const QkProblem& p, hipStream_t stream);
+
+struct AttnProblem {
+  const void* q;
+  int64_t rows, q_row, q_head;
+  int hq, hkv, group, dim;
+  bdr_dtype dt;
+  int fp8;
+  const void *k_cache, *v_cache;
+  int pages, page;
+  int64_t page_stride, token_stride, head_stride;
+  const float *k_scale, *v_scale;
+  const int32_t* table;
+  int batch, width;
+  const int32_t* offsets;
+  const int32_t* kv_len;
+  float scale;
+  int causal, window;
+  void* out;
+  float* lse;              // may be NULL
+};
+// (sizes alone decide: pointers and strides need not be set)
+size_t attn_workspace(const AttnProblem& p);
+hipError_t launch_attn(const AttnProblem& p, void* workspace, hipStream_t stream);
+
 inline size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace bdr

@@ -741,6 +741,157 @@ int dspark_distill_backward(const void* hidden, int64_t rows, int64_t hidden_siz
                             void* d_lm_head_w, void* d_markov_w1, void* d_markov_w2,
                             void* workspace, size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * The drafter's attention over its paged context.
+ *
+ * Between the fc that fuses the target's features and the LM head the drafter's
+ * layers attend from a block's positions to the context in a cache ([card]
+ * "Usage": 16 requests at a time, an fp8 cache among the flags).  The pages give
+ * no arithmetic; the textbook definitions below are used.
+ *
+ * The cache holds keys and values in pages of page_size positions.  Element
+ * (page, i, h, d) of either lies at page * page_stride + i * token_stride +
+ * h * head_stride + d (elements of the cache's type, the same strides for
+ * both), so pages x positions x heads x features, heads before positions, and
+ * keys and values page by page beside each other are all taken as they are.
+ * Slot s is position s % page_size of page s / page_size.  The cache is of the
+ * tensors' dtype, or (k_scale and v_scale given, bf16 tensors) E4M3 codes as in
+ * dflash_fuse_fc_fp8 whose values are code * scale[h], one fp32 scale per kv
+ * head.  block_table[b, c] is the page of request b's positions
+ * [c * page_size, (c + 1) * page_size).
+ *
+ * The three calls allocate nothing, hold no state between calls and may be
+ * captured; their sums have a fixed order, so the same inputs give the same
+ * bits.  Their outputs may share memory with nothing else that they are given,
+ * except where an output "may be" an input.
+ * ------------------------------------------------------------------------- */
+
+/* spec_slots -- pages and slots of a step's new tokens, from device lengths.
+ *
+ * Request b holds cached[b] tokens in the first page_count[b] columns of its
+ * row of block_table and gets new_tokens[b] more (a negative count: none).  A
+ * request with cached[b] < 0 is over: its pages go back on the free stack, the
+ * last page of the last such request first, and it holds none.  Then, in the
+ * order of the requests, each gets the pages that it lacks for
+ *   ceil((cached[b] + new_tokens[b]) / page_size)
+ * columns (at most max_pages) from the top of the stack.  Pages held beyond
+ * that (drafts that were rejected) are kept.  New tokens lie behind one another
+ * in the order of the requests:
+ *   query_offsets[b] = sum_{c < b} new_tokens[c]   [batch + 1]
+ *   kv_len[b]        = cached[b] + new_tokens[b]   (0 where the request is over)
+ *   positions[i]     = position of token i in its request
+ *   slots[i]         = block_table[b, position / page_size] * page_size + position % page_size
+ * and rows behind the last token (a padded batch) have position 0 and slot -1.
+ * Where the stack or the row is too short, the tokens without a page have slot
+ * -1 and status counts the tokens without one (those past max_rows among them):
+ * the step is then to be repeated with more pages.
+ *
+ *   cached, new_tokens, page_count   [batch] int32; 0 <= batch <= 2^20
+ *   block_table     [batch, max_pages] int32, entries of new columns written;
+ *                   max_pages >= 1, page_size >= 1, max_pages * page_size <= 2^30
+ *   free_pages      [free_capacity] int32 stack, its first *free_count entries
+ *                   are free pages; pages that come back past the capacity are
+ *                   dropped
+ *   max_rows        0 .. 2^24, rows of positions and slots
+ *   page_count_out  [batch] int32 out, may be page_count
+ *   free_count_out  [1] int32 out, may be free_count
+ *   status          [1] int32 out
+ * With batch == 0 the outputs are those of a step without tokens.  No
+ * workspace.
+ */
+int spec_slots(const int32_t* cached, const int32_t* new_tokens, int64_t batch, int64_t max_pages,
+               int page_size, int32_t* block_table, const int32_t* page_count,
+               int32_t* free_pages, int64_t free_capacity, const int32_t* free_count,
+               int64_t max_rows, int32_t* query_offsets, int32_t* kv_len, int32_t* positions,
+               int32_t* slots, int32_t* page_count_out, int32_t* free_count_out,
+               int32_t* status, void* stream);
+
+/* dspark_qk_norm_rope -- root-mean-square norm of each query and key head,
+ * rotation by position, and keys and values into the cache.
+ *
+ *   y      = x (sum_d x[d]^2 / D + eps)^-1/2 weight[d]    (weights NULL: y = x)
+ *   a_i    = positions[m] * inv_freq[i],  i < rot_dim / 2
+ *   (y1, y2) -> (y1 cos a_i - y2 sin a_i, y2 cos a_i + y1 sin a_i)
+ * for the pairs (i, i + rot_dim / 2), or interleaved (2 i, 2 i + 1), of the first
+ * rot_dim features; the others stay.  The angle is the product in 64 bits.
+ * Queries go to q_out, keys to k_out and / or slot slots[m] of the cache, values
+ * to the same slot; a slot outside [0, pages * page_size) is not written.  Norm
+ * and rotation are fp32; each output is rounded once (E4M3: of y / k_scale[h],
+ * v / v_scale[h]; magnitudes past 448 become 448).  A slot that two rows name
+ * gets one of them, by features.
+ *
+ *   q, k, v      [rows, heads, D] dtype at row and head strides in elements
+ *                (multiples of 8 (bf16) or 4 (f32), >= 0): views of one
+ *                projection's output do.  q NULL with q_heads == 0; v NULL
+ *                without a cache
+ *   rows         0 <= rows < 2^24; 0 <= q_heads, 1 <= kv_heads, together <= 1024;
+ *                head_dim D 64, 128 or 256
+ *   positions    [rows] int32; inv_freq [rot_dim / 2] fp32; rot_dim a multiple of
+ *                16 in 16 .. D
+ *   q_weight, k_weight  [D] dtype, both or neither; eps finite, >= 0
+ *   q_out        [rows, q_heads, D] dtype, contiguous, may be q where q is
+ *                contiguous
+ *   k_out        [rows, kv_heads, D] dtype, contiguous, or NULL; may be k likewise
+ *   slots        [rows] int32 with a cache; k_cache, v_cache both or neither
+ *   pages >= 1, page_size >= 1, pages * page_size < 2^31; cache strides
+ *                multiples of 16 bytes that keep all elements apart
+ *   k_scale, v_scale  [kv_heads] fp32, both or neither (not 0)
+ */
+int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k,
+                        int64_t k_row_stride, int64_t k_head_stride, const void* v,
+                        int64_t v_row_stride, int64_t v_head_stride, int64_t rows, int q_heads,
+                        int kv_heads, int head_dim, bdr_dtype dt, const int32_t* positions,
+                        const float* inv_freq, int rot_dim, int interleaved,
+                        const void* q_weight, const void* k_weight, float eps, void* q_out,
+                        void* k_out, const int32_t* slots, void* k_cache, void* v_cache,
+                        int64_t pages, int page_size, int64_t page_stride, int64_t token_stride,
+                        int64_t head_stride, const float* k_scale, const float* v_scale,
+                        void* stream);
+
+/* dflash_paged_attention -- attention of each request's new tokens over its
+ * cached positions, the new tokens' own among them.
+ *
+ * Request b's n = query_offsets[b + 1] - query_offsets[b] tokens are the last of
+ * its kv_len[b] positions: token j is at p = kv_len[b] - n + j and sees
+ *   t < kv_len[b],  t <= p where causal,  t > p - window where window > 0
+ * (causal == 0: a drafted block whose positions see one another).  Query head g
+ * reads kv head g / (q_heads / kv_heads):
+ *   w_t = scale q . k_t,  out = sum_t exp(w_t) v_t / sum_t exp(w_t),
+ *   lse = log sum_t exp(w_t)
+ * A token that sees nothing has out 0 and lse -inf.  Rows of no request are left
+ * as they were.  Keys and values that no token sees may hold anything; a table
+ * entry outside [0, pages) reads as keys and values of 0.  Products take bf16
+ * (fp32) operands with fp32 sums; softmax statistics and sums are fp32; the
+ * probabilities are rounded to bf16 as the second product's operand.
+ *
+ *   q              [rows, q_heads, D] dtype at row and head strides in elements
+ *                  (as above); 0 <= rows, rows * q_heads <= 2^30; D 64, 128, 256;
+ *                  q_heads a multiple of kv_heads
+ *   k_cache, v_cache, pages, page_size, strides, k_scale, v_scale   as above
+ *                  (strides >= 0)
+ *   block_table    [batch, max_pages] int32; 0 <= batch <= 2^20;
+ *                  max_pages * page_size <= 2^30
+ *   query_offsets  [batch + 1] int32 ascending; kv_len [batch] int32 (taken as at
+ *                  most max_pages * page_size)
+ *   scale          finite, > 0; window >= 0 (0: none)
+ *   out            [rows, q_heads, D] dtype, contiguous
+ *   lse            [rows, q_heads] fp32, or NULL
+ *   workspace      >= dflash_paged_attention_workspace_bytes(...); any contents
+ *                  will do; may be NULL when that returns 0
+ */
+size_t dflash_paged_attention_workspace_bytes(int64_t rows, int q_heads, int kv_heads,
+                                              int head_dim, bdr_dtype dt, int64_t batch,
+                                              int64_t max_pages, int page_size);
+int dflash_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                           int64_t rows, int q_heads, int kv_heads, int head_dim, bdr_dtype dt,
+                           const void* k_cache, const void* v_cache, int64_t pages,
+                           int page_size, int64_t page_stride, int64_t token_stride,
+                           int64_t head_stride, const float* k_scale, const float* v_scale,
+                           const int32_t* block_table, int64_t batch, int64_t max_pages,
+                           const int32_t* query_offsets, const int32_t* kv_len, float scale,
+                           int causal, int window, void* out, float* lse, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif
