@@ -22,6 +22,8 @@
 // a lane's registers hold them; V is read with the same order).
 #pragma once
 
+#include <type_traits>
+
 #include "train_device.h"
 
 namespace bdr {
@@ -129,73 +131,218 @@ __device__ __forceinline__ int64_t uniform_i64(int64_t v) {
 }
 
 // -------------------------------------------------------------- kernel
-template <typename C_, typename S_, int D_, int WM_, int WN_, int RT_, int KT_>
-struct AttnTile {
+// Many rows: WM waves hold 32 rows each and share the tiles of keys in LDS.
+template <typename C_, typename S_, int D_, int WM_, int KT_>
+struct AttnMany {
   using C = C_;                       // cache element: uint16_t (bf16), uint8_t (e4m3) or float
   using S = S_;                       // queries, output and LDS: uint16_t or float
-  static constexpr int D = D_;
-  // WM waves hold different rows and share their keys' tiles in LDS, or (WM = 1) WN
-  // waves hold the same rows and walk key tiles of their own, joined at the end
-  static constexpr int WM = WM_, WN = WN_;
-  static constexpr int RT = RT_;      // 32-row tiles of a wave
+  static constexpr bool kFew = false;
+  static constexpr int D = D_, WM = WM_;
   static constexpr int KT = KT_;      // keys of a tile
-  static constexpr int THREADS = 64 * WM * WN;
-  static constexpr int BM = 32 * WM * RT;
+  static constexpr int THREADS = 64 * WM;
+  static constexpr int BM = 32 * WM;
   static constexpr int ES = static_cast<int>(sizeof(S));
   static constexpr int ROWB = D * ES;                    // bytes of an LDS row
   static constexpr int PER16 = 16 / static_cast<int>(sizeof(C));   // cache elements of 16 bytes
   static constexpr int CPR = D / PER16;                  // 16-byte pieces of a cache row
-  static constexpr int SHARE = 64 * WM;                  // threads that load a tile
+  static constexpr int SHARE = THREADS;                  // threads that load a tile
   static constexpr int LOADS = KT * CPR / SHARE;         // 16-byte loads of a thread, K or V
   static constexpr int TILE_BYTES = KT * ROWB;           // K or V of a tile
-  static constexpr int BUFS = WM > 1 ? 2 : 1;
-  static constexpr int JOIN_BYTES = WN > 1 ? 32 * D * 4 : 0;   // a wave's O of 32 rows
-  static constexpr int WAVE_BYTES = std::max(2 * TILE_BYTES * BUFS, JOIN_BYTES);
-  static constexpr int LDS_BYTES = WAVE_BYTES * WN;
-  static constexpr int QN = ROWB / 32;                   // 16-byte query pieces of a lane and row
-  static_assert(WM == 1 || WN == 1, "rows or keys are split over the waves");
+  static constexpr int LDS_BYTES = 4 * TILE_BYTES;       // two buffers
+  static constexpr int QN = ROWB / 32;                   // 16-byte query pieces of a lane
+  static constexpr int SIMD_WAVES = LDS_BYTES <= 79 * 1024 && D <= 128 ? 2 : 1;
   static_assert(KT % 32 == 0 && KT <= 64, "a lane looks up one key's page");
   static_assert(LOADS * SHARE == KT * CPR, "loads split evenly");
   static_assert(LDS_BYTES <= 160 * 1024, "tile fits");
 };
 
-// Places of the 16-byte chunks c of LDS row r, so that 16 lanes that read a chunk of 16
-// rows (keys), and 32 lanes that read 64 bytes of 4 rows (values), meet distinct banks.
-template <int ROWB>
-__device__ __forceinline__ uint32_t key_place(uint32_t r, uint32_t c) {
-  const uint32_t x = ROWB >= 256 ? r & 15u : (r >> 1) & 7u;
-  return r * ROWB + ((c ^ x) << 4);
-}
-template <int ROWB>
-__device__ __forceinline__ uint32_t value_place(uint32_t r, uint32_t c) {
-  const uint32_t x = ROWB >= 256 ? (r & 3u) << 2 : (r & 2u) << 1;
-  return r * ROWB + ((c ^ x) << 4);
-}
-
-// 16 e4m3 codes as bf16 (every code's value is one)
-__device__ __forceinline__ void widen16(u32x4_t v, u32x4_t& a, u32x4_t& b) {
-  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const bf16x2_t lo = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, false);
-    const bf16x2_t hi = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, true);
-    const uint32_t l = __builtin_bit_cast(uint32_t, lo), h = __builtin_bit_cast(uint32_t, hi);
-    if (i < 2) {
-      a[2 * i] = l;
-      a[2 * i + 1] = h;
-    } else {
-      b[2 * (i - 2)] = l;
-      b[2 * (i - 2) + 1] = h;
-    }
-  }
-}
-
-template <typename T>
-struct AttnState {
-  f32x16_t o[T::RT][T::D / 32];   // O^T: features 32 i + 8 (r / 4) + 4 (lane / 32) + r % 4 of query lane % 32
-  float m[T::RT], l[T::RT];       // running maximum (units of log2), this half wave's sum
+// Few rows: WN waves hold the same RT x 16 rows and walk key tiles of their own, each through
+// LDS of its own, joined at the end.  Tiles come straight from the cache to LDS as they are
+// stored there.
+template <typename C_, typename S_, int D_, int RT_>
+struct AttnFew {
+  using C = C_;
+  using S = S_;
+  static constexpr bool kFew = true;
+  static constexpr int D = D_, RT = RT_;
+  static constexpr int CS = static_cast<int>(sizeof(C)), ES = static_cast<int>(sizeof(S));
+  static constexpr int ROWB = D * CS;                    // bytes of an LDS row
+  static constexpr int KT = CS == 1 ? 64 : 32;
+  static constexpr int WN = 4;
+  static constexpr int THREADS = 64 * WN;
+  static constexpr int BM = 16 * RT;
+  static constexpr int CPR = ROWB / 16;                  // 16-byte chunks of a row
+  static constexpr int RPL = 64 / CPR;                   // rows of a wave's load
+  static constexpr int LOADS = KT / RPL;
+  static constexpr int TILE_BYTES = KT * ROWB;
+  static constexpr int WAVE_BYTES = 2 * TILE_BYTES;      // (a wave's O of 16 rows, fp32, fits)
+  // Queries stay in LDS where two waves of a SIMD have no registers for them.
+  static constexpr bool QLDS = D == 128 && RT >= 3;
+  static constexpr int Q_AT = WAVE_BYTES * WN;
+  static constexpr int LDS_BYTES = Q_AT + (QLDS ? BM * D * ES : 0);
+  static constexpr int QN = D * ES / 64;                 // 16-byte query pieces of a lane and row
+  static constexpr int SIMD_WAVES = LDS_BYTES <= 80 * 1024 ? 2 : 1;
+  static_assert(CPR <= 64 && KT % RPL == 0, "a load is whole rows");
+  static_assert(16 * D * 4 + 128 <= WAVE_BYTES, "a wave's output and statistics fit its tiles' place");
+  static_assert(LDS_BYTES <= 160 * 1024, "tiles fit");
 };
 
+// Places of the 16-byte chunks c of LDS row r: an XOR by the row, so that the lanes of one
+// pass meet distinct banks.  Keys: 16 lanes read one chunk of 16 rows.
+template <int ROWB>
+__device__ __forceinline__ uint32_t key_turn(uint32_t r) {
+  return ROWB >= 256 ? r & 15u : ROWB == 128 ? (r >> 1) & 7u : (r >> 2) & 3u;
+}
+template <int ROWB>
+__device__ __forceinline__ uint32_t key_place(uint32_t r, uint32_t c) {
+  return r * ROWB + ((c ^ key_turn<ROWB>(r)) << 4);
+}
+// Values: what a pass of 32 lanes reads depends on the kind of read.
+template <typename T>
+__device__ __forceinline__ uint32_t value_turn(uint32_t r) {
+  constexpr int ROWB = T::ROWB;
+  if constexpr (!T::kFew)                           // 64 bytes of rows r .. r + 3
+    return ROWB >= 256 ? (r & 3u) << 2 : (r & 2u) << 1;
+  else if constexpr (sizeof(typename T::C) == 2)    // 32 bytes of rows r .. r + 7
+    return ROWB >= 256 ? (r & 7u) << 1 : r & 6u;
+  else if constexpr (sizeof(typename T::C) == 4)    // 64 bytes of rows r, r + 4, r + 8, r + 12
+    return ((r >> 2) & 3u) << 2;
+  else                                              // 16 bytes of rows r .. r + 7 and r + 16 .. r + 23
+    return ROWB >= 256 ? (r & 7u) | ((r >> 1) & 8u)
+                       : ROWB == 128 ? ((r >> 1) & 3u) | ((r >> 2) & 4u) : ((r >> 2) & 1u) | ((r >> 3) & 2u);
+}
+template <typename T>
+__device__ __forceinline__ uint32_t value_place(uint32_t r, uint32_t c) {
+  return r * T::ROWB + ((c ^ value_turn<T>(r)) << 4);
+}
+
+// 8 e4m3 codes as bf16 (every code's value is one)
+__device__ __forceinline__ bf16x8_t widen8(uint32_t v, uint32_t w) {
+  typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, false);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v, 1.0f, true);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, false);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(w, 1.0f, true);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+// and 16
+__device__ __forceinline__ void widen16(u32x4_t v, u32x4_t& a, u32x4_t& b) {
+  a = __builtin_bit_cast(u32x4_t, widen8(v.x, v.y));
+  b = __builtin_bit_cast(u32x4_t, widen8(v.z, v.w));
+}
+
+// Page ids of the tile after the next.  They are asked for behind the loads of a tile and used
+// after those have been waited for: an address that depends on them never holds up a tile.
+struct AttnPage {
+  int32_t id;       // of this lane's key, -1: not read
+  uint32_t place;   // in the page
+};
+
+// What both kinds of kernels share.
+template <typename T>
+struct AttnLoader {
+  using S = typename T::S;
+  using C = typename T::C;
+
+  static __device__ __forceinline__ AttnPage page_of(const AttnProblem& p, const int32_t* table, int key0,
+                                                     int lo, int hi, int lane) {
+    const int key = key0 + (T::KT == 64 ? lane : lane & 31);
+    AttnPage a{-1, 0};
+    if (key >= lo && key < hi) {
+      const uint32_t col = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page);
+      a.place = static_cast<uint32_t>(key) - col * p.page;
+      a.id = table[col];
+    }
+    return a;
+  }
+
+  // A lane's 16-byte pieces of row r of the packed rows: features place(i) on.
+  template <int QN, typename Place>
+  static __device__ __forceinline__ void load_q(const AttnProblem& p, const AttnSeq& s, int h, int r, Place place,
+                                                bool flip, u32x4_t (&q)[QN]) {
+    const bool in = r < s.n * p.group;
+    const int j = in ? r / p.group : 0;
+    const int head = in ? h * p.group + (r - j * p.group) : 0;
+    const S* at = static_cast<const S*>(p.q) + static_cast<int64_t>(s.first + j) * p.q_row +
+                  static_cast<int64_t>(head) * p.q_head;
+    const uint32_t sign = flip ? (T::ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
+#pragma unroll
+    for (int i = 0; i < QN; ++i) {
+      const u32x4_t v = in ? load16(at + place(i)) : u32x4_t{0, 0, 0, 0};
+      q[i] = u32x4_t{v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign};
+    }
+  }
+
+  // four features of an output row: out = o / l
+  static __device__ __forceinline__ void put(const AttnArgs& g, int first, int h, int r, int d, f32x4_t o,
+                                             float m, float l, float v_scale) {
+    const AttnProblem& p = g.p;
+    const int j = r / p.group;
+    const int head = h * p.group + (r - j * p.group);
+    const int64_t row = (static_cast<int64_t>(first) + j) * p.hq + head;
+    const float inv = l > 0.f ? v_scale / l : 0.f;
+    S* out = static_cast<S*>(p.out) + row * T::D + d;
+    if constexpr (T::ES == 2)
+      *reinterpret_cast<uint2*>(out) = uint2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
+    else
+      *reinterpret_cast<f32x4_t*>(out) = f32x4_t{o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
+    if (p.lse && d == 0) p.lse[row] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+  }
+};
+
+// Scores of a lane's column: mask, running maximum and sum, probabilities in place.  N values of
+// keys key0 + key_of(i); `fold` takes the maximum over the lanes that hold the column's other keys.
+// Returns the factor of what was summed before.
+template <int N, typename KeyOf, typename Fold>
+__device__ __forceinline__ float softmax_step(float (&s)[N], bool edge, int lo, int hi, float scale2, KeyOf key_of,
+                                              Fold fold, float& m, float& l) {
+  if (edge) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      const int key = key_of(i);
+      if (key < lo || key >= hi) s[i] = -INFINITY;
+    }
+  }
+  float top = s[0];
+#pragma unroll
+  for (int i = 1; i < N; ++i) top = fmaxf(top, s[i]);
+  const float next = fmaxf(m, fold(top) * scale2);
+  const float ref = next == -INFINITY ? 0.f : next;   // (nothing seen yet)
+  const float f = __builtin_amdgcn_exp2f(m - ref);
+  m = next;
+  float sum = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale2, -ref));
+    sum += s[i];
+  }
+  l = l * f + sum;
+  return f;
+}
+
+// maximum over lanes l, l ^ 32 (and l ^ 16)
+__device__ __forceinline__ float max_xor32(float v) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+__device__ __forceinline__ float max_xor16(float v) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+
+// four 16-bit values of column lane % 16 from 4 rows x 16 columns that a group of 16 lanes names,
+// 8 bytes each
+__device__ __forceinline__ i16x4_t read_tr(const char* p) {
+  typedef __attribute__((address_space(3))) i16x4_t* lds_t;
+  return __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_t)p);
+}
+__device__ __forceinline__ bf16x8_t join_tr(i16x4_t x, i16x4_t y) {
+  typedef short i16x8_t __attribute__((ext_vector_type(8)));
+  const i16x8_t a = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+  return __builtin_bit_cast(bf16x8_t, a);
+}
+
+// -------------------------------------------------------------- many rows
 // A staged tile: what a thread holds of the next keys and values.
 template <typename T>
 struct AttnStage {
@@ -204,41 +351,27 @@ struct AttnStage {
 };
 
 template <typename T>
-struct AttnBody {
+struct AttnManyBody : AttnLoader<T> {
+  using L = AttnLoader<T>;
   using S = typename T::S;
   using C = typename T::C;
-  using Plan = AttnPlan<T::BM, T::KT>;
 
-  // where key t of a tile lies in the cache (elements from the head's base), and whether it is read
-  static __device__ __forceinline__ void look_up(const AttnProblem& p, const int32_t* table, int key0,
-                                                 int lo, int hi, int lane, int64_t& off, uint64_t& live) {
-    const int key = key0 + (T::KT == 64 ? lane : lane & 31);
-    bool in = key >= lo && key < hi;
-    off = 0;
-    if (in) {
-      const uint32_t col = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page);
-      const int32_t page = table[col];
-      in = page >= 0 && page < p.pages;
-      if (in)
-        off = page * p.page_stride + (static_cast<uint32_t>(key) - col * p.page) * p.token_stride;
-    }
-    live = __ballot(in);
-  }
-
-  static __device__ __forceinline__ void load(const C* kb, const C* vb, int64_t off, uint64_t live, int st,
+  static __device__ __forceinline__ void load(const AttnProblem& p, const C* kb, const C* vb, AttnPage a, int st,
                                               AttnStage<T>& g) {
+    const bool in = a.id >= 0 && a.id < p.pages;
+    g.live = __ballot(in);
+    // a key that is not read takes the first page's first row, and is cleared below
+    const int64_t off = in ? a.id * p.page_stride + a.place * p.token_stride : 0;
     const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
 #pragma unroll
     for (int i = 0; i < T::LOADS; ++i) {
       const int idx = st + T::SHARE * i;
       const int row = idx / T::CPR, c = idx % T::CPR;
       const uint32_t l = __shfl(lo, row), h = __shfl(hi, row);
-      // a key that is not read takes the first page's first row, and is cleared below
       const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l) + c * T::PER16;
       g.k[i] = load16(kb + at);
       g.v[i] = load16(vb + at);
     }
-    g.live = live;
   }
 
   static __device__ __forceinline__ void store(char* lk, char* lv, int st, AttnStage<T>& g) {
@@ -256,33 +389,16 @@ struct AttnBody {
         *reinterpret_cast<u32x4_t*>(lk + key_place<T::ROWB>(row, 2 * c)) = a;
         *reinterpret_cast<u32x4_t*>(lk + key_place<T::ROWB>(row, 2 * c + 1)) = b;
         widen16(v, a, b);
-        *reinterpret_cast<u32x4_t*>(lv + value_place<T::ROWB>(row, 2 * c)) = a;
-        *reinterpret_cast<u32x4_t*>(lv + value_place<T::ROWB>(row, 2 * c + 1)) = b;
+        *reinterpret_cast<u32x4_t*>(lv + value_place<T>(row, 2 * c)) = a;
+        *reinterpret_cast<u32x4_t*>(lv + value_place<T>(row, 2 * c + 1)) = b;
       } else {
         *reinterpret_cast<u32x4_t*>(lk + key_place<T::ROWB>(row, c)) = k;
-        *reinterpret_cast<u32x4_t*>(lv + value_place<T::ROWB>(row, c)) = v;
+        *reinterpret_cast<u32x4_t*>(lv + value_place<T>(row, c)) = v;
       }
     }
   }
 
-  // 16-byte pieces of a row tile's queries: piece s of a lane is chunk 2 s + lane / 32 of query lane % 32
-  static __device__ __forceinline__ void load_q(const AttnProblem& p, const AttnSeq& s, int h, int r0,
-                                                int lane, bool flip, u32x4_t (&q)[T::QN]) {
-    const int r = r0 + (lane & 31);
-    const bool in = r < s.n * p.group;
-    const int j = in ? r / p.group : 0;
-    const int head = in ? h * p.group + (r - j * p.group) : 0;
-    const S* at = static_cast<const S*>(p.q) + static_cast<int64_t>(s.first + j) * p.q_row +
-                  static_cast<int64_t>(head) * p.q_head + (lane >> 5) * (16 / T::ES);
-    const uint32_t sign = flip ? (T::ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
-#pragma unroll
-    for (int i = 0; i < T::QN; ++i) {
-      const u32x4_t v = in ? load16(at + i * (32 / T::ES)) : u32x4_t{0, 0, 0, 0};
-      q[i] = u32x4_t{v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign};
-    }
-  }
-
-  // S^T of 32 keys against 32 queries
+  // S^T of 32 keys against the wave's 32 queries: keys 8 (r / 4) + 4 (lane / 32) + r % 4 of query lane % 32
   static __device__ __forceinline__ f32x16_t scores(const char* lk, int sub, int lane,
                                                     const u32x4_t (&q)[T::QN]) {
     f32x16_t c = {};
@@ -303,33 +419,22 @@ struct AttnBody {
   }
 
   // O^T += V^T P^T of 32 keys, whose probabilities a lane holds as the scores' registers lie
-  static __device__ __forceinline__ void add_values(const char* lv, int sub, int lane,
-                                                    const f32x16_t (&p)[T::RT], AttnState<T>& st) {
+  static __device__ __forceinline__ void add_values(const char* lv, int sub, int lane, const float* p,
+                                                    f32x16_t (&o)[T::D / 32]) {
     const int half = lane >> 5;
     if constexpr (T::ES == 2) {
 #pragma unroll
       for (int ks = 0; ks < 2; ++ks) {
-        u32x4_t b[T::RT];
+        u32x4_t b;
 #pragma unroll
-        for (int rt = 0; rt < T::RT; ++rt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) b[rt][e] = pack_bf16(p[rt][8 * ks + 2 * e], p[rt][8 * ks + 2 * e + 1]);
-        // lanes of a group of 16 read 4 keys x 16 features, each 8 bytes, and get a column of it
+        for (int e = 0; e < 4; ++e) b[e] = pack_bf16(p[8 * ks + 2 * e], p[8 * ks + 2 * e + 1]);
         const uint32_t row = 32 * sub + 16 * ks + 4 * half + ((lane & 15) >> 2);
 #pragma unroll
         for (int i = 0; i < T::D / 32; ++i) {
           const uint32_t c = 4 * i + ((lane >> 3) & 2) + ((lane >> 1) & 1);
-          typedef __attribute__((address_space(3))) i16x4_t* lds_t;
-          const i16x4_t x = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_t)(lv + value_place<T::ROWB>(row, c) + (lane & 1) * 8));
-          const i16x4_t y = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (lds_t)(lv + value_place<T::ROWB>(row + 8, c) + (lane & 1) * 8));
-          typedef short i16x8_t __attribute__((ext_vector_type(8)));
-          const i16x8_t a = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-#pragma unroll
-          for (int rt = 0; rt < T::RT; ++rt)
-            st.o[rt][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8_t, a), __builtin_bit_cast(bf16x8_t, b[rt]), st.o[rt][i], 0, 0, 0);
+          const bf16x8_t a = join_tr(read_tr(lv + value_place<T>(row, c) + (lane & 1) * 8),
+                                     read_tr(lv + value_place<T>(row + 8, c) + (lane & 1) * 8));
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, __builtin_bit_cast(bf16x8_t, b), o[i], 0, 0, 0);
         }
       }
     } else {
@@ -339,86 +444,11 @@ struct AttnBody {
 #pragma unroll
         for (int i = 0; i < T::D / 32; ++i) {
           const uint32_t d = 32 * i + (lane & 31);
-          const float a = *reinterpret_cast<const float*>(lv + value_place<T::ROWB>(row, d / 4) + (d & 3) * 4);
-#pragma unroll
-          for (int rt = 0; rt < T::RT; ++rt)
-            st.o[rt][i] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[rt][r], st.o[rt][i], 0, 0, 0);
+          const float a = *reinterpret_cast<const float*>(lv + value_place<T>(row, d / 4) + (d & 3) * 4);
+          o[i] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[r], o[i], 0, 0, 0);
         }
       }
     }
-  }
-
-  // One tile of keys [key0, key0 + KT): row_lo / row_hi bound what a lane's query sees; `edge`
-  // where some query of the wave does not see all of it.
-  static __device__ __forceinline__ void tile(const char* lk, const char* lv, int key0, int lane, bool edge,
-                                              float scale2, const u32x4_t (&q)[T::RT][T::QN],
-                                              const int (&row_lo)[T::RT], const int (&row_hi)[T::RT],
-                                              AttnState<T>& st) {
-    constexpr int SUB = T::KT / 32;
-    f32x16_t s[SUB][T::RT];
-#pragma unroll
-    for (int u = 0; u < SUB; ++u)
-#pragma unroll
-      for (int rt = 0; rt < T::RT; ++rt) s[u][rt] = scores(lk, u, lane, q[rt]);
-    if (edge) {
-#pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int key = key0 + 32 * u + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
-#pragma unroll
-          for (int rt = 0; rt < T::RT; ++rt)
-            if (key < row_lo[rt] || key >= row_hi[rt]) s[u][rt][r] = -INFINITY;
-        }
-    }
-#pragma unroll
-    for (int rt = 0; rt < T::RT; ++rt) {
-      float top = s[0][rt][0];
-#pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) top = fmaxf(top, s[u][rt][r]);
-      top = fmaxf(top, __shfl_xor(top, 32));   // the other half wave holds the other keys
-      const float m = fmaxf(st.m[rt], top * scale2);
-      if (__any(m > st.m[rt])) {
-        const float f = __builtin_amdgcn_exp2f(st.m[rt] - (m == -INFINITY ? 0.f : m));
-        st.l[rt] *= f;
-#pragma unroll
-        for (int i = 0; i < T::D / 32; ++i)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) st.o[rt][i][r] *= f;
-        st.m[rt] = m;
-      }
-      const float ref = m == -INFINITY ? 0.f : m;   // (nothing seen yet)
-      float sum = 0.f;
-#pragma unroll
-      for (int u = 0; u < SUB; ++u)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float e = __builtin_amdgcn_exp2f(fmaf(s[u][rt][r], scale2, -ref));
-          s[u][rt][r] = e;
-          sum += e;
-        }
-      st.l[rt] += sum;
-    }
-#pragma unroll
-    for (int u = 0; u < SUB; ++u) add_values(lv, u, lane, s[u], st);
-  }
-
-  // rows of the output: out = o / l, or a partial
-  static __device__ __forceinline__ void put(const AttnArgs& g, const AttnSeq& s, int h, int r, int d,
-                                             f32x4_t o, float m, float l, float v_scale) {
-    const AttnProblem& p = g.p;
-    const int j = r / p.group;
-    const int head = h * p.group + (r - j * p.group);
-    const int64_t row = (static_cast<int64_t>(s.first) + j) * p.hq + head;
-    const float inv = l > 0.f ? v_scale / l : 0.f;
-    S* out = static_cast<S*>(p.out) + row * T::D + d;
-    if constexpr (T::ES == 2)
-      *reinterpret_cast<uint2*>(out) = uint2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
-    else
-      *reinterpret_cast<f32x4_t*>(out) = f32x4_t{o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-    if (p.lse && d == 0) p.lse[row] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
   }
 
   // One row tile over key tiles [ta, tb).  slot < 0: the output itself, else a partial there.
@@ -427,9 +457,8 @@ struct AttnBody {
     const AttnProblem& p = g.p;
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int lane = static_cast<int>(threadIdx.x) & 63;
-    const int wm = T::WM > 1 ? wave : 0, wn = T::WM > 1 ? 0 : wave;
-    const int st_id = T::WM > 1 ? static_cast<int>(threadIdx.x) : lane;   // place among the loading threads
-    const int r0 = m * T::BM + wm * 32 * T::RT;
+    const int tid = static_cast<int>(threadIdx.x);
+    const int r0 = m * T::BM + wave * 32;
     const int rows = s.n * p.group;
     float scale2 = g.scale2, v_scale = 1.f;
     if constexpr (sizeof(C) == 1) {
@@ -439,139 +468,391 @@ struct AttnBody {
     const bool flip = scale2 < 0.f;   // the running maximum wants a positive scale
     scale2 = fmaxf(fabsf(scale2), 1e-30f);
 
-    u32x4_t q[T::RT][T::QN];
-    int row_lo[T::RT], row_hi[T::RT];
-    AttnState<T> st;
-#pragma unroll
-    for (int rt = 0; rt < T::RT; ++rt) {
-      load_q(p, s, h, r0 + 32 * rt, lane, flip, q[rt]);
-      const int at = s.len - s.n + (r0 + 32 * rt + (lane & 31)) / p.group;
-      row_hi[rt] = p.causal ? min(at + 1, s.len) : s.len;
-      row_lo[rt] = p.window ? at - p.window + 1 : 0;
-      st.m[rt] = -INFINITY;
-      st.l[rt] = 0.f;
-#pragma unroll
-      for (int i = 0; i < T::D / 32; ++i) st.o[rt][i] = f32x16_t{};
-    }
-    // the wave's rows all see the keys [see_lo, see_hi)
-    const int first = s.len - s.n + r0 / p.group;
-    const int last = s.len - s.n + min(r0 + 32 * T::RT - 1, rows - 1) / p.group;
-    const int see_hi = p.causal ? min(first + 1, s.len) : s.len;
-    const int see_lo = p.window ? last - p.window + 1 : 0;
-
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
     const C* kb = static_cast<const C*>(p.k_cache) + h * p.head_stride;
     const C* vb = static_cast<const C*>(p.v_cache) + h * p.head_stride;
-    char* const base = lds + wn * T::WAVE_BYTES;
-
     AttnStage<T> stage;
-    int64_t off;
-    uint64_t live;
-    int t = ta + wn;
-    if (t < tb) {
-      look_up(p, table, t * T::KT, lo, hi, lane, off, live);
-      load(kb, vb, off, live, st_id, stage);
-      if (t + T::WN < tb) look_up(p, table, (t + T::WN) * T::KT, lo, hi, lane, off, live);
-    }
+    AttnPage page = L::page_of(p, table, ta * T::KT, lo, hi, lane);
+    load(p, kb, vb, page, tid, stage);
+    page = L::page_of(p, table, (ta + 1) * T::KT, lo, hi, lane);
+
+    u32x4_t q[T::QN];
+    L::load_q(p, s, h, r0 + (lane & 31), [&](int i) { return (2 * i + (lane >> 5)) * (16 / T::ES); }, flip, q);
+    const int at = s.len - s.n + (r0 + (lane & 31)) / p.group;
+    const int row_hi = p.causal ? min(at + 1, s.len) : s.len;
+    const int row_lo = p.window ? at - p.window + 1 : 0;
+    f32x16_t o[T::D / 32];
+    float mx = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < T::D / 32; ++i) o[i] = f32x16_t{};
+    // the wave's rows all see the keys [see_lo, see_hi)
+    const int first = s.len - s.n + r0 / p.group;
+    const int last = s.len - s.n + min(r0 + 31, rows - 1) / p.group;
+    const int see_hi = p.causal ? min(first + 1, s.len) : s.len;
+    const int see_lo = p.window ? last - p.window + 1 : 0;
+
     int buf = 0;
-    for (; t < tb; t += T::WN) {
-      char* lk = base + buf * 2 * T::TILE_BYTES;
+    for (int t = ta; t < tb; ++t) {
+      char* lk = lds + buf * 2 * T::TILE_BYTES;
       char* lv = lk + T::TILE_BYTES;
-      store(lk, lv, st_id, stage);
-      if (t + T::WN < tb) {
-        load(kb, vb, off, live, st_id, stage);
-        if (t + 2 * T::WN < tb) look_up(p, table, (t + 2 * T::WN) * T::KT, lo, hi, lane, off, live);
+      store(lk, lv, tid, stage);
+      if (t + 1 < tb) {
+        load(p, kb, vb, page, tid, stage);
+        page = L::page_of(p, table, (t + 2) * T::KT, lo, hi, lane);
       }
-      if constexpr (T::WM > 1) {
-        // one barrier a tile: the buffer written next was last read before the barrier after that
-        __syncthreads();
-        buf ^= 1;
-      } else {
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      }
+      // one barrier a tile: the buffer written next was last read before the barrier after that
+      __syncthreads();
+      buf ^= 1;
+      if (r0 >= rows) continue;
       const int key0 = t * T::KT;
       const bool edge = key0 < see_lo || key0 + T::KT > see_hi;
-      if (T::WM == 1 || r0 < rows)
-        tile(lk, lv, key0, lane, edge, scale2, q, row_lo, row_hi, st);
-      if constexpr (T::WM == 1) __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    }
+      float pr[T::KT / 2];
 #pragma unroll
-    for (int rt = 0; rt < T::RT; ++rt) st.l[rt] += __shfl_xor(st.l[rt], 32);
-
-    if constexpr (T::WM > 1) {
+      for (int u = 0; u < T::KT / 32; ++u) {
+        const f32x16_t c = scores(lk, u, lane, q);
 #pragma unroll
-      for (int rt = 0; rt < T::RT; ++rt) {
-        const int rl = wm * 32 * T::RT + 32 * rt + (lane & 31);   // row in the tile
-        const int r = m * T::BM + rl;
-        if (r < rows) {
-          if (slot >= 0 && lane < 32) g.part_ml[slot * T::BM + rl] = float2{st.m[rt], st.l[rt]};
-#pragma unroll
-          for (int i = 0; i < T::D / 32; ++i)
-#pragma unroll
-            for (int x = 0; x < 4; ++x) {
-              const int d = 32 * i + 8 * x + 4 * (lane >> 5);
-              const f32x4_t o = {st.o[rt][i][4 * x], st.o[rt][i][4 * x + 1], st.o[rt][i][4 * x + 2],
-                                 st.o[rt][i][4 * x + 3]};
-              if (slot >= 0)
-                *reinterpret_cast<f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + d) = o;
-              else
-                put(g, s, h, r, d, o, st.m[rt], st.l[rt], v_scale);
-            }
-        }
+        for (int r = 0; r < 16; ++r) pr[16 * u + r] = c[r];
       }
-      __syncthreads();   // the tiles in LDS are read: the next row tile may overwrite them
-    } else {
-      // join the waves' states through LDS, 32 rows at a time
-      __shared__ float2 ml[T::WN][32];
-#pragma unroll
-      for (int rt = 0; rt < T::RT; ++rt) {
-        const int qi = lane & 31;
+      const float was = mx;
+      const float f = softmax_step<T::KT / 2>(
+          pr, edge, row_lo, row_hi, scale2,
+          [&](int i) { return key0 + 32 * (i / 16) + 8 * (i % 16 / 4) + 4 * (lane >> 5) + i % 4; }, max_xor32, mx, l);
+      if (__any(mx > was)) {
 #pragma unroll
         for (int i = 0; i < T::D / 32; ++i)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t c = 8 * i + 2 * x + (lane >> 5);   // 16-byte chunk of the row
-            *reinterpret_cast<f32x4_t*>(base + qi * T::D * 4 + ((c ^ (qi & 15)) << 4)) =
-                f32x4_t{st.o[rt][i][4 * x], st.o[rt][i][4 * x + 1], st.o[rt][i][4 * x + 2], st.o[rt][i][4 * x + 3]};
-          }
-        if (lane < 32) ml[wn][qi] = float2{st.m[rt], st.l[rt]};
-        __syncthreads();
-        for (int idx = static_cast<int>(threadIdx.x); idx < 32 * (T::D / 4); idx += T::THREADS) {
-          const int qr = idx / (T::D / 4), c = idx % (T::D / 4);
-          const int rl = 32 * rt + qr;
-          const int r = m * T::BM + rl;
-          if (r < rows) {
-            float mm = ml[0][qr].x;
+          for (int r = 0; r < 16; ++r) o[i][r] *= f;
+      }
 #pragma unroll
-            for (int w = 1; w < T::WN; ++w) mm = fmaxf(mm, ml[w][qr].x);
-            const float ref = mm == -INFINITY ? 0.f : mm;
-            float l = 0.f;
-            f32x4_t o = {0.f, 0.f, 0.f, 0.f};
+      for (int u = 0; u < T::KT / 32; ++u) add_values(lv, u, lane, pr + 16 * u, o);
+    }
+    l += __shfl_xor(l, 32);
+
+    const int rl = wave * 32 + (lane & 31);   // row in the tile
+    const int r = m * T::BM + rl;
+    if (r < rows) {
+      if (slot >= 0 && lane < 32) g.part_ml[slot * T::BM + rl] = float2{mx, l};
 #pragma unroll
-            for (int w = 0; w < T::WN; ++w) {
-              const float f = __builtin_amdgcn_exp2f(ml[w][qr].x - ref);
-              l += f * ml[w][qr].y;
-              const f32x4_t ow =
-                  *reinterpret_cast<const f32x4_t*>(lds + w * T::WAVE_BYTES + qr * T::D * 4 + ((c ^ (qr & 15)) << 4));
-              o += f * ow;
-            }
-            if (slot >= 0) {
-              *reinterpret_cast<f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + 4 * c) = o;
-              if (c == 0) g.part_ml[slot * T::BM + rl] = float2{mm, l};
-            } else {
-              put(g, s, h, r, 4 * c, o, mm, l, v_scale);
-            }
+      for (int i = 0; i < T::D / 32; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int d = 32 * i + 8 * x + 4 * (lane >> 5);
+          const f32x4_t v = {o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]};
+          if (slot >= 0)
+            *reinterpret_cast<f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + d) = v;
+          else
+            L::put(g, s.first, h, r, d, v, mx, l, v_scale);
+        }
+    }
+    __syncthreads();   // the tiles in LDS are read: the next row tile may overwrite them
+  }
+};
+
+// -------------------------------------------------------------- few rows
+static __device__ const uint32_t kZeros16[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
+
+// 16 bytes per lane, cache -> LDS: lane l's land at dst + 16 l (dst uniform)
+__device__ __forceinline__ void copy_lds16(const char* src, char* dst) {
+  __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+}
+
+template <typename T>
+struct AttnFewBody : AttnLoader<T> {
+  using L = AttnLoader<T>;
+  using S = typename T::S;
+  using C = typename T::C;
+
+  // A tile of keys and values on its way to LDS.  Where all its keys are read and the rows of a
+  // load lie in one page, the page is the load's own scalar; else every lane looks its row up,
+  // and keys that are not read come from zeros.
+  static __device__ __forceinline__ void load(const AttnProblem& p, const char* kb, const char* vb, AttnPage a,
+                                              int lane, char* lk, char* lv) {
+    constexpr uint64_t kAll = T::KT == 64 ? ~0ull : 0xFFFFFFFFull;
+    const bool in = a.id >= 0 && a.id < p.pages;
+    const uint64_t live = __ballot(in) & kAll;
+    asm volatile("" : "+v"(lane));   // (offsets are made anew: held over the loop they take 4 LOADS registers)
+    const uint32_t sub = lane / T::CPR, pos = lane % T::CPR;
+    // the turns of rows RPL i and sub are of different bits
+    const uint32_t kc = (pos ^ key_turn<T::ROWB>(sub)) << 4, vc = (pos ^ value_turn<T>(sub)) << 4;
+    if (live == kAll && p.page % T::RPL == 0 && p.token_stride < (1 << 30) / 64) {
+      const uint32_t mine = sub * static_cast<uint32_t>(p.token_stride) * T::CS;
+#pragma unroll
+      for (int i = 0; i < T::LOADS; ++i) {
+        const int id = __builtin_amdgcn_readlane(a.id, T::RPL * i);
+        const int place = __builtin_amdgcn_readlane(static_cast<int>(a.place), T::RPL * i);
+        const int64_t off = (id * p.page_stride + place * p.token_stride) * T::CS;
+        copy_lds16(kb + off + (mine + (kc ^ (key_turn<T::ROWB>(T::RPL * i) << 4))), lk + 1024 * i);
+        copy_lds16(vb + off + (mine + (vc ^ (value_turn<T>(T::RPL * i) << 4))), lv + 1024 * i);
+      }
+    } else {
+      const int64_t off = in ? (a.id * p.page_stride + a.place * p.token_stride) * T::CS : 0;
+      const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
+#pragma unroll 1
+      for (int i = 0; i < T::LOADS; ++i) {
+        const uint32_t row = T::RPL * i + sub;
+        const uint32_t l = __shfl(lo, row), h = __shfl(hi, row);
+        const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l);
+        const bool read = (live >> row) & 1;
+        const char* zero = reinterpret_cast<const char*>(kZeros16);
+        copy_lds16(read ? kb + at + (kc ^ (key_turn<T::ROWB>(T::RPL * i) << 4)) : zero, lk + 1024 * i);
+        copy_lds16(read ? vb + at + (vc ^ (value_turn<T>(T::RPL * i) << 4)) : zero, lv + 1024 * i);
+      }
+    }
+  }
+
+  // first feature of query piece i of lane group grp: as the keys' operand takes them
+  static __device__ __forceinline__ int q_place(int i, int grp) {
+    if constexpr (T::CS == 1) return 64 * (i / 2) + 16 * grp + 8 * (i % 2);
+    return (4 * i + grp) * (16 / T::ES);
+  }
+
+  // query piece i of row tile rt: a register, or LDS (as keys lie there)
+  static __device__ __forceinline__ uint32_t q_lds(int row, int i, int grp) {
+    return T::Q_AT + key_place<T::D * T::ES>(row, q_place(i, grp) * T::ES / 16);
+  }
+
+  // S^T of 32 keys against RT x 16 queries: pr[rt][4 u + r] of key 16 u + 4 (lane / 16) + r of query lane % 16
+  static __device__ __forceinline__ void scores(const char* lds, const char* lk, int sub, int lane,
+                                                const u32x4_t (&q)[T::RT][T::QLDS ? 1 : T::QN],
+                                                float (&pr)[T::RT][8]) {
+    f32x4_t c[2][T::RT];
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int rt = 0; rt < T::RT; ++rt) c[u][rt] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    auto query = [&](int rt, int i) -> u32x4_t {
+      if constexpr (T::QLDS) return load16(lds + q_lds(16 * rt + (lane & 15), i, lane >> 4));
+      else return q[rt][i];
+    };
+    const uint32_t row = 32 * sub + (lane & 15);
+#pragma unroll
+    for (int i = 0; i < T::ROWB / 64; ++i) {
+      u32x4_t a[2];
+#pragma unroll
+      for (int u = 0; u < 2; ++u) a[u] = load16(lk + key_place<T::ROWB>(row + 16 * u, 4 * i + (lane >> 4)));
+      if constexpr (T::CS == 1) {
+        u32x4_t x[2], y[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) widen16(a[u], x[u], y[u]);
+#pragma unroll
+        for (int rt = 0; rt < T::RT; ++rt) {
+          const u32x4_t q0 = query(rt, 2 * i), q1 = query(rt, 2 * i + 1);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            c[u][rt] = mma16(x[u], q0, c[u][rt], S{});
+            c[u][rt] = mma16(y[u], q1, c[u][rt], S{});
           }
         }
-        __syncthreads();
+      } else {
+#pragma unroll
+        for (int rt = 0; rt < T::RT; ++rt) {
+          const u32x4_t q0 = query(rt, i);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) c[u][rt] = mma16(a[u], q0, c[u][rt], S{});
+        }
       }
+    }
+#pragma unroll
+    for (int rt = 0; rt < T::RT; ++rt)
+#pragma unroll
+      for (int i = 0; i < 8; ++i) pr[rt][i] = c[i / 4][rt][i % 4];
+  }
+
+  // O^T += V^T P^T of 32 keys: features 16 i + 4 (lane / 16) + r of query lane % 16.  A lane's
+  // probabilities pr[0 .. 4) are of keys 4 (lane / 16) + r, pr[4 .. 8) of those plus 16.
+  static __device__ __forceinline__ void add_values(const char* lv, int sub, int lane,
+                                                    const float (&pr)[T::RT][8],
+                                                    f32x4_t (&o)[T::RT][T::D / 16]) {
+    const int grp = lane >> 4;
+    if constexpr (T::ES == 2) {
+      u32x4_t b[T::RT];
+#pragma unroll
+      for (int rt = 0; rt < T::RT; ++rt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          b[rt][e] = pack_bf16(pr[rt][2 * e], pr[rt][2 * e + 1]);
+#pragma unroll
+      for (int i = 0; i < T::D / 16; ++i) {
+        bf16x8_t a;
+        if constexpr (T::CS == 2) {
+          const uint32_t row = 32 * sub + 4 * grp + ((lane & 15) >> 2);
+          const uint32_t c = 2 * i + ((lane >> 1) & 1);
+          a = join_tr(read_tr(lv + value_place<T>(row, c) + (lane & 1) * 8),
+                      read_tr(lv + value_place<T>(row + 16, c) + (lane & 1) * 8));
+        } else {
+          // 8 rows x 16 codes of a group of 16 lanes, 8 bytes each; a lane gets a column of it
+          const uint32_t e = (lane & 15) >> 1;
+          const uint32_t row = 32 * sub + 4 * grp + (e & 3) + 4 * (e & 4);
+          typedef int i32x2_t __attribute__((ext_vector_type(2)));
+          typedef __attribute__((address_space(3))) i32x2_t* lds_t;
+          const i32x2_t x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_t)(lv + value_place<T>(row, i) + (lane & 1) * 8));
+          a = widen8(x.x, x.y);
+        }
+#pragma unroll
+        for (int rt = 0; rt < T::RT; ++rt)
+          o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, b[rt]), o[rt][i], 0, 0, 0);
+      }
+    } else {
+#pragma unroll
+      for (int x = 0; x < 8; ++x) {
+        const uint32_t row = 32 * sub + 16 * (x / 4) + 4 * grp + x % 4;
+#pragma unroll
+        for (int i = 0; i < T::D / 16; ++i) {
+          const uint32_t d = 16 * i + (lane & 15);
+          const float a = *reinterpret_cast<const float*>(lv + value_place<T>(row, d / 4) + (d & 3) * 4);
+#pragma unroll
+          for (int rt = 0; rt < T::RT; ++rt)
+            o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x4f32(a, pr[rt][x], o[rt][i], 0, 0, 0);
+        }
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void run(const AttnArgs& g, const AttnSeq& s, int b, int h, int m, int ta,
+                                             int tb, int lo, int hi, int64_t slot, char* lds) {
+    const AttnProblem& p = g.p;
+    const int wn = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    const int r0 = m * T::BM;
+    const int rows = s.n * p.group;
+    float scale2 = g.scale2, v_scale = 1.f;
+    if constexpr (sizeof(C) == 1) {
+      scale2 *= p.k_scale[h];
+      v_scale = p.v_scale[h];
+    }
+    const bool flip = scale2 < 0.f;   // the running maximum wants a positive scale
+    scale2 = fmaxf(fabsf(scale2), 1e-30f);
+
+    const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
+    const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_stride * T::CS;
+    const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_stride * T::CS;
+    char* const lk = lds + wn * T::WAVE_BYTES;
+    char* const lv = lk + T::TILE_BYTES;
+    AttnPage page{};
+    int t = ta + wn;
+    if (t < tb) {
+      page = L::page_of(p, table, t * T::KT, lo, hi, lane);
+      load(p, kb, vb, page, lane, lk, lv);
+      page = L::page_of(p, table, (t + T::WN) * T::KT, lo, hi, lane);
+    }
+    u32x4_t q[T::RT][T::QLDS ? 1 : T::QN];
+    int row_lo[T::RT], row_hi[T::RT];
+    f32x4_t o[T::RT][T::D / 16];
+    float mx[T::RT], l[T::RT];
+#pragma unroll
+    for (int rt = 0; rt < T::RT; ++rt) {
+      const int r = r0 + 16 * rt + (lane & 15);
+      if constexpr (T::QLDS) {
+        if (wn == rt) {   // (WN waves, a row tile each: RT <= WN)
+          u32x4_t x[T::QN];
+          L::load_q(p, s, h, r, [&](int i) { return q_place(i, lane >> 4); }, flip, x);
+#pragma unroll
+          for (int i = 0; i < T::QN; ++i)
+            *reinterpret_cast<u32x4_t*>(lds + q_lds(16 * rt + (lane & 15), i, lane >> 4)) = x[i];
+        }
+      } else {
+        L::load_q(p, s, h, r, [&](int i) { return q_place(i, lane >> 4); }, flip, q[rt]);
+      }
+      const int at = s.len - s.n + r / p.group;
+      row_hi[rt] = p.causal ? min(at + 1, s.len) : s.len;
+      row_lo[rt] = p.window ? at - p.window + 1 : 0;
+      mx[rt] = -INFINITY;
+      l[rt] = 0.f;
+#pragma unroll
+      for (int i = 0; i < T::D / 16; ++i) o[rt][i] = f32x4_t{0.f, 0.f, 0.f, 0.f};
+    }
+    // the rows all see the keys [see_lo, see_hi)
+    const int first = s.len - s.n + r0 / p.group;
+    const int last = s.len - s.n + min(r0 + T::BM - 1, rows - 1) / p.group;
+    const int see_hi = p.causal ? min(first + 1, s.len) : s.len;
+    const int see_lo = p.window ? last - p.window + 1 : 0;
+
+    if constexpr (T::QLDS) __syncthreads();   // the queries are in LDS
+    for (; t < tb; t += T::WN) {
+      // the wave's own LDS: it waits for its own loads, and the next tile's are behind its reads
+      asm volatile("" ::: "memory");
+      BDR_WAIT_VM(0);
+      asm volatile("" ::: "memory");
+      const int key0 = t * T::KT;
+      const bool edge = key0 < see_lo || key0 + T::KT > see_hi;
+#pragma unroll
+      for (int u = 0; u < T::KT / 32; ++u) {
+        float pr[T::RT][8];
+        scores(lds, lk, u, lane, q, pr);
+#pragma unroll
+        for (int rt = 0; rt < T::RT; ++rt) {
+          const float was = mx[rt];
+          const float f = softmax_step<8>(
+              pr[rt], edge, row_lo[rt], row_hi[rt], scale2,
+              [&](int i) { return key0 + 32 * u + 16 * (i / 4) + 4 * (lane >> 4) + i % 4; },
+              [](float v) { return max_xor32(max_xor16(v)); }, mx[rt], l[rt]);
+          if (__any(mx[rt] > was)) {
+#pragma unroll
+            for (int i = 0; i < T::D / 16; ++i) o[rt][i] *= f;
+          }
+        }
+        add_values(lv, u, lane, pr, o);
+      }
+      // every read of the tile has returned before the next one overwrites it
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      if (t + T::WN < tb) {
+        load(p, kb, vb, page, lane, lk, lv);
+        page = L::page_of(p, table, (t + 2 * T::WN) * T::KT, lo, hi, lane);
+      }
+    }
+
+    // join the waves' states through LDS, 16 rows at a time
+    auto ml = [&](int w) { return reinterpret_cast<float2*>(lds + w * T::WAVE_BYTES + 16 * T::D * 4); };
+#pragma unroll
+    for (int rt = 0; rt < T::RT; ++rt) {
+      const int qi = lane & 15;
+      l[rt] += __shfl_xor(l[rt], 16);
+      l[rt] += __shfl_xor(l[rt], 32);
+#pragma unroll
+      for (int i = 0; i < T::D / 16; ++i) {
+        const uint32_t c = 4 * i + (lane >> 4);   // 16-byte chunk of the row
+        *reinterpret_cast<f32x4_t*>(lk + qi * T::D * 4 + ((c ^ qi) << 4)) = o[rt][i];
+      }
+      if (lane < 16) ml(wn)[qi] = float2{mx[rt], l[rt]};
+      __syncthreads();
+      for (int idx = static_cast<int>(threadIdx.x); idx < 16 * (T::D / 4); idx += T::THREADS) {
+        const int qr = idx / (T::D / 4), c = idx % (T::D / 4);
+        const int rl = 16 * rt + qr;
+        const int r = r0 + rl;
+        if (r < rows) {
+          float mm = ml(0)[qr].x;
+#pragma unroll
+          for (int w = 1; w < T::WN; ++w) mm = fmaxf(mm, ml(w)[qr].x);
+          const float ref = mm == -INFINITY ? 0.f : mm;
+          float ls = 0.f;
+          f32x4_t v = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int w = 0; w < T::WN; ++w) {
+            const float f = __builtin_amdgcn_exp2f(ml(w)[qr].x - ref);
+            ls += f * ml(w)[qr].y;
+            v += f * *reinterpret_cast<const f32x4_t*>(lds + w * T::WAVE_BYTES + qr * T::D * 4 + ((c ^ qr) << 4));
+          }
+          if (slot >= 0) {
+            *reinterpret_cast<f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + 4 * c) = v;
+            if (c == 0) g.part_ml[slot * T::BM + rl] = float2{mm, ls};
+          } else {
+            L::put(g, s.first, h, r, 4 * c, v, mm, ls, v_scale);
+          }
+        }
+      }
+      __syncthreads();
     }
   }
 };
 
+template <typename T>
+using AttnBody = std::conditional_t<T::kFew, AttnFewBody<T>, AttnManyBody<T>>;
+
 // The workgroup's share of all key tiles, row tile by row tile.
 template <typename T>
-__global__ __launch_bounds__(T::THREADS) void attn_kernel(const AttnArgs g) {
+__global__ __launch_bounds__(T::THREADS, T::SIMD_WAVES) void attn_kernel(const AttnArgs g) {
   using Plan = AttnPlan<T::BM, T::KT>;
   __shared__ __attribute__((aligned(16))) char lds[T::LDS_BYTES];
   const AttnProblem& p = g.p;
@@ -639,15 +920,9 @@ __global__ __launch_bounds__(T::THREADS) void attn_kernel(const AttnArgs g) {
       int lo, hi, t0, t1;
       Plan::range(p, s, m, lo, hi, t0, t1);
       const int nt = t1 - t0;
-      if (g.whole) {
-        AttnBody<T>::run(g, s, b, h, m, t0, t1, lo, hi, -1, lds);
-        x += 1;
-        fresh = false;
-        break;
-      }
       if (inner < done + nt) {
-        const int from = inner - done;
-        const int to = static_cast<int>(min(static_cast<int64_t>(nt), from + (end - x)));
+        const int from = g.whole ? 0 : inner - done;
+        const int to = g.whole ? nt : static_cast<int>(min(static_cast<int64_t>(nt), from + (end - x)));
         int64_t slot = -1;
         if (from > 0) {
           slot = 2 * w;
@@ -665,6 +940,7 @@ __global__ __launch_bounds__(T::THREADS) void attn_kernel(const AttnArgs g) {
           slot = 2 * w + 1;
         }
         AttnBody<T>::run(g, s, b, h, m, t0 + from, t0 + to, lo, hi, slot, lds);
+        if (g.whole) return;
         x += to - from;
         inner += to - from;
         fresh = false;
@@ -672,7 +948,7 @@ __global__ __launch_bounds__(T::THREADS) void attn_kernel(const AttnArgs g) {
       done += nt;
     }
     if (x >= end) break;
-    if (!g.whole) x += s.cost - inner;   // what the unit costs less than its request's units at most
+    x += s.cost - inner;   // what the unit costs less than its request's units at most
     inner = 0;
     if (++u == s.units) {
       u = 0;
@@ -696,9 +972,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs g) {
   const int32_t* rec = g.record + w * kRecord;
   const int last = rec[4];
   if (last < 0) return;
-  AttnSeq s{};
-  s.first = rec[0];
-  s.n = rec[1];
+  const int first = rec[0], rows = rec[1] * p.group;
   const int h = rec[2], m = rec[3];
   float v_scale = 1.f;
   if constexpr (sizeof(typename T::C) == 1) v_scale = p.v_scale[h];
@@ -707,7 +981,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs g) {
   for (int rl = blockIdx.y * PER + static_cast<int>(threadIdx.x) / (T::D / 4); rl < T::BM;
        rl += PER * static_cast<int>(gridDim.y)) {
     const int r = m * T::BM + rl;
-    if (r >= s.n * p.group) break;
+    if (r >= rows) break;
     float mm = -INFINITY;
     for (int64_t i = w - 1; i <= last; ++i)
       mm = fmaxf(mm, g.part_ml[(i == w - 1 ? 2 * i + 1 : 2 * i) * T::BM + rl].x);
@@ -721,7 +995,7 @@ __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs g) {
       l += f * ml.y;
       o += f * *reinterpret_cast<const f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + 4 * c);
     }
-    AttnBody<T>::put(g, s, h, r, 4 * c, o, mm, l, v_scale);
+    AttnLoader<T>::put(g, first, h, r, 4 * c, o, mm, l, v_scale);
   }
 }
 

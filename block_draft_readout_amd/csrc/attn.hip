@@ -12,7 +12,7 @@ namespace {
 constexpr int64_t kCus = 256;   // compute units of an MI355X
 
 struct Choice {
-  int which;          // 0 few, 1 some, 2 many rows
+  int few;            // 16-row tiles of a few-row variant, 0: many rows
   int bm;             // rows of a row tile
   int64_t slabs, min_share;
   int whole;
@@ -22,11 +22,9 @@ Choice choose(const AttnProblem& p) {
   Choice c{};
   // rows of a request and kv head on average
   const int64_t rows = (p.rows * p.group + p.batch - 1) / p.batch;
-  const bool wide = p.dim == 256;
-  c.which = rows <= 32 ? 0 : rows <= 64 ? 1 : 2;
-  if (p.dt == BDR_F32 && (wide || c.which == 1)) c.which = 2;
-  if (wide && c.which == 1) c.which = 2;
-  c.bm = c.which == 0 ? 32 : c.which == 1 ? 64 : 128;
+  const int most = p.dt == BDR_F32 ? (p.dim == 256 ? 0 : 2) : p.dim == 256 ? 2 : 4;
+  c.few = rows <= 16 * most ? static_cast<int>((rows + 15) / 16) : 0;
+  c.bm = c.few ? 16 * c.few : 128;
   // row tiles at most
   const int64_t tiles = ((p.rows * p.group + c.bm - 1) / c.bm + p.batch) * p.hkv;
   const int64_t longest = static_cast<int64_t>(p.width) * p.page;
@@ -63,8 +61,8 @@ hipError_t launch_attn(const AttnProblem& p, void* workspace, hipStream_t stream
     at += align256(slots * sizeof(float2));
     g.record = reinterpret_cast<int32_t*>(at);
   }
-  if (p.dt == BDR_F32) return launch_attn_f32(g, c.which, stream);
-  return p.fp8 ? launch_attn_fp8(g, c.which, stream) : launch_attn_bf16(g, c.which, stream);
+  if (p.dt == BDR_F32) return launch_attn_f32(g, c.few, stream);
+  return p.fp8 ? launch_attn_fp8(g, c.few, stream) : launch_attn_bf16(g, c.few, stream);
 }
 
 }  // namespace bdr

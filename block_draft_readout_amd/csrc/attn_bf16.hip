@@ -3,19 +3,11 @@
 
 namespace bdr {
 
-template <int D, int KT>
-static hipError_t run(const AttnArgs& g, int which, hipStream_t stream) {
-  if (which == 0) return run_attn<AttnTile<uint16_t, uint16_t, D, 1, 4, 1, 32>>(g, stream);
-  if constexpr (D <= 128)
-    if (which == 1) return run_attn<AttnTile<uint16_t, uint16_t, D, 1, 4, 2, 32>>(g, stream);
-  return run_attn<AttnTile<uint16_t, uint16_t, D, 4, 1, 1, KT>>(g, stream);
-}
-
-hipError_t launch_attn_bf16(const AttnArgs& g, int which, hipStream_t stream) {
+hipError_t launch_attn_bf16(const AttnArgs& g, int few, hipStream_t stream) {
   switch (g.p.dim) {
-    case 64: return run<64, 64>(g, which, stream);
-    case 128: return run<128, 64>(g, which, stream);
-    default: return run<256, 32>(g, which, stream);
+    case 64: return run_attn_dim<uint16_t, uint16_t, 64, 64, 4>(g, few, stream);
+    case 128: return run_attn_dim<uint16_t, uint16_t, 128, 64, 4>(g, few, stream);
+    default: return run_attn_dim<uint16_t, uint16_t, 256, 32, 2>(g, few, stream);
   }
 }
 

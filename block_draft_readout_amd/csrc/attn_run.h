@@ -5,10 +5,10 @@
 
 namespace bdr {
 
-// which: 0 few rows, 1 some rows, 2 many rows
-hipError_t launch_attn_bf16(const AttnArgs& g, int which, hipStream_t stream);
-hipError_t launch_attn_fp8(const AttnArgs& g, int which, hipStream_t stream);
-hipError_t launch_attn_f32(const AttnArgs& g, int which, hipStream_t stream);
+// few: 16-row tiles of a few-row variant, 0: the many-row variant
+hipError_t launch_attn_bf16(const AttnArgs& g, int few, hipStream_t stream);
+hipError_t launch_attn_fp8(const AttnArgs& g, int few, hipStream_t stream);
+hipError_t launch_attn_f32(const AttnArgs& g, int few, hipStream_t stream);
 
 template <typename T>
 hipError_t run_attn(const AttnArgs& g, hipStream_t stream) {
@@ -17,10 +17,23 @@ hipError_t run_attn(const AttnArgs& g, hipStream_t stream) {
   if (!g.whole && g.slabs > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_join_kernel<T>), dim3(static_cast<uint32_t>(g.slabs - 1), 4), dim3(256), 0,
+    hipLaunchKernelGGL((attn_join_kernel<T>), dim3(static_cast<uint32_t>(g.slabs - 1), (T::BM + 15) / 16), dim3(256), 0,
                        stream, g);
   }
   return hipGetLastError();
+}
+
+// the built variants of a head size
+template <typename C, typename S, int D, int KT, int FEW>
+hipError_t run_attn_dim(const AttnArgs& g, int few, hipStream_t stream) {
+  switch (few) {
+    case 1: return run_attn<AttnFew<C, S, D, 1>>(g, stream);
+    case 2: return run_attn<AttnFew<C, S, D, 2>>(g, stream);
+    case 3: if constexpr (FEW >= 3) return run_attn<AttnFew<C, S, D, 3>>(g, stream); break;
+    case 4: if constexpr (FEW >= 4) return run_attn<AttnFew<C, S, D, 4>>(g, stream); break;
+    default: return run_attn<AttnMany<C, S, D, 4, KT>>(g, stream);
+  }
+  return hipErrorInvalidValue;
 }
 
 }  // namespace bdr
