@@ -9,11 +9,12 @@
 // n tokens and the `group` heads of a kv head are packed into n * group rows, BM
 // of which make a row tile.  A row tile walks its visible keys in tiles of KT.
 // Lengths live on the device and differ widely, so the launch has a fixed number
-// of workgroups and each takes an equal, contiguous share of all key tiles of all
-// (request, kv head, row tile): it finds its place from the lengths by a prefix
-// sum.  A row tile that ends up with several workgroups gets partial (O, m, l) in
-// the workspace, which a second launch joins in order: nothing depends on the
-// order of arrival.
+// of workgroups per kv head and each takes an equal, contiguous share of the key
+// tiles of all (request, row tile): it finds its place from the lengths by a
+// prefix sum.  The workgroups of a share are side by side, one per kv head, and
+// read the heads of the same positions at the same time.  A row tile that ends
+// up with several workgroups gets partial (O, m, l) in the workspace, which a
+// second launch joins in order: nothing depends on the order of arrival.
 //
 // Products.  S is computed transposed (keys are the rows of the MFMA's result), so
 // a lane holds one query's column: its maximum, sum and rescaling are the lane's
@@ -33,16 +34,16 @@ typedef short i16x4_t __attribute__((ext_vector_type(4)));
 
 struct AttnArgs {
   AttnProblem p;
-  int64_t slabs;        // workgroups of the schedule
+  int64_t shares;       // of a kv head's work: a workgroup for each and kv head
   int64_t min_share;    // key tiles that a workgroup takes at least
   int whole;            // each row tile is one workgroup's
   float scale2;         // scale * log2(e)
-  float* part_o;        // [2 * slabs][BM][D]
-  float2* part_ml;      // [2 * slabs][BM] (m in units of log2, l)
-  int32_t* record;      // [slabs][kRecord] what the join needs
+  float* part_o;        // [shares][hkv][2][BM][D]
+  float2* part_ml;      // [shares][hkv][2][BM] (m in units of log2, l)
+  int32_t* record;      // [shares][hkv][kRecord] what the join needs
 };
 
-constexpr int kRecord = 8;   // first row, tokens, kv head, row tile, last workgroup (-1: nothing to join)
+constexpr int kRecord = 4;   // first row, tokens, row tile, last share (-1: nothing to join)
 
 // -------------------------------------------------------------- schedule
 // A request: its rows, row tiles and what they cost in key tiles.  A unit is a row
@@ -51,7 +52,7 @@ constexpr int kRecord = 8;   // first row, tokens, kv head, row tile, last workg
 struct AttnSeq {
   int32_t first, n, len;
   int32_t tiles;    // row tiles
-  int32_t units;    // per kv head
+  int32_t units;
   int32_t cost;     // key tiles of a unit
   bool paired;
 };
@@ -113,8 +114,8 @@ struct AttnPlan {
     return s;
   }
   // cost of the whole request
-  static __device__ __forceinline__ int64_t total(const AttnProblem& p, const AttnSeq& s) {
-    return static_cast<int64_t>(p.hkv) * s.units * s.cost;
+  static __device__ __forceinline__ int64_t total(const AttnSeq& s) {
+    return static_cast<int64_t>(s.units) * s.cost;
   }
 };
 
@@ -551,10 +552,11 @@ struct AttnManyBody : AttnLoader<T> {
 // -------------------------------------------------------------- few rows
 static __device__ const uint32_t kZeros16[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
 
-// 16 bytes per lane, cache -> LDS: lane l's land at dst + 16 l (dst uniform)
+// 16 bytes per lane, cache -> LDS: lane l's land at dst + 16 l (dst uniform).  Non-temporal: few
+// rows read the cache once (16 x 8 rows over 16384 positions: 223 -> 204 us).
 __device__ __forceinline__ void copy_lds16(const char* src, char* dst) {
   __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)src,
-                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 0);
+                                   (__attribute__((address_space(3))) void*)dst, 16, 0, 2);
 }
 
 template <typename T>
@@ -850,38 +852,35 @@ struct AttnFewBody : AttnLoader<T> {
 template <typename T>
 using AttnBody = std::conditional_t<T::kFew, AttnFewBody<T>, AttnManyBody<T>>;
 
-// The workgroup's share of all key tiles, row tile by row tile.
+// The workgroup's share of one kv head's key tiles, row tile by row tile.
 template <typename T>
 __global__ __launch_bounds__(T::THREADS, T::SIMD_WAVES) void attn_kernel(const AttnArgs g) {
   using Plan = AttnPlan<T::BM, T::KT>;
   __shared__ __attribute__((aligned(16))) char lds[T::LDS_BYTES];
   const AttnProblem& p = g.p;
   const int lane = static_cast<int>(threadIdx.x) & 63;
-  // neighbouring shares, which read the same keys, on one XCD
-  const int64_t per_xcd = (g.slabs + 7) / 8;
-  const int64_t w = static_cast<int64_t>(blockIdx.x % 8) * per_xcd + blockIdx.x / 8;
-  if (w >= g.slabs) return;   // whole workgroup
+  const int h = static_cast<int>(blockIdx.x) % p.hkv;
+  const int64_t w = static_cast<int>(blockIdx.x) / p.hkv;
   // every wave sums and searches for itself: no barriers
   int64_t all = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 64) {
     const int b = b0 + lane;
-    all += b < p.batch ? Plan::total(p, Plan::seq(p, g.whole, b)) : 0;
+    all += b < p.batch ? Plan::total(Plan::seq(p, g.whole, b)) : 0;
   }
   all = uniform_i64(wave_sum_i64(all));
-  const int64_t share = g.whole ? 1 : max(g.min_share, (all + g.slabs - 1) / g.slabs);
+  const int64_t share = g.whole ? 1 : max(g.min_share, (all + g.shares - 1) / g.shares);
   int64_t x = w * share;
   const int64_t end = min(x + share, all);
-  if (x >= end) {
-    if (threadIdx.x == 0 && !g.whole) g.record[w * kRecord + 4] = -1;
-    return;
-  }
+  int32_t* const rec = g.record + blockIdx.x * kRecord;
+  if (threadIdx.x == 0 && !g.whole) rec[3] = -1;
+  if (x >= end) return;
   // the request that holds x
   int b = 0;
   int64_t base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 64) {
     const int bl = b0 + lane;
-    int64_t c = bl < p.batch ? Plan::total(p, Plan::seq(p, g.whole, bl)) : 0;
-    const int64_t own = c;
+    const int64_t own = bl < p.batch ? Plan::total(Plan::seq(p, g.whole, bl)) : 0;
+    int64_t c = own;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
       const int64_t u = __shfl_up(c, d);
@@ -898,52 +897,38 @@ __global__ __launch_bounds__(T::THREADS, T::SIMD_WAVES) void attn_kernel(const A
   }
   b = __builtin_amdgcn_readfirstlane(b);
   AttnSeq s = Plan::seq(p, g.whole, b);
-  int64_t in_req = x - base;
-  int64_t unit = in_req / s.cost;
-  int inner = static_cast<int>(in_req - unit * s.cost);
-  int h = static_cast<int>(unit / s.units);
-  int u = static_cast<int>(unit - static_cast<int64_t>(h) * s.units);
-  bool fresh = true;   // nothing done yet: a partial here is continued from the workgroup before
-  if (threadIdx.x == 0 && !g.whole) g.record[w * kRecord + 4] = -1;
+  int u = static_cast<int>((x - base) / s.cost);
+  int inner = static_cast<int>(x - base - static_cast<int64_t>(u) * s.cost);
   while (x < end) {
     // the unit's row tiles: the longer, then (paired) the shorter
     int done = 0;
     for (int part = 0; part < 2 && x < end; ++part) {
-      int m;
-      if (s.paired) {
-        m = part == 0 ? s.tiles - 1 - u : u;
-        if (part == 1 && m == s.tiles - 1 - u) break;
-      } else {
-        if (part == 1) break;
-        m = u;
-      }
+      const int m = s.paired && part == 0 ? s.tiles - 1 - u : u;
+      if (part == 1 && (!s.paired || u == s.tiles - 1 - u)) break;
       int lo, hi, t0, t1;
       Plan::range(p, s, m, lo, hi, t0, t1);
       const int nt = t1 - t0;
       if (inner < done + nt) {
         const int from = g.whole ? 0 : inner - done;
         const int to = g.whole ? nt : static_cast<int>(min(static_cast<int64_t>(nt), from + (end - x)));
-        int64_t slot = -1;
+        int64_t slot = -1;   // of a partial: what the workgroup before began, or what the next goes on with
         if (from > 0) {
-          slot = 2 * w;
-          if (threadIdx.x == 0 && fresh) {
-            // x - from is where the row tile begins; the first border inside it does the join
+          slot = 2 * blockIdx.x;
+          if (threadIdx.x == 0) {
+            // x0 is where the row tile begins; the first border inside it does the join
             const int64_t x0 = x - from;
-            int32_t* rec = g.record + w * kRecord;
             rec[0] = s.first;
             rec[1] = s.n;
-            rec[2] = h;
-            rec[3] = m;
-            rec[4] = x0 / share == w - 1 ? static_cast<int32_t>((x0 + nt - 1) / share) : -1;
+            rec[2] = m;
+            rec[3] = x0 / share == w - 1 ? static_cast<int32_t>((x0 + nt - 1) / share) : -1;
           }
         } else if (to < nt) {
-          slot = 2 * w + 1;
+          slot = 2 * blockIdx.x + 1;
         }
         AttnBody<T>::run(g, s, b, h, m, t0 + from, t0 + to, lo, hi, slot, lds);
         if (g.whole) return;
         x += to - from;
         inner += to - from;
-        fresh = false;
       }
       done += nt;
     }
@@ -952,48 +937,62 @@ __global__ __launch_bounds__(T::THREADS, T::SIMD_WAVES) void attn_kernel(const A
     inner = 0;
     if (++u == s.units) {
       u = 0;
-      if (++h == p.hkv) {
-        h = 0;
-        do {
-          if (++b >= p.batch) return;
-          s = Plan::seq(p, g.whole, b);
-        } while (s.units == 0);
-      }
+      do {
+        if (++b >= p.batch) return;
+        s = Plan::seq(p, g.whole, b);
+      } while (s.units == 0);
     }
   }
 }
 
-// Joins the partials of the row tiles that several workgroups share: blockIdx.x + 1 is
+// Joins the partials of the row tiles that several workgroups share: blockIdx.x + hkv is
 // the workgroup whose share begins inside one, blockIdx.y the rows.
 template <typename T>
 __global__ __launch_bounds__(256) void attn_join_kernel(const AttnArgs g) {
   const AttnProblem& p = g.p;
-  const int64_t w = blockIdx.x + 1;
-  const int32_t* rec = g.record + w * kRecord;
-  const int last = rec[4];
+  const int h = static_cast<int>(blockIdx.x) % p.hkv;
+  const int w = static_cast<int>(blockIdx.x) / p.hkv + 1;
+  const int32_t* rec = g.record + static_cast<int64_t>(blockIdx.x + p.hkv) * kRecord;
+  const int last = rec[3];
   if (last < 0) return;
-  const int first = rec[0], rows = rec[1] * p.group;
-  const int h = rec[2], m = rec[3];
+  const int first = rec[0], rows = rec[1] * p.group, m = rec[2];
   float v_scale = 1.f;
   if constexpr (sizeof(typename T::C) == 1) v_scale = p.v_scale[h];
-  constexpr int PER = 256 / (T::D / 4);   // rows at a time
+  constexpr int PER = 256 / (T::D / 4);   // rows of a workgroup
+  constexpr int AHEAD = 8;                // partials asked for together: their latency bounds this
   const int c = static_cast<int>(threadIdx.x) % (T::D / 4);
-  for (int rl = blockIdx.y * PER + static_cast<int>(threadIdx.x) / (T::D / 4); rl < T::BM;
-       rl += PER * static_cast<int>(gridDim.y)) {
+  for (int rl = blockIdx.y * PER + static_cast<int>(threadIdx.x) / (T::D / 4);
+       rl < T::BM && m * T::BM + rl < rows; rl += PER * static_cast<int>(gridDim.y)) {
     const int r = m * T::BM + rl;
-    if (r >= rows) break;
-    float mm = -INFINITY;
-    for (int64_t i = w - 1; i <= last; ++i)
-      mm = fmaxf(mm, g.part_ml[(i == w - 1 ? 2 * i + 1 : 2 * i) * T::BM + rl].x);
-    const float ref = mm == -INFINITY ? 0.f : mm;
-    float l = 0.f;
+    float mm = -INFINITY, l = 0.f;
     f32x4_t o = {0.f, 0.f, 0.f, 0.f};
-    for (int64_t i = w - 1; i <= last; ++i) {
-      const int64_t slot = i == w - 1 ? 2 * i + 1 : 2 * i;
-      const float2 ml = g.part_ml[slot * T::BM + rl];
-      const float f = __builtin_amdgcn_exp2f(ml.x - ref);
-      l += f * ml.y;
-      o += f * *reinterpret_cast<const f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + 4 * c);
+    for (int i0 = w - 1; i0 <= last; i0 += AHEAD) {
+      float2 ml[AHEAD];
+      f32x4_t part[AHEAD];
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const int at = min(i0 + i, last);
+        const int64_t slot = (2 * (static_cast<int64_t>(at) * p.hkv + h) + (at == w - 1 ? 1 : 0)) * T::BM + rl;
+        ml[i] = g.part_ml[slot];
+        part[i] = *reinterpret_cast<const f32x4_t*>(g.part_o + slot * T::D + 4 * c);
+      }
+      float top = mm;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        if (i0 + i > last) ml[i] = float2{-INFINITY, 0.f};
+        top = fmaxf(top, ml[i].x);
+      }
+      const float ref = top == -INFINITY ? 0.f : top;
+      const float f0 = __builtin_amdgcn_exp2f(mm - ref);
+      l *= f0;
+      o *= f0;
+#pragma unroll
+      for (int i = 0; i < AHEAD; ++i) {
+        const float f = __builtin_amdgcn_exp2f(ml[i].x - ref);
+        l += f * ml[i].y;
+        if (i0 + i <= last) o += f * part[i];
+      }
+      mm = top;
     }
     AttnLoader<T>::put(g, first, h, r, 4 * c, o, mm, l, v_scale);
   }

@@ -14,7 +14,7 @@ constexpr int64_t kCus = 256;   // compute units of an MI355X
 struct Choice {
   int few;            // 16-row tiles of a few-row variant, 0: many rows
   int bm;             // rows of a row tile
-  int64_t slabs, min_share;
+  int64_t shares, min_share;
   int whole;
 };
 
@@ -25,11 +25,11 @@ Choice choose(const AttnProblem& p) {
   const int most = p.dt == BDR_F32 ? (p.dim == 256 ? 0 : 2) : p.dim == 256 ? 2 : 4;
   c.few = rows <= 16 * most ? static_cast<int>((rows + 15) / 16) : 0;
   c.bm = c.few ? 16 * c.few : 128;
-  // row tiles at most
-  const int64_t tiles = ((p.rows * p.group + c.bm - 1) / c.bm + p.batch) * p.hkv;
   const int64_t longest = static_cast<int64_t>(p.width) * p.page;
   c.whole = longest <= 256;
-  c.slabs = c.whole ? tiles : 2 * kCus;
+  // row tiles at most, or two workgroups a compute unit
+  c.shares = c.whole ? (p.rows * p.group + c.bm - 1) / c.bm + p.batch
+                     : std::max<int64_t>(1, 2 * kCus / p.hkv);
   c.min_share = 8;
   return c;
 }
@@ -39,21 +39,21 @@ Choice choose(const AttnProblem& p) {
 size_t attn_workspace(const AttnProblem& p) {
   const Choice c = choose(p);
   if (c.whole) return 0;
-  const size_t slots = 2 * static_cast<size_t>(c.slabs) * c.bm;
+  const size_t slots = 2 * static_cast<size_t>(c.shares) * p.hkv * c.bm;
   return align256(slots * p.dim * sizeof(float)) + align256(slots * sizeof(float2)) +
-         align256(static_cast<size_t>(c.slabs) * kRecord * sizeof(int32_t));
+         align256(static_cast<size_t>(c.shares) * p.hkv * kRecord * sizeof(int32_t));
 }
 
 hipError_t launch_attn(const AttnProblem& p, void* workspace, hipStream_t stream) {
   const Choice c = choose(p);
   AttnArgs g{};
   g.p = p;
-  g.slabs = c.slabs;
+  g.shares = c.shares;
   g.min_share = c.min_share;
   g.whole = c.whole;
   g.scale2 = p.scale * kLog2e;
   if (!c.whole) {
-    const size_t slots = 2 * static_cast<size_t>(c.slabs) * c.bm;
+    const size_t slots = 2 * static_cast<size_t>(c.shares) * p.hkv * c.bm;
     char* at = static_cast<char*>(workspace);
     g.part_o = reinterpret_cast<float*>(at);
     at += align256(slots * p.dim * sizeof(float));

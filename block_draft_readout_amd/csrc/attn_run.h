@@ -12,13 +12,14 @@ hipError_t launch_attn_f32(const AttnArgs& g, int few, hipStream_t stream);
 
 template <typename T>
 hipError_t run_attn(const AttnArgs& g, hipStream_t stream) {
-  const int64_t grid = (g.slabs + 7) / 8 * 8;
-  hipLaunchKernelGGL((attn_kernel<T>), dim3(static_cast<uint32_t>(grid)), dim3(T::THREADS), 0, stream, g);
-  if (!g.whole && g.slabs > 1) {
+  const uint32_t grid = static_cast<uint32_t>(g.shares * g.p.hkv);
+  hipLaunchKernelGGL((attn_kernel<T>), dim3(grid), dim3(T::THREADS), 0, stream, g);
+  if (!g.whole && g.shares > 1) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    hipLaunchKernelGGL((attn_join_kernel<T>), dim3(static_cast<uint32_t>(g.slabs - 1), (T::BM + 15) / 16), dim3(256), 0,
-                       stream, g);
+    // row blocks: most workgroups find nothing to join, so no more than tall tiles need
+    constexpr int blocks = std::min(8, T::BM * (T::D / 4) / 256);
+    hipLaunchKernelGGL((attn_join_kernel<T>), dim3(grid - g.p.hkv, blocks), dim3(256), 0, stream, g);
   }
   return hipGetLastError();
 }
