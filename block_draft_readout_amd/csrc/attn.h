@@ -132,28 +132,28 @@ __device__ __forceinline__ int64_t uniform_i64(int64_t v) {
 }
 
 // -------------------------------------------------------------- kernel
-// Many rows: WM waves hold 32 rows each and share the tiles of keys in LDS.
-template <typename C_, typename S_, int D_, int WM_, int KT_>
+// Many rows: WM waves hold RT x 32 rows each and share the tiles of keys in LDS.
+template <typename C_, typename S_, int D_, int WM_, int RT_, int KT_>
 struct AttnMany {
   using C = C_;                       // cache element: uint16_t (bf16), uint8_t (e4m3) or float
   using S = S_;                       // queries, output and LDS: uint16_t or float
   static constexpr bool kFew = false;
-  static constexpr int D = D_, WM = WM_;
+  static constexpr int D = D_, WM = WM_, RT = RT_;
   static constexpr int KT = KT_;      // keys of a tile
   static constexpr int THREADS = 64 * WM;
-  static constexpr int BM = 32 * WM;
-  static constexpr int ES = static_cast<int>(sizeof(S));
+  static constexpr int BM = 32 * WM * RT;
+  static constexpr int CS = static_cast<int>(sizeof(C)), ES = static_cast<int>(sizeof(S));
   static constexpr int ROWB = D * ES;                    // bytes of an LDS row
-  static constexpr int PER16 = 16 / static_cast<int>(sizeof(C));   // cache elements of 16 bytes
+  static constexpr int PER16 = 16 / CS;                  // cache elements of 16 bytes
   static constexpr int CPR = D / PER16;                  // 16-byte pieces of a cache row
-  static constexpr int SHARE = THREADS;                  // threads that load a tile
-  static constexpr int LOADS = KT * CPR / SHARE;         // 16-byte loads of a thread, K or V
+  static constexpr int LOADS = KT * CPR / THREADS;       // 16-byte loads of a thread, K or V
+  static constexpr int RPL = CPR > 64 ? 1 : 64 / CPR;    // rows of a wave's load
   static constexpr int TILE_BYTES = KT * ROWB;           // K or V of a tile
   static constexpr int LDS_BYTES = 4 * TILE_BYTES;       // two buffers
-  static constexpr int QN = ROWB / 32;                   // 16-byte query pieces of a lane
-  static constexpr int SIMD_WAVES = LDS_BYTES <= 79 * 1024 && D <= 128 ? 2 : 1;
+  static constexpr int QN = ROWB / 32;                   // 16-byte query pieces of a lane and row
+  static constexpr int SIMD_WAVES = RT == 1 && LDS_BYTES <= 80 * 1024 && D * ES <= 256 ? 2 : 1;
   static_assert(KT % 32 == 0 && KT <= 64, "a lane looks up one key's page");
-  static_assert(LOADS * SHARE == KT * CPR, "loads split evenly");
+  static_assert(LOADS * THREADS == KT * CPR, "loads split evenly");
   static_assert(LDS_BYTES <= 160 * 1024, "tile fits");
 };
 
@@ -298,6 +298,7 @@ template <int N, typename KeyOf, typename Fold>
 __device__ __forceinline__ float softmax_step(float (&s)[N], bool edge, int lo, int hi, float scale2, KeyOf key_of,
                                               Fold fold, float& m, float& l) {
   if (edge) {
+    asm volatile("");   // (a branch: few tiles lie on an edge)
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int key = key_of(i);
@@ -344,110 +345,151 @@ __device__ __forceinline__ bf16x8_t join_tr(i16x4_t x, i16x4_t y) {
 }
 
 // -------------------------------------------------------------- many rows
-// A staged tile: what a thread holds of the next keys and values.
-template <typename T>
-struct AttnStage {
-  u32x4_t k[T::LOADS], v[T::LOADS];
-  uint64_t live;                  // bit t: key t of the tile is read (others are zeros)
-};
-
+// Tiles go cache -> registers -> LDS, in two buffers, with one barrier a tile; the two waves of a
+// SIMD run the matrix unit and the vector unit (exponentials) in turn.
 template <typename T>
 struct AttnManyBody : AttnLoader<T> {
   using L = AttnLoader<T>;
   using S = typename T::S;
   using C = typename T::C;
 
-  static __device__ __forceinline__ void load(const AttnProblem& p, const C* kb, const C* vb, AttnPage a, int st,
-                                              AttnStage<T>& g) {
+  // What a thread holds of a tile of keys and values.
+  struct Stage {
+    u32x4_t k[T::LOADS], v[T::LOADS];
+    uint64_t live;                  // bit t: row t of the tile is read (others are zeros)
+  };
+  static constexpr uint64_t kAll = T::KT == 64 ? ~0ull : 0xFFFFFFFFull;
+
+  // Every lane looks a key up; a load's rows take their offsets from the lanes that did.  Where
+  // they lie in one page, one offset is the load's own scalar.
+  static __device__ __forceinline__ void load(const AttnProblem& p, const char* kb, const char* vb, AttnPage a,
+                                              int tid, Stage& g) {
     const bool in = a.id >= 0 && a.id < p.pages;
-    g.live = __ballot(in);
-    // a key that is not read takes the first page's first row, and is cleared below
-    const int64_t off = in ? a.id * p.page_stride + a.place * p.token_stride : 0;
+    g.live = __ballot(in) & kAll;
+    // a row that is not read takes the first page's first row, and is cleared on its way to LDS
+    const int64_t off = in ? (a.id * p.page_stride + a.place * p.token_stride) * T::CS : 0;
     const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
+    asm volatile("" : "+v"(tid));   // (offsets are made anew rather than held over the loop)
+    const uint32_t c = static_cast<uint32_t>(tid % T::CPR) * 16;
+    if (g.live == kAll && p.page % T::RPL == 0 && p.token_stride < (1 << 30) / 64) {
+      const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+      const uint32_t mine = (tid & 63) / T::CPR * static_cast<uint32_t>(p.token_stride) * T::CS + c;
 #pragma unroll
-    for (int i = 0; i < T::LOADS; ++i) {
-      const int idx = st + T::SHARE * i;
-      const int row = idx / T::CPR, c = idx % T::CPR;
-      const uint32_t l = __shfl(lo, row), h = __shfl(hi, row);
-      const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l) + c * T::PER16;
-      g.k[i] = load16(kb + at);
-      g.v[i] = load16(vb + at);
-    }
-  }
-
-  static __device__ __forceinline__ void store(char* lk, char* lv, int st, AttnStage<T>& g) {
-    constexpr uint64_t kAll = T::KT == 64 ? ~0ull : 0xFFFFFFFFull;
-    const bool clear = (g.live & kAll) != kAll;
-#pragma unroll
-    for (int i = 0; i < T::LOADS; ++i) {
-      const int idx = st + T::SHARE * i;
-      const int row = idx / T::CPR, c = idx % T::CPR;
-      u32x4_t k = g.k[i], v = g.v[i];
-      if (clear && !((g.live >> row) & 1)) k = v = u32x4_t{0, 0, 0, 0};
-      if constexpr (sizeof(C) == 1) {
-        u32x4_t a, b;
-        widen16(k, a, b);
-        *reinterpret_cast<u32x4_t*>(lk + key_place<T::ROWB>(row, 2 * c)) = a;
-        *reinterpret_cast<u32x4_t*>(lk + key_place<T::ROWB>(row, 2 * c + 1)) = b;
-        widen16(v, a, b);
-        *reinterpret_cast<u32x4_t*>(lv + value_place<T>(row, 2 * c)) = a;
-        *reinterpret_cast<u32x4_t*>(lv + value_place<T>(row, 2 * c + 1)) = b;
-      } else {
-        *reinterpret_cast<u32x4_t*>(lk + key_place<T::ROWB>(row, c)) = k;
-        *reinterpret_cast<u32x4_t*>(lv + value_place<T>(row, c)) = v;
-      }
-    }
-  }
-
-  // S^T of 32 keys against the wave's 32 queries: keys 8 (r / 4) + 4 (lane / 32) + r % 4 of query lane % 32
-  static __device__ __forceinline__ f32x16_t scores(const char* lk, int sub, int lane,
-                                                    const u32x4_t (&q)[T::QN]) {
-    f32x16_t c = {};
-    const uint32_t row = 32 * sub + (lane & 31);
-#pragma unroll
-    for (int i = 0; i < T::QN; ++i) {
-      const u32x4_t a = load16(lk + key_place<T::ROWB>(row, 2 * i + (lane >> 5)));
-      if constexpr (T::ES == 2) {
-        c = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8_t, a),
-                                                    __builtin_bit_cast(bf16x8_t, q[i]), c, 0, 0, 0);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(a[e]), __uint_as_float(q[i][e]), c, 0, 0, 0);
-      }
-    }
-    return c;
-  }
-
-  // O^T += V^T P^T of 32 keys, whose probabilities a lane holds as the scores' registers lie
-  static __device__ __forceinline__ void add_values(const char* lv, int sub, int lane, const float* p,
-                                                    f32x16_t (&o)[T::D / 32]) {
-    const int half = lane >> 5;
-    if constexpr (T::ES == 2) {
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        u32x4_t b;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) b[e] = pack_bf16(p[8 * ks + 2 * e], p[8 * ks + 2 * e + 1]);
-        const uint32_t row = 32 * sub + 16 * ks + 4 * half + ((lane & 15) >> 2);
-#pragma unroll
-        for (int i = 0; i < T::D / 32; ++i) {
-          const uint32_t c = 4 * i + ((lane >> 3) & 2) + ((lane >> 1) & 1);
-          const bf16x8_t a = join_tr(read_tr(lv + value_place<T>(row, c) + (lane & 1) * 8),
-                                     read_tr(lv + value_place<T>(row + 8, c) + (lane & 1) * 8));
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, __builtin_bit_cast(bf16x8_t, b), o[i], 0, 0, 0);
-        }
+      for (int i = 0; i < T::LOADS; ++i) {
+        const int row = (64 * wave + T::THREADS * i) / T::CPR;
+        const uint32_t l = __builtin_amdgcn_readlane(lo, row), h = __builtin_amdgcn_readlane(hi, row);
+        const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l);
+        g.k[i] = load16(kb + at + mine);
+        g.v[i] = load16(vb + at + mine);
       }
     } else {
 #pragma unroll
-      for (int r = 0; r < 16; ++r) {
-        const uint32_t row = 32 * sub + 8 * (r / 4) + 4 * half + r % 4;
+      for (int i = 0; i < T::LOADS; ++i) {
+        const int row = (tid + T::THREADS * i) / T::CPR;
+        const uint32_t l = __shfl(lo, row), h = __shfl(hi, row);
+        const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l) + c;
+        g.k[i] = load16(kb + at);
+        g.v[i] = load16(vb + at);
+      }
+    }
+  }
+
+  static __device__ __forceinline__ void store16(char* lds, uint32_t at, uint32_t at_next, u32x4_t v) {
+    if constexpr (T::CS == 1) {
+      u32x4_t x, y;
+      widen16(v, x, y);
+      *reinterpret_cast<u32x4_t*>(lds + at) = x;
+      *reinterpret_cast<u32x4_t*>(lds + at_next) = y;
+    } else {
+      *reinterpret_cast<u32x4_t*>(lds + at) = v;
+    }
+  }
+  static __device__ __forceinline__ void store(char* lk, char* lv, int tid, Stage& g) {
+    if (g.live != kAll) {
+      asm volatile("");   // (a branch: rare)
 #pragma unroll
-        for (int i = 0; i < T::D / 32; ++i) {
-          const uint32_t d = 32 * i + (lane & 31);
-          const float a = *reinterpret_cast<const float*>(lv + value_place<T>(row, d / 4) + (d & 3) * 4);
-          o[i] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[r], o[i], 0, 0, 0);
+      for (int i = 0; i < T::LOADS; ++i)
+        if (!((g.live >> ((tid + T::THREADS * i) / T::CPR)) & 1)) g.k[i] = g.v[i] = u32x4_t{0, 0, 0, 0};
+    }
+    constexpr int W = T::ES / T::CS;   // 16-byte chunks in LDS of a piece
+#pragma unroll
+    for (int i = 0; i < T::LOADS; ++i) {
+      const int idx = tid + T::THREADS * i;
+      const uint32_t row = idx / T::CPR, c = W * (idx % T::CPR);
+      store16(lk, key_place<T::ROWB>(row, c), key_place<T::ROWB>(row, c + W - 1), g.k[i]);
+      store16(lv, value_place<T>(row, c), value_place<T>(row, c + W - 1), g.v[i]);
+    }
+  }
+
+  // 16-byte operand pieces of 32 keys: piece i is chunk 2 i + lane / 32 of key lane % 32
+  static __device__ __forceinline__ void read_keys(const char* lk, int sub, int lane, u32x4_t (&k)[T::QN]) {
+    const uint32_t row = 32 * sub + (lane & 31);
+#pragma unroll
+    for (int i = 0; i < T::QN; ++i) k[i] = load16(lk + key_place<T::ROWB>(row, 2 * i + (lane >> 5)));
+  }
+
+  // S^T of 32 keys against the wave's queries: keys 8 (r / 4) + 4 (lane / 32) + r % 4 of query lane % 32
+  static __device__ __forceinline__ void scores(const u32x4_t (&k)[T::QN], const u32x4_t (&q)[T::RT][T::QN],
+                                                f32x16_t (&c)[T::RT]) {
+#pragma unroll
+    for (int rt = 0; rt < T::RT; ++rt) c[rt] = f32x16_t{};
+#pragma unroll
+    for (int i = 0; i < T::QN; ++i) {
+#pragma unroll
+      for (int rt = 0; rt < T::RT; ++rt) {
+        if constexpr (T::ES == 2) {
+          c[rt] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              __builtin_bit_cast(bf16x8_t, k[i]), __builtin_bit_cast(bf16x8_t, q[rt][i]), c[rt], 0, 0, 0);
+        } else {
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            c[rt] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(k[i][e]), __uint_as_float(q[rt][i][e]),
+                                                         c[rt], 0, 0, 0);
         }
+      }
+    }
+  }
+
+  // Operand pieces of 16 values (bf16): features 32 i + lane % 32 of the keys that a lane's
+  // probabilities are of
+  static __device__ __forceinline__ void read_values(const char* lv, int sub, int ks, int lane,
+                                                     bf16x8_t (&v)[T::D / 32]) {
+    const uint32_t row = 32 * sub + 16 * ks + 4 * (lane >> 5) + ((lane & 15) >> 2);
+#pragma unroll
+    for (int i = 0; i < T::D / 32; ++i) {
+      const uint32_t c = 4 * i + ((lane >> 3) & 2) + ((lane >> 1) & 1);
+      v[i] = join_tr(read_tr(lv + value_place<T>(row, c) + (lane & 1) * 8),
+                     read_tr(lv + value_place<T>(row + 8, c) + (lane & 1) * 8));
+    }
+  }
+
+  // O^T += V^T P^T of 16 keys: registers 8 ks .. 8 ks + 7 of the probabilities
+  static __device__ __forceinline__ void add_values(const bf16x8_t (&v)[T::D / 32], int ks,
+                                                    const f32x16_t (&p)[T::RT], f32x16_t (&o)[T::RT][T::D / 32]) {
+    u32x4_t b[T::RT];
+#pragma unroll
+    for (int rt = 0; rt < T::RT; ++rt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) b[rt][e] = pack_bf16(p[rt][8 * ks + 2 * e], p[rt][8 * ks + 2 * e + 1]);
+#pragma unroll
+    for (int i = 0; i < T::D / 32; ++i)
+#pragma unroll
+      for (int rt = 0; rt < T::RT; ++rt)
+        o[rt][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[i], __builtin_bit_cast(bf16x8_t, b[rt]), o[rt][i], 0, 0, 0);
+  }
+  // (fp32: straight from LDS)
+  static __device__ __forceinline__ void add_values_f32(const char* lv, int sub, int lane, const f32x16_t (&p)[T::RT],
+                                                        f32x16_t (&o)[T::RT][T::D / 32]) {
+#pragma unroll
+    for (int r = 0; r < 16; ++r) {
+      const uint32_t row = 32 * sub + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+#pragma unroll
+      for (int i = 0; i < T::D / 32; ++i) {
+        const uint32_t d = 32 * i + (lane & 31);
+        const float a = *reinterpret_cast<const float*>(lv + value_place<T>(row, d / 4) + (d & 3) * 4);
+#pragma unroll
+        for (int rt = 0; rt < T::RT; ++rt)
+          o[rt][i] = __builtin_amdgcn_mfma_f32_32x32x2f32(a, p[rt][r], o[rt][i], 0, 0, 0);
       }
     }
   }
@@ -459,7 +501,7 @@ struct AttnManyBody : AttnLoader<T> {
     const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
     const int lane = static_cast<int>(threadIdx.x) & 63;
     const int tid = static_cast<int>(threadIdx.x);
-    const int r0 = m * T::BM + wave * 32;
+    const int r0 = m * T::BM + wave * 32 * T::RT;
     const int rows = s.n * p.group;
     float scale2 = g.scale2, v_scale = 1.f;
     if constexpr (sizeof(C) == 1) {
@@ -470,80 +512,148 @@ struct AttnManyBody : AttnLoader<T> {
     scale2 = fmaxf(fabsf(scale2), 1e-30f);
 
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
-    const C* kb = static_cast<const C*>(p.k_cache) + h * p.head_stride;
-    const C* vb = static_cast<const C*>(p.v_cache) + h * p.head_stride;
-    AttnStage<T> stage;
+    const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_stride * T::CS;
+    const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_stride * T::CS;
+    char* now = lds;                             // keys and values of a tile
+    char* other = lds + 2 * T::TILE_BYTES;
+    Stage stage;
     AttnPage page = L::page_of(p, table, ta * T::KT, lo, hi, lane);
     load(p, kb, vb, page, tid, stage);
     page = L::page_of(p, table, (ta + 1) * T::KT, lo, hi, lane);
 
-    u32x4_t q[T::QN];
-    L::load_q(p, s, h, r0 + (lane & 31), [&](int i) { return (2 * i + (lane >> 5)) * (16 / T::ES); }, flip, q);
-    const int at = s.len - s.n + (r0 + (lane & 31)) / p.group;
-    const int row_hi = p.causal ? min(at + 1, s.len) : s.len;
-    const int row_lo = p.window ? at - p.window + 1 : 0;
-    f32x16_t o[T::D / 32];
-    float mx = -INFINITY, l = 0.f;
+    u32x4_t q[T::RT][T::QN];
+    int row_lo[T::RT], row_hi[T::RT];
+    f32x16_t o[T::RT][T::D / 32];
+    float mx[T::RT], l[T::RT];
 #pragma unroll
-    for (int i = 0; i < T::D / 32; ++i) o[i] = f32x16_t{};
+    for (int rt = 0; rt < T::RT; ++rt) {
+      const int r = r0 + 32 * rt + (lane & 31);
+      L::load_q(p, s, h, r, [&](int i) { return (2 * i + (lane >> 5)) * (16 / T::ES); }, flip, q[rt]);
+      const int at = s.len - s.n + r / p.group;
+      row_hi[rt] = p.causal ? min(at + 1, s.len) : s.len;
+      row_lo[rt] = p.window ? at - p.window + 1 : 0;
+      mx[rt] = -INFINITY;
+      l[rt] = 0.f;
+#pragma unroll
+      for (int i = 0; i < T::D / 32; ++i) o[rt][i] = f32x16_t{};
+    }
     // the wave's rows all see the keys [see_lo, see_hi)
     const int first = s.len - s.n + r0 / p.group;
-    const int last = s.len - s.n + min(r0 + 31, rows - 1) / p.group;
+    const int last = s.len - s.n + min(r0 + 32 * T::RT - 1, rows - 1) / p.group;
     const int see_hi = p.causal ? min(first + 1, s.len) : s.len;
     const int see_lo = p.window ? last - p.window + 1 : 0;
 
-    int buf = 0;
+    constexpr int SUB = T::KT / 32;
     for (int t = ta; t < tb; ++t) {
-      char* lk = lds + buf * 2 * T::TILE_BYTES;
-      char* lv = lk + T::TILE_BYTES;
-      store(lk, lv, tid, stage);
+      store(now, now + T::TILE_BYTES, tid, stage);
       if (t + 1 < tb) {
         load(p, kb, vb, page, tid, stage);
         page = L::page_of(p, table, (t + 2) * T::KT, lo, hi, lane);
       }
       // one barrier a tile: the buffer written next was last read before the barrier after that
       __syncthreads();
-      buf ^= 1;
+      const char* lk = now;
+      const char* lv = now + T::TILE_BYTES;
+      now = other;
+      other = const_cast<char*>(lk);
       if (r0 >= rows) continue;
       const int key0 = t * T::KT;
-      const bool edge = key0 < see_lo || key0 + T::KT > see_hi;
-      float pr[T::KT / 2];
+      f32x16_t sc[SUB][T::RT];
 #pragma unroll
-      for (int u = 0; u < T::KT / 32; ++u) {
-        const f32x16_t c = scores(lk, u, lane, q);
-#pragma unroll
-        for (int r = 0; r < 16; ++r) pr[16 * u + r] = c[r];
+      for (int u = 0; u < SUB; ++u) {
+        u32x4_t k[T::QN];
+        read_keys(lk, u, lane, k);
+        scores(k, q, sc[u]);
       }
-      const float was = mx;
-      const float f = softmax_step<T::KT / 2>(
-          pr, edge, row_lo, row_hi, scale2,
-          [&](int i) { return key0 + 32 * (i / 16) + 8 * (i % 16 / 4) + 4 * (lane >> 5) + i % 4; }, max_xor32, mx, l);
-      if (__any(mx > was)) {
+      // operands of the next 32 keys are asked for while these are multiplied
+      __builtin_amdgcn_sched_group_barrier(0x100, T::QN, 0);
+#pragma unroll
+      for (int i = 0; i < T::QN * (SUB - 1); ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x8, T::RT, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+      __builtin_amdgcn_sched_group_barrier(0x8, T::RT * T::QN, 0);
+      if (key0 < see_lo || key0 + T::KT > see_hi) {
+        asm volatile("");   // (a branch: few tiles lie on an edge)
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int key = key0 + 32 * u + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+#pragma unroll
+            for (int rt = 0; rt < T::RT; ++rt)
+              if (key < row_lo[rt] || key >= row_hi[rt]) sc[u][rt][r] = -INFINITY;
+          }
+      }
+      float ref[T::RT], f[T::RT];
+      bool grew = false;
+#pragma unroll
+      for (int rt = 0; rt < T::RT; ++rt) {
+        float top = sc[0][rt][0];
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[u][rt][r]);
+        const float most = fmaxf(mx[rt], max_xor32(top) * scale2);
+        ref[rt] = most == -INFINITY ? 0.f : most;   // (nothing seen yet)
+        f[rt] = __builtin_amdgcn_exp2f(mx[rt] - ref[rt]);
+        grew = grew || most > mx[rt];
+        mx[rt] = most;
+      }
+      if (__any(grew)) {
+        asm volatile("");
+#pragma unroll
+        for (int rt = 0; rt < T::RT; ++rt) {
+          l[rt] *= f[rt];
+#pragma unroll
+          for (int i = 0; i < T::D / 32; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) o[rt][i][r] *= f[rt];
+        }
+      }
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+        for (int rt = 0; rt < T::RT; ++rt) {
+          float sum = 0.f;
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            sc[u][rt][r] = __builtin_amdgcn_exp2f(fmaf(sc[u][rt][r], scale2, -ref[rt]));
+            sum += sc[u][rt][r];
+          }
+          l[rt] += sum;
+        }
+        if constexpr (T::ES == 2) {
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks) {
+            bf16x8_t v[T::D / 32];
+            read_values(lv, u, ks, lane, v);
+            add_values(v, ks, sc[u], o);
+          }
+        } else {
+          add_values_f32(lv, u, lane, sc[u], o);
+        }
+      }
+    }
+#pragma unroll
+    for (int rt = 0; rt < T::RT; ++rt) {
+      l[rt] += __shfl_xor(l[rt], 32);
+      const int rl = (wave * T::RT + rt) * 32 + (lane & 31);   // row in the tile
+      const int r = m * T::BM + rl;
+      if (r < rows) {
+        if (slot >= 0 && lane < 32) g.part_ml[slot * T::BM + rl] = float2{mx[rt], l[rt]};
 #pragma unroll
         for (int i = 0; i < T::D / 32; ++i)
 #pragma unroll
-          for (int r = 0; r < 16; ++r) o[i][r] *= f;
+          for (int x = 0; x < 4; ++x) {
+            const int d = 32 * i + 8 * x + 4 * (lane >> 5);
+            const f32x4_t v = {o[rt][i][4 * x], o[rt][i][4 * x + 1], o[rt][i][4 * x + 2], o[rt][i][4 * x + 3]};
+            if (slot >= 0)
+              *reinterpret_cast<f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + d) = v;
+            else
+              L::put(g, s.first, h, r, d, v, mx[rt], l[rt], v_scale);
+          }
       }
-#pragma unroll
-      for (int u = 0; u < T::KT / 32; ++u) add_values(lv, u, lane, pr + 16 * u, o);
-    }
-    l += __shfl_xor(l, 32);
-
-    const int rl = wave * 32 + (lane & 31);   // row in the tile
-    const int r = m * T::BM + rl;
-    if (r < rows) {
-      if (slot >= 0 && lane < 32) g.part_ml[slot * T::BM + rl] = float2{mx, l};
-#pragma unroll
-      for (int i = 0; i < T::D / 32; ++i)
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int d = 32 * i + 8 * x + 4 * (lane >> 5);
-          const f32x4_t v = {o[i][4 * x], o[i][4 * x + 1], o[i][4 * x + 2], o[i][4 * x + 3]};
-          if (slot >= 0)
-            *reinterpret_cast<f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + d) = v;
-          else
-            L::put(g, s.first, h, r, d, v, mx, l, v_scale);
-        }
     }
     __syncthreads();   // the tiles in LDS are read: the next row tile may overwrite them
   }
@@ -790,6 +900,7 @@ struct AttnFewBody : AttnLoader<T> {
               [&](int i) { return key0 + 32 * u + 16 * (i / 4) + 4 * (lane >> 4) + i % 4; },
               [](float v) { return max_xor32(max_xor16(v)); }, mx[rt], l[rt]);
           if (__any(mx[rt] > was)) {
+            asm volatile("");
 #pragma unroll
             for (int i = 0; i < T::D / 16; ++i) o[rt][i] *= f;
           }

@@ -9,10 +9,11 @@ namespace bdr {
 
 namespace {
 
-constexpr int64_t kCus = 256;   // compute units of an MI355X
+constexpr int64_t kCus = 256;                    // compute units of an MI355X
+constexpr int64_t kMaxGrid = int64_t(1) << 20;   // workgroups
 
 struct Choice {
-  int few;            // 16-row tiles of a few-row variant, 0: many rows
+  int few;            // 16-row tiles of a few-row variant; 0, -1: many rows in tiles of 128, 256
   int bm;             // rows of a row tile
   int64_t shares, min_share;
   int whole;
@@ -24,12 +25,12 @@ Choice choose(const AttnProblem& p) {
   const int64_t rows = (p.rows * p.group + p.batch - 1) / p.batch;
   const int most = p.dt == BDR_F32 ? (p.dim == 256 ? 0 : 2) : p.dim == 256 ? 2 : 4;
   c.few = rows <= 16 * most ? static_cast<int>((rows + 15) / 16) : 0;
-  c.bm = c.few ? 16 * c.few : 128;
+  if (false && c.few == 0 && rows > 192 && p.dt == BDR_BF16 && p.dim < 256) c.few = -1;
+  c.bm = c.few > 0 ? 16 * c.few : c.few == 0 ? 128 : 256;
   const int64_t longest = static_cast<int64_t>(p.width) * p.page;
-  c.whole = longest <= 256;
-  // row tiles at most, or two workgroups a compute unit
-  c.shares = c.whole ? (p.rows * p.group + c.bm - 1) / c.bm + p.batch
-                     : std::max<int64_t>(1, 2 * kCus / p.hkv);
+  const int64_t tiles = (p.rows * p.group + c.bm - 1) / c.bm + p.batch;   // row tiles at most
+  c.whole = longest <= 256 && tiles * p.hkv <= kMaxGrid;
+  c.shares = c.whole ? tiles : std::max<int64_t>(1, 2 * kCus / p.hkv);
   c.min_share = 8;
   return c;
 }

@@ -5,7 +5,7 @@
 
 namespace bdr {
 
-// few: 16-row tiles of a few-row variant, 0: the many-row variant
+// few: 16-row tiles of a few-row variant, 0 or -1: many rows, in row tiles of 128 or 256
 hipError_t launch_attn_bf16(const AttnArgs& g, int few, hipStream_t stream);
 hipError_t launch_attn_fp8(const AttnArgs& g, int few, hipStream_t stream);
 hipError_t launch_attn_f32(const AttnArgs& g, int few, hipStream_t stream);
@@ -25,14 +25,15 @@ hipError_t run_attn(const AttnArgs& g, hipStream_t stream) {
 }
 
 // the built variants of a head size
-template <typename C, typename S, int D, int KT, int FEW>
+template <typename C, typename S, int D, int KT, int FEW, bool TALL>
 hipError_t run_attn_dim(const AttnArgs& g, int few, hipStream_t stream) {
   switch (few) {
     case 1: return run_attn<AttnFew<C, S, D, 1>>(g, stream);
     case 2: return run_attn<AttnFew<C, S, D, 2>>(g, stream);
     case 3: if constexpr (FEW >= 3) return run_attn<AttnFew<C, S, D, 3>>(g, stream); break;
     case 4: if constexpr (FEW >= 4) return run_attn<AttnFew<C, S, D, 4>>(g, stream); break;
-    default: return run_attn<AttnMany<C, S, D, 4, KT>>(g, stream);
+    case -1: if constexpr (TALL) return run_attn<AttnMany<C, S, D, 4, 2, KT>>(g, stream); break;
+    default: return run_attn<AttnMany<C, S, D, 4, 1, KT>>(g, stream);
   }
   return hipErrorInvalidValue;
 }
