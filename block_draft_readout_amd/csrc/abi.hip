@@ -1174,6 +1174,7 @@ constexpr int64_t kMaxContext = int64_t(1) << 30;    // positions of a block tab
 constexpr int64_t kMaxSlotRows = int64_t(1) << 24;
 constexpr int64_t kMaxQueryVectors = int64_t(1) << 30;
 constexpr int kMaxHeads = 1024;
+constexpr int64_t kMaxStride = (int64_t(1) << 30) - 1;   // of a cache, elements: under 2^32 bytes
 
 int table_shape(int64_t batch, int64_t max_pages, int64_t page_size) {
   if (batch < 0) return fail(BDR_EINVAL, "batch must be >= 0");
@@ -1241,9 +1242,8 @@ int cache_shape(const Cache& c, int kv_heads, int dt) {
   if (c.page_stride < 0 || c.token_stride < 0 || c.head_stride < 0 || c.page_stride % e ||
       c.token_stride % e || c.head_stride % e)
     return fail(BDR_EINVAL, "the cache's strides must be multiples of 16 bytes and >= 0");
-  if (c.page_stride > kMaxElems / c.pages || c.token_stride > kMaxElems / c.page ||
-      c.head_stride > kMaxElems / kv_heads)
-    return fail(BDR_EUNSUPPORTED, "the cache's strides are too large");
+  if (c.page_stride > kMaxStride || c.token_stride > kMaxStride || c.head_stride > kMaxStride)
+    return fail(BDR_EUNSUPPORTED, "the cache's strides must be < 2^30 elements");
   return BDR_OK;
 }
 
@@ -1533,9 +1533,10 @@ int dflash_paged_attention(const void* q, int64_t q_row_stride, int64_t q_head_s
   p.k_cache = k_cache;
   p.v_cache = v_cache;
   p.pages = static_cast<int>(pages);
-  p.page_stride = page_stride;
-  p.token_stride = token_stride;
-  p.head_stride = head_stride;
+  const int64_t ce = cache_elem(c, dt);
+  p.page_bytes = static_cast<uint32_t>(page_stride * ce);
+  p.token_bytes = static_cast<uint32_t>(token_stride * ce);
+  p.head_bytes = head_stride * ce;
   p.k_scale = k_scale;
   p.v_scale = v_scale;
   p.table = block_table;

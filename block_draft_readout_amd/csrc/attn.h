@@ -38,6 +38,8 @@ struct AttnArgs {
   int64_t min_share;    // key tiles that a workgroup takes at least
   int whole;            // each row tile is one workgroup's
   float scale2;         // scale * log2(e)
+  uint32_t page_magic;  // key / page = mulhi(2 key, page_magic) >> page_shift, keys below 2^30
+  int page_shift;
   float* part_o;        // [shares][hkv][2][BM][D]
   float2* part_ml;      // [shares][hkv][2][BM] (m in units of log2, l)
   int32_t* record;      // [shares][hkv][kRecord] what the join needs
@@ -137,7 +139,7 @@ template <typename C_, typename S_, int D_, int WM_, int RT_, int KT_>
 struct AttnMany {
   using C = C_;                       // cache element: uint16_t (bf16), uint8_t (e4m3) or float
   using S = S_;                       // queries, output and LDS: uint16_t or float
-  static constexpr bool kFew = false;
+  static constexpr bool kFew = false, kTall = false;
   static constexpr int D = D_, WM = WM_, RT = RT_;
   static constexpr int KT = KT_;      // keys of a tile
   static constexpr int THREADS = 64 * WM;
@@ -157,6 +159,15 @@ struct AttnMany {
   static_assert(LDS_BYTES <= 160 * 1024, "tile fits");
 };
 
+// Very many rows: eight waves, two of a SIMD in opposite phases (see the body).
+template <typename C_, typename S_, int D_, int KT_>
+struct AttnTall : AttnMany<C_, S_, D_, 8, 1, KT_> {
+  using Base = AttnMany<C_, S_, D_, 8, 1, KT_>;
+  static constexpr bool kTall = true;
+  static constexpr int LDS_BYTES = 7 * Base::TILE_BYTES;   // three buffers of keys, four of values
+  static constexpr int SIMD_WAVES = 2;
+};
+
 // Few rows: WN waves hold the same RT x 16 rows and walk key tiles of their own, each through
 // LDS of its own, joined at the end.  Tiles come straight from the cache to LDS as they are
 // stored there.
@@ -164,7 +175,7 @@ template <typename C_, typename S_, int D_, int RT_>
 struct AttnFew {
   using C = C_;
   using S = S_;
-  static constexpr bool kFew = true;
+  static constexpr bool kFew = true, kTall = false;
   static constexpr int D = D_, RT = RT_;
   static constexpr int CS = static_cast<int>(sizeof(C)), ES = static_cast<int>(sizeof(S));
   static constexpr int ROWB = D * CS;                    // bytes of an LDS row
@@ -232,11 +243,12 @@ __device__ __forceinline__ void widen16(u32x4_t v, u32x4_t& a, u32x4_t& b) {
   b = __builtin_bit_cast(u32x4_t, widen8(v.z, v.w));
 }
 
-// Page ids of the tile after the next.  They are asked for behind the loads of a tile and used
-// after those have been waited for: an address that depends on them never holds up a tile.
+// A lane's key of a tile to come.  The page's id is asked for behind the loads of an earlier
+// tile and used after those have been waited for: an address that depends on it never holds up a
+// tile.
 struct AttnPage {
-  int32_t id;       // of this lane's key, -1: not read
-  uint32_t place;   // in the page
+  int32_t id;
+  int32_t place;   // in the page; -1: the key is not read
 };
 
 // What both kinds of kernels share.
@@ -245,16 +257,23 @@ struct AttnLoader {
   using S = typename T::S;
   using C = typename T::C;
 
-  static __device__ __forceinline__ AttnPage page_of(const AttnProblem& p, const int32_t* table, int key0,
-                                                     int lo, int hi, int lane) {
+  static __device__ __forceinline__ AttnPage page_of(const AttnArgs& g, const int32_t* table, int key0, int lo,
+                                                     int hi, int lane) {
     const int key = key0 + (T::KT == 64 ? lane : lane & 31);
-    AttnPage a{-1, 0};
-    if (key >= lo && key < hi) {
-      const uint32_t col = static_cast<uint32_t>(key) / static_cast<uint32_t>(p.page);
-      a.place = static_cast<uint32_t>(key) - col * p.page;
-      a.id = table[col];
-    }
-    return a;
+    const int at = max(min(max(key, lo), hi - 1), 0);   // (a key of the table, whatever lo and hi)
+    const uint32_t col = __umulhi(2u * at, g.page_magic) >> g.page_shift;
+    return AttnPage{table[col], key == at && key < hi ? static_cast<int32_t>(at - col * g.p.page) : -1};
+  }
+  // its bytes from the head's first, 0 and false where it is not read
+  static __device__ __forceinline__ uint64_t offset_of(const AttnProblem& p, AttnPage a, bool& in) {
+    in = a.place >= 0 && static_cast<uint32_t>(a.id) < static_cast<uint32_t>(p.pages);
+    const uint64_t off = static_cast<uint64_t>(static_cast<uint32_t>(a.id)) * p.page_bytes +
+                         static_cast<uint64_t>(static_cast<uint32_t>(a.place)) * p.token_bytes;
+    return in ? off : 0;
+  }
+  // rows of one load lie in one page, its offsets in 32 bits
+  static __device__ __forceinline__ bool whole_loads(const AttnProblem& p) {
+    return p.page % T::RPL == 0 && p.token_bytes < (1u << 31) / 64;
   }
 
   // A lane's 16-byte pieces of row r of the packed rows: features place(i) on.
@@ -362,23 +381,22 @@ struct AttnManyBody : AttnLoader<T> {
 
   // Every lane looks a key up; a load's rows take their offsets from the lanes that did.  Where
   // they lie in one page, one offset is the load's own scalar.
-  static __device__ __forceinline__ void load(const AttnProblem& p, const char* kb, const char* vb, AttnPage a,
-                                              int tid, Stage& g) {
-    const bool in = a.id >= 0 && a.id < p.pages;
-    g.live = __ballot(in) & kAll;
+  // off, live: what offset_of gave the lanes
+  static __device__ __forceinline__ void load_at(const AttnProblem& p, const char* kb, const char* vb, uint64_t off,
+                                                 uint64_t live, int tid, Stage& g) {
     // a row that is not read takes the first page's first row, and is cleared on its way to LDS
-    const int64_t off = in ? (a.id * p.page_stride + a.place * p.token_stride) * T::CS : 0;
     const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
     asm volatile("" : "+v"(tid));   // (offsets are made anew rather than held over the loop)
     const uint32_t c = static_cast<uint32_t>(tid % T::CPR) * 16;
-    if (g.live == kAll && p.page % T::RPL == 0 && p.token_stride < (1 << 30) / 64) {
+    g.live = live;
+    if (live == kAll && L::whole_loads(p)) {
       const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-      const uint32_t mine = (tid & 63) / T::CPR * static_cast<uint32_t>(p.token_stride) * T::CS + c;
+      const uint32_t mine = (tid & 63) / T::CPR * p.token_bytes + c;
 #pragma unroll
       for (int i = 0; i < T::LOADS; ++i) {
         const int row = (64 * wave + T::THREADS * i) / T::CPR;
         const uint32_t l = __builtin_amdgcn_readlane(lo, row), h = __builtin_amdgcn_readlane(hi, row);
-        const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l);
+        const uint64_t at = (static_cast<uint64_t>(h) << 32) | l;
         g.k[i] = load16(kb + at + mine);
         g.v[i] = load16(vb + at + mine);
       }
@@ -387,11 +405,17 @@ struct AttnManyBody : AttnLoader<T> {
       for (int i = 0; i < T::LOADS; ++i) {
         const int row = (tid + T::THREADS * i) / T::CPR;
         const uint32_t l = __shfl(lo, row), h = __shfl(hi, row);
-        const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l) + c;
-        g.k[i] = load16(kb + at);
-        g.v[i] = load16(vb + at);
+        const uint64_t at = (static_cast<uint64_t>(h) << 32) | l;
+        g.k[i] = load16(kb + at + c);
+        g.v[i] = load16(vb + at + c);
       }
     }
+  }
+  static __device__ __forceinline__ void load(const AttnProblem& p, const char* kb, const char* vb, AttnPage a,
+                                              int tid, Stage& g) {
+    bool in;
+    const uint64_t off = L::offset_of(p, a, in);
+    load_at(p, kb, vb, off, __ballot(in) & kAll, tid, g);
   }
 
   static __device__ __forceinline__ void store16(char* lds, uint32_t at, uint32_t at_next, u32x4_t v) {
@@ -404,21 +428,31 @@ struct AttnManyBody : AttnLoader<T> {
       *reinterpret_cast<u32x4_t*>(lds + at) = v;
     }
   }
-  static __device__ __forceinline__ void store(char* lk, char* lv, int tid, Stage& g) {
-    if (g.live != kAll) {
-      asm volatile("");   // (a branch: rare)
+  // rows that are not read become zeros
+  static __device__ __forceinline__ void clear(int tid, Stage& g) {
+    asm volatile("");   // (a branch: rare)
 #pragma unroll
-      for (int i = 0; i < T::LOADS; ++i)
-        if (!((g.live >> ((tid + T::THREADS * i) / T::CPR)) & 1)) g.k[i] = g.v[i] = u32x4_t{0, 0, 0, 0};
-    }
+    for (int i = 0; i < T::LOADS; ++i)
+      if (!((g.live >> ((tid + T::THREADS * i) / T::CPR)) & 1)) g.k[i] = g.v[i] = u32x4_t{0, 0, 0, 0};
+  }
+  template <typename Keys>   // true_type: keys' places, false_type: values'
+  static __device__ __forceinline__ void store_one(char* lds, int tid, const u32x4_t (&x)[T::LOADS], Keys) {
     constexpr int W = T::ES / T::CS;   // 16-byte chunks in LDS of a piece
+    auto place = [](uint32_t r, uint32_t c) {
+      if constexpr (Keys::value) return key_place<T::ROWB>(r, c);
+      else return value_place<T>(r, c);
+    };
 #pragma unroll
     for (int i = 0; i < T::LOADS; ++i) {
       const int idx = tid + T::THREADS * i;
       const uint32_t row = idx / T::CPR, c = W * (idx % T::CPR);
-      store16(lk, key_place<T::ROWB>(row, c), key_place<T::ROWB>(row, c + W - 1), g.k[i]);
-      store16(lv, value_place<T>(row, c), value_place<T>(row, c + W - 1), g.v[i]);
+      store16(lds, place(row, c), place(row, c + W - 1), x[i]);
     }
+  }
+  static __device__ __forceinline__ void store(char* lk, char* lv, int tid, Stage& g) {
+    if (g.live != kAll) clear(tid, g);
+    store_one(lk, tid, g.k, std::true_type{});
+    store_one(lv, tid, g.v, std::false_type{});
   }
 
   // 16-byte operand pieces of 32 keys: piece i is chunk 2 i + lane / 32 of key lane % 32
@@ -494,6 +528,31 @@ struct AttnManyBody : AttnLoader<T> {
     }
   }
 
+  // a wave's rows, from row `first` of the tile on: the output, or a partial in `slot`
+  static __device__ __forceinline__ void put_rows(const AttnArgs& g, const AttnSeq& s, int h, int m, int first,
+                                                  int lane, int64_t slot, const f32x16_t (&o)[T::RT][T::D / 32],
+                                                  const float (&mx)[T::RT], const float (&l)[T::RT], float v_scale) {
+#pragma unroll
+    for (int rt = 0; rt < T::RT; ++rt) {
+      const int rl = first + 32 * rt + (lane & 31);   // row in the tile
+      const int r = m * T::BM + rl;
+      if (r < s.n * g.p.group) {
+        if (slot >= 0 && lane < 32) g.part_ml[slot * T::BM + rl] = float2{mx[rt], l[rt]};
+#pragma unroll
+        for (int i = 0; i < T::D / 32; ++i)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int d = 32 * i + 8 * x + 4 * (lane >> 5);
+            const f32x4_t v = {o[rt][i][4 * x], o[rt][i][4 * x + 1], o[rt][i][4 * x + 2], o[rt][i][4 * x + 3]};
+            if (slot >= 0)
+              *reinterpret_cast<f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + d) = v;
+            else
+              L::put(g, s.first, h, r, d, v, mx[rt], l[rt], v_scale);
+          }
+      }
+    }
+  }
+
   // One row tile over key tiles [ta, tb).  slot < 0: the output itself, else a partial there.
   static __device__ __forceinline__ void run(const AttnArgs& g, const AttnSeq& s, int b, int h, int m, int ta,
                                              int tb, int lo, int hi, int64_t slot, char* lds) {
@@ -512,14 +571,14 @@ struct AttnManyBody : AttnLoader<T> {
     scale2 = fmaxf(fabsf(scale2), 1e-30f);
 
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
-    const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_stride * T::CS;
-    const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_stride * T::CS;
+    const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_bytes;
+    const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_bytes;
     char* now = lds;                             // keys and values of a tile
     char* other = lds + 2 * T::TILE_BYTES;
     Stage stage;
-    AttnPage page = L::page_of(p, table, ta * T::KT, lo, hi, lane);
+    AttnPage page = L::page_of(g, table, ta * T::KT, lo, hi, lane);
     load(p, kb, vb, page, tid, stage);
-    page = L::page_of(p, table, (ta + 1) * T::KT, lo, hi, lane);
+    page = L::page_of(g, table, (ta + 1) * T::KT, lo, hi, lane);
 
     u32x4_t q[T::RT][T::QN];
     int row_lo[T::RT], row_hi[T::RT];
@@ -548,7 +607,7 @@ struct AttnManyBody : AttnLoader<T> {
       store(now, now + T::TILE_BYTES, tid, stage);
       if (t + 1 < tb) {
         load(p, kb, vb, page, tid, stage);
-        page = L::page_of(p, table, (t + 2) * T::KT, lo, hi, lane);
+        page = L::page_of(g, table, (t + 2) * T::KT, lo, hi, lane);
       }
       // one barrier a tile: the buffer written next was last read before the barrier after that
       __syncthreads();
@@ -636,25 +695,199 @@ struct AttnManyBody : AttnLoader<T> {
       }
     }
 #pragma unroll
-    for (int rt = 0; rt < T::RT; ++rt) {
-      l[rt] += __shfl_xor(l[rt], 32);
-      const int rl = (wave * T::RT + rt) * 32 + (lane & 31);   // row in the tile
-      const int r = m * T::BM + rl;
-      if (r < rows) {
-        if (slot >= 0 && lane < 32) g.part_ml[slot * T::BM + rl] = float2{mx[rt], l[rt]};
+    for (int rt = 0; rt < T::RT; ++rt) l[rt] += __shfl_xor(l[rt], 32);
+    put_rows(g, s, h, m, wave * T::RT * 32, lane, slot, o, mx, l, v_scale);
+    __syncthreads();   // the tiles in LDS are read: the next row tile may overwrite them
+  }
+};
+
+// -------------------------------------------------------------- very many rows
+// Waves w and w + 4 share a SIMD.  A wave goes through two phases a tile: softmax (with the
+// copies: a tile's way through registers to LDS) and products (this tile's values, the next one's
+// scores).  The second four waves start one barrier late, so at any time one wave of a SIMD has
+// the matrix unit and the other the vector unit; a barrier ends every phase.
+template <typename T>
+struct AttnTallBody : AttnManyBody<T> {
+  using M = AttnManyBody<T>;
+  using L = AttnLoader<T>;
+  using S = typename T::S;
+  using C = typename T::C;
+  static constexpr int SUB = T::KT / 32;
+
+  static __device__ __forceinline__ void run(const AttnArgs& g, const AttnSeq& s, int b, int h, int m, int ta,
+                                             int tb, int lo, int hi, int64_t slot, char* lds) {
+    const AttnProblem& p = g.p;
+    const int wave = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) >> 6);
+    const int lane = static_cast<int>(threadIdx.x) & 63;
+    const int tid = static_cast<int>(threadIdx.x);
+    const int r0 = m * T::BM + wave * 32;
+    const int rows = s.n * p.group;
+    float scale2 = g.scale2, v_scale = 1.f;
+    if constexpr (sizeof(C) == 1) {
+      scale2 *= p.k_scale[h];
+      v_scale = p.v_scale[h];
+    }
+    const bool flip = scale2 < 0.f;   // the running maximum wants a positive scale
+    scale2 = fmaxf(fabsf(scale2), 1e-30f);
+
+    const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
+    const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_bytes;
+    const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_bytes;
+    // buffers of keys: of the next tile, the one after, and to fill; of values: of this tile, the
+    // next two, and to fill
+    char* k1 = lds + T::TILE_BYTES;
+    char* k2 = lds + 2 * T::TILE_BYTES;
+    char* k3 = lds;
+    char* v0 = lds + 3 * T::TILE_BYTES;
+    char* v1 = lds + 4 * T::TILE_BYTES;
+    char* v2 = lds + 5 * T::TILE_BYTES;
+    char* v3 = lds + 6 * T::TILE_BYTES;
+
+    typename M::Stage stage;
+    {
+      typename M::Stage x0;
+      const AttnPage p0 = L::page_of(g, table, ta * T::KT, lo, hi, lane);
+      const AttnPage p1 = L::page_of(g, table, (ta + 1) * T::KT, lo, hi, lane);
+      M::load(p, kb, vb, p0, tid, x0);
+      M::load(p, kb, vb, p1, tid, stage);
+      M::store(k3, v0, tid, x0);
+      M::store(k1, v1, tid, stage);
+    }
+    AttnPage page = L::page_of(g, table, (ta + 2) * T::KT, lo, hi, lane);
+    M::load(p, kb, vb, page, tid, stage);   // of tile t + 2 from here on
+    page = L::page_of(g, table, (ta + 3) * T::KT, lo, hi, lane);
+
+    u32x4_t q[1][T::QN];
+    L::load_q(p, s, h, r0 + (lane & 31), [&](int i) { return (2 * i + (lane >> 5)) * (16 / T::ES); }, flip, q[0]);
+    const int at = s.len - s.n + (r0 + (lane & 31)) / p.group;
+    const int row_hi = p.causal ? min(at + 1, s.len) : s.len;
+    const int row_lo = p.window ? at - p.window + 1 : 0;
+    f32x16_t o[1][T::D / 32];
+    float mx = -INFINITY, l = 0.f;
+#pragma unroll
+    for (int i = 0; i < T::D / 32; ++i) o[0][i] = f32x16_t{};
+    // the wave's rows all see the keys [see_lo, see_hi)
+    const int first = s.len - s.n + r0 / p.group;
+    const int last = s.len - s.n + min(r0 + 31, rows - 1) / p.group;
+    const int see_hi = p.causal ? min(first + 1, s.len) : s.len;
+    const int see_lo = p.window ? last - p.window + 1 : 0;
+
+    __syncthreads();
+    if (wave >= 4) __syncthreads();
+
+    f32x16_t sc[SUB];
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      u32x4_t k[T::QN];
+      M::read_keys(k3, u, lane, k);
+      f32x16_t c[1];
+      M::scores(k, q, c);
+      sc[u] = c[0];
+    }
+    for (int t = ta; t < tb; ++t) {
+      // ---- softmax
+      u32x4_t pr[SUB][2];   // probabilities, as the second product's operands
+      bf16x8_t first_v[T::D / 32];
+      const int key0 = t * T::KT;
+      if (key0 < see_lo || key0 + T::KT > see_hi) {
+        asm volatile("");   // (a branch: few tiles lie on an edge)
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int key = key0 + 32 * u + 8 * (r / 4) + 4 * (lane >> 5) + r % 4;
+            if (key < row_lo || key >= row_hi) sc[u][r] = -INFINITY;
+          }
+      }
+      float top = sc[0][0];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) top = fmaxf(top, sc[u][r]);
+      const float most = fmaxf(mx, max_xor32(top) * scale2);
+      const float ref = most == -INFINITY ? 0.f : most;   // (nothing seen yet)
+      if (__any(most > mx)) {
+        asm volatile("");
+        const float f = __builtin_amdgcn_exp2f(mx - ref);
+        l *= f;
 #pragma unroll
         for (int i = 0; i < T::D / 32; ++i)
 #pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            const int d = 32 * i + 8 * x + 4 * (lane >> 5);
-            const f32x4_t v = {o[rt][i][4 * x], o[rt][i][4 * x + 1], o[rt][i][4 * x + 2], o[rt][i][4 * x + 3]};
-            if (slot >= 0)
-              *reinterpret_cast<f32x4_t*>(g.part_o + (slot * T::BM + rl) * T::D + d) = v;
-            else
-              L::put(g, s.first, h, r, d, v, mx[rt], l[rt], v_scale);
-          }
+          for (int r = 0; r < 16; ++r) o[0][i][r] *= f;
       }
+      mx = most;
+      M::read_values(v0, 0, 0, lane, first_v);   // the first operands of the products
+      float sum = 0.f;
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          sc[u][r] = __builtin_amdgcn_exp2f(fmaf(sc[u][r], scale2, -ref));
+          sum += sc[u][r];
+        }
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pr[u][ks][e] = pack_bf16(sc[u][8 * ks + 2 * e], sc[u][8 * ks + 2 * e + 1]);
+      }
+      l += sum;
+      // (the probabilities belong to this phase)
+#pragma unroll
+      for (int x = 0; x < 2 * SUB; ++x)
+        asm volatile("" : "+v"(pr[x / 2][x % 2].x), "+v"(pr[x / 2][x % 2].y), "+v"(pr[x / 2][x % 2].z),
+                          "+v"(pr[x / 2][x % 2].w));
+      __syncthreads();
+      // ---- products: this tile's values, the next one's scores; and the copies between them.  In
+      // every step the operands of the next are asked for, then the products of this one begun.
+      if (stage.live != M::kAll) M::clear(tid, stage);
+      __builtin_amdgcn_s_setprio(1);
+      bool in;
+      const uint64_t off = L::offset_of(p, page, in);
+      const uint64_t live = __ballot(in) & M::kAll;
+      u32x4_t k[2][T::QN];
+#pragma unroll
+      for (int x = 0; x < 2 * SUB; ++x) {
+        bf16x8_t v[T::D / 32];
+        if (x + 1 < 2 * SUB) M::read_values(v0, (x + 1) / 2, (x + 1) % 2, lane, v);
+        else M::read_keys(k1, 0, lane, k[0]);
+        if (x == 0) M::store_one(k2, tid, stage.k, std::true_type{});
+        if (x == 1) M::store_one(v2, tid, stage.v, std::false_type{});
+#pragma unroll
+        for (int i = 0; i < T::D / 32; ++i)
+          o[0][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+              first_v[i], __builtin_bit_cast(bf16x8_t, pr[x / 2][x % 2]), o[0][i], 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < T::D / 32; ++i) first_v[i] = v[i];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      // (past the last tile: keys and values that nobody reads)
+      M::load_at(p, kb, vb, off, live, tid, stage);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        if (u + 1 < SUB) M::read_keys(k1, u + 1, lane, k[(u + 1) % 2]);
+        if (u == 0) page = L::page_of(g, table, (t + 4) * T::KT, lo, hi, lane);
+        f32x16_t c[1];
+        M::scores(k[u % 2], q, c);
+        sc[u] = c[0];
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      __builtin_amdgcn_s_setprio(0);
+      char* const k_old = k3;
+      k3 = k1;
+      k1 = k2;
+      k2 = k_old;
+      char* const v_old = v0;
+      v0 = v1;
+      v1 = v2;
+      v2 = v3;
+      v3 = v_old;
+      __syncthreads();
     }
+    if (wave < 4) __syncthreads();   // (the second four have one more behind them)
+    l += __shfl_xor(l, 32);
+    const float ms[1] = {mx}, ls[1] = {l};
+    M::put_rows(g, s, h, m, wave * 32, lane, slot, o, ms, ls, v_scale);
     __syncthreads();   // the tiles in LDS are read: the next row tile may overwrite them
   }
 };
@@ -681,30 +914,29 @@ struct AttnFewBody : AttnLoader<T> {
   static __device__ __forceinline__ void load(const AttnProblem& p, const char* kb, const char* vb, AttnPage a,
                                               int lane, char* lk, char* lv) {
     constexpr uint64_t kAll = T::KT == 64 ? ~0ull : 0xFFFFFFFFull;
-    const bool in = a.id >= 0 && a.id < p.pages;
+    bool in;
+    const uint64_t off = L::offset_of(p, a, in);
     const uint64_t live = __ballot(in) & kAll;
+    const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
     asm volatile("" : "+v"(lane));   // (offsets are made anew: held over the loop they take 4 LOADS registers)
     const uint32_t sub = lane / T::CPR, pos = lane % T::CPR;
     // the turns of rows RPL i and sub are of different bits
     const uint32_t kc = (pos ^ key_turn<T::ROWB>(sub)) << 4, vc = (pos ^ value_turn<T>(sub)) << 4;
-    if (live == kAll && p.page % T::RPL == 0 && p.token_stride < (1 << 30) / 64) {
-      const uint32_t mine = sub * static_cast<uint32_t>(p.token_stride) * T::CS;
+    if (live == kAll && L::whole_loads(p)) {
+      const uint32_t mine = sub * p.token_bytes;
 #pragma unroll
       for (int i = 0; i < T::LOADS; ++i) {
-        const int id = __builtin_amdgcn_readlane(a.id, T::RPL * i);
-        const int place = __builtin_amdgcn_readlane(static_cast<int>(a.place), T::RPL * i);
-        const int64_t off = (id * p.page_stride + place * p.token_stride) * T::CS;
-        copy_lds16(kb + off + (mine + (kc ^ (key_turn<T::ROWB>(T::RPL * i) << 4))), lk + 1024 * i);
-        copy_lds16(vb + off + (mine + (vc ^ (value_turn<T>(T::RPL * i) << 4))), lv + 1024 * i);
+        const uint32_t l = __builtin_amdgcn_readlane(lo, T::RPL * i), h = __builtin_amdgcn_readlane(hi, T::RPL * i);
+        const uint64_t at = (static_cast<uint64_t>(h) << 32) | l;
+        copy_lds16(kb + at + (mine + (kc ^ (key_turn<T::ROWB>(T::RPL * i) << 4))), lk + 1024 * i);
+        copy_lds16(vb + at + (mine + (vc ^ (value_turn<T>(T::RPL * i) << 4))), lv + 1024 * i);
       }
     } else {
-      const int64_t off = in ? (a.id * p.page_stride + a.place * p.token_stride) * T::CS : 0;
-      const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
 #pragma unroll 1
       for (int i = 0; i < T::LOADS; ++i) {
         const uint32_t row = T::RPL * i + sub;
         const uint32_t l = __shfl(lo, row), h = __shfl(hi, row);
-        const int64_t at = static_cast<int64_t>((static_cast<uint64_t>(h) << 32) | l);
+        const uint64_t at = (static_cast<uint64_t>(h) << 32) | l;
         const bool read = (live >> row) & 1;
         const char* zero = reinterpret_cast<const char*>(kZeros16);
         copy_lds16(read ? kb + at + (kc ^ (key_turn<T::ROWB>(T::RPL * i) << 4)) : zero, lk + 1024 * i);
@@ -837,16 +1069,16 @@ struct AttnFewBody : AttnLoader<T> {
     scale2 = fmaxf(fabsf(scale2), 1e-30f);
 
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
-    const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_stride * T::CS;
-    const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_stride * T::CS;
+    const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_bytes;
+    const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_bytes;
     char* const lk = lds + wn * T::WAVE_BYTES;
     char* const lv = lk + T::TILE_BYTES;
     AttnPage page{};
     int t = ta + wn;
     if (t < tb) {
-      page = L::page_of(p, table, t * T::KT, lo, hi, lane);
+      page = L::page_of(g, table, t * T::KT, lo, hi, lane);
       load(p, kb, vb, page, lane, lk, lv);
-      page = L::page_of(p, table, (t + T::WN) * T::KT, lo, hi, lane);
+      page = L::page_of(g, table, (t + T::WN) * T::KT, lo, hi, lane);
     }
     u32x4_t q[T::RT][T::QLDS ? 1 : T::QN];
     int row_lo[T::RT], row_hi[T::RT];
@@ -912,7 +1144,7 @@ struct AttnFewBody : AttnLoader<T> {
       __builtin_amdgcn_sched_barrier(0);
       if (t + T::WN < tb) {
         load(p, kb, vb, page, lane, lk, lv);
-        page = L::page_of(p, table, (t + 2 * T::WN) * T::KT, lo, hi, lane);
+        page = L::page_of(g, table, (t + 2 * T::WN) * T::KT, lo, hi, lane);
       }
     }
 
@@ -961,7 +1193,8 @@ struct AttnFewBody : AttnLoader<T> {
 };
 
 template <typename T>
-using AttnBody = std::conditional_t<T::kFew, AttnFewBody<T>, AttnManyBody<T>>;
+using AttnBody =
+    std::conditional_t<T::kFew, AttnFewBody<T>, std::conditional_t<T::kTall, AttnTallBody<T>, AttnManyBody<T>>>;
 
 // The workgroup's share of one kv head's key tiles, row tile by row tile.
 template <typename T>

@@ -25,24 +25,32 @@ Choice choose(const AttnProblem& p) {
   const int64_t rows = (p.rows * p.group + p.batch - 1) / p.batch;
   const int most = p.dt == BDR_F32 ? (p.dim == 256 ? 0 : 2) : p.dim == 256 ? 2 : 4;
   c.few = rows <= 16 * most ? static_cast<int>((rows + 15) / 16) : 0;
-  if (false && c.few == 0 && rows > 192 && p.dt == BDR_BF16 && p.dim < 256) c.few = -1;
+  if (c.few == 0 && rows > 192 && p.dt == BDR_BF16 && (p.dim == 128 || (p.dim == 64 && !p.fp8))) c.few = -1;
   c.bm = c.few > 0 ? 16 * c.few : c.few == 0 ? 128 : 256;
   const int64_t longest = static_cast<int64_t>(p.width) * p.page;
   const int64_t tiles = (p.rows * p.group + c.bm - 1) / c.bm + p.batch;   // row tiles at most
   c.whole = longest <= 256 && tiles * p.hkv <= kMaxGrid;
-  c.shares = c.whole ? tiles : std::max<int64_t>(1, 2 * kCus / p.hkv);
+  c.shares = c.whole ? tiles : std::max<int64_t>(1, (c.few < 0 ? 1 : 2) * kCus / p.hkv);
   c.min_share = 8;
   return c;
 }
 
 }  // namespace
 
-size_t attn_workspace(const AttnProblem& p) {
+static size_t workspace_of(const AttnProblem& p) {
   const Choice c = choose(p);
   if (c.whole) return 0;
   const size_t slots = 2 * static_cast<size_t>(c.shares) * p.hkv * c.bm;
   return align256(slots * p.dim * sizeof(float)) + align256(slots * sizeof(float2)) +
          align256(static_cast<size_t>(c.shares) * p.hkv * kRecord * sizeof(int32_t));
+}
+
+// (whatever the cache holds: its type is not among the sizes that are asked for)
+size_t attn_workspace(const AttnProblem& p) {
+  AttnProblem a = p, b = p;
+  a.fp8 = 0;
+  b.fp8 = 1;
+  return std::max(workspace_of(a), workspace_of(b));
 }
 
 hipError_t launch_attn(const AttnProblem& p, void* workspace, hipStream_t stream) {
@@ -53,6 +61,9 @@ hipError_t launch_attn(const AttnProblem& p, void* workspace, hipStream_t stream
   g.min_share = c.min_share;
   g.whole = c.whole;
   g.scale2 = p.scale * kLog2e;
+  // s = ceil(log2 page), magic = ceil(2^(31 + s) / page): exact for keys below 2^31
+  while ((int64_t(1) << g.page_shift) < p.page) ++g.page_shift;
+  g.page_magic = static_cast<uint32_t>(((uint64_t(1) << (31 + g.page_shift)) + p.page - 1) / p.page);
   if (!c.whole) {
     const size_t slots = 2 * static_cast<size_t>(c.shares) * p.hkv * c.bm;
     char* at = static_cast<char*>(workspace);

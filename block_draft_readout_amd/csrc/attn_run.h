@@ -32,7 +32,7 @@ hipError_t run_attn_dim(const AttnArgs& g, int few, hipStream_t stream) {
     case 2: return run_attn<AttnFew<C, S, D, 2>>(g, stream);
     case 3: if constexpr (FEW >= 3) return run_attn<AttnFew<C, S, D, 3>>(g, stream); break;
     case 4: if constexpr (FEW >= 4) return run_attn<AttnFew<C, S, D, 4>>(g, stream); break;
-    case -1: if constexpr (TALL) return run_attn<AttnMany<C, S, D, 4, 2, KT>>(g, stream); break;
+    case -1: if constexpr (TALL) return run_attn<AttnTall<C, S, D, KT>>(g, stream); break;
     default: return run_attn<AttnMany<C, S, D, 4, 1, KT>>(g, stream);
   }
   return hipErrorInvalidValue;

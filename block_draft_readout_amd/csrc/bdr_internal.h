@@ -166,7 +166,8 @@ struct AttnProblem {
   int fp8;
   const void *k_cache, *v_cache;
   int pages, page;
-  int64_t page_stride, token_stride, head_stride;
+  uint32_t page_bytes, token_bytes;   // strides of the cache
+  int64_t head_bytes;
   const float *k_scale, *v_scale;
   const int32_t* table;
   int batch, width;

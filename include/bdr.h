@@ -834,7 +834,8 @@ int spec_slots(const int32_t* cached, const int32_t* new_tokens, int64_t batch, 
  *   k_out        [rows, kv_heads, D] dtype, contiguous, or NULL; may be k likewise
  *   slots        [rows] int32 with a cache; k_cache, v_cache both or neither
  *   pages >= 1, page_size >= 1, pages * page_size < 2^31; cache strides
- *                multiples of 16 bytes that keep all elements apart
+ *                multiples of 16 bytes, < 2^30 elements, that keep all
+ *                elements apart
  *   k_scale, v_scale  [kv_heads] fp32, both or neither (not 0)
  */
 int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k,
@@ -868,7 +869,7 @@ int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stri
  *                  (as above); 0 <= rows, rows * q_heads <= 2^30; D 64, 128, 256;
  *                  q_heads a multiple of kv_heads
  *   k_cache, v_cache, pages, page_size, strides, k_scale, v_scale   as above
- *                  (strides >= 0)
+ *                  (elements may lie over each other)
  *   block_table    [batch, max_pages] int32; 0 <= batch <= 2^20;
  *                  max_pages * page_size <= 2^30
  *   query_offsets  [batch + 1] int32 ascending; kv_len [batch] int32 (taken as at

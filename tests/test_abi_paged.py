@@ -87,7 +87,7 @@ def test_qk_refusals(A):
     assert _qk(A, dt=A.BDR_F32, ks=at(12), vs=at(13)) == E      # codes go with bf16
     assert _qk(A, pages=0) == E and _qk(A, page=0) == E and _qk(A, pages=1 << 28) == U
     assert _qk(A, ts=260) == E and _qk(A, hs=-128) == E and _qk(A, ks=at(12), vs=at(13), ts=264) == E
-    assert _qk(A, ps=1 << 45) == U
+    assert _qk(A, ps=1 << 30) == U and _qk(A, ts=1 << 30) == U and _qk(A, hs=1 << 30) == U
 
 
 def test_qk_overlaps(A):
@@ -122,6 +122,7 @@ def test_attention_refusals(A):
     assert _attn(A, batch=-1) == E and _attn(A, batch=(1 << 20) + 1) == U and _attn(A, width=0) == E
     assert _attn(A, width=1 << 27) == U
     assert _attn(A, pages=0) == E and _attn(A, page=0) == E and _attn(A, pages=1 << 28) == U
+    assert _attn(A, ps=1 << 30) == U
     assert _attn(A, ts=4) == E and _attn(A, ps=-8) == E and _attn(A, ks=at(9)) == E
     assert _attn(A, dt=A.BDR_F32, ks=at(9), vs=at(10)) == E and _attn(A, ks=at(9) + 1, vs=at(10)) == E
     assert _attn(A, qr=1020) == E and _attn(A, qh=-8) == E
