@@ -8,7 +8,6 @@ head.  Request b's position t is at ``block_table[b, t // page_size]``, place ``
 """
 from __future__ import annotations
 
-import math
 from typing import Dict, Optional
 
 import torch
@@ -19,9 +18,29 @@ from .training import _dtype, _need, _on, _ptr, _space, _stream, _tensor
 __all__ = ["spec_slots", "dspark_qk_norm_rope", "dflash_paged_attention"]
 
 
+_I32, _F32, _U8 = torch.int32, torch.float32, torch.uint8
+
+
 def _ints(t, name: str, shape, device) -> torch.Tensor:
     _tensor(t, name)
-    return _need(t, name, shape, torch.int32, device)
+    return _need(t, name, shape, _I32, device)
+
+
+# The calls serve single tokens, where the host's time is the call's: what is right is seen by one
+# expression, and only what is not goes through the checks that say why.
+def _is(t, dtype, shape, device) -> bool:
+    return (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape
+            and t.device == device and t.is_contiguous())
+
+
+def _call(name: str, fn, device, *args) -> None:
+    if torch._C._cuda_getDevice() == device.index:
+        rc = fn(*args, torch._C._cuda_getCurrentRawStream(device.index))
+    else:
+        with _on(device):
+            rc = fn(*args, _stream(device))
+    if rc:
+        _abi.check(name, rc)
 
 
 def spec_slots(cached: torch.Tensor, new_tokens: torch.Tensor, block_table: torch.Tensor,
@@ -43,91 +62,90 @@ def spec_slots(cached: torch.Tensor, new_tokens: torch.Tensor, block_table: torc
     _tensor(cached, "cached")
     if not cached.is_cuda or cached.dim() != 1:
         raise ValueError("cached must be a device tensor [B]")
-    dev, B = cached.device, cached.shape[0]
-    _ints(cached, "cached", (B,), dev)
-    _ints(new_tokens, "new_tokens", (B,), dev)
     _tensor(block_table, "block_table")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
-    width = block_table.shape[1]
-    _ints(block_table, "block_table", (B, width), dev)
-    _ints(page_count, "page_count", (B,), dev)
     _tensor(free_pages, "free_pages")
-    capacity = free_pages.numel()
-    _ints(free_pages, "free_pages", (capacity,), dev)
-    _ints(free_count, "free_count", (1,), dev)
-    res = dict(out) if out is not None else {}
-    shapes = {"query_offsets": (B + 1,), "kv_len": (B,), "positions": (max_rows,),
-              "slots": (max_rows,), "page_count": (B,), "free_count": (1,), "status": (1,)}
-    for name in res:
-        if name not in shapes:
-            raise ValueError(f"unknown output {name!r}: one of {', '.join(shapes)}")
+    dev, B, width, capacity = cached.device, cached.shape[0], block_table.shape[1], free_pages.numel()
+    for t, name, shape in ((cached, "cached", (B,)), (new_tokens, "new_tokens", (B,)),
+                           (block_table, "block_table", (B, width)), (page_count, "page_count", (B,)),
+                           (free_pages, "free_pages", (capacity,)), (free_count, "free_count", (1,))):
+        if not _is(t, _I32, shape, dev):
+            _ints(t, name, shape, dev)
     if max_rows < 0:
         raise ValueError("max_rows must be >= 0")
-    missing = [n for n in shapes if n not in res]
-    for name in res:
-        _ints(res[name], f"out[{name!r}]", shapes[name], dev)
-    if missing:
+    if out is None:
         # one allocation for all of them, each at a 16-byte boundary
-        sizes = [math.prod(shapes[n]) for n in missing]
-        flat = torch.empty(sum((s + 3) & ~3 for s in sizes), dtype=torch.int32, device=dev)
-        at = 0
-        for name, s in zip(missing, sizes):
-            res[name] = flat[at:at + s]
-            at += (s + 3) & ~3
-    with _on(dev):
-        _abi.check("spec_slots", L.spec_slots(
-            cached.data_ptr(), new_tokens.data_ptr(), B, width, page_size, block_table.data_ptr(),
-            page_count.data_ptr(), free_pages.data_ptr(), capacity, free_count.data_ptr(), max_rows,
-            res["query_offsets"].data_ptr(), res["kv_len"].data_ptr(), res["positions"].data_ptr(),
-            res["slots"].data_ptr(), res["page_count"].data_ptr(), res["free_count"].data_ptr(),
-            res["status"].data_ptr(), _stream(dev)))
+        b1, b, r = (B + 4) & ~3, (B + 3) & ~3, (max_rows + 3) & ~3
+        parts = torch.empty(b1 + 2 * b + 2 * r + 8, dtype=_I32, device=dev).split_with_sizes(
+            (B + 1, b1 - B - 1, B, b - B, max_rows, r - max_rows, max_rows, r - max_rows, B, b - B, 1, 3, 1, 3))
+        res = {"query_offsets": parts[0], "kv_len": parts[2], "positions": parts[4], "slots": parts[6],
+               "page_count": parts[8], "free_count": parts[10], "status": parts[12]}
+    else:
+        res = dict(out)
+        shapes = {"query_offsets": (B + 1,), "kv_len": (B,), "positions": (max_rows,),
+                  "slots": (max_rows,), "page_count": (B,), "free_count": (1,), "status": (1,)}
+        for name in res:
+            if name not in shapes:
+                raise ValueError(f"unknown output {name!r}: one of {', '.join(shapes)}")
+        for name, shape in shapes.items():
+            if name not in res:
+                res[name] = torch.empty(shape, dtype=_I32, device=dev)
+            elif not _is(res[name], _I32, shape, dev):
+                _ints(res[name], f"out[{name!r}]", shape, dev)
+    _call("spec_slots", L.spec_slots, dev, cached.data_ptr(), new_tokens.data_ptr(), B, width, page_size,
+          block_table.data_ptr(), page_count.data_ptr(), free_pages.data_ptr(), capacity,
+          free_count.data_ptr(), max_rows, res["query_offsets"].data_ptr(), res["kv_len"].data_ptr(),
+          res["positions"].data_ptr(), res["slots"].data_ptr(), res["page_count"].data_ptr(),
+          res["free_count"].data_ptr(), res["status"].data_ptr())
     return res
 
 
-def _heads(t: torch.Tensor, name: str, rows, dtype, device):
-    """[rows, heads, D] with unit stride along D: (row stride, head stride)."""
-    _tensor(t, name)
-    if t.device != device or t.dim() != 3 or t.shape[0] != rows:
-        raise ValueError(f"{name} must be [{rows}, heads, D] on {device}")
-    if t.dtype != dtype:
+def _heads(t, name: str, rows, dim, dtype, device):
+    """[rows, heads, D] with unit stride along D: (heads, row stride, head stride)."""
+    if not (isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device and t.dim() == 3):
+        _tensor(t, name)
+        if t.device != device or t.dim() != 3:
+            raise ValueError(f"{name} must be [{rows}, heads, {dim}] on {device}")
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    n, heads, d = t.shape
     row, head, one = t.stride()
-    if t.shape[2] != 1 and one != 1:
-        raise ValueError(f"{name} must have unit stride along D")
-    # the stride of an axis of one entry says nothing
-    return (row if t.shape[0] > 1 else 0), (head if t.shape[1] > 1 else t.shape[2])
+    if n != rows or d != dim or one != 1:
+        raise ValueError(f"{name} must be [{rows}, heads, {dim}] with unit stride along D")
+    # (the stride of an axis of one entry says nothing)
+    return heads, (row if n > 1 else 0), (head if heads > 1 else d)
 
 
 def _cache(k_cache, v_cache, k_scale, v_scale, heads: int, dim: int, dtype, device):
-    """Checked cache arguments: (pages, page_size, strides, k_scale, v_scale pointers)."""
+    """Checked cache arguments: pages, page_size, strides."""
+    want = dtype if k_scale is None else _U8
     for name, t in (("k_cache", k_cache), ("v_cache", v_cache)):
-        _tensor(t, name)
-        if t.device != device or t.dim() != 4 or t.shape[2:] != (heads, dim):
-            raise ValueError(f"{name} must be [pages, page_size, {heads}, {dim}] on {device}")
-        want = dtype if k_scale is None else torch.uint8
-        if t.dtype != want:
+        if not (isinstance(t, torch.Tensor) and t.dtype is want and t.device == device and t.dim() == 4):
+            _tensor(t, name)
+            if t.device != device or t.dim() != 4:
+                raise ValueError(f"{name} must be [pages, page_size, {heads}, {dim}] on {device}")
             raise TypeError(f"{name} must be {want}, got {t.dtype}")
-        if t.stride(3) != 1:
-            raise ValueError(f"{name} must have unit stride along D")
-    if v_cache.shape != k_cache.shape:
+    shape, stride = k_cache.shape, k_cache.stride()
+    pages, page, h, d = shape
+    if h != heads or d != dim or stride[3] != 1:
+        raise ValueError(f"k_cache must be [pages, page_size, {heads}, {dim}] with unit stride along D")
+    if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape")
-    pages, page = k_cache.shape[:2]
-    # (the stride of an axis of one entry says nothing: the tightest place is as good)
-    stride = [s for s in k_cache.stride()[:3]]
-    for i, n in enumerate(k_cache.shape[:3]):
-        if n == 1:
-            stride[i] = 0
-        elif v_cache.stride(i) != stride[i]:
-            raise ValueError("k_cache and v_cache must have the same strides")
+    if 1 in shape:   # the stride of an axis of one entry says nothing
+        stride = tuple(0 if n == 1 else s for n, s in zip(shape, stride))
+        same = stride == tuple(0 if n == 1 else s for n, s in zip(shape, v_cache.stride()))
+    else:
+        same = stride == v_cache.stride()
+    if not same:
+        raise ValueError("k_cache and v_cache must have the same strides")
     if (k_scale is None) != (v_scale is None):
         raise ValueError("k_scale and v_scale must both be given or both be None")
     if k_scale is not None:
-        _tensor(k_scale, "k_scale")
-        _tensor(v_scale, "v_scale")
-        _need(k_scale, "k_scale", (heads,), torch.float32, device)
-        _need(v_scale, "v_scale", (heads,), torch.float32, device)
-    return pages, page, stride
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if not _is(t, _F32, (heads,), device):
+                _tensor(t, name)
+                _need(t, name, (heads,), _F32, device)
+    return pages, page, stride[0], stride[1], stride[2]
 
 
 def dspark_qk_norm_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: Optional[torch.Tensor],
@@ -154,53 +172,56 @@ def dspark_qk_norm_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: Optional[
     _tensor(k, "k")
     if not k.is_cuda or k.dim() != 3:
         raise ValueError("k must be a device tensor [N, Hkv, D]")
-    dev, dt = k.device, _dtype(k, "k")
-    n, hkv, d = k.shape
-    kr, kh = _heads(k, "k", n, k.dtype, dev)
+    dev, dtype = k.device, k.dtype
+    dt = _dtype(k, "k")
+    n, _, d = k.shape
+    hkv, kr, kh = _heads(k, "k", n, d, dtype, dev)
     hq = qr = qh = vr = vh = 0
+    qp = qo = vp = ko = sp = kc = vc = None
     if q is not None:
-        qr, qh = _heads(q, "q", n, k.dtype, dev)
-        hq = q.shape[1]
-        if q.shape[2] != d:
-            raise ValueError(f"q must be [{n}, Hq, {d}]")
+        hq, qr, qh = _heads(q, "q", n, d, dtype, dev)
+        qp = q.data_ptr()
         if q_out is None:
-            q_out = torch.empty((n, hq, d), dtype=k.dtype, device=dev)
-        else:
+            q_out = torch.empty((n, hq, d), dtype=dtype, device=dev)
+        elif not _is(q_out, dtype, (n, hq, d), dev):
             _tensor(q_out, "q_out")
-            _need(q_out, "q_out", (n, hq, d), k.dtype, dev)
+            _need(q_out, "q_out", (n, hq, d), dtype, dev)
+        qo = q_out.data_ptr()
     elif q_out is not None:
         raise ValueError("q_out is given without q")
-    _ints(positions, "positions", (n,), dev)
+    if not _is(positions, _I32, (n,), dev):
+        _ints(positions, "positions", (n,), dev)
     _tensor(inv_freq, "inv_freq")
     half = inv_freq.numel()
-    _need(inv_freq, "inv_freq", (half,), torch.float32, dev)
+    if not _is(inv_freq, _F32, (half,), dev):
+        _need(inv_freq, "inv_freq", (half,), _F32, dev)
     for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
-        if w is not None:
+        if w is not None and not _is(w, dtype, (d,), dev):
             _tensor(w, name)
-            _need(w, name, (d,), k.dtype, dev)
-    pages = page = 1
-    strides = (0, 0, 0)
+            _need(w, name, (d,), dtype, dev)
+    cache = (1, 1, 0, 0, 0)
     if k_cache is not None or v_cache is not None:
         if v is None or slots is None:
             raise ValueError("v and slots are needed with a cache")
-        vr, vh = _heads(v, "v", n, k.dtype, dev)
-        if v.shape != k.shape:
+        hv, vr, vh = _heads(v, "v", n, d, dtype, dev)
+        if hv != hkv:
             raise ValueError(f"v must be [{n}, {hkv}, {d}]")
-        pages, page, strides = _cache(k_cache, v_cache, k_scale, v_scale, hkv, d, k.dtype, dev)
-        _ints(slots, "slots", (n,), dev)
+        cache = _cache(k_cache, v_cache, k_scale, v_scale, hkv, d, dtype, dev)
+        if not _is(slots, _I32, (n,), dev):
+            _ints(slots, "slots", (n,), dev)
+        vp, sp, kc, vc = v.data_ptr(), slots.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
     elif k_scale is not None or v_scale is not None:
         raise ValueError("scales are given without a cache")
     elif k_out is None:
-        k_out = torch.empty((n, hkv, d), dtype=k.dtype, device=dev)
+        k_out = torch.empty((n, hkv, d), dtype=dtype, device=dev)
     if k_out is not None:
-        _tensor(k_out, "k_out")
-        _need(k_out, "k_out", (n, hkv, d), k.dtype, dev)
-    with _on(dev):
-        _abi.check("dspark_qk_norm_rope", L.dspark_qk_norm_rope(
-            _ptr(q), qr, qh, k.data_ptr(), kr, kh, _ptr(v), vr, vh, n, hq, hkv, d, dt,
-            positions.data_ptr(), inv_freq.data_ptr(), 2 * half, int(interleaved), _ptr(q_weight),
-            _ptr(k_weight), eps, _ptr(q_out), _ptr(k_out), _ptr(slots), _ptr(k_cache),
-            _ptr(v_cache), pages, page, *strides, _ptr(k_scale), _ptr(v_scale), _stream(dev)))
+        if not _is(k_out, dtype, (n, hkv, d), dev):
+            _tensor(k_out, "k_out")
+            _need(k_out, "k_out", (n, hkv, d), dtype, dev)
+        ko = k_out.data_ptr()
+    _call("dspark_qk_norm_rope", L.dspark_qk_norm_rope, dev, qp, qr, qh, k.data_ptr(), kr, kh, vp, vr, vh,
+          n, hq, hkv, d, dt, positions.data_ptr(), inv_freq.data_ptr(), 2 * half, interleaved,
+          _ptr(q_weight), _ptr(k_weight), eps, qo, ko, sp, kc, vc, *cache, _ptr(k_scale), _ptr(v_scale))
     return q_out, k_out
 
 
@@ -224,33 +245,33 @@ def dflash_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     _tensor(q, "q")
     if not q.is_cuda or q.dim() != 3:
         raise ValueError("q must be a device tensor [N, Hq, D]")
-    dev, dt = q.device, _dtype(q, "q")
-    n, hq, d = q.shape
-    qr, qh = _heads(q, "q", n, q.dtype, dev)
+    dev, dtype = q.device, q.dtype
+    dt = _dtype(q, "q")
+    n, _, d = q.shape
+    hq, qr, qh = _heads(q, "q", n, d, dtype, dev)
     _tensor(k_cache, "k_cache")
     if k_cache.dim() != 4:
         raise ValueError("k_cache must be [pages, page_size, Hkv, D]")
     hkv = k_cache.shape[2]
-    pages, page, strides = _cache(k_cache, v_cache, k_scale, v_scale, hkv, d, q.dtype, dev)
+    cache = _cache(k_cache, v_cache, k_scale, v_scale, hkv, d, dtype, dev)
     _tensor(block_table, "block_table")
     if block_table.dim() != 2:
         raise ValueError("block_table must be [B, max_pages]")
     b, width = block_table.shape
-    _ints(block_table, "block_table", (b, width), dev)
-    _ints(query_offsets, "query_offsets", (b + 1,), dev)
-    _ints(kv_len, "kv_len", (b,), dev)
+    for t, name, shape in ((block_table, "block_table", (b, width)),
+                           (query_offsets, "query_offsets", (b + 1,)), (kv_len, "kv_len", (b,))):
+        if not _is(t, _I32, shape, dev):
+            _ints(t, name, shape, dev)
     if out is None:
-        out = torch.empty((n, hq, d), dtype=q.dtype, device=dev)
-    else:
+        out = torch.empty((n, hq, d), dtype=dtype, device=dev)
+    elif not _is(out, dtype, (n, hq, d), dev):
         _tensor(out, "out")
-        _need(out, "out", (n, hq, d), q.dtype, dev)
-    sums = torch.empty((n, hq), dtype=torch.float32, device=dev) if lse else None
-    need = L.dflash_paged_attention_workspace_bytes(n, hq, hkv, d, dt, b, width, page)
+        _need(out, "out", (n, hq, d), dtype, dev)
+    sums = torch.empty((n, hq), dtype=_F32, device=dev) if lse else None
+    need = L.dflash_paged_attention_workspace_bytes(n, hq, hkv, d, dt, b, width, cache[1])
     wp, wn, _keep = _space(need, dev, workspace)
-    with _on(dev):
-        _abi.check("dflash_paged_attention", L.dflash_paged_attention(
-            q.data_ptr(), qr, qh, n, hq, hkv, d, dt, k_cache.data_ptr(), v_cache.data_ptr(), pages,
-            page, *strides, _ptr(k_scale), _ptr(v_scale), block_table.data_ptr(), b, width,
-            query_offsets.data_ptr(), kv_len.data_ptr(), d ** -0.5 if scale is None else scale,
-            int(causal), window, out.data_ptr(), _ptr(sums), wp, wn, _stream(dev)))
+    _call("dflash_paged_attention", L.dflash_paged_attention, dev, q.data_ptr(), qr, qh, n, hq, hkv, d, dt,
+          k_cache.data_ptr(), v_cache.data_ptr(), *cache, _ptr(k_scale), _ptr(v_scale),
+          block_table.data_ptr(), b, width, query_offsets.data_ptr(), kv_len.data_ptr(),
+          d ** -0.5 if scale is None else scale, causal, window, out.data_ptr(), _ptr(sums), wp, wn)
     return (out, sums) if lse else out
