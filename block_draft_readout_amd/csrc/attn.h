@@ -171,7 +171,7 @@ struct AttnTall : AttnMany<C_, S_, D_, 8, 1, KT_> {
 // Few rows: WN waves hold the same RT x 16 rows and walk key tiles of their own, each through
 // LDS of its own, joined at the end.  Tiles come straight from the cache to LDS as they are
 // stored there.
-template <typename C_, typename S_, int D_, int RT_>
+template <typename C_, typename S_, int D_, int RT_, int WN_>
 struct AttnFew {
   using C = C_;
   using S = S_;
@@ -180,7 +180,7 @@ struct AttnFew {
   static constexpr int CS = static_cast<int>(sizeof(C)), ES = static_cast<int>(sizeof(S));
   static constexpr int ROWB = D * CS;                    // bytes of an LDS row
   static constexpr int KT = CS == 1 ? 64 : 32;
-  static constexpr int WN = 4;
+  static constexpr int WN = WN_;
   static constexpr int THREADS = 64 * WN;
   static constexpr int BM = 16 * RT;
   static constexpr int CPR = ROWB / 16;                  // 16-byte chunks of a row
@@ -191,9 +191,10 @@ struct AttnFew {
   // Queries stay in LDS where two waves of a SIMD have no registers for them.
   static constexpr bool QLDS = D == 128 && RT >= 3;
   static constexpr int Q_AT = WAVE_BYTES * WN;
-  static constexpr int LDS_BYTES = Q_AT + (QLDS ? BM * D * ES : 0);
+  static constexpr int PAGE_AT = Q_AT + (QLDS ? BM * D * ES : 0);   // page ids of a tile, 256 bytes a wave
+  static constexpr int LDS_BYTES = PAGE_AT + 256 * WN;
   static constexpr int QN = D * ES / 64;                 // 16-byte query pieces of a lane and row
-  static constexpr int SIMD_WAVES = LDS_BYTES <= 80 * 1024 ? 2 : 1;
+  static constexpr int SIMD_WAVES = WN == 8 || (LDS_BYTES <= 80 * 1024 && D * RT <= (CS == 1 ? 256 : 384)) ? 2 : 1;
   static_assert(CPR <= 64 && KT % RPL == 0, "a load is whole rows");
   static_assert(16 * D * 4 + 128 <= WAVE_BYTES, "a wave's output and statistics fit its tiles' place");
   static_assert(LDS_BYTES <= 160 * 1024, "tiles fit");
@@ -257,12 +258,20 @@ struct AttnLoader {
   using S = typename T::S;
   using C = typename T::C;
 
-  static __device__ __forceinline__ AttnPage page_of(const AttnArgs& g, const int32_t* table, int key0, int lo,
-                                                     int hi, int lane) {
+  // column of the table and place in the page
+  static __device__ __forceinline__ uint32_t column_of(const AttnArgs& g, int key0, int lo, int hi, int lane,
+                                                       int32_t& place) {
     const int key = key0 + (T::KT == 64 ? lane : lane & 31);
     const int at = max(min(max(key, lo), hi - 1), 0);   // (a key of the table, whatever lo and hi)
     const uint32_t col = __umulhi(2u * at, g.page_magic) >> g.page_shift;
-    return AttnPage{table[col], key == at && key < hi ? static_cast<int32_t>(at - col * g.p.page) : -1};
+    place = key == at && key < hi ? static_cast<int32_t>(at - col * g.p.page) : -1;
+    return col;
+  }
+  static __device__ __forceinline__ AttnPage page_of(const AttnArgs& g, const int32_t* table, int key0, int lo,
+                                                     int hi, int lane) {
+    AttnPage a;
+    a.id = table[column_of(g, key0, lo, hi, lane, a.place)];
+    return a;
   }
   // its bytes from the head's first, 0 and false where it is not read
   static __device__ __forceinline__ uint64_t offset_of(const AttnProblem& p, AttnPage a, bool& in) {
@@ -893,6 +902,51 @@ struct AttnTallBody : AttnManyBody<T> {
 };
 
 // -------------------------------------------------------------- few rows
+// 32-bit LDS address
+__device__ __forceinline__ uint32_t lds_offset(const char* p) {
+  return static_cast<uint32_t>(reinterpret_cast<uintptr_t>((__attribute__((address_space(3))) const char*)p));
+}
+
+// Transposing reads of four operands at LDS addresses a[i] + O0, a[i] + O1 (four 16-bit values of
+// column lane % 16 from 4 rows x 16 columns each).  With its own wait: the compiler takes the
+// intrinsic for a possible write to LDS and waits for the copies in flight before it.
+template <int O0, int O1>
+__device__ __forceinline__ void read_tr4(const uint32_t (&a)[4], bf16x8_t (&v)[4]) {
+  i16x4_t l[4], h[4];
+  asm volatile(
+      "ds_read_b64_tr_b16 %0, %8 offset:%c12\n\t"
+      "ds_read_b64_tr_b16 %1, %8 offset:%c13\n\t"
+      "ds_read_b64_tr_b16 %2, %9 offset:%c12\n\t"
+      "ds_read_b64_tr_b16 %3, %9 offset:%c13\n\t"
+      "ds_read_b64_tr_b16 %4, %10 offset:%c12\n\t"
+      "ds_read_b64_tr_b16 %5, %10 offset:%c13\n\t"
+      "ds_read_b64_tr_b16 %6, %11 offset:%c12\n\t"
+      "ds_read_b64_tr_b16 %7, %11 offset:%c13\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(l[0]), "=&v"(h[0]), "=&v"(l[1]), "=&v"(h[1]), "=&v"(l[2]), "=&v"(h[2]), "=&v"(l[3]), "=&v"(h[3])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0), "n"(O1)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = join_tr(l[i], h[i]);
+}
+// the same of e4m3: 8 codes of a column from 8 rows x 16 columns, widened
+template <int O0>
+__device__ __forceinline__ void read_tr4_codes(const uint32_t (&a)[4], bf16x8_t (&v)[4]) {
+  typedef uint32_t u32x2_t __attribute__((ext_vector_type(2)));
+  u32x2_t x[4];
+  asm volatile(
+      "ds_read_b64_tr_b8 %0, %4 offset:%c8\n\t"
+      "ds_read_b64_tr_b8 %1, %5 offset:%c8\n\t"
+      "ds_read_b64_tr_b8 %2, %6 offset:%c8\n\t"
+      "ds_read_b64_tr_b8 %3, %7 offset:%c8\n\t"
+      "s_waitcnt lgkmcnt(0)"
+      : "=&v"(x[0]), "=&v"(x[1]), "=&v"(x[2]), "=&v"(x[3])
+      : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0)
+      : "memory");
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = widen8(x[i].x, x[i].y);
+}
+
 static __device__ const uint32_t kZeros16[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
 
 // 16 bytes per lane, cache -> LDS: lane l's land at dst + 16 l (dst uniform).  Non-temporal: few
@@ -908,41 +962,65 @@ struct AttnFewBody : AttnLoader<T> {
   using S = typename T::S;
   using C = typename T::C;
 
-  // A tile of keys and values on its way to LDS.  Where all its keys are read and the rows of a
-  // load lie in one page, the page is the load's own scalar; else every lane looks its row up,
-  // and keys that are not read come from zeros.
-  static __device__ __forceinline__ void load(const AttnProblem& p, const char* kb, const char* vb, AttnPage a,
-                                              int lane, char* lk, char* lv) {
-    constexpr uint64_t kAll = T::KT == 64 ? ~0ull : 0xFFFFFFFFull;
+  // Where a tile's keys lie: from page ids that have arrived.
+  struct Way {
+    uint32_t lo, hi;   // this lane's key's bytes from the head's first
+    uint64_t live;     // bit t: key t of the tile is read (others come from zeros)
+  };
+  static constexpr uint64_t kAll = T::KT == 64 ? ~0ull : 0xFFFFFFFFull;
+  static __device__ __forceinline__ Way way(const AttnProblem& p, AttnPage a) {
     bool in;
     const uint64_t off = L::offset_of(p, a, in);
-    const uint64_t live = __ballot(in) & kAll;
-    const int lo = static_cast<int>(off), hi = static_cast<int>(off >> 32);
+    return Way{static_cast<uint32_t>(off), static_cast<uint32_t>(off >> 32), __ballot(in) & kAll};
+  }
+
+  // Page ids of a tile to come, through LDS: a register would make the compiler wait for all loads
+  // in flight, the last tile's values among them, where it is used.
+  static __device__ __forceinline__ int32_t ask(const AttnArgs& g, const int32_t* table, int key0, int lo, int hi,
+                                                int lane, char* ids) {
+    int32_t place;
+    const int32_t* at = table + L::column_of(g, key0, lo, hi, lane, place);
+    __builtin_amdgcn_global_load_lds((const __attribute__((address_space(1))) void*)at,
+                                     (__attribute__((address_space(3))) void*)ids, 4, 0, 0);
+    return place;
+  }
+  static __device__ __forceinline__ AttnPage asked(const char* ids, int lane, int32_t place) {
+    return AttnPage{*reinterpret_cast<const int32_t*>(ids + 4 * lane), place};
+  }
+
+  // A tile of keys or values on its way to LDS, LOADS loads.  Where all its keys are read and the
+  // rows of a load lie in one page, the offset is the load's own scalar; else every lane takes its
+  // row's, and keys that are not read come from zeros.  (turn: of a row's chunks in LDS.)
+  template <typename Turn>
+  static __device__ __forceinline__ void load(const AttnProblem& p, const char* base, const Way& w, int lane,
+                                              char* to, Turn turn) {
     asm volatile("" : "+v"(lane));   // (offsets are made anew: held over the loop they take 4 LOADS registers)
     const uint32_t sub = lane / T::CPR, pos = lane % T::CPR;
-    // the turns of rows RPL i and sub are of different bits
-    const uint32_t kc = (pos ^ key_turn<T::ROWB>(sub)) << 4, vc = (pos ^ value_turn<T>(sub)) << 4;
-    if (live == kAll && L::whole_loads(p)) {
+    const uint32_t c = (pos ^ turn(sub)) << 4;   // (the turns of rows RPL i and sub are of different bits)
+    if (w.live == kAll && L::whole_loads(p)) {
       const uint32_t mine = sub * p.token_bytes;
 #pragma unroll
       for (int i = 0; i < T::LOADS; ++i) {
-        const uint32_t l = __builtin_amdgcn_readlane(lo, T::RPL * i), h = __builtin_amdgcn_readlane(hi, T::RPL * i);
+        const uint32_t l = __builtin_amdgcn_readlane(w.lo, T::RPL * i), h = __builtin_amdgcn_readlane(w.hi, T::RPL * i);
         const uint64_t at = (static_cast<uint64_t>(h) << 32) | l;
-        copy_lds16(kb + at + (mine + (kc ^ (key_turn<T::ROWB>(T::RPL * i) << 4))), lk + 1024 * i);
-        copy_lds16(vb + at + (mine + (vc ^ (value_turn<T>(T::RPL * i) << 4))), lv + 1024 * i);
+        copy_lds16(base + at + (mine + (c ^ (turn(T::RPL * i) << 4))), to + 1024 * i);
       }
     } else {
 #pragma unroll 1
       for (int i = 0; i < T::LOADS; ++i) {
         const uint32_t row = T::RPL * i + sub;
-        const uint32_t l = __shfl(lo, row), h = __shfl(hi, row);
+        const uint32_t l = __shfl(static_cast<int>(w.lo), row), h = __shfl(static_cast<int>(w.hi), row);
         const uint64_t at = (static_cast<uint64_t>(h) << 32) | l;
-        const bool read = (live >> row) & 1;
         const char* zero = reinterpret_cast<const char*>(kZeros16);
-        copy_lds16(read ? kb + at + (kc ^ (key_turn<T::ROWB>(T::RPL * i) << 4)) : zero, lk + 1024 * i);
-        copy_lds16(read ? vb + at + (vc ^ (value_turn<T>(T::RPL * i) << 4)) : zero, lv + 1024 * i);
+        copy_lds16((w.live >> row) & 1 ? base + at + (c ^ (turn(T::RPL * i) << 4)) : zero, to + 1024 * i);
       }
     }
+  }
+  static __device__ __forceinline__ void load_keys(const AttnProblem& p, const char* kb, const Way& w, int lane, char* lk) {
+    load(p, kb, w, lane, lk, [](uint32_t r) { return key_turn<T::ROWB>(r); });
+  }
+  static __device__ __forceinline__ void load_values(const AttnProblem& p, const char* vb, const Way& w, int lane, char* lv) {
+    load(p, vb, w, lane, lv, [](uint32_t r) { return value_turn<T>(r); });
   }
 
   // first feature of query piece i of lane group grp: as the keys' operand takes them
@@ -1016,26 +1094,30 @@ struct AttnFewBody : AttnLoader<T> {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           b[rt][e] = pack_bf16(pr[rt][2 * e], pr[rt][2 * e + 1]);
+      // 8 bytes of row `row` (and of 16 rows on) per lane; the turns of the chunks 2 i (i, e4m3) and
+      // of the lane's own are of different bits
+      const uint32_t e = (lane & 15) >> 1;
+      const uint32_t row = T::CS == 2 ? 4 * grp + ((lane & 15) >> 2) : 4 * grp + (e & 3) + 4 * (e & 4);
+      const uint32_t at = lds_offset(lv) + value_place<T>(row, T::CS == 2 ? (lane >> 1) & 1 : 0) + (lane & 1) * 8;
 #pragma unroll
-      for (int i = 0; i < T::D / 16; ++i) {
-        bf16x8_t a;
+      for (int i0 = 0; i0 < T::D / 16; i0 += 4) {
+        uint32_t ad[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) ad[i] = at ^ ((i0 + i) * 16 * T::CS);
+        bf16x8_t a[4];
         if constexpr (T::CS == 2) {
-          const uint32_t row = 32 * sub + 4 * grp + ((lane & 15) >> 2);
-          const uint32_t c = 2 * i + ((lane >> 1) & 1);
-          a = join_tr(read_tr(lv + value_place<T>(row, c) + (lane & 1) * 8),
-                      read_tr(lv + value_place<T>(row + 16, c) + (lane & 1) * 8));
+          if (sub == 0) read_tr4<0, 16 * T::ROWB>(ad, a);
+          else read_tr4<32 * T::ROWB, 48 * T::ROWB>(ad, a);
         } else {
-          // 8 rows x 16 codes of a group of 16 lanes, 8 bytes each; a lane gets a column of it
-          const uint32_t e = (lane & 15) >> 1;
-          const uint32_t row = 32 * sub + 4 * grp + (e & 3) + 4 * (e & 4);
-          typedef int i32x2_t __attribute__((ext_vector_type(2)));
-          typedef __attribute__((address_space(3))) i32x2_t* lds_t;
-          const i32x2_t x = __builtin_amdgcn_ds_read_tr8_b64_v2i32((lds_t)(lv + value_place<T>(row, i) + (lane & 1) * 8));
-          a = widen8(x.x, x.y);
+          if (sub == 0) read_tr4_codes<0>(ad, a);
+          else read_tr4_codes<32 * T::ROWB>(ad, a);
         }
 #pragma unroll
-        for (int rt = 0; rt < T::RT; ++rt)
-          o[rt][i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, __builtin_bit_cast(bf16x8_t, b[rt]), o[rt][i], 0, 0, 0);
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+          for (int rt = 0; rt < T::RT; ++rt)
+            o[rt][i0 + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], __builtin_bit_cast(bf16x8_t, b[rt]),
+                                                                     o[rt][i0 + i], 0, 0, 0);
       }
     } else {
 #pragma unroll
@@ -1073,12 +1155,17 @@ struct AttnFewBody : AttnLoader<T> {
     const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_bytes;
     char* const lk = lds + wn * T::WAVE_BYTES;
     char* const lv = lk + T::TILE_BYTES;
-    AttnPage page{};
+    // A tile's loads: its keys', the page ids of the tile after it, its values'.  They return in
+    // that order, so what is in flight tells what has arrived.
     int t = ta + wn;
+    Way w{};
+    char* const ids = lds + T::PAGE_AT + 256 * wn;
+    int32_t place = 0;
     if (t < tb) {
-      page = L::page_of(g, table, t * T::KT, lo, hi, lane);
-      load(p, kb, vb, page, lane, lk, lv);
-      page = L::page_of(g, table, (t + T::WN) * T::KT, lo, hi, lane);
+      w = way(p, L::page_of(g, table, t * T::KT, lo, hi, lane));
+      load_keys(p, kb, w, lane, lk);
+      place = ask(g, table, (t + T::WN) * T::KT, lo, hi, lane, ids);
+      load_values(p, vb, w, lane, lv);
     }
     u32x4_t q[T::RT][T::QLDS ? 1 : T::QN];
     int row_lo[T::RT], row_hi[T::RT];
@@ -1114,38 +1201,55 @@ struct AttnFewBody : AttnLoader<T> {
 
     if constexpr (T::QLDS) __syncthreads();   // the queries are in LDS
     for (; t < tb; t += T::WN) {
-      // the wave's own LDS: it waits for its own loads, and the next tile's are behind its reads
+      // The wave's own LDS: it waits for its own loads only.  Keys (and page ids) are there when the
+      // values' loads alone are in flight.
       asm volatile("" ::: "memory");
-      BDR_WAIT_VM(0);
+      BDR_WAIT_VM(T::LOADS);
       asm volatile("" ::: "memory");
       const int key0 = t * T::KT;
       const bool edge = key0 < see_lo || key0 + T::KT > see_hi;
+      const bool more = t + T::WN < tb;
+      float pr[T::KT / 32][T::RT][8];
 #pragma unroll
-      for (int u = 0; u < T::KT / 32; ++u) {
-        float pr[T::RT][8];
-        scores(lds, lk, u, lane, q, pr);
-#pragma unroll
-        for (int rt = 0; rt < T::RT; ++rt) {
-          const float was = mx[rt];
-          const float f = softmax_step<8>(
-              pr[rt], edge, row_lo[rt], row_hi[rt], scale2,
-              [&](int i) { return key0 + 32 * u + 16 * (i / 4) + 4 * (lane >> 4) + i % 4; },
-              [](float v) { return max_xor32(max_xor16(v)); }, mx[rt], l[rt]);
-          if (__any(mx[rt] > was)) {
-            asm volatile("");
-#pragma unroll
-            for (int i = 0; i < T::D / 16; ++i) o[rt][i] *= f;
-          }
-        }
-        add_values(lv, u, lane, pr, o);
-      }
-      // every read of the tile has returned before the next one overwrites it
+      for (int u = 0; u < T::KT / 32; ++u) scores(lds, lk, u, lane, q, pr[u]);
+      const AttnPage page = asked(ids, lane, place);
+      // every read of the keys and ids has returned: the next tile's take their place
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      if (t + T::WN < tb) {
-        load(p, kb, vb, page, lane, lk, lv);
-        page = L::page_of(g, table, (t + 2 * T::WN) * T::KT, lo, hi, lane);
+      if (more) {
+        w = way(p, page);
+        load_keys(p, kb, w, lane, lk);
+        place = ask(g, table, (t + 2 * T::WN) * T::KT, lo, hi, lane, ids);
       }
+#pragma unroll
+      for (int rt = 0; rt < T::RT; ++rt) {
+        float z[T::KT / 4];
+#pragma unroll
+        for (int i = 0; i < T::KT / 4; ++i) z[i] = pr[i / 8][rt][i % 8];
+        const float was = mx[rt];
+        const float f = softmax_step<T::KT / 4>(
+            z, edge, row_lo[rt], row_hi[rt], scale2,
+            [&](int i) { return key0 + 16 * (i / 4) + 4 * (lane >> 4) + i % 4; },
+            [](float v) { return max_xor32(max_xor16(v)); }, mx[rt], l[rt]);
+        if (__any(mx[rt] > was)) {
+          asm volatile("");
+#pragma unroll
+          for (int i = 0; i < T::D / 16; ++i) o[rt][i] *= f;
+        }
+#pragma unroll
+        for (int i = 0; i < T::KT / 4; ++i) pr[i / 8][rt][i % 8] = z[i];
+      }
+      // values: what is in flight behind them are the next keys and page ids
+      asm volatile("" ::: "memory");
+      if (more) BDR_WAIT_VM(T::LOADS + 1);
+      else BDR_WAIT_VM(0);
+      asm volatile("" ::: "memory");
+#pragma unroll
+      for (int u = 0; u < T::KT / 32; ++u) add_values(lv, u, lane, pr[u], o);
+      // every read of the values has returned
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      if (more) load_values(p, vb, w, lane, lv);
     }
 
     // join the waves' states through LDS, 16 rows at a time

@@ -29,7 +29,9 @@ Choice choose(const AttnProblem& p) {
   c.bm = c.few > 0 ? 16 * c.few : c.few == 0 ? 128 : 256;
   const int64_t longest = static_cast<int64_t>(p.width) * p.page;
   const int64_t tiles = (p.rows * p.group + c.bm - 1) / c.bm + p.batch;   // row tiles at most
-  c.whole = longest <= 256 && tiles * p.hkv <= kMaxGrid;
+  // one launch instead of two where a workgroup is through its keys in a few rounds of its waves
+  const int64_t at_once = c.few > 0 ? 128 * few_waves(p.fp8 ? 1 : p.dt == BDR_F32 ? 4 : 2, p.dim) : 256;
+  c.whole = longest <= at_once && tiles * p.hkv <= kMaxGrid;
   c.shares = c.whole ? tiles : std::max<int64_t>(1, (c.few < 0 ? 1 : 2) * kCus / p.hkv);
   c.min_share = 8;
   return c;

@@ -10,6 +10,11 @@ hipError_t launch_attn_bf16(const AttnArgs& g, int few, hipStream_t stream);
 hipError_t launch_attn_fp8(const AttnArgs& g, int few, hipStream_t stream);
 hipError_t launch_attn_f32(const AttnArgs& g, int few, hipStream_t stream);
 
+// waves of a few-row workgroup that takes whole row tiles: 16 KB of LDS each
+constexpr int few_waves(size_t cache_elem, int dim) {
+  return cache_elem == 1 ? (dim <= 128 ? 8 : 4) : cache_elem * dim <= 256 ? 8 : 4;
+}
+
 template <typename T>
 hipError_t run_attn(const AttnArgs& g, hipStream_t stream) {
   const uint32_t grid = static_cast<uint32_t>(g.shares * g.p.hkv);
@@ -24,14 +29,22 @@ hipError_t run_attn(const AttnArgs& g, hipStream_t stream) {
   return hipGetLastError();
 }
 
+// Few rows.  Where a row tile is one workgroup's, eight waves walk its keys if their tiles fit LDS.
+template <typename C, typename S, int D, int RT>
+hipError_t run_attn_few(const AttnArgs& g, hipStream_t stream) {
+  if constexpr (few_waves(sizeof(C), D) == 8)
+    if (g.whole) return run_attn<AttnFew<C, S, D, RT, 8>>(g, stream);
+  return run_attn<AttnFew<C, S, D, RT, 4>>(g, stream);
+}
+
 // the built variants of a head size
 template <typename C, typename S, int D, int KT, int FEW, bool TALL>
 hipError_t run_attn_dim(const AttnArgs& g, int few, hipStream_t stream) {
   switch (few) {
-    case 1: return run_attn<AttnFew<C, S, D, 1>>(g, stream);
-    case 2: return run_attn<AttnFew<C, S, D, 2>>(g, stream);
-    case 3: if constexpr (FEW >= 3) return run_attn<AttnFew<C, S, D, 3>>(g, stream); break;
-    case 4: if constexpr (FEW >= 4) return run_attn<AttnFew<C, S, D, 4>>(g, stream); break;
+    case 1: return run_attn_few<C, S, D, 1>(g, stream);
+    case 2: return run_attn_few<C, S, D, 2>(g, stream);
+    case 3: if constexpr (FEW >= 3) return run_attn_few<C, S, D, 3>(g, stream); break;
+    case 4: if constexpr (FEW >= 4) return run_attn_few<C, S, D, 4>(g, stream); break;
     case -1: if constexpr (TALL) return run_attn<AttnTall<C, S, D, KT>>(g, stream); break;
     default: return run_attn<AttnMany<C, S, D, 4, 1, KT>>(g, stream);
   }

@@ -75,12 +75,11 @@ def spec_slots(cached: torch.Tensor, new_tokens: torch.Tensor, block_table: torc
     if max_rows < 0:
         raise ValueError("max_rows must be >= 0")
     if out is None:
-        # one allocation for all of them, each at a 16-byte boundary
-        b1, b, r = (B + 4) & ~3, (B + 3) & ~3, (max_rows + 3) & ~3
-        parts = torch.empty(b1 + 2 * b + 2 * r + 8, dtype=_I32, device=dev).split_with_sizes(
-            (B + 1, b1 - B - 1, B, b - B, max_rows, r - max_rows, max_rows, r - max_rows, B, b - B, 1, 3, 1, 3))
-        res = {"query_offsets": parts[0], "kv_len": parts[2], "positions": parts[4], "slots": parts[6],
-               "page_count": parts[8], "free_count": parts[10], "status": parts[12]}
+        # one allocation for all of them
+        parts = torch.empty(3 * B + 2 * max_rows + 3, dtype=_I32, device=dev).split_with_sizes(
+            (B + 1, B, max_rows, max_rows, B, 1, 1))
+        res = dict(zip(("query_offsets", "kv_len", "positions", "slots", "page_count", "free_count", "status"),
+                       parts))
     else:
         res = dict(out)
         shapes = {"query_offsets": (B + 1,), "kv_len": (B,), "positions": (max_rows,),
