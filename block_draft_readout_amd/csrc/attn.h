@@ -187,17 +187,22 @@ struct AttnFew {
   static constexpr int RPL = 64 / CPR;                   // rows of a wave's load
   static constexpr int LOADS = KT / RPL;
   static constexpr int TILE_BYTES = KT * ROWB;
-  static constexpr int WAVE_BYTES = 2 * TILE_BYTES;      // (a wave's O of 16 rows, fp32, fits)
+  // Two waves of a SIMD cover each other's waits; where registers are for one, it has two tiles in
+  // LDS, and the next one's loads are in flight under a whole tile's work.
+  static constexpr bool kTwo = D * RT <= (CS == 1 ? 256 : 384);
+  static constexpr int BUFS = D == 128 && !kTwo && WN_ == 4 ? 2 : 1;
+  static constexpr int WAVE_BYTES = 2 * TILE_BYTES * BUFS;   // (a wave's O of 16 rows, fp32, fits)
   // Queries stay in LDS where two waves of a SIMD have no registers for them.
   static constexpr bool QLDS = D == 128 && RT >= 3;
   static constexpr int Q_AT = WAVE_BYTES * WN;
   static constexpr int PAGE_AT = Q_AT + (QLDS ? BM * D * ES : 0);   // page ids of a tile, 256 bytes a wave
   static constexpr int LDS_BYTES = PAGE_AT + 256 * WN;
   static constexpr int QN = D * ES / 64;                 // 16-byte query pieces of a lane and row
-  static constexpr int SIMD_WAVES = WN == 8 || (LDS_BYTES <= 80 * 1024 && D * RT <= (CS == 1 ? 256 : 384)) ? 2 : 1;
+  static constexpr int SIMD_WAVES = WN == 8 || (LDS_BYTES <= 80 * 1024 && kTwo) ? 2 : 1;
   static_assert(CPR <= 64 && KT % RPL == 0, "a load is whole rows");
   static_assert(16 * D * 4 + 128 <= WAVE_BYTES, "a wave's output and statistics fit its tiles' place");
   static_assert(LDS_BYTES <= 160 * 1024, "tiles fit");
+  static_assert(2 * LOADS + 1 < 64, "loads in flight can be counted");
 };
 
 // Places of the 16-byte chunks c of LDS row r: an XOR by the row, so that the lanes of one
@@ -1153,8 +1158,10 @@ struct AttnFewBody : AttnLoader<T> {
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
     const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_bytes;
     const char* vb = static_cast<const char*>(p.v_cache) + h * p.head_bytes;
-    char* const lk = lds + wn * T::WAVE_BYTES;
-    char* const lv = lk + T::TILE_BYTES;
+    char* const base = lds + wn * T::WAVE_BYTES;
+    char* lk = base;
+    char* lv = lk + T::TILE_BYTES;
+    char* other = base + 2 * T::TILE_BYTES;   // (two tiles)
     // A tile's loads: its keys', the page ids of the tile after it, its values'.  They return in
     // that order, so what is in flight tells what has arrived.
     int t = ta + wn;
@@ -1209,17 +1216,30 @@ struct AttnFewBody : AttnLoader<T> {
       const int key0 = t * T::KT;
       const bool edge = key0 < see_lo || key0 + T::KT > see_hi;
       const bool more = t + T::WN < tb;
+      if constexpr (T::BUFS == 2) {
+        const AttnPage page = asked(ids, lane, place);
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) {
+          w = way(p, page);
+          load_keys(p, kb, w, lane, other);
+          place = ask(g, table, (t + 2 * T::WN) * T::KT, lo, hi, lane, ids);
+          load_values(p, vb, w, lane, other + T::TILE_BYTES);
+        }
+      }
       float pr[T::KT / 32][T::RT][8];
 #pragma unroll
       for (int u = 0; u < T::KT / 32; ++u) scores(lds, lk, u, lane, q, pr[u]);
-      const AttnPage page = asked(ids, lane, place);
-      // every read of the keys and ids has returned: the next tile's take their place
-      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-      __builtin_amdgcn_sched_barrier(0);
-      if (more) {
-        w = way(p, page);
-        load_keys(p, kb, w, lane, lk);
-        place = ask(g, table, (t + 2 * T::WN) * T::KT, lo, hi, lane, ids);
+      if constexpr (T::BUFS == 1) {
+        const AttnPage page = asked(ids, lane, place);
+        // every read of the keys and ids has returned: the next tile's take their place
+        asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+        __builtin_amdgcn_sched_barrier(0);
+        if (more) {
+          w = way(p, page);
+          load_keys(p, kb, w, lane, lk);
+          place = ask(g, table, (t + 2 * T::WN) * T::KT, lo, hi, lane, ids);
+        }
       }
 #pragma unroll
       for (int rt = 0; rt < T::RT; ++rt) {
@@ -1239,9 +1259,9 @@ struct AttnFewBody : AttnLoader<T> {
 #pragma unroll
         for (int i = 0; i < T::KT / 4; ++i) pr[i / 8][rt][i % 8] = z[i];
       }
-      // values: what is in flight behind them are the next keys and page ids
+      // values: what is in flight behind them are the next keys and page ids (and values)
       asm volatile("" ::: "memory");
-      if (more) BDR_WAIT_VM(T::LOADS + 1);
+      if (more) BDR_WAIT_VM(T::LOADS * T::BUFS + 1);
       else BDR_WAIT_VM(0);
       asm volatile("" ::: "memory");
 #pragma unroll
@@ -1249,8 +1269,16 @@ struct AttnFewBody : AttnLoader<T> {
       // every read of the values has returned
       asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      if (more) load_values(p, vb, w, lane, lv);
+      if constexpr (T::BUFS == 1) {
+        if (more) load_values(p, vb, w, lane, lv);
+      } else {
+        char* const last = lk;
+        lk = other;
+        lv = other + T::TILE_BYTES;
+        other = last;
+      }
     }
+    lk = base;
 
     // join the waves' states through LDS, 16 rows at a time
     auto ml = [&](int w) { return reinterpret_cast<float2*>(lds + w * T::WAVE_BYTES + 16 * T::D * 4); };

@@ -32,7 +32,7 @@ Choice choose(const AttnProblem& p) {
   // one launch instead of two where a workgroup is through its keys in a few rounds of its waves
   const int64_t at_once = c.few > 0 ? 128 * few_waves(p.fp8 ? 1 : p.dt == BDR_F32 ? 4 : 2, p.dim) : 256;
   c.whole = longest <= at_once && tiles * p.hkv <= kMaxGrid;
-  c.shares = c.whole ? tiles : std::max<int64_t>(1, (c.few < 0 ? 1 : 2) * kCus / p.hkv);
+  c.shares = c.whole ? tiles : std::max<int64_t>(1, attn_per_cu(c.few, p.fp8 ? 1 : p.dt == BDR_F32 ? 4 : 2, p.dim) * kCus / p.hkv);
   c.min_share = 8;
   return c;
 }

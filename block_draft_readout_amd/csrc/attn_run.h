@@ -10,6 +10,13 @@ hipError_t launch_attn_bf16(const AttnArgs& g, int few, hipStream_t stream);
 hipError_t launch_attn_fp8(const AttnArgs& g, int few, hipStream_t stream);
 hipError_t launch_attn_f32(const AttnArgs& g, int few, hipStream_t stream);
 
+// Workgroups that a compute unit holds of a variant that shares row tiles (few as below).
+constexpr int attn_per_cu(int few, int cache_elem, int dim) {
+  if (few < 0) return 1;
+  if (few == 0) return cache_elem * dim <= 256 && dim <= 128 ? 2 : 1;
+  return dim * few <= (cache_elem == 1 ? 256 : 384) && cache_elem * dim <= 256 && dim <= 128 ? 2 : 1;
+}
+
 // waves of a few-row workgroup that takes whole row tiles: 16 KB of LDS each
 constexpr int few_waves(size_t cache_elem, int dim) {
   return cache_elem == 1 ? (dim <= 128 ? 8 : 4) : cache_elem * dim <= 256 ? 8 : 4;

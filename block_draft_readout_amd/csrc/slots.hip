@@ -6,11 +6,12 @@
 // with c_b < 0 is over and pushes its pages first.  Token positions and slots
 // follow from the prefix sums of n_b.
 //
-// A few numbers per request and token: latency bounds it, so one workgroup does
-// everything for up to kFillRows tokens (the prefix sums of 1024 requests at a
-// time, then the tokens' slots from the table that the workgroup has just
-// written), and only beyond that a second launch fills the tokens' slots with
-// the whole chip.
+// A few numbers per request and token: latency bounds it.  Up to 1024 requests
+// one workgroup holds one per thread: one prefix sum over all that is counted,
+// then pages and tokens find their request by bisection in LDS, and a token's
+// page is taken from the stack rather than from the table entry that another
+// thread is writing.  More requests go through in chunks of 1024.  More tokens
+// than kFillRows are filled by a second launch with the whole chip.
 
 #include <algorithm>
 
@@ -33,6 +34,7 @@ template <int NV>
 __device__ __forceinline__ void block_scan(int64_t (&v)[NV], int64_t (&total)[NV], int64_t* red) {
   const int lane = static_cast<int>(threadIdx.x) & 63;
   const int wave = static_cast<int>(threadIdx.x) >> 6;
+  const int waves = static_cast<int>(blockDim.x) >> 6;
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
 #pragma unroll
@@ -50,8 +52,7 @@ __device__ __forceinline__ void block_scan(int64_t (&v)[NV], int64_t (&total)[NV
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
     int64_t before = 0, all = 0;
-#pragma unroll
-    for (int w = 0; w < kPlanWaves; ++w) {
+    for (int w = 0; w < waves; ++w) {
       const int64_t s = red[i * kPlanWaves + w];
       if (w < wave) before += s;
       all += s;
@@ -188,6 +189,100 @@ __global__ __launch_bounds__(kPlanThreads) void slot_plan_kernel(const SlotArgs 
   }
 }
 
+// the last i in [0, n) with at[i] <= x (at ascending, at[0] <= x)
+template <typename I>
+__device__ __forceinline__ int bisect(const I* at, int n, I x) {
+  int lo = 0, hi = n;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if (at[mid] <= x) lo = mid; else hi = mid;
+  }
+  return lo;
+}
+
+// At most a request per thread.
+__global__ __launch_bounds__(kPlanThreads) void slot_plan_small_kernel(const SlotArgs g) {
+  const SlotProblem& p = g.p;
+  __shared__ int64_t red[3 * kPlanWaves];
+  __shared__ int32_t off_s[kPlanThreads], start_s[kPlanThreads], have_s[kPlanThreads], count_s[kPlanThreads];
+  __shared__ int64_t first_s[kPlanThreads], back_s[kPlanThreads];
+  __shared__ unsigned long long fine_s;
+  const int tid = static_cast<int>(threadIdx.x);
+  const int threads = static_cast<int>(blockDim.x);
+  const bool live = tid < p.batch;
+  const int32_t c = live ? p.cached[tid] : 0;
+  const int32_t held = live ? min(max(p.count[tid], 0), p.width) : 0;
+  const int32_t fresh = live ? max(p.fresh[tid], 0) : 0;
+  const int64_t top0 = min(max(*p.free_count, 0), p.capacity);
+  const bool over = c < 0;
+  const int32_t have = over ? 0 : held;
+  const int32_t n = over ? 0 : fresh;
+  const int64_t len = over ? 0 : static_cast<int64_t>(c) + n;
+  const int64_t need = min((len + p.page - 1) / p.page, static_cast<int64_t>(p.width));
+  const int64_t grow = max(need - have, static_cast<int64_t>(0));
+  if (tid == 0) fine_s = 0;
+  int64_t v[3] = {n, grow, over ? held : 0}, t[3];
+  block_scan(v, t, red);
+  const int64_t off = v[0] - n, first = v[1] - grow;
+  const int64_t top = min(top0 + t[2], static_cast<int64_t>(p.capacity));
+  const int32_t got = static_cast<int32_t>(min(max(top - first, static_cast<int64_t>(0)), grow));
+  if (live) {
+    off_s[tid] = clamp_i32(off);
+    start_s[tid] = c;
+    have_s[tid] = have;
+    count_s[tid] = have + got;
+    first_s[tid] = first;
+    back_s[tid] = v[2] - (over ? held : 0);
+    p.offsets[tid] = clamp_i32(off);
+    p.kv_len[tid] = clamp_i32(len);
+    p.count_out[tid] = have + got;
+    const int64_t covered =
+        min(max(static_cast<int64_t>(have + got) * p.page - max(c, 0), static_cast<int64_t>(0)), static_cast<int64_t>(n));
+    const int64_t fine = min(max(p.rows - off, static_cast<int64_t>(0)), covered);
+    if (fine > 0) atomicAdd(&fine_s, static_cast<unsigned long long>(fine));   // (whole numbers: any order)
+  }
+  __syncthreads();
+  if (tid == 0) {
+    p.offsets[p.batch] = clamp_i32(t[0]);
+    *p.free_out = static_cast<int32_t>(max(top - t[1], static_cast<int64_t>(0)));
+    *p.status = clamp_i32(t[0] - static_cast<int64_t>(fine_s));
+  }
+  if (t[2] > 0) {   // (uniform) page i of those that come back, in the order of the table: the last goes first
+    for (int64_t i = tid; i < t[2]; i += threads) {
+      const int b = bisect(back_s, p.batch, i);
+      const int64_t to = top0 + t[2] - 1 - i;
+      if (to < p.capacity) p.free_pages[to] = p.table[static_cast<int64_t>(b) * p.width + (i - back_s[b])];
+    }
+    __syncthreads();   // the stack is whole
+  }
+  const int64_t given = min(t[1], top);
+  for (int64_t i = tid; i < given; i += threads) {
+    const int32_t page = p.free_pages[top - 1 - i];
+    const int b = bisect(first_s, p.batch, i);
+    p.table[static_cast<int64_t>(b) * p.width + have_s[b] + (i - first_s[b])] = page;
+  }
+  if (!g.fill) return;
+  const int32_t total = clamp_i32(t[0]);
+#pragma unroll 2
+  for (int i = tid; i < p.rows; i += threads) {
+    int32_t pos = 0, slot = -1;
+    if (i < total) {
+      const int b = bisect(off_s, p.batch, i);
+      const int64_t at = static_cast<int64_t>(start_s[b]) + (i - off_s[b]);
+      const int64_t col = at / p.page;
+      pos = clamp_i32(at);
+      if (col < count_s[b]) {
+        const int32_t page = col < have_s[b] ? p.table[static_cast<int64_t>(b) * p.width + col]
+                                             : p.free_pages[top - 1 - first_s[b] - (col - have_s[b])];
+        const int64_t at_slot = static_cast<int64_t>(page) * p.page + (at - col * p.page);
+        if (at_slot >= 0 && at_slot < 0x7FFFFFFF) slot = static_cast<int32_t>(at_slot);
+      }
+    }
+    p.positions[i] = pos;
+    p.slots[i] = slot;
+  }
+}
+
 __global__ __launch_bounds__(256) void slot_fill_kernel(const SlotArgs g) {
   const int32_t i = static_cast<int32_t>(blockIdx.x * 256 + threadIdx.x);
   if (i < g.p.rows) fill_row(g.p, i, g.p.offsets[g.p.batch]);
@@ -197,7 +292,13 @@ constexpr int kFillRows = 4096;
 
 hipError_t launch_slots(const SlotProblem& p, hipStream_t stream) {
   const SlotArgs g{p, p.rows <= kFillRows};
-  hipLaunchKernelGGL(slot_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, g);
+  if (p.batch <= kPlanThreads) {
+    // (few waves pass their barriers sooner)
+    const int threads = p.batch <= 256 && p.rows <= 1024 ? 256 : kPlanThreads;
+    hipLaunchKernelGGL(slot_plan_small_kernel, dim3(1), dim3(threads), 0, stream, g);
+  } else {
+    hipLaunchKernelGGL(slot_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, g);
+  }
   if (!g.fill) {
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
