@@ -68,7 +68,7 @@ __device__ __forceinline__ int32_t clamp_i32(int64_t v) {
 
 // slot of position `pos` of a request with `count` pages, -1 where it has no page
 __device__ __forceinline__ int32_t slot_of(const int32_t* row, int32_t count, int64_t pos, int32_t page) {
-  const int64_t col = pos / page;
+  const int64_t col = static_cast<uint32_t>(pos) / static_cast<uint32_t>(page);   // (positions: below 2^32)
   if (col >= count) return -1;
   const int64_t s = static_cast<int64_t>(row[col]) * page + (pos - col * page);
   return s < 0 || s > 0x7FFFFFFE ? -1 : static_cast<int32_t>(s);
@@ -189,16 +189,21 @@ __global__ __launch_bounds__(kPlanThreads) void slot_plan_kernel(const SlotArgs 
   }
 }
 
-// the last i in [0, n) with at[i] <= x (at ascending, at[0] <= x)
+// the last i in [0, n) with at[i] <= x (kPlanThreads entries, the first n ascending, at[0] <= x);
+// always as many steps, so that several of them run together
 template <typename I>
 __device__ __forceinline__ int bisect(const I* at, int n, I x) {
-  int lo = 0, hi = n;
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) >> 1;
-    if (at[mid] <= x) lo = mid; else hi = mid;
+  int lo = 0;
+#pragma unroll
+  for (int step = kPlanThreads / 2; step > 0; step >>= 1) {
+    const int mid = lo + step;
+    const I v = at[mid];
+    lo = mid < n && v <= x ? mid : lo;
   }
   return lo;
 }
+
+constexpr int kTogether = 4;   // pages or tokens of a thread whose loads are in flight together
 
 // At most a request per thread.
 __global__ __launch_bounds__(kPlanThreads) void slot_plan_small_kernel(const SlotArgs g) {
@@ -218,7 +223,10 @@ __global__ __launch_bounds__(kPlanThreads) void slot_plan_small_kernel(const Slo
   const int32_t have = over ? 0 : held;
   const int32_t n = over ? 0 : fresh;
   const int64_t len = over ? 0 : static_cast<int64_t>(c) + n;
-  const int64_t need = min((len + p.page - 1) / p.page, static_cast<int64_t>(p.width));
+  // (len: below 2^32)
+  const int64_t need = len ? min(static_cast<int64_t>((static_cast<uint32_t>(len) - 1u) / static_cast<uint32_t>(p.page)) + 1,
+                                 static_cast<int64_t>(p.width))
+                           : 0;
   const int64_t grow = max(need - have, static_cast<int64_t>(0));
   if (tid == 0) fine_s = 0;
   int64_t v[3] = {n, grow, over ? held : 0}, t[3];
@@ -226,6 +234,7 @@ __global__ __launch_bounds__(kPlanThreads) void slot_plan_small_kernel(const Slo
   const int64_t off = v[0] - n, first = v[1] - grow;
   const int64_t top = min(top0 + t[2], static_cast<int64_t>(p.capacity));
   const int32_t got = static_cast<int32_t>(min(max(top - first, static_cast<int64_t>(0)), grow));
+  int64_t fine = 0;
   if (live) {
     off_s[tid] = clamp_i32(off);
     start_s[tid] = c;
@@ -238,9 +247,11 @@ __global__ __launch_bounds__(kPlanThreads) void slot_plan_small_kernel(const Slo
     p.count_out[tid] = have + got;
     const int64_t covered =
         min(max(static_cast<int64_t>(have + got) * p.page - max(c, 0), static_cast<int64_t>(0)), static_cast<int64_t>(n));
-    const int64_t fine = min(max(p.rows - off, static_cast<int64_t>(0)), covered);
-    if (fine > 0) atomicAdd(&fine_s, static_cast<unsigned long long>(fine));   // (whole numbers: any order)
+    fine = min(max(p.rows - off, static_cast<int64_t>(0)), covered);
   }
+#pragma unroll
+  for (int d = 32; d >= 1; d >>= 1) fine += __shfl_xor(fine, d);
+  if ((tid & 63) == 0) atomicAdd(&fine_s, static_cast<unsigned long long>(fine));   // (whole numbers: any order)
   __syncthreads();
   if (tid == 0) {
     p.offsets[p.batch] = clamp_i32(t[0]);
@@ -248,10 +259,20 @@ __global__ __launch_bounds__(kPlanThreads) void slot_plan_small_kernel(const Slo
     *p.status = clamp_i32(t[0] - static_cast<int64_t>(fine_s));
   }
   if (t[2] > 0) {   // (uniform) page i of those that come back, in the order of the table: the last goes first
-    for (int64_t i = tid; i < t[2]; i += threads) {
-      const int b = bisect(back_s, p.batch, i);
-      const int64_t to = top0 + t[2] - 1 - i;
-      if (to < p.capacity) p.free_pages[to] = p.table[static_cast<int64_t>(b) * p.width + (i - back_s[b])];
+    for (int64_t i0 = tid; i0 < t[2]; i0 += kTogether * threads) {
+      int32_t page[kTogether];
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        const int64_t i = min(i0 + j * threads, t[2] - 1);
+        const int b = bisect(back_s, p.batch, i);
+        page[j] = p.table[static_cast<int64_t>(b) * p.width + (i - back_s[b])];
+      }
+#pragma unroll
+      for (int j = 0; j < kTogether; ++j) {
+        const int64_t i = i0 + j * threads;
+        const int64_t to = top0 + t[2] - 1 - i;
+        if (i < t[2] && to < p.capacity) p.free_pages[to] = page[j];
+      }
     }
     __syncthreads();   // the stack is whole
   }
@@ -263,23 +284,33 @@ __global__ __launch_bounds__(kPlanThreads) void slot_plan_small_kernel(const Slo
   }
   if (!g.fill) return;
   const int32_t total = clamp_i32(t[0]);
-#pragma unroll 2
-  for (int i = tid; i < p.rows; i += threads) {
-    int32_t pos = 0, slot = -1;
-    if (i < total) {
-      const int b = bisect(off_s, p.batch, i);
-      const int64_t at = static_cast<int64_t>(start_s[b]) + (i - off_s[b]);
-      const int64_t col = at / p.page;
-      pos = clamp_i32(at);
-      if (col < count_s[b]) {
-        const int32_t page = col < have_s[b] ? p.table[static_cast<int64_t>(b) * p.width + col]
-                                             : p.free_pages[top - 1 - first_s[b] - (col - have_s[b])];
-        const int64_t at_slot = static_cast<int64_t>(page) * p.page + (at - col * p.page);
-        if (at_slot >= 0 && at_slot < 0x7FFFFFFF) slot = static_cast<int32_t>(at_slot);
+  for (int i0 = tid; i0 < p.rows; i0 += kTogether * threads) {
+    int32_t pos[kTogether], page[kTogether], in[kTogether];
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const int i = i0 + j * threads;
+      pos[j] = 0;
+      page[j] = -1;
+      in[j] = 0;
+      if (i < total && i < p.rows) {
+        const int b = bisect(off_s, p.batch, i);
+        const int64_t at = static_cast<int64_t>(start_s[b]) + (i - off_s[b]);
+        const int64_t col = static_cast<uint32_t>(at) / static_cast<uint32_t>(p.page);   // (at: below 2^32)
+        pos[j] = clamp_i32(at);
+        in[j] = static_cast<int32_t>(at - col * p.page);
+        if (col < count_s[b])
+          page[j] = col < have_s[b] ? p.table[static_cast<int64_t>(b) * p.width + col]
+                                    : p.free_pages[top - 1 - first_s[b] - (col - have_s[b])];
       }
     }
-    p.positions[i] = pos;
-    p.slots[i] = slot;
+#pragma unroll
+    for (int j = 0; j < kTogether; ++j) {
+      const int i = i0 + j * threads;
+      if (i >= p.rows) break;
+      const int64_t slot = static_cast<int64_t>(page[j]) * p.page + in[j];
+      p.positions[i] = pos[j];
+      p.slots[i] = page[j] >= 0 && slot < 0x7FFFFFFF ? static_cast<int32_t>(slot) : -1;
+    }
   }
 }
 
