@@ -231,6 +231,23 @@ def test_large_and_small_scores():
     c.check(c.run())
 
 
+@pytest.mark.parametrize("rate", [0.04, 0.17, 0.6, -0.3])   # scores' growth with a key
+@pytest.mark.parametrize("n, hq, hkv, d, dt", [(1, 4, 1, 128, torch.bfloat16), (9, 5, 1, 64, torch.bfloat16),
+                                               (90, 2, 2, 128, torch.bfloat16), (300, 1, 1, 128, torch.bfloat16),
+                                               (150, 1, 1, 256, torch.bfloat16), (40, 2, 1, 128, torch.float32),
+                                               (7, 2, 2, 64, torch.float32)])
+def test_scores_that_grow(n, hq, hkv, d, dt, rate):
+    c = Case(hq * d + n, [(n, 700), (min(n, 33), 33)], hq, hkv, d, 16, dt, spread=0.5)
+    c.q[..., 0] = d ** 0.5
+    for b, (_, length) in enumerate(c.lens):
+        t = torch.arange(length, device="cuda")
+        ramp = (rate * t).to(dt)
+        c.kc[c.table[b].long()[t // c.page], t % c.page, :, 0] = ramp[:, None]
+        c.k[b][:, :, 0] = _f64(ramp)[:, None]
+    for causal, window in ((True, 0), (False, 0), (True, 97)):
+        c.check(c.run(causal=causal, window=window), causal=causal, window=window)
+
+
 def test_caches_beyond_32_bit_offsets():
     """Pages of 4 MB apart: the last ones lie past 2^32 elements."""
     hkv, d, page = 1, 128, 16
