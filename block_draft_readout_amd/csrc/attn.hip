@@ -19,20 +19,37 @@ struct Choice {
   int whole;
 };
 
+// Measured: 16 requests' tokens over 8192 bf16 keys, 40 query and 8 kv heads of 128, pages of 16,
+// unless said otherwise; one kind of kernel against the next.
+//
+// Few rows, each wave with all of them and keys of its own, up to 64 packed rows (40 rows 107
+// against 120 us, 50 rows 112 against 121; at 80 they no longer fit the registers): what bounds
+// them is the cache's bytes.  Wider rows hold fewer (D = 256: 32 rows 65 against 68 us; fp32 of 256:
+// none, four waves' tiles are more than LDS holds).
+// Row tiles of 128, keys shared by four waves, up to 128 rows (65 rows 120 against 163 us, 80 rows
+// 125 against 176: a tile of 256 would be empty for the most part).
+// Row tiles of 256, two waves of a SIMD in opposite phases, past that (130 rows 177 against 183 us,
+// 200 rows 185 against 198, 520 rows 482 against 557); built where their registers and LDS suffice.
 Choice choose(const AttnProblem& p) {
   Choice c{};
   // rows of a request and kv head on average
   const int64_t rows = (p.rows * p.group + p.batch - 1) / p.batch;
   const int most = p.dt == BDR_F32 ? (p.dim == 256 ? 0 : 2) : p.dim == 256 ? 2 : 4;
   c.few = rows <= 16 * most ? static_cast<int>((rows + 15) / 16) : 0;
-  if (c.few == 0 && rows > 192 && p.dt == BDR_BF16 && (p.dim == 128 || (p.dim == 64 && !p.fp8))) c.few = -1;
+  if (c.few == 0 && rows > 128 && p.dt == BDR_BF16 && (p.dim == 128 || (p.dim == 64 && !p.fp8))) c.few = -1;
   c.bm = c.few > 0 ? 16 * c.few : c.few == 0 ? 128 : 256;
   const int64_t longest = static_cast<int64_t>(p.width) * p.page;
   const int64_t tiles = (p.rows * p.group + c.bm - 1) / c.bm + p.batch;   // row tiles at most
-  // one launch instead of two where a workgroup is through its keys in a few rounds of its waves
-  const int64_t at_once = c.few > 0 ? 128 * few_waves(p.fp8 ? 1 : p.dt == BDR_F32 ? 4 : 2, p.dim) : 256;
+  const int elem = p.fp8 ? 1 : p.dt == BDR_F32 ? 4 : 2;
+  // One launch instead of two where the longest table is through in a few rounds of a workgroup's
+  // waves.  A token over 100 keys 8.2 against 11.3 us, over 1000 the same, over 2000 23 against 13.7;
+  // 4 x 100 tokens over 200 keys 22 against 59 us.
+  const int64_t at_once = c.few > 0 ? 128 * few_waves(elem, p.dim) : 256;
   c.whole = longest <= at_once && tiles * p.hkv <= kMaxGrid;
-  c.shares = c.whole ? tiles : std::max<int64_t>(1, attn_per_cu(c.few, p.fp8 ? 1 : p.dt == BDR_F32 ? 4 : 2, p.dim) * kCus / p.hkv);
+  // else as many shares as the chip holds at once
+  c.shares = c.whole ? tiles : std::max<int64_t>(1, attn_per_cu(c.few, elem, p.dim) * kCus / p.hkv);
+  // key tiles that are worth a workgroup and its partials (8 tokens over 4096 keys, one request: 19
+  // us, with 2 tiles 26, with 24 tiles 25; 4 x 100 tokens over 2048 keys 47.5, 48 and 82 us)
   c.min_share = 8;
   return c;
 }

@@ -53,7 +53,7 @@ hipError_t run_attn_dim(const AttnArgs& g, int few, hipStream_t stream) {
     case 3: if constexpr (FEW >= 3) return run_attn_few<C, S, D, 3>(g, stream); break;
     case 4: if constexpr (FEW >= 4) return run_attn_few<C, S, D, 4>(g, stream); break;
     case -1: if constexpr (TALL) return run_attn<AttnTall<C, S, D, KT>>(g, stream); break;
-    default: return run_attn<AttnMany<C, S, D, 4, 1, KT>>(g, stream);
+    default: return run_attn<AttnMany<C, S, D, 4, KT>>(g, stream);
   }
   return hipErrorInvalidValue;
 }

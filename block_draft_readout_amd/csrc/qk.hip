@@ -241,7 +241,8 @@ __global__ __launch_bounds__(kQkThreads) void qk_kernel(const QkProblem g) {
 template <typename S, int D, bool FP8>
 static hipError_t run_qk(const QkProblem& g, hipStream_t stream) {
   // few tokens: a workgroup each; many: a wave each, so that a vector's two loads per
-  // lane and a token's angles come from the same wave's work
+  // lane and a token's angles come from the same wave's work (40 + 2 x 8 heads of 128, bf16:
+  // 1024 tokens 9.8 against 12.6 us, 2048 15.6 against 14.6, 8192 55.5 against 44.9 = 5.2 TB/s)
   if (g.rows >= 2048)
     hipLaunchKernelGGL((qk_kernel<S, D, FP8, 4>), dim3(static_cast<uint32_t>((g.rows + 3) / 4)),
                        dim3(kQkThreads), 0, stream, g);

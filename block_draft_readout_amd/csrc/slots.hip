@@ -319,6 +319,8 @@ __global__ __launch_bounds__(256) void slot_fill_kernel(const SlotArgs g) {
   if (i < g.p.rows) fill_row(g.p, i, g.p.offsets[g.p.batch]);
 }
 
+// Past this the rows are filled by the whole chip in a second launch (1000 requests with 1 to 64
+// tokens each: 19 us, all in one workgroup 29).
 constexpr int kFillRows = 4096;
 
 hipError_t launch_slots(const SlotProblem& p, hipStream_t stream) {
