@@ -833,6 +833,7 @@ int spec_slots(const int32_t* cached, const int32_t* new_tokens, int64_t batch, 
  *                contiguous
  *   k_out        [rows, kv_heads, D] dtype, contiguous, or NULL; may be k likewise
  *   slots        [rows] int32 with a cache; k_cache, v_cache both or neither
+ *                (two tokens with one slot: which of them each feature is from is open)
  *   pages >= 1, page_size >= 1, pages * page_size < 2^31; cache strides
  *                multiples of 16 bytes, < 2^30 elements, that keep all
  *                elements apart
