@@ -21,9 +21,10 @@
 // own, and the 32 x 32 result's registers are, rounded to bf16, the operand of the
 // second product as they lie (the keys of a step are taken in the order in which
 // a lane's registers hold them; V is read with the same order).
-// That rounding is half a step of 2^-8 of each weight, what the output's own bf16
-// rounding may be; the sum l takes the weights before it.  Scores, O, m and l are
-// fp32, and fp32 tensors have fp32 products throughout (MFMA 32x32x2).
+// That rounding is half a step of each weight: 2^-8 in bf16, what the output's own
+// rounding may be, and 2^-11 for e4m3 values, which fp16 holds as well as bf16, so that
+// their weights are fp16.  The sum l takes the weights before it.  Scores, O, m and l
+// are fp32, and fp32 tensors have fp32 products throughout (MFMA 32x32x2).
 #pragma once
 
 #include <type_traits>
@@ -252,6 +253,41 @@ __device__ __forceinline__ void widen16(u32x4_t v, u32x4_t& a, u32x4_t& b) {
   b = __builtin_bit_cast(u32x4_t, widen8(v.z, v.w));
 }
 
+// Values and their weights as the second product takes them: bf16, or fp16 where the cache holds
+// e4m3 codes (every code's value is one, and a weight keeps 11 bits for 8 at the same rate).
+typedef _Float16 f16x8_t __attribute__((ext_vector_type(8)));
+__device__ __forceinline__ bf16x8_t widen8_half(uint32_t v, uint32_t w) {   // 16 bits each, whatever their type
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  const f16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 1.0f, false);
+  const f16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(v, 1.0f, true);
+  const f16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, false);
+  const f16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(w, 1.0f, true);
+  return __builtin_bit_cast(bf16x8_t, f16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]});
+}
+template <typename C>
+__device__ __forceinline__ uint32_t pack_weights(float x, float y) {
+  if constexpr (sizeof(C) == 1) {
+    typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(uint32_t, f16x2_t{static_cast<_Float16>(x), static_cast<_Float16>(y)});
+  } else {
+    return pack_bf16(x, y);
+  }
+}
+template <typename C>
+__device__ __forceinline__ f32x4_t weigh(bf16x8_t v, u32x4_t w, f32x4_t o) {
+  if constexpr (sizeof(C) == 1)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8_t, v), __builtin_bit_cast(f16x8_t, w), o, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(v, __builtin_bit_cast(bf16x8_t, w), o, 0, 0, 0);
+}
+template <typename C>
+__device__ __forceinline__ f32x16_t weigh(bf16x8_t v, u32x4_t w, f32x16_t o) {
+  if constexpr (sizeof(C) == 1)
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8_t, v), __builtin_bit_cast(f16x8_t, w), o, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(v, __builtin_bit_cast(bf16x8_t, w), o, 0, 0, 0);
+}
+
 // A lane's key of a tile to come.  The page's id is asked for behind the loads of an earlier
 // tile and used after those have been waited for: an address that depends on it never holds up a
 // tile.
@@ -259,6 +295,20 @@ struct AttnPage {
   int32_t id;
   int32_t place;   // in the page; -1: the key is not read
 };
+
+// The reference that a row's exponentials are taken against follows the row's maximum only where
+// that has grown by more than kSlack (a factor of 2^8): probabilities are 256 at most then, which
+// costs no precision in floating point, and sums of 2^31 of them stay in range.  The maximum of
+// random scores still grows in every second of the first hundred tiles, and a new reference scales
+// all sums.  Nothing seen yet: a reference of 0.
+// fp16 weights are taken 2^7 larger (2^15 at most): those down to 2^-21 of the reference's keep all
+// their bits.  Sums and partials hold that factor too; it cancels in out, and lse takes it out.
+constexpr float kSlack = 8.f;
+template <typename C>
+constexpr float kLift = sizeof(C) == 1 ? 7.f : 0.f;
+template <typename C>
+constexpr float kDown = sizeof(C) == 1 ? 0x1p-7f : 1.f;
+__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
 
 // What both kinds of kernels share.
 template <typename T>
@@ -323,22 +373,15 @@ struct AttnLoader {
       *reinterpret_cast<uint2*>(out) = uint2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
     else
       *reinterpret_cast<f32x4_t*>(out) = f32x4_t{o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
-    if (p.lse && d == 0) p.lse[row] = l > 0.f ? (m + __builtin_amdgcn_logf(l)) * kLn2 : -INFINITY;
+    if (p.lse && d == 0)
+      p.lse[row] = l > 0.f ? (m + __builtin_amdgcn_logf(l * kDown<C>)) * kLn2 : -INFINITY;
   }
 };
-
-// The reference that a row's exponentials are taken against follows the row's maximum only where
-// that has grown by more than kSlack (a factor of 2^8): probabilities are 256 at most then, which
-// costs no precision in floating point, and sums of 2^31 of them stay in range.  The maximum of
-// random scores still grows in every second of the first hundred tiles, and a new reference scales
-// all sums.  Nothing seen yet: a reference of 0.
-constexpr float kSlack = 8.f;
-__device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
 
 // Scores of a lane's column: mask, running maximum and sum, probabilities in place.  N values of
 // keys key0 + key_of(i); `fold` takes the maximum over the lanes that hold the column's other keys.
 // Returns the factor of what was summed before.
-template <int N, typename KeyOf, typename Fold>
+template <typename C, int N, typename KeyOf, typename Fold>
 __device__ __forceinline__ float softmax_step(float (&s)[N], bool edge, int lo, int hi, float scale2, KeyOf key_of,
                                               Fold fold, float& m, float& l) {
   if (edge) {
@@ -360,7 +403,7 @@ __device__ __forceinline__ float softmax_step(float (&s)[N], bool edge, int lo, 
   float sum = 0.f;
 #pragma unroll
   for (int i = 0; i < N; ++i) {
-    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale2, -ref));
+    s[i] = __builtin_amdgcn_exp2f(fmaf(s[i], scale2, kLift<C> - ref));
     sum += s[i];
   }
   l = l * f + sum;
@@ -444,10 +487,16 @@ struct AttnManyBody : AttnLoader<T> {
     load_at(p, kb, vb, off, __ballot(in) & kAll, tid, g);
   }
 
-  static __device__ __forceinline__ void store16(char* lds, uint32_t at, uint32_t at_next, u32x4_t v) {
+  template <typename Keys>
+  static __device__ __forceinline__ void store16(char* lds, uint32_t at, uint32_t at_next, u32x4_t v, Keys) {
     if constexpr (T::CS == 1) {
       u32x4_t x, y;
-      widen16(v, x, y);
+      if constexpr (Keys::value) {
+        widen16(v, x, y);
+      } else {
+        x = __builtin_bit_cast(u32x4_t, widen8_half(v.x, v.y));
+        y = __builtin_bit_cast(u32x4_t, widen8_half(v.z, v.w));
+      }
       *reinterpret_cast<u32x4_t*>(lds + at) = x;
       *reinterpret_cast<u32x4_t*>(lds + at_next) = y;
     } else {
@@ -472,7 +521,7 @@ struct AttnManyBody : AttnLoader<T> {
     for (int i = 0; i < T::LOADS; ++i) {
       const int idx = tid + T::THREADS * i;
       const uint32_t row = idx / T::CPR, c = W * (idx % T::CPR);
-      store16(lds, place(row, c), place(row, c + W - 1), x[i]);
+      store16(lds, place(row, c), place(row, c + W - 1), x[i], Keys{});
     }
   }
   static __device__ __forceinline__ void store(char* lk, char* lv, int tid, Stage& g) {
@@ -510,7 +559,7 @@ struct AttnManyBody : AttnLoader<T> {
     }
   }
 
-  // Operand pieces of 16 values (bf16): features 32 i + lane % 32 of the keys that a lane's
+  // Operand pieces of 16 values (16 bits each): features 32 i + lane % 32 of the keys that a lane's
   // probabilities are of
   static __device__ __forceinline__ void read_values(const char* lv, int sub, int ks, int lane,
                                                      bf16x8_t (&v)[T::D / 32]) {
@@ -530,12 +579,12 @@ struct AttnManyBody : AttnLoader<T> {
 #pragma unroll
     for (int rt = 0; rt < T::RT; ++rt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) b[rt][e] = pack_bf16(p[rt][8 * ks + 2 * e], p[rt][8 * ks + 2 * e + 1]);
+      for (int e = 0; e < 4; ++e) b[rt][e] = pack_weights<C>(p[rt][8 * ks + 2 * e], p[rt][8 * ks + 2 * e + 1]);
 #pragma unroll
     for (int i = 0; i < T::D / 32; ++i)
 #pragma unroll
       for (int rt = 0; rt < T::RT; ++rt)
-        o[rt][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(v[i], __builtin_bit_cast(bf16x8_t, b[rt]), o[rt][i], 0, 0, 0);
+        o[rt][i] = weigh<C>(v[i], b[rt], o[rt][i]);
   }
   // (fp32: straight from LDS)
   static __device__ __forceinline__ void add_values_f32(const char* lv, int sub, int lane, const f32x16_t (&p)[T::RT],
@@ -710,7 +759,7 @@ struct AttnManyBody : AttnLoader<T> {
         hold();
       }
 #pragma unroll
-      for (int rt = 0; rt < T::RT; ++rt) ref[rt] = reference(mx[rt]);
+      for (int rt = 0; rt < T::RT; ++rt) ref[rt] = reference(mx[rt]) - kLift<C>;
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
 #pragma unroll
@@ -856,7 +905,7 @@ struct AttnTallBody : AttnManyBody<T> {
 #pragma unroll
           for (int r = 0; r < 16; ++r) o[0][i][r] *= f;
       }
-      const float ref = reference(mx);
+      const float ref = reference(mx) - kLift<C>;
       M::read_values(v0, 0, 0, lane, first_v);   // the first operands of the products
       float sum = 0.f;
 #pragma unroll
@@ -869,7 +918,7 @@ struct AttnTallBody : AttnManyBody<T> {
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) pr[u][ks][e] = pack_bf16(sc[u][8 * ks + 2 * e], sc[u][8 * ks + 2 * e + 1]);
+          for (int e = 0; e < 4; ++e) pr[u][ks][e] = pack_weights<C>(sc[u][8 * ks + 2 * e], sc[u][8 * ks + 2 * e + 1]);
       }
       l += sum;
       // (the probabilities belong to this phase)
@@ -895,8 +944,7 @@ struct AttnTallBody : AttnManyBody<T> {
         if (x == 1) M::store_one(v2, tid, stage.v, std::false_type{});
 #pragma unroll
         for (int i = 0; i < T::D / 32; ++i)
-          o[0][i] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-              first_v[i], __builtin_bit_cast(bf16x8_t, pr[x / 2][x % 2]), o[0][i], 0, 0, 0);
+          o[0][i] = weigh<C>(first_v[i], pr[x / 2][x % 2], o[0][i]);
 #pragma unroll
         for (int i = 0; i < T::D / 32; ++i) first_v[i] = v[i];
         __builtin_amdgcn_sched_barrier(0);
@@ -976,7 +1024,7 @@ __device__ __forceinline__ void read_tr4_codes(const uint32_t (&a)[4], bf16x8_t 
       : "v"(a[0]), "v"(a[1]), "v"(a[2]), "v"(a[3]), "n"(O0)
       : "memory");
 #pragma unroll
-  for (int i = 0; i < 4; ++i) v[i] = widen8(x[i].x, x[i].y);
+  for (int i = 0; i < 4; ++i) v[i] = widen8_half(x[i].x, x[i].y);
 }
 
 static __device__ const uint32_t kZeros16[4] __attribute__((aligned(16))) = {0, 0, 0, 0};
@@ -1125,7 +1173,7 @@ struct AttnFewBody : AttnLoader<T> {
       for (int rt = 0; rt < T::RT; ++rt)
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          b[rt][e] = pack_bf16(pr[rt][2 * e], pr[rt][2 * e + 1]);
+          b[rt][e] = pack_weights<C>(pr[rt][2 * e], pr[rt][2 * e + 1]);
       // 8 bytes of row `row` (and of 16 rows on) per lane; the turns of the chunks 2 i (i, e4m3) and
       // of the lane's own are of different bits
       const uint32_t e = (lane & 15) >> 1;
@@ -1148,8 +1196,7 @@ struct AttnFewBody : AttnLoader<T> {
         for (int i = 0; i < 4; ++i)
 #pragma unroll
           for (int rt = 0; rt < T::RT; ++rt)
-            o[rt][i0 + i] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[i], __builtin_bit_cast(bf16x8_t, b[rt]),
-                                                                     o[rt][i0 + i], 0, 0, 0);
+            o[rt][i0 + i] = weigh<C>(a[i], b[rt], o[rt][i0 + i]);
       }
     } else {
 #pragma unroll
@@ -1274,7 +1321,7 @@ struct AttnFewBody : AttnLoader<T> {
 #pragma unroll
         for (int i = 0; i < T::KT / 4; ++i) z[i] = pr[i / 8][rt][i % 8];
         const float was = mx[rt];
-        const float f = softmax_step<T::KT / 4>(
+        const float f = softmax_step<C, T::KT / 4>(
             z, edge, row_lo[rt], row_hi[rt], scale2,
             [&](int i) { return key0 + 16 * (i / 4) + 4 * (lane >> 4) + i % 4; },
             [](float v) { return max_xor32(max_xor16(v)); }, mx[rt], l[rt]);
