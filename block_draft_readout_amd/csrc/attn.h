@@ -22,9 +22,10 @@
 // second product as they lie (the keys of a step are taken in the order in which
 // a lane's registers hold them; V is read with the same order).
 // That rounding is half a step of each weight: 2^-8 in bf16, what the output's own
-// rounding may be, and 2^-11 for e4m3 values, which fp16 holds as well as bf16, so that
-// their weights are fp16.  The sum l takes the weights before it.  Scores, O, m and l
-// are fp32, and fp32 tensors have fp32 products throughout (MFMA 32x32x2).
+// rounding may be (2^-16 for few rows, whose weights go in as the sum of two bf16), and
+// 2^-11 for e4m3 values, which fp16 holds as well as bf16, so that their weights are
+// fp16.  The sum l takes the weights before it.  Scores, O, m and l are fp32, and fp32
+// tensors have fp32 products throughout (MFMA 32x32x2).
 #pragma once
 
 #include <type_traits>
@@ -202,6 +203,11 @@ struct AttnFew {
   static constexpr int PAGE_AT = Q_AT + (QLDS ? BM * D * ES : 0);   // page ids of a tile, 256 bytes a wave
   static constexpr int LDS_BYTES = PAGE_AT + 256 * WN;
   static constexpr int QN = D * ES / 64;                 // 16-byte query pieces of a lane and row
+  // bf16 terms of a weight.  The second one's products fit under the cache's loads (16 x 8 rows
+  // over up to 32768 positions 180.1 against 182.4 us, one token over 1000 12.8 against 13.2), but
+  // not where four tiles of 128 have a SIMD's registers for one wave (104 against 118 us), nor
+  // under many rows (2048 tokens over 16384: 515 against 758 us; D 256: 395 against 478).
+  static constexpr int TERMS = CS == 2 && (D * RT <= 384 || D == 256) ? 2 : 1;
   static constexpr int SIMD_WAVES = WN == 8 || (LDS_BYTES <= 80 * 1024 && kTwo) ? 2 : 1;
   static_assert(CPR <= 64 && KT % RPL == 0, "a load is whole rows");
   static_assert(16 * D * 4 + 128 <= WAVE_BYTES, "a wave's output and statistics fit its tiles' place");
@@ -1168,12 +1174,17 @@ struct AttnFewBody : AttnLoader<T> {
                                                     f32x4_t (&o)[T::RT][T::D / 16]) {
     const int grp = lane >> 4;
     if constexpr (T::ES == 2) {
-      u32x4_t b[T::RT];
+      u32x4_t b[T::TERMS][T::RT];
 #pragma unroll
       for (int rt = 0; rt < T::RT; ++rt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          b[rt][e] = pack_weights<C>(pr[rt][2 * e], pr[rt][2 * e + 1]);
+        for (int e = 0; e < 4; ++e) {
+          const float x = pr[rt][2 * e], y = pr[rt][2 * e + 1];
+          const uint32_t w = pack_weights<C>(x, y);
+          b[0][rt][e] = w;
+          if constexpr (T::TERMS == 2)
+            b[1][rt][e] = pack_bf16(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xFFFF0000u));
+        }
       // 8 bytes of row `row` (and of 16 rows on) per lane; the turns of the chunks 2 i (i, e4m3) and
       // of the lane's own are of different bits
       const uint32_t e = (lane & 15) >> 1;
@@ -1193,10 +1204,12 @@ struct AttnFewBody : AttnLoader<T> {
           else read_tr4_codes<32 * T::ROWB>(ad, a);
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int x = 0; x < T::TERMS; ++x)
 #pragma unroll
-          for (int rt = 0; rt < T::RT; ++rt)
-            o[rt][i0 + i] = weigh<C>(a[i], b[rt], o[rt][i0 + i]);
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int rt = 0; rt < T::RT; ++rt)
+              o[rt][i0 + i] = weigh<C>(a[i], b[x][rt], o[rt][i0 + i]);
       }
     } else {
 #pragma unroll

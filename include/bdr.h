@@ -864,8 +864,9 @@ int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stri
  * as they were.  Keys and values that no token sees may hold anything; a table
  * entry outside [0, pages) reads as keys and values of 0.  Products take bf16
  * (fp32) operands with fp32 sums; softmax statistics and sums are fp32; the
- * probabilities are rounded to bf16 as the second product's operand, to fp16
- * where the cache holds E4M3 codes (which fp16 holds exactly).
+ * probabilities are rounded to bf16 as the second product's operand (few rows:
+ * to the sum of two bf16), to fp16 where the cache holds E4M3 codes (which fp16
+ * holds exactly).
  *
  *   q              [rows, q_heads, D] dtype at row and head strides in elements
  *                  (as above); 0 <= rows, rows * q_heads <= 2^30; D 64, 128, 256;
