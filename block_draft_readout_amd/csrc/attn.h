@@ -373,14 +373,14 @@ struct AttnLoader {
     const int j = r / p.group;
     const int head = h * p.group + (r - j * p.group);
     const int64_t row = (static_cast<int64_t>(first) + j) * p.hq + head;
-    const float inv = l > 0.f ? v_scale / l : 0.f;
+    const float inv = l == 0.f ? 0.f : v_scale / l;   // (NaN stays)
     S* out = static_cast<S*>(p.out) + row * T::D + d;
     if constexpr (T::ES == 2)
       *reinterpret_cast<uint2*>(out) = uint2{pack_bf16(o[0] * inv, o[1] * inv), pack_bf16(o[2] * inv, o[3] * inv)};
     else
       *reinterpret_cast<f32x4_t*>(out) = f32x4_t{o[0] * inv, o[1] * inv, o[2] * inv, o[3] * inv};
     if (p.lse && d == 0)
-      p.lse[row] = l > 0.f ? (m + __builtin_amdgcn_logf(l * kDown<C>)) * kLn2 : -INFINITY;
+      p.lse[row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l * kDown<C>)) * kLn2;
   }
 };
 
