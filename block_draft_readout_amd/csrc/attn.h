@@ -316,6 +316,20 @@ template <typename C>
 constexpr float kDown = sizeof(C) == 1 ? 0x1p-7f : 1.f;
 __device__ __forceinline__ float reference(float m) { return m == -INFINITY ? 0.f : m; }
 
+// What the queries take over from the scores' factor, so that it is a positive number, as the
+// running maximum wants it: the sign, or that it is no number (the scale of a head's keys).  Keys
+// that a row does not see stay out of it that way.
+struct AttnSign {
+  bool flip, nan;
+};
+template <typename C>
+__device__ __forceinline__ AttnSign positive(float& scale2) {
+  const bool nan = sizeof(C) == 1 && !(fabsf(scale2) < INFINITY);   // (the call's own scale is a number)
+  const bool flip = scale2 < 0.f;
+  scale2 = nan ? 1.f : fmaxf(fabsf(scale2), 1e-30f);   // (0 times a masked score is no number)
+  return AttnSign{flip, nan};
+}
+
 // What both kinds of kernels share.
 template <typename T>
 struct AttnLoader {
@@ -352,17 +366,20 @@ struct AttnLoader {
   // A lane's 16-byte pieces of row r of the packed rows: features place(i) on.
   template <int QN, typename Place>
   static __device__ __forceinline__ void load_q(const AttnProblem& p, const AttnSeq& s, int h, int r, Place place,
-                                                bool flip, u32x4_t (&q)[QN]) {
+                                                AttnSign f, u32x4_t (&q)[QN]) {
     const bool in = r < s.n * p.group;
     const int j = in ? r / p.group : 0;
     const int head = in ? h * p.group + (r - j * p.group) : 0;
     const S* at = static_cast<const S*>(p.q) + static_cast<int64_t>(s.first + j) * p.q_row +
                   static_cast<int64_t>(head) * p.q_head;
-    const uint32_t sign = flip ? (T::ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
+    // (of all types: queries that nothing touches here would be waited for in the loop over the keys, and each
+    // tile's loads with them: 426 us for 396, 24 requests' chunks over 12000 bf16 keys of 256)
+    const uint32_t sign = f.flip ? (T::ES == 2 ? 0x80008000u : 0x80000000u) : 0u;
+    const uint32_t nan = f.nan ? (T::ES == 2 ? 0x7FFF7FFFu : 0x7FFFFFFFu) : 0u;
 #pragma unroll
     for (int i = 0; i < QN; ++i) {
       const u32x4_t v = in ? load16(at + place(i)) : u32x4_t{0, 0, 0, 0};
-      q[i] = u32x4_t{v.x ^ sign, v.y ^ sign, v.z ^ sign, v.w ^ sign};
+      q[i] = u32x4_t{(v.x ^ sign) | nan, (v.y ^ sign) | nan, (v.z ^ sign) | nan, (v.w ^ sign) | nan};
     }
   }
 
@@ -648,8 +665,7 @@ struct AttnManyBody : AttnLoader<T> {
       scale2 *= p.k_scale[h];
       v_scale = p.v_scale[h];
     }
-    const bool flip = scale2 < 0.f;   // the running maximum wants a positive scale
-    scale2 = fmaxf(fabsf(scale2), 1e-30f);
+    const AttnSign sign = positive<C>(scale2);
 
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
     const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_bytes;
@@ -668,7 +684,7 @@ struct AttnManyBody : AttnLoader<T> {
 #pragma unroll
     for (int rt = 0; rt < T::RT; ++rt) {
       const int r = r0 + 32 * rt + (lane & 31);
-      L::load_q(p, s, h, r, [&](int i) { return (2 * i + (lane >> 5)) * (16 / T::ES); }, flip, q[rt]);
+      L::load_q(p, s, h, r, [&](int i) { return (2 * i + (lane >> 5)) * (16 / T::ES); }, sign, q[rt]);
       const int at = s.len - s.n + r / p.group;
       row_hi[rt] = p.causal ? min(at + 1, s.len) : s.len;
       row_lo[rt] = p.window ? at - p.window + 1 : 0;
@@ -823,8 +839,7 @@ struct AttnTallBody : AttnManyBody<T> {
       scale2 *= p.k_scale[h];
       v_scale = p.v_scale[h];
     }
-    const bool flip = scale2 < 0.f;   // the running maximum wants a positive scale
-    scale2 = fmaxf(fabsf(scale2), 1e-30f);
+    const AttnSign sign = positive<C>(scale2);
 
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
     const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_bytes;
@@ -854,7 +869,7 @@ struct AttnTallBody : AttnManyBody<T> {
     page = L::page_of(g, table, (ta + 3) * T::KT, lo, hi, lane);
 
     u32x4_t q[1][T::QN];
-    L::load_q(p, s, h, r0 + (lane & 31), [&](int i) { return (2 * i + (lane >> 5)) * (16 / T::ES); }, flip, q[0]);
+    L::load_q(p, s, h, r0 + (lane & 31), [&](int i) { return (2 * i + (lane >> 5)) * (16 / T::ES); }, sign, q[0]);
     const int at = s.len - s.n + (r0 + (lane & 31)) / p.group;
     const int row_hi = p.causal ? min(at + 1, s.len) : s.len;
     const int row_lo = p.window ? at - p.window + 1 : 0;
@@ -1239,8 +1254,7 @@ struct AttnFewBody : AttnLoader<T> {
       scale2 *= p.k_scale[h];
       v_scale = p.v_scale[h];
     }
-    const bool flip = scale2 < 0.f;   // the running maximum wants a positive scale
-    scale2 = fmaxf(fabsf(scale2), 1e-30f);
+    const AttnSign sign = positive<C>(scale2);
 
     const int32_t* table = p.table + static_cast<int64_t>(b) * p.width;
     const char* kb = static_cast<const char*>(p.k_cache) + h * p.head_bytes;
@@ -1271,13 +1285,13 @@ struct AttnFewBody : AttnLoader<T> {
       if constexpr (T::QLDS) {
         if (wn == rt) {   // (WN waves, a row tile each: RT <= WN)
           u32x4_t x[T::QN];
-          L::load_q(p, s, h, r, [&](int i) { return q_place(i, lane >> 4); }, flip, x);
+          L::load_q(p, s, h, r, [&](int i) { return q_place(i, lane >> 4); }, sign, x);
 #pragma unroll
           for (int i = 0; i < T::QN; ++i)
             *reinterpret_cast<u32x4_t*>(lds + q_lds(16 * rt + (lane & 15), i, lane >> 4)) = x[i];
         }
       } else {
-        L::load_q(p, s, h, r, [&](int i) { return q_place(i, lane >> 4); }, flip, q[rt]);
+        L::load_q(p, s, h, r, [&](int i) { return q_place(i, lane >> 4); }, sign, q[rt]);
       }
       const int at = s.len - s.n + r / p.group;
       row_hi[rt] = p.causal ? min(at + 1, s.len) : s.len;

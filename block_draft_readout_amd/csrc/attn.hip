@@ -2,6 +2,7 @@
 // workgroups, and the workspace of its partials.
 
 #include <algorithm>
+#include <limits>
 
 #include "attn_run.h"
 
@@ -79,7 +80,7 @@ hipError_t launch_attn(const AttnProblem& p, void* workspace, hipStream_t stream
   g.shares = c.shares;
   g.min_share = c.min_share;
   g.whole = c.whole;
-  g.scale2 = p.scale * kLog2e;
+  g.scale2 = std::min(p.scale * kLog2e, std::numeric_limits<float>::max());
   // s = ceil(log2 page), magic = ceil(2^(31 + s) / page): exact for keys below 2^31
   while ((int64_t(1) << g.page_shift) < p.page) ++g.page_shift;
   g.page_magic = static_cast<uint32_t>(((uint64_t(1) << (31 + g.page_shift)) + p.page - 1) / p.page);

@@ -861,14 +861,14 @@ int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stri
  *   w_t = scale q . k_t,  out = sum_t exp(w_t) v_t / sum_t exp(w_t),
  *   lse = log sum_t exp(w_t)
  * A token that sees nothing, or scores of -inf alone, has out 0 and lse -inf; one
- * that sees a score of NaN or +inf has out and lse NaN.  Rows of no request are
- * left as they were.  Keys and values that no token sees may hold anything; a
- * value that is infinite or NaN and that some token of a request sees may also
- * make others of that request NaN.  A table entry outside [0, pages) reads as keys
- * and values of 0.  Products take bf16 (fp32) operands with fp32 sums; softmax
- * statistics and sums are fp32; the probabilities are rounded to bf16 as the second
- * product's operand (few rows: to the sum of two bf16), to fp16 where the cache
- * holds E4M3 codes (which fp16 holds exactly).
+ * that sees a score of NaN or +inf, or keys whose k_scale is no finite number, has
+ * out and lse NaN.  Rows of no request are left as they were.  Keys and values that
+ * no token sees may hold anything; a value that is infinite or NaN and that some
+ * token of a request sees may also make others of that request NaN.  A table entry
+ * outside [0, pages) reads as keys and values of 0.  Products take bf16 (fp32)
+ * operands with fp32 sums; softmax statistics and sums are fp32; the probabilities
+ * are rounded to bf16 as the second product's operand (few rows: to the sum of two
+ * bf16), to fp16 where the cache holds E4M3 codes (which fp16 holds exactly).
  *
  *   q              [rows, q_heads, D] dtype at row and head strides in elements
  *                  (as above); 0 <= rows, rows * q_heads <= 2^30; D 64, 128, 256;

@@ -92,3 +92,36 @@ def test_rows_with_no_weight():
         want = c.run()
         assert (want[0][:n, 2:] == 0).all() and (want[1][:n, 2:] == float("-inf")).all()
         c.check(want, requests=[1])
+
+
+E4M3 = [k for k in range(len(KINDS)) if KINDS[k][5]]
+
+
+@pytest.mark.parametrize("scale", [float("nan"), float("inf"), float("-inf")])
+@pytest.mark.parametrize("length", LENGTHS)
+@pytest.mark.parametrize("kind", E4M3)
+def test_scale_that_is_no_number(kind, length, scale):
+    """Of one kv head's keys: its rows are NaN where they see something, the others as they were."""
+    c = _case(kind, length)
+    group = c.hq // c.hkv
+    lens = [(n, length) for n, length in c.lens]
+    c.kv_len[1] = 0                          # request 1 sees nothing
+    want = c.run()
+    c.scales[0][0] = scale
+    out, lse = c.run()
+    n = lens[0][0]
+    assert out[:n, :group].isnan().all() and lse[:n, :group].isnan().all()
+    assert (out[n:n + 2] == 0).all() and (lse[n:n + 2] == float("-inf")).all()
+    _same((out, lse), want, (slice(0, n), slice(group, None)))
+
+
+@pytest.mark.parametrize("length", LENGTHS)
+@pytest.mark.parametrize("kind", E4M3)
+def test_negative_scales(kind, length):
+    c = _case(kind, length)
+    for scale, held in zip(c.scales, (c.k, c.v)):
+        scale[0] *= -1
+        for x in held:
+            x[:, 0] *= -1
+    for causal, window in ((True, 0), (False, 70)):
+        c.check(c.run(causal=causal, window=window), causal, window)
