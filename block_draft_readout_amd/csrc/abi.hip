@@ -1400,7 +1400,9 @@ int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stri
   BDR_TRY(no_overlap({ck}, {sq, sk, sv, oq, ok}));   // (keys and values may interleave)
   BDR_TRY(no_overlap({cv}, {sq, sk, sv, oq, ok}));
   auto in_place = [&](const void* in, const void* out, int64_t row, int64_t head, int heads) {
-    return in == out && head == head_dim && row == static_cast<int64_t>(heads) * head_dim;
+    // contiguous (the stride of an axis of one entry says nothing)
+    return in == out && (heads == 1 || head == head_dim) &&
+           (rows == 1 || row == static_cast<int64_t>(heads) * head_dim);
   };
   if (!(q_heads && in_place(q, q_out, q_row_stride, q_head_stride, q_heads))) BDR_TRY(no_overlap({oq}, {sq}));
   if (!(k_out && in_place(k, k_out, k_row_stride, k_head_stride, kv_heads))) BDR_TRY(no_overlap({ok}, {sk}));

@@ -1,0 +1,31 @@
+"""Host-side checks of the paged attention's calls that their documentation allows, by what is refused
+behind them: nothing is launched."""
+import pytest
+
+from test_abi_paged import A, _qk, at  # noqa: F401
+
+
+def _refusal(A, **k):
+    assert _qk(A, **k) == A.BDR_EINVAL
+    return A.load().bdr_last_error().decode()
+
+
+# rows, heads, row stride, head stride: contiguous ones (an axis of one entry has any stride)
+CONTIGUOUS = [(10, 8, 1024, 128), (1, 8, 1024, 128), (1, 8, 0, 128), (1, 8, 4096, 128), (10, 1, 128, 0),
+              (10, 1, 128, 512), (1, 1, 0, 0), (1, 1, 64, 256)]
+STRIDED = [(10, 8, 2048, 128), (2, 8, 0, 128), (10, 8, 1024, 256), (1, 8, 0, 256), (10, 1, 256, 128)]
+
+
+@pytest.mark.parametrize("rows,heads,row,head", CONTIGUOUS)
+def test_in_place_where_contiguous(A, rows, heads, row, head):  # noqa: F811
+    # the queries over themselves pass; the keys over the values, looked at later, do not
+    q = dict(rows=rows, hq=heads, qr=row, qh=head, q_out=at(0), k_out=at(2))
+    assert _refusal(A, **q) == "k_out overlaps v"
+    k = dict(rows=rows, hkv=heads, kr=row, kh=head, k_out=at(1), q_out=at(2), ps=16 * 1024, ts=1024)
+    assert _refusal(A, **k) == "q_out overlaps v"
+
+
+@pytest.mark.parametrize("rows,heads,row,head", STRIDED)
+def test_in_place_where_strided(A, rows, heads, row, head):  # noqa: F811
+    assert _refusal(A, rows=rows, hq=heads, qr=row, qh=head, q_out=at(0)) == "q_out overlaps q"
+    assert _refusal(A, rows=rows, hkv=heads, kr=row, kh=head, k_out=at(1), ps=16 * 1024, ts=1024) == "k_out overlaps k"
