@@ -74,6 +74,8 @@ def spec_slots(cached: torch.Tensor, new_tokens: torch.Tensor, block_table: torc
             _ints(t, name, shape, dev)
     if max_rows < 0:
         raise ValueError("max_rows must be >= 0")
+    if not -0x80000000 <= page_size <= 0x7FFFFFFF:   # (ctypes would cut it to 32 bits)
+        raise ValueError("page_size must be < 2^31")
     if out is None:
         # one allocation for all of them
         parts = torch.empty(3 * B + 2 * max_rows + 3, dtype=_I32, device=dev).split_with_sizes(
@@ -128,6 +130,8 @@ def _cache(k_cache, v_cache, k_scale, v_scale, heads: int, dim: int, dtype, devi
     pages, page, h, d = shape
     if h != heads or d != dim or stride[3] != 1:
         raise ValueError(f"k_cache must be [pages, page_size, {heads}, {dim}] with unit stride along D")
+    if page > 0x7FFFFFFF:
+        raise ValueError("page_size must be < 2^31")
     if v_cache.shape != shape:
         raise ValueError("k_cache and v_cache must have one shape")
     if 1 in shape:   # the stride of an axis of one entry says nothing
@@ -266,11 +270,13 @@ def dflash_paged_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torc
     elif not _is(out, dtype, (n, hq, d), dev):
         _tensor(out, "out")
         _need(out, "out", (n, hq, d), dtype, dev)
+    if window < 0:
+        raise ValueError("window must be >= 0")
     sums = torch.empty((n, hq), dtype=_F32, device=dev) if lse else None
     need = L.dflash_paged_attention_workspace_bytes(n, hq, hkv, d, dt, b, width, cache[1])
     wp, wn, _keep = _space(need, dev, workspace)
     _call("dflash_paged_attention", L.dflash_paged_attention, dev, q.data_ptr(), qr, qh, n, hq, hkv, d, dt,
           k_cache.data_ptr(), v_cache.data_ptr(), *cache, _ptr(k_scale), _ptr(v_scale),
           block_table.data_ptr(), b, width, query_offsets.data_ptr(), kv_len.data_ptr(),
-          d ** -0.5 if scale is None else scale, causal, window, out.data_ptr(), _ptr(sums), wp, wn)
+          d ** -0.5 if scale is None else scale, causal, min(window, 0x7FFFFFFF), out.data_ptr(), _ptr(sums), wp, wn)
     return (out, sums) if lse else out

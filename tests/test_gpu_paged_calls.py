@@ -2,6 +2,7 @@
 import pytest
 
 from gpu_util import log
+from test_gpu_paged_attention import Case
 from test_gpu_paged_qk import _case
 
 pytestmark = pytest.mark.gpu
@@ -23,3 +24,25 @@ def test_in_place_of_single_rows_and_heads(n, hq, hkv, d, dt):
     want = bdr().dspark_qk_norm_rope(q, k, None, pos, f, q_weight=wq, k_weight=wk)
     got = bdr().dspark_qk_norm_rope(q, k, None, pos, f, q_weight=wq, k_weight=wk, q_out=q, k_out=k)
     assert got[0] is q and got[1] is k and torch.equal(q, want[0]) and torch.equal(k, want[1])
+
+
+@pytest.mark.parametrize("page_size", [(1 << 32) + 16, -(1 << 32) + 16, 1 << 31])
+def test_page_sizes_past_32_bits(page_size):
+    z = lambda *s: torch.zeros(*s, dtype=torch.int32, device="cuda")
+    with pytest.raises((ValueError, bdr().BdrError)):
+        bdr().spec_slots(z(2), z(2), z(2, 1), z(2), z(2), z(1), page_size, 8)
+    if page_size > 0:   # a cache whose positions lie over each other
+        cache = torch.zeros(1, 1, 2, 64, dtype=torch.bfloat16, device="cuda").expand(1, page_size, 2, 64)
+        with pytest.raises((ValueError, bdr().BdrError)):
+            bdr().dflash_paged_attention(cache[0, :1], cache, cache, z(1, 1), z(2), z(1))
+
+
+def test_windows_past_32_bits():
+    c = Case(1, [(4, 200), (70, 90)], 4, 2, 64, 16)
+    want = c.run()
+    for window in (1 << 31, 1 << 32, (1 << 32) + 5, (1 << 40) - 1):   # past every context: none
+        got = c.run(window=window)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    for window in (-1, -(1 << 32), -(1 << 32) + 7):
+        with pytest.raises((ValueError, bdr().BdrError)):
+            c.run(window=window)
