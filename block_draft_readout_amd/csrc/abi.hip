@@ -1343,6 +1343,7 @@ int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stri
   if (rot_dim < 16 || rot_dim > head_dim || rot_dim % 16)
     return fail(BDR_EINVAL, "rot_dim %d must be a multiple of 16 in 16 .. head_dim", rot_dim);
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(BDR_EINVAL, "eps must be finite and >= 0");
+  if (q_heads == 0 && k_weight) q_weight = k_weight;   // (there is nothing that would read it)
   if ((q_weight == nullptr) != (k_weight == nullptr))
     return fail(BDR_EINVAL, "q_weight and k_weight must both be given or both be NULL");
   if ((k_cache == nullptr) != (v_cache == nullptr))
@@ -1376,8 +1377,8 @@ int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stri
   BDR_TRY(need_ptr(positions, "positions", 4));
   BDR_TRY(need_ptr(inv_freq, "inv_freq", 4));
   if (q_weight) {
-    BDR_TRY(need_ptr(q_weight, "q_weight"));
     BDR_TRY(need_ptr(k_weight, "k_weight"));
+    BDR_TRY(need_ptr(q_weight, "q_weight"));
   }
   const int64_t es = dt == BDR_BF16 ? 2 : 4;
   const Span sq{q_heads ? q : nullptr, q_heads ? head_span(rows, q_row_stride, q_heads, q_head_stride, head_dim) * es : 0, "q"};
@@ -1389,8 +1390,8 @@ int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stri
   const Span ck{k_cache, cb, "k_cache"}, cv{v_cache, cb, "v_cache"};
   const std::initializer_list<Span> rest = {{positions, rows * 4, "positions"},
                                             {inv_freq, rot_dim * 2, "inv_freq"},
-                                            {q_weight, head_dim * es, "q_weight"},
                                             {k_weight, head_dim * es, "k_weight"},
+                                            {q_weight, head_dim * es, "q_weight"},
                                             {cached ? slots : nullptr, rows * 4, "slots"},
                                             {k_scale, kv_heads * 4, "k_scale"},
                                             {v_scale, kv_heads * 4, "v_scale"}};

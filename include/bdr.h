@@ -828,7 +828,8 @@ int spec_slots(const int32_t* cached, const int32_t* new_tokens, int64_t batch, 
  *                head_dim D 64, 128 or 256
  *   positions    [rows] int32; inv_freq [rot_dim / 2] fp32; rot_dim a multiple of
  *                16 in 16 .. D
- *   q_weight, k_weight  [D] dtype, both or neither; eps finite, >= 0
+ *   q_weight, k_weight  [D] dtype, both or neither (with k_weight, q_weight is not
+ *                looked at where q_heads == 0); eps finite, >= 0
  *   q_out        [rows, q_heads, D] dtype, contiguous, may be q where q is
  *                contiguous
  *   k_out        [rows, kv_heads, D] dtype, contiguous, or NULL; may be k likewise

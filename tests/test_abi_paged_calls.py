@@ -29,3 +29,14 @@ def test_in_place_where_contiguous(A, rows, heads, row, head):  # noqa: F811
 def test_in_place_where_strided(A, rows, heads, row, head):  # noqa: F811
     assert _refusal(A, rows=rows, hq=heads, qr=row, qh=head, q_out=at(0)) == "q_out overlaps q"
     assert _refusal(A, rows=rows, hkv=heads, kr=row, kh=head, k_out=at(1), ps=16 * 1024, ts=1024) == "k_out overlaps k"
+
+
+def test_weights_without_queries(A):  # noqa: F811
+    """The keys' weight alone passes (the keys over the values do not), the queries' alone does not."""
+    none = dict(hq=0, q=None, q_out=None)
+    assert _refusal(A, **none, wq=None, k_out=at(2)) == "k_out overlaps v"
+    assert _refusal(A, **none, wq=at(5) + 2, k_out=at(2)) == "k_out overlaps v"
+    assert "weight" in _refusal(A, **none, wk=None)
+    assert "k_weight" in _refusal(A, **none, wq=None, wk=at(6) + 2)
+    assert "k_weight" in _refusal(A, **none, wq=None, k_out=at(6))
+    assert "weight" in _refusal(A, wq=None) and "weight" in _refusal(A, wk=None)

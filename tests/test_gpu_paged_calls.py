@@ -46,3 +46,19 @@ def test_windows_past_32_bits():
     for window in (-1, -(1 << 32), -(1 << 32) + 7):
         with pytest.raises((ValueError, bdr().BdrError)):
             c.run(window=window)
+
+
+@pytest.mark.parametrize("n,d,dt,inter", [(1, 128, torch.bfloat16, False), (2100, 64, torch.bfloat16, True),
+                                          (7, 256, torch.float32, False)])
+def test_weight_of_keys_without_queries(n, d, dt, inter):
+    """A drafter's context has keys and values alone: no weight of queries is needed, and none is read."""
+    q, k, v, wq, wk, f, pos = _case(n + d, n, 4, 2, d, d, dt)
+    slots = torch.randperm(n + 5, device="cuda")[:n].int()
+    caches = [[torch.zeros(n + 5, 1, 2, d, dtype=dt, device="cuda") for _ in range(2)] for _ in range(3)]
+    for (kc, vc), weights in zip(caches, (dict(q_weight=wq, k_weight=wk), dict(k_weight=wk),
+                                          dict(q_weight=torch.full_like(wk, float("nan")), k_weight=wk))):
+        bdr().dspark_qk_norm_rope(None, k, v, pos, f, interleaved=inter, slots=slots, k_cache=kc, v_cache=vc, **weights)
+    for kc, vc in caches[1:]:
+        assert torch.equal(kc, caches[0][0]) and torch.equal(vc, caches[0][1])
+    with_q = bdr().dspark_qk_norm_rope(q, k, None, pos, f, q_weight=wq, k_weight=wk, interleaved=inter)[1]
+    assert torch.equal(caches[1][0][slots.long(), 0], with_q)
