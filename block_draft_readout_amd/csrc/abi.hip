@@ -1244,6 +1244,9 @@ int cache_shape(const Cache& c, int kv_heads, int dt) {
     return fail(BDR_EINVAL, "the cache's strides must be multiples of 16 bytes and >= 0");
   if (c.page_stride > kMaxStride || c.token_stride > kMaxStride || c.head_stride > kMaxStride)
     return fail(BDR_EUNSUPPORTED, "the cache's strides must be < 2^30 elements");
+  // (its bytes stay within 63 bits, so that what overlaps it is seen)
+  if (c.pages * c.page_stride > kMaxElems || c.page * c.token_stride > kMaxElems)
+    return fail(BDR_EUNSUPPORTED, "the cache must span at most 2^40 elements");
   return BDR_OK;
 }
 

@@ -837,7 +837,8 @@ int spec_slots(const int32_t* cached, const int32_t* new_tokens, int64_t batch, 
  *                (two tokens with one slot: which of them each feature is from is open)
  *   pages >= 1, page_size >= 1, pages * page_size < 2^31; cache strides
  *                multiples of 16 bytes, < 2^30 elements, that keep all
- *                elements apart
+ *                elements apart; pages * page_stride and page_size *
+ *                token_stride at most 2^40
  *   k_scale, v_scale  [kv_heads] fp32, both or neither (not 0)
  */
 int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* k,

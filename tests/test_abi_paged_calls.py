@@ -2,7 +2,7 @@
 behind them: nothing is launched."""
 import pytest
 
-from test_abi_paged import A, _qk, at  # noqa: F401
+from test_abi_paged import A, _attn, _qk, at  # noqa: F401
 
 
 def _refusal(A, **k):
@@ -40,3 +40,13 @@ def test_weights_without_queries(A):  # noqa: F811
     assert "k_weight" in _refusal(A, **none, wq=None, wk=at(6) + 2)
     assert "k_weight" in _refusal(A, **none, wq=None, k_out=at(6))
     assert "weight" in _refusal(A, wq=None) and "weight" in _refusal(A, wk=None)
+
+
+def test_caches_past_all_memory(A):  # noqa: F811
+    """Pages and strides whose product passes 63 bits of bytes: what lies in such a cache is not seen."""
+    far = dict(dt=A.BDR_F32, page=1, pages=(1 << 31) - 1, ps=(1 << 30) - 4, ts=(1 << 30) - 4, hs=(1 << 30) - 4, hkv=2)
+    assert _attn(A, out=at(1), **far) == A.BDR_EUNSUPPORTED
+    assert _qk(A, k_out=at(10), **far) == A.BDR_EUNSUPPORTED
+    wide = dict(dt=A.BDR_F32, page=(1 << 31) - 1, pages=1, ps=0, ts=(1 << 30) - 4, hs=128, hkv=2)
+    assert _attn(A, out=at(1), **wide) == A.BDR_EUNSUPPORTED
+    assert _qk(A, k_out=at(10), **wide) == A.BDR_EUNSUPPORTED
