@@ -1272,7 +1272,9 @@ struct AttnFewBody : AttnLoader<T> {
     if (t < tb) {
       w = way(p, L::page_of(g, table, t * T::KT, lo, hi, lane));
       load_keys(p, kb, w, lane, lk);
+      __builtin_amdgcn_sched_barrier(0);   // (the order that the waits count on)
       place = ask(g, table, (t + T::WN) * T::KT, lo, hi, lane, ids);
+      __builtin_amdgcn_sched_barrier(0);
       load_values(p, vb, w, lane, lv);
     }
     u32x4_t q[T::RT][T::QLDS ? 1 : T::QN];
@@ -1324,7 +1326,9 @@ struct AttnFewBody : AttnLoader<T> {
         if (more) {
           w = way(p, page);
           load_keys(p, kb, w, lane, other);
+          __builtin_amdgcn_sched_barrier(0);   // (the order that the waits count on)
           place = ask(g, table, (t + 2 * T::WN) * T::KT, lo, hi, lane, ids);
+          __builtin_amdgcn_sched_barrier(0);
           load_values(p, vb, w, lane, other + T::TILE_BYTES);
         }
       }
@@ -1339,6 +1343,7 @@ struct AttnFewBody : AttnLoader<T> {
         if (more) {
           w = way(p, page);
           load_keys(p, kb, w, lane, lk);
+          __builtin_amdgcn_sched_barrier(0);
           place = ask(g, table, (t + 2 * T::WN) * T::KT, lo, hi, lane, ids);
         }
       }
