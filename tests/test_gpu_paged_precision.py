@@ -92,3 +92,23 @@ def test_small_weights_of_codes(n, down):
     top = 64 * _f64(c.scales[0])[0] * 128
     c.q.fill_(down * np.log(2) * 128 ** 0.5 / top)
     _check(c, c.run(causal=False), 2.0 ** -11, False)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_sine_and_cosine_are_rounded_once(interleaved):
+    """Pairs of (1, 0) turn into (cos a, sin a): half a step of fp32, where the angle's own 2^-53 of at
+    most 2^20 quarter turns, taken for its product and for 2 / pi, leaves 2^-32."""
+    import block_draft_readout_amd as m
+    n, d = 3000, 64
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x = torch.zeros(n, 1, d, device="cuda")
+    one, zero = (slice(0, d, 2), slice(1, d, 2)) if interleaved else (slice(0, d // 2), slice(d // 2, d))
+    x[..., one] = 1
+    pos = torch.randint(-(1 << 20), 1 << 20, (n,), generator=g, device="cuda").int()
+    pos[0] = 0
+    f = 1e4 ** (-torch.arange(d // 2, device="cuda", dtype=torch.float32) * 2 / d)
+    got = _f64(m.dspark_qk_norm_rope(x, x, None, pos, f, interleaved=interleaved)[0][:, 0])
+    a = _f64(pos)[:, None] * _f64(f)
+    for y, ref in ((got[:, one], np.cos(a)), (got[:, zero], np.sin(a))):
+        step = np.spacing(np.abs(ref).astype(np.float32)).astype(np.float64)
+        assert (np.abs(y - ref) <= 0.51 * step + 2.0 ** -32).all()
