@@ -1,9 +1,10 @@
 // Attention of new tokens over a paged cache (gfx950): types, schedule and kernel.
 //
 //   out[q] = sum_t softmax_t(scale q . k[t]) v[t]  over the positions t that the
-//   token sees, in one pass with a running maximum m and sum l: a tile of keys
-//   gives S = K Q^T, m' = max(m, max S), P = 2^(S - m'), and
-//   O = O 2^(m - m') + V^T P,  l = l 2^(m - m') + sum P;  out = O / l.
+//   token sees, in one pass with a running reference r and sum l: a tile of keys
+//   gives S = K Q^T, P = 2^(S - r'), and
+//   O = O 2^(r - r') + V^T P,  l = l 2^(r - r') + sum P;  out = O / l,
+//   where r' is max S if that exceeds r by more than kSlack, else r.
 //
 // Work.  The query heads that share a kv head read the same keys, so request b's
 // n tokens and the `group` heads of a kv head are packed into n * group rows, BM

@@ -31,6 +31,13 @@ struct Choice {
 // 125 against 176: a tile of 256 would be empty for the most part).
 // Row tiles of 256, two waves of a SIMD in opposite phases, past that (130 rows 177 against 183 us,
 // 200 rows 185 against 198, 520 rows 482 against 557); built where their registers and LDS suffice.
+// A last tile that is mostly empty costs a whole one: 260 rows 265 us, 520 rows 461.
+//
+// The rows are those of a request on average, and the measured requests are alike: the lengths are
+// on the device.  A call whose requests differ much is best made in two: a chunk of 2048 tokens
+// over 8192 keys (4 query heads a kv head) takes 267 us, 31 single tokens over 2000 to 8000 keys
+// 115, both together 427; with 255 single tokens, whose kernel the chunk then shares, 1561 against
+// 267 + 846.
 Choice choose(const AttnProblem& p) {
   Choice c{};
   // rows of a request and kv head on average
@@ -44,7 +51,11 @@ Choice choose(const AttnProblem& p) {
   const int elem = p.fp8 ? 1 : p.dt == BDR_F32 ? 4 : 2;
   // One launch instead of two where the longest table is through in a few rounds of a workgroup's
   // waves.  A token over 100 keys 8.2 against 11.3 us, over 1000 the same, over 2000 23 against 13.7;
-  // 4 x 100 tokens over 200 keys 22 against 59 us.
+  // 4 x 100 tokens over 200 keys 21 against 58 us, 8 prompts of 128 18 against 60; fp32, 5 x 7
+  // tokens over 128 keys 11 against 28 us, over 512 19 against 24, over 1001 29 against 25.  It is
+  // the table's width that is known here: contexts as short in a wide table take the longer times.
+  // Every workgroup looks through the lengths of all requests: 1000 tokens over up to 1024 keys 628
+  // against 405 us.
   const int64_t at_once = c.few > 0 ? 128 * few_waves(elem, p.dim) : 256;
   c.whole = longest <= at_once && tiles * p.hkv <= kMaxGrid;
   // else as many shares as the chip holds at once

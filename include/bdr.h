@@ -784,7 +784,9 @@ int dspark_distill_backward(const void* hidden, int64_t rows, int64_t hidden_siz
  * and rows behind the last token (a padded batch) have position 0 and slot -1.
  * Where the stack or the row is too short, the tokens without a page have slot
  * -1 and status counts the tokens without one (those past max_rows among them):
- * the step is then to be repeated with more pages.
+ * the step is then to be repeated with more pages.  A page is whatever number the
+ * table or the stack holds; one that is negative, or whose slots pass 2^31, gives
+ * slot -1 too and is not counted.
  *
  *   cached, new_tokens, page_count   [batch] int32; 0 <= batch <= 2^20
  *   block_table     [batch, max_pages] int32, entries of new columns written;
@@ -817,8 +819,7 @@ int spec_slots(const int32_t* cached, const int32_t* new_tokens, int64_t batch, 
  * Queries go to q_out, keys to k_out and / or slot slots[m] of the cache, values
  * to the same slot; a slot outside [0, pages * page_size) is not written.  Norm
  * and rotation are fp32; each output is rounded once (E4M3: of y / k_scale[h],
- * v / v_scale[h]; magnitudes past 448 become 448).  A slot that two rows name
- * gets one of them, by features.
+ * v / v_scale[h]; magnitudes past 448 become 448).
  *
  *   q, k, v      [rows, heads, D] dtype at row and head strides in elements
  *                (multiples of 8 (bf16) or 4 (f32), >= 0): views of one
@@ -870,7 +871,8 @@ int dspark_qk_norm_rope(const void* q, int64_t q_row_stride, int64_t q_head_stri
  * outside [0, pages) reads as keys and values of 0.  Products take bf16 (fp32)
  * operands with fp32 sums; softmax statistics and sums are fp32; the probabilities
  * are rounded to bf16 as the second product's operand (few rows: to the sum of two
- * bf16), to fp16 where the cache holds E4M3 codes (which fp16 holds exactly).
+ * bf16), to fp16 where the cache holds E4M3 codes (which fp16 holds exactly; below
+ * 2^-21 of a row's largest, to steps of 2^-31 of it).
  *
  *   q              [rows, q_heads, D] dtype at row and head strides in elements
  *                  (as above); 0 <= rows, rows * q_heads <= 2^30; D 64, 128, 256;
