@@ -23,7 +23,7 @@
 // second product as they lie (the keys of a step are taken in the order in which
 // a lane's registers hold them; V is read with the same order).
 // That rounding is half a step of each weight: 2^-8 in bf16, what the output's own
-// rounding may be (2^-16 for few rows, whose weights go in as the sum of two bf16), and
+// rounding may be (2^-15 for few rows, whose weights go in as the sum of two bf16), and
 // 2^-11 for e4m3 values, which fp16 holds as well as bf16, so that their weights are
 // fp16.  The sum l takes the weights before it.  Scores, O, m and l are fp32, and fp32
 // tensors have fp32 products throughout (MFMA 32x32x2).
@@ -205,7 +205,7 @@ struct AttnFew {
   static constexpr int LDS_BYTES = PAGE_AT + 256 * WN;
   static constexpr int QN = D * ES / 64;                 // 16-byte query pieces of a lane and row
   // bf16 terms of a weight.  The second one's products fit under the cache's loads (16 x 8 rows
-  // over up to 32768 positions 180.1 against 182.4 us, one token over 1000 12.8 against 13.2), but
+  // over up to 32768 positions 179.7 against 182.0 us, one token over 1000 12.7 against 13.3), but
   // not where four tiles of 128 have a SIMD's registers for one wave (104 against 118 us), nor
   // under many rows (2048 tokens over 16384: 515 against 758 us; D 256: 395 against 478).
   static constexpr int TERMS = CS == 2 && (D * RT <= 384 || D == 256) ? 2 : 1;
@@ -279,6 +279,15 @@ __device__ __forceinline__ uint32_t pack_weights(float x, float y) {
   } else {
     return pack_bf16(x, y);
   }
+}
+// Two terms of bf16 weights: their upper bits and the rest, at most 2^-7 of them and rounded.  Neither
+// is negative, and the rest is never 0 (2^-126 is nothing beside a weight): an infinite value
+// stays infinite.
+__device__ __forceinline__ uint2 split_weights(float x, float y) {
+  const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
+  return uint2{__builtin_amdgcn_perm(b, a, 0x07060302u),
+               pack_bf16(fmaxf(x - __uint_as_float(a & 0xFFFF0000u), 0x1p-126f),
+                         fmaxf(y - __uint_as_float(b & 0xFFFF0000u), 0x1p-126f))};
 }
 template <typename C>
 __device__ __forceinline__ f32x4_t weigh(bf16x8_t v, u32x4_t w, f32x4_t o) {
@@ -1196,10 +1205,13 @@ struct AttnFewBody : AttnLoader<T> {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float x = pr[rt][2 * e], y = pr[rt][2 * e + 1];
-          const uint32_t w = pack_weights<C>(x, y);
-          b[0][rt][e] = w;
-          if constexpr (T::TERMS == 2)
-            b[1][rt][e] = pack_bf16(x - __uint_as_float(w << 16), y - __uint_as_float(w & 0xFFFF0000u));
+          if constexpr (T::TERMS == 2) {
+            const uint2 w = split_weights(x, y);
+            b[0][rt][e] = w.x;
+            b[1][rt][e] = w.y;
+          } else {
+            b[0][rt][e] = pack_weights<C>(x, y);
+          }
         }
       // 8 bytes of row `row` (and of 16 rows on) per lane; the turns of the chunks 2 i (i, e4m3) and
       // of the lane's own are of different bits

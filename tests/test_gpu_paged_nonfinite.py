@@ -82,6 +82,27 @@ def test_infinite_keys(kind, length):
     _same((out, lse), want, slice(n, n + 2))
 
 
+@pytest.mark.parametrize("length", LENGTHS)
+@pytest.mark.parametrize("kind", [k for k in range(len(KINDS)) if not KINDS[k][5]])
+def test_infinite_values(kind, length):
+    """An infinite value that all rows of a request see is infinite in its feature, and only there; two
+    of both signs leave no number."""
+    n, hq, hkv, d, dt, _ = KINDS[kind]
+    c = Case(kind + length, [(n, length), (2, 40)], hq, hkv, d, 16, dt, spread=0.5, behind=1)
+    group = hq // hkv
+    want = c.run(causal=False)
+    inf = float("inf")
+    at = lambda t: (c.table[0, t // 16].long(), t % 16, 0)
+    c.vc[at(0)][3], c.vc[at(length - 1)][4] = inf, -inf
+    c.vc[at(11)][5], c.vc[at(length // 2)][5] = inf, -inf
+    out, lse = c.run(causal=False)
+    assert (out[:n, :group, 3] == inf).all() and (out[:n, :group, 4] == -inf).all()
+    assert out[:n, :group, 5].isnan().all()
+    out, one = out.clone(), want[0].clone()
+    out[:n, :group, 3:6] = one[:n, :group, 3:6] = 0
+    _same((out[:-1], lse[:-1]), (one[:-1], want[1][:-1]), slice(None))
+
+
 def test_rows_with_no_weight():
     """All scores that a row sees are -inf: no weight, as where it sees nothing."""
     for n, length in ((2, 100), (90, 100), (2, 3000)):

@@ -3,8 +3,8 @@
 Tolerance of an output, A = sum_t w_t |v_t|, s the largest sum of |scale q_d k_d| of the row, L keys,
 v the largest value, eps = 2^-24:
   output     half a step of bf16: 2^-8 |out|
-  weights    half a step each, W A: 2^-11 (fp16, for e4m3 caches), 2^-16 (few rows of bf16: the
-             rest of a rounding, at most 2^-8, rounded again)
+  weights    half a step each, W A: 2^-11 (fp16, for e4m3 caches), 2^-15 (few rows of bf16: the
+             upper 8 bits leave at most 2^-7, which is rounded, 2^-8 of it)
   fp16       weights below 2^-21 of the reference's have a step of 2^-31 of it, the reference's own
              weight is 1 of the sum: half a step of L weights, L 2^-32 v
   the rest   scores, exponentials and fp32 sums: 2 ((D + 4) eps s + (L + 70) eps) A
@@ -72,7 +72,7 @@ def test_weights_of_few_rows(n, group, d):
     for lens in ([(n, n + 6), (n, n + 1)], [(n, 1500), (n, 333)]):
         c = Case(n + d, lens, 2 * group, 2, d, 16, spread=0.3)
         _balance(c)
-        _check(c, c.run(causal=False), 2.0 ** -16, False)
+        _check(c, c.run(causal=False), 2.0 ** -15, False)
 
 
 @pytest.mark.parametrize("down", [20, 22, 26])
