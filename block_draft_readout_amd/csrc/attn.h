@@ -281,13 +281,13 @@ __device__ __forceinline__ uint32_t pack_weights(float x, float y) {
   }
 }
 // Two terms of bf16 weights: their upper bits and the rest, at most 2^-7 of them and rounded.  Neither
-// is negative, and the rest is never 0 (2^-126 is nothing beside a weight): an infinite value
-// stays infinite.
+// is negative, and the rest, a last bit of fp32 too large, is 0 with the weight alone: an infinite
+// value stays infinite.
 __device__ __forceinline__ uint2 split_weights(float x, float y) {
   const uint32_t a = __float_as_uint(x), b = __float_as_uint(y);
   return uint2{__builtin_amdgcn_perm(b, a, 0x07060302u),
-               pack_bf16(fmaxf(x - __uint_as_float(a & 0xFFFF0000u), 0x1p-126f),
-                         fmaxf(y - __uint_as_float(b & 0xFFFF0000u), 0x1p-126f))};
+               pack_bf16(fmaf(x, 1.f + 0x1p-23f, -__uint_as_float(a & 0xFFFF0000u)),
+                         fmaf(y, 1.f + 0x1p-23f, -__uint_as_float(b & 0xFFFF0000u)))};
 }
 template <typename C>
 __device__ __forceinline__ f32x4_t weigh(bf16x8_t v, u32x4_t w, f32x4_t o) {

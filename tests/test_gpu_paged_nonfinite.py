@@ -103,6 +103,20 @@ def test_infinite_values(kind, length):
     _same((out[:-1], lse[:-1]), (one[:-1], want[1][:-1]), slice(None))
 
 
+@pytest.mark.parametrize("length", LENGTHS)
+@pytest.mark.parametrize("kind", [k for k in range(len(KINDS)) if not KINDS[k][5] and KINDS[k][0] > 1])
+def test_large_values_that_others_see(kind, length):
+    """Values near the largest number, of positions that a row does not see, do not reach it."""
+    c = _case(kind, length)
+    n, group = c.lens[0][0], c.hq // c.hkv
+    want = c.run()
+    c.vc[c.table[0, (length - 1) // 16].long(), (length - 1) % 16, 0] = 3e38
+    got = c.run()
+    for a, b in zip(got, want):   # all but the last token's rows of that head
+        a[n - 1, :group] = b[n - 1, :group] = 0
+    _same((got[0][:-1], got[1][:-1]), (want[0][:-1], want[1][:-1]), slice(None))
+
+
 def test_rows_with_no_weight():
     """All scores that a row sees are -inf: no weight, as where it sees nothing."""
     for n, length in ((2, 100), (90, 100), (2, 3000)):
