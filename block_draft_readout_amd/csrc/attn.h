@@ -336,7 +336,7 @@ template <typename C>
 __device__ __forceinline__ AttnSign positive(float& scale2) {
   const bool nan = sizeof(C) == 1 && !(fabsf(scale2) < INFINITY);   // (the call's own scale is a number)
   const bool flip = scale2 < 0.f;
-  scale2 = nan ? 1.f : fmaxf(fabsf(scale2), 1e-30f);   // (0 times a masked score is no number)
+  scale2 = nan ? 1.f : fmaxf(fabsf(scale2), 0x1p-126f);   // (0 times a masked score is no number)
   return AttnSign{flip, nan};
 }
 

@@ -163,9 +163,9 @@ def dspark_qk_norm_rope(q: Optional[torch.Tensor], k: torch.Tensor, v: Optional[
                         q_out: Optional[torch.Tensor] = None,
                         k_out: Optional[torch.Tensor] = None):
     """Root-mean-square norm of each head of q [N, Hq, D] and k [N, Hkv, D] (weights [D], k_weight
-    alone without queries; None: no norm), then the rotation of the first 2 * len(inv_freq) features by positions[n] * inv_freq
-    (fp32), in pairs (i, i + half) or interleaved (2 i, 2 i + 1).  q, k and v may be views of one
-    projection's output (unit stride along D).
+    alone without queries; None: no norm), then the rotation of the first 2 * len(inv_freq)
+    features by positions[n] * inv_freq (fp32), in pairs (i, i + half) or interleaved (2 i, 2 i + 1).
+    q, k and v may be views of one projection's output (unit stride along D).
 
     With a cache, k and v [N, Hkv, D] are written at slots [N] of k_cache and v_cache (a slot
     outside the cache is skipped; uint8 caches take E4M3 codes of x / scale[head]).  Returns

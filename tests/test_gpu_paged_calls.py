@@ -62,3 +62,12 @@ def test_weight_of_keys_without_queries(n, d, dt, inter):
         assert torch.equal(kc, caches[0][0]) and torch.equal(vc, caches[0][1])
     with_q = bdr().dspark_qk_norm_rope(q, k, None, pos, f, q_weight=wq, k_weight=wk, interleaved=inter)[1]
     assert torch.equal(caches[1][0][slots.long(), 0], with_q)
+
+
+@pytest.mark.parametrize("n,dt", [(2, torch.bfloat16), (50, torch.bfloat16), (90, torch.bfloat16), (5, torch.float32)])
+def test_small_scales_of_large_queries(n, dt):
+    """Every finite scale counts: queries 2^110 times as large with a scale 2^-110 of the usual one."""
+    c = Case(n, [(n, 300), (1, 40)], 4, 2, 128, 16, dt)
+    want = c.run(scale=0.0625)
+    got = c.run(q=c.q * 2.0 ** 110, scale=0.0625 * 2.0 ** -110)
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
